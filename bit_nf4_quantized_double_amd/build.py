@@ -21,7 +21,8 @@ LIB = os.path.join(PKG, "libqlora.so")
 # The same sources with every raw global access range checked (skipped and
 # counted when outside its buffer; qlora_debug_oob_count reads the count).
 LIB_CHECKED = os.path.join(PKG, "libqlora_checked.so")
-SOURCES = ["nf4_table.cpp", "codec.hip", "gemm.hip", "skinny.hip", "lora.hip", "adapter.hip", "merge.hip", "abi.hip"]
+SOURCES = ["nf4_table.cpp", "codec.hip", "gemm.hip", "skinny.hip", "lora.hip", "adapter.hip", "merge.hip", "rows.hip", "int8.hip",
+           "abi.hip", "abi_int8.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -33,10 +34,12 @@ FLAGS = [
     "-fhip-fp32-correctly-rounded-divide-sqrt",
     "-Wall", "-Wno-unused-function",
 ]
-# The codec and the merge produce bit-exact results: no multiply-add is fused
-# behind the source's back there (the few fused ones are written explicitly).
+# The codec, the merge and the row quantizers produce bit-exact results: no
+# multiply-add is fused behind the source's back there (the few fused ones are
+# written explicitly).
 # Elsewhere products accumulate on the matrix cores and contraction is free.
-CONTRACT = {"codec.hip": "-ffp-contract=off", "merge.hip": "-ffp-contract=off"}
+CONTRACT = {"codec.hip": "-ffp-contract=off", "merge.hip": "-ffp-contract=off",
+            "rows.hip": "-ffp-contract=off"}
 
 
 def _compile(src: str, obj: str, checked: bool = False) -> None:

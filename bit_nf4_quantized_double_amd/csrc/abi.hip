@@ -10,6 +10,7 @@
 #include <string>
 
 #include "../../include/qlora.h"
+#include "abi.h"
 #include "common.h"
 #include "gemm_args.h"
 #include "skinny_args.h"
@@ -40,6 +41,8 @@ uint64_t oob_count_skinny(bool reset);
 uint64_t oob_count_lora(bool reset);
 uint64_t oob_count_adapter(bool reset);
 uint64_t oob_count_merge(bool reset);
+uint64_t oob_count_rows(bool reset);
+uint64_t oob_count_int8(bool reset);
 hipError_t launch_lora_down(const uint16_t* X, int M, int K, const uint16_t* A, int r, float s, uint16_t* U,
                             float* part, DropMask drop, bool f16, hipStream_t st);
 size_t rowdot_part_bytes(int64_t M, int64_t Kd, int r);
@@ -73,9 +76,9 @@ int device_compute_units() {
 
 }  // namespace qlora
 
-namespace {
+static thread_local std::string g_last_error;
 
-thread_local std::string g_last_error;
+namespace qlora {
 
 int fail(int status, const std::string& msg) {
   g_last_error = msg;
@@ -86,9 +89,14 @@ int hip_fail(hipError_t e, const char* where) {
   return fail(QLORA_ERR_HIP, std::string(where) + ": " + hipGetErrorString(e));
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+}  // namespace qlora
 
-size_t round_up(size_t x) { return (x + 255) & ~(size_t)255; }
+namespace {
+
+using qlora::aligned16;
+using qlora::fail;
+using qlora::hip_fail;
+using qlora::round_up;
 
 // Validates the frozen weight descriptor.
 int check_weight(const qlora_nf4_weight* w) {
@@ -223,7 +231,8 @@ int qlora_debug_oob_count(uint64_t* count, int reset) {
   if (!qlora::kBoundsChecked) return fail(QLORA_ERR_INVALID_ARG, "not the bounds-checked build");
   const bool rs = reset != 0;
   const uint64_t c[] = {qlora::oob_count_codec(rs), qlora::oob_count_gemm(rs), qlora::oob_count_skinny(rs),
-                        qlora::oob_count_lora(rs), qlora::oob_count_adapter(rs), qlora::oob_count_merge(rs)};
+                        qlora::oob_count_lora(rs), qlora::oob_count_adapter(rs), qlora::oob_count_merge(rs),
+                        qlora::oob_count_rows(rs), qlora::oob_count_int8(rs)};
   uint64_t total = 0;
   for (uint64_t v : c) {
     if (v == ~(uint64_t)0) return fail(QLORA_ERR_HIP, "reading the out-of-bounds counters failed");

@@ -124,6 +124,9 @@ def _load(path: str) -> ctypes.CDLL:
         fn = getattr(L, name)
         fn.restype = res
         fn.argtypes = args
+    from . import int8, rows  # their own entry points of the same library
+    rows._bind(L)
+    int8._bind(L)
     _loaded[path] = L
     return L
 

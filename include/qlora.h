@@ -372,6 +372,143 @@ int qlora_dequant_format(int format, int64_t n_out, int64_t k_in, const uint8_t 
                          hipStream_t stream);
 int qlora_format_table(int format, float out[16]);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Around and instead of the 4-bit linears of a decoder block: RMS norm with
+ * the residual's addition, SwiGLU, and a matrix product in 8-bit integers.
+ * Training uses the 16-bit forms and their backward passes; serving a merged
+ * model in 8 bits uses the 8-bit ones, where the norm and SwiGLU write the
+ * product's operand themselves.
+ *
+ * `dtype` is the element type of 16-bit inputs and outputs (QLORA_BF16 or
+ * QLORA_F16; QLORA_F32 where said).  Inputs marked [M, K] (ld) are row-major
+ * with rows `ld` elements apart (ld >= K) and need only be aligned to their
+ * element size; rows that are 16-byte aligned are read faster.  Outputs are
+ * contiguous and 16-byte aligned.  Any M and K from 0 on; sizes that leave
+ * nothing to do are no-ops.
+ *
+ * Quantized rows.  A row x of K values becomes int8 codes and one fp32 scale:
+ *     amax = max(max|x|, 1e-30),  scale = amax / 127,
+ *     code = 127 x / amax, rounded to nearest, ties to even  (|code| <= 127).
+ * A row that holds an infinity or a NaN gets zero codes and a NaN scale, so
+ * every value and product of it is NaN.  Codes are stored in operand tiles of
+ * the matrix cores, an opaque layout of qlora_int8_rows_bytes(M, K) bytes for
+ * rows and qlora_int8_weight_bytes(n_out, k_in) for a weight (columns padded
+ * to 128, rows to 16 or 32; the two layouts differ); qlora_int8_dequant_rows
+ * and _weight read them back.  The reduction of a product is at most 133144
+ * (QLORA_ERR_SHAPE beyond): its int32 sum is exact.
+ */
+enum { QLORA_BF16 = 0, QLORA_F16 = 1, QLORA_F32 = 2 };
+
+/* Widest row the norms take. */
+#define QLORA_MAX_NORM_WIDTH 32768
+
+/* A frozen 8-bit weight: borrowed device pointers, never written. */
+typedef struct {
+  int64_t n_out;         /* rows of W (output features) */
+  int64_t k_in;          /* columns of W (input features) */
+  const int8_t *codes;   /* qlora_int8_weight_bytes(n_out, k_in) */
+  const int8_t *codes_t; /* NULL, or the transpose's codes, qlora_int8_weight_bytes(k_in, n_out): the backward's */
+  const float *scale;    /* [n_out] */
+} qlora_int8_weight;
+
+/* Host functions: bytes of the opaque layouts (0 for sizes out of range). */
+size_t qlora_int8_weight_bytes(int64_t n_out, int64_t k_in);
+size_t qlora_int8_rows_bytes(int64_t M, int64_t K);
+
+/*
+ * Weight preparation, done once.
+ *   qlora_int8_quantize_weight   W [n_out, k_in] (ldw) in bf16, fp16 or fp32, quantized row by row
+ *   qlora_int8_pack_weight       W8 int8 [n_out, k_in] (ldw), codes from elsewhere, into the layout (its scales
+ *                                are used as they are: W = scale[n] W8[n][k]; codes of -128 are allowed)
+ *   qlora_int8_transpose_weight  the codes of W^T for the backward (n_out <= 133144)
+ *   qlora_int8_dequant_weight    E(scale[n] code) as 16-bit [n_out, k_in]
+ */
+int qlora_int8_quantize_weight(const void *W, int dtype, int64_t ldw, int64_t n_out, int64_t k_in,
+                               int8_t *codes, float *scale, hipStream_t stream);
+int qlora_int8_pack_weight(const int8_t *W8, int64_t ldw, int64_t n_out, int64_t k_in,
+                           int8_t *codes, hipStream_t stream);
+int qlora_int8_transpose_weight(const qlora_int8_weight *w, int8_t *codes_t, hipStream_t stream);
+int qlora_int8_dequant_weight(const qlora_int8_weight *w, uint16_t *W16, int dtype, hipStream_t stream);
+
+/*
+ * Quantize rows: X [M, K] (ldx) in bf16, fp16 or fp32; col_scale (fp32 [K] or
+ * NULL) multiplies the columns first, in fp32.  And back: E(scale[m] code).
+ */
+int qlora_int8_quantize_rows(const void *X, int dtype, int64_t ldx, int64_t M, int64_t K,
+                             const float *col_scale, int8_t *codes, float *scale, hipStream_t stream);
+int qlora_int8_dequant_rows(const int8_t *codes, const float *scale, int64_t M, int64_t K,
+                            uint16_t *X16, int dtype, hipStream_t stream);
+
+/*
+ * Y[m][n] = E(sx[m] scale[n] sum_k qx[m][k] code[n][k] + bias[n]), scales in
+ * fp32, rounded once; bias has the output's type, or is NULL.
+ *   qlora_int8_linear_fwd   X [M, k_in] (ldx) is quantized on the way in
+ *   qlora_int8_linear_rows  the rows are quantized already (by
+ *                           qlora_int8_quantize_rows, qlora_rms_norm_int8 or qlora_swiglu_int8)
+ *   qlora_int8_linear_bwd   dX [M, k_in] = E(sd[m] sum_n qd[m][n] code[n][k]) with qd, sd the quantized rows of
+ *                           dY[m][n] scale[n]: the gradient of the forward with its rounding to 8 bits passed
+ *                           straight through.  Needs codes_t.  There is no dW: the weight is frozen.
+ * Workspace: qlora_int8_workspace_bytes(QLORA_OP_FWD / _BWD, M, n_out, k_in),
+ * and qlora_int8_rows_workspace_bytes for _rows; the part for split sums is
+ * optional (without room the product runs unsplit, with the same result).
+ */
+size_t qlora_int8_workspace_bytes(int op, int64_t M, int64_t n_out, int64_t k_in);
+size_t qlora_int8_rows_workspace_bytes(int64_t M, int64_t n_out, int64_t k_in);
+int qlora_int8_linear_fwd(const qlora_int8_weight *w, const void *X, int64_t ldx, int64_t M,
+                          const uint16_t *bias, uint16_t *Y, int dtype, void *ws, size_t ws_bytes,
+                          hipStream_t stream);
+int qlora_int8_linear_rows(const qlora_int8_weight *w, const int8_t *codes, const float *scale,
+                           int64_t M, const uint16_t *bias, uint16_t *Y, int dtype, void *ws,
+                           size_t ws_bytes, hipStream_t stream);
+int qlora_int8_linear_bwd(const qlora_int8_weight *w, const void *dY, int64_t lddy, int64_t M,
+                          uint16_t *dX, int dtype, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * RMS norm with the residual's addition:
+ *     h = E(x + residual)  (h = x without a residual: H is then not written)
+ *     y = h gamma rstd,  rstd = 1 / sqrt(mean_k h^2 + eps), in fp32
+ * h is rounded to 16 bits because it is stored so, and the norm is of the
+ * stored values.  gamma: [K], of the rows' type or fp32 (gamma_dtype).  eps
+ * at least 1e-12.  K <= QLORA_MAX_NORM_WIDTH.  H may be X or the residual
+ * itself (same pointer and stride K).  A row whose sum of squares passes fp32
+ * gives rstd = 0 (y = 0) or, in 8 bits, a NaN row.
+ *   qlora_rms_norm_fwd   Y 16-bit [M, K], rstd fp32 [M] (for the backward)
+ *   qlora_rms_norm_int8  y quantized by rows from its fp32 values
+ *   qlora_rms_norm_bwd   from dY, H (X without a residual), rstd: with hat = h rstd and g = dY gamma,
+ *                          dX = E(dH + rstd (g - hat mean_k(g hat)))   (the residual's gradient as well)
+ *                          dgamma fp32 [K] = sum_m dY hat
+ *                        dH (or NULL): the gradient that reaches H by itself, as the residual stream.  dX may be
+ *                        dY or dH itself (same pointer and stride K).  Same inputs, same bits: no atomics.
+ *                        M == 0 writes zeros to dgamma.
+ */
+size_t qlora_rms_norm_bwd_workspace_bytes(int64_t M, int64_t K);
+int qlora_rms_norm_fwd(const void *X, int64_t ldx, const void *residual, int64_t ldr,
+                       const void *gamma, int gamma_dtype, int64_t M, int64_t K, float eps,
+                       uint16_t *H, uint16_t *Y, float *rstd, int dtype, hipStream_t stream);
+int qlora_rms_norm_int8(const void *X, int64_t ldx, const void *residual, int64_t ldr,
+                        const void *gamma, int gamma_dtype, int64_t M, int64_t K, float eps,
+                        uint16_t *H, int8_t *codes, float *scale, int dtype, hipStream_t stream);
+int qlora_rms_norm_bwd(const void *dY, int64_t lddy, const void *H, int64_t ldh, const float *rstd,
+                       const void *gamma, int gamma_dtype, const void *dH, int64_t lddh, int64_t M,
+                       int64_t K, uint16_t *dX, float *dgamma, int dtype, void *ws, size_t ws_bytes,
+                       hipStream_t stream);
+
+/*
+ * SwiGLU: y = g s u with s = 1 / (1 + e^-g), in fp32.  G and U [M, K] (ldg,
+ * ldu) may be the halves of one product's output.
+ *   qlora_swiglu_fwd   Y 16-bit [M, K]
+ *   qlora_swiglu_int8  y quantized by rows from its fp32 values (K <= 133144)
+ *   qlora_swiglu_bwd   dG = dY u s (1 + g (1 - s)),  dU = dY g s, 16-bit [M, K]
+ */
+int qlora_swiglu_fwd(const void *G, int64_t ldg, const void *U, int64_t ldu, int64_t M, int64_t K,
+                     uint16_t *Y, int dtype, hipStream_t stream);
+int qlora_swiglu_int8(const void *G, int64_t ldg, const void *U, int64_t ldu, int64_t M, int64_t K,
+                      int8_t *codes, float *scale, int dtype, hipStream_t stream);
+int qlora_swiglu_bwd(const void *dY, int64_t lddy, const void *G, int64_t ldg, const void *U,
+                     int64_t ldu, int64_t M, int64_t K, uint16_t *dG, uint16_t *dU, int dtype,
+                     hipStream_t stream);
+
 /* Host function: static description of a status code. */
 const char *qlora_status_string(int status);
 
