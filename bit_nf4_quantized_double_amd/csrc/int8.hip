@@ -3,10 +3,9 @@
 //   out[m][n] = E(sx[m] sw[n] sum_k x[m][k] w[n][k] + bias[n])
 //
 // x and w are int8 codes in operand tiles (int8_layout.h); the sum is exact
-// in int32 on the matrix cores (v_mfma_i32_32x32x32_i8), the scales are
-// applied in fp32, token first, and the result is rounded once to the 16-bit
-// output type.  w is the A operand, x the B operand: a lane then holds 16
-// consecutive outputs of one token.
+// in int32 on the matrix cores, the scales are applied in fp32, token first,
+// and the result is rounded once to the 16-bit output type.  w is the A
+// operand, x the B operand: a lane then holds consecutive outputs of a token.
 #include <algorithm>
 #include <climits>
 
@@ -19,6 +18,11 @@ namespace {
 typedef __attribute__((ext_vector_type(4))) int i32x4;
 typedef __attribute__((ext_vector_type(16))) int i32x16;
 
+// Stores that need no more than their elements' alignment (the hardware takes
+// any; rows of an odd number of outputs start anywhere).
+struct __attribute__((packed, aligned(2))) Un8 { uint32_t x, y; };
+struct __attribute__((packed, aligned(2))) Un16 { uint32_t x, y, z, w; };
+
 __device__ __forceinline__ i32x4 as_i32x4(uint4 u) { return __builtin_bit_cast(i32x4, u); }
 
 // Strips [first, total) of a tiled matrix as a buffer: what lies past its end
@@ -29,76 +33,301 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t strips_rsrc(const int8_t* p, i
   return make_rsrc(p + (first < total ? first : 0) * 16 * kp, (uint32_t)min(bytes, (int64_t)0x7fffffff));
 }
 
-// Up to 4 consecutive outputs n0 .. n0 + 3 of token m.
+// One output value.
 template <typename E>
-__device__ __forceinline__ void store4(const Int8GemmArgs& a, int64_t m, int64_t n0, const int* acc, float sx,
-                                       bool vec) {
+__device__ __forceinline__ float finish(const Int8GemmArgs& a, int sum, float sx, int64_t n) {
+  const bool ok = n < a.n && in_bounds(n, 1, a.n);
+  float y = (float)sum * sx;
+  if (a.sw) y *= ok ? a.sw[n] : 0.f;
+  if (a.bias) y += ok ? E::widen(a.bias[n]) : 0.f;
+  return y;
+}
+
+__device__ __forceinline__ float token_scale(const Int8GemmArgs& a, int64_t m) {
+  return m < a.m && in_bounds(m, 1, a.m) ? a.sx[m] : 0.f;
+}
+
+// 4 consecutive outputs n0 .. n0 + 3 of token m, as far as they exist (n0 a
+// multiple of 4).
+template <typename E>
+__device__ __forceinline__ void store4(const Int8GemmArgs& a, int64_t m, int64_t n0, i32x4 sum, float sx) {
   if (m >= a.m || n0 >= a.n) return;
-  float y[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const bool ok = n0 + i < a.n;
-    y[i] = (float)acc[i] * sx;
-    if (a.sw) y[i] *= ok && in_bounds(n0 + i, 1, a.n) ? a.sw[n0 + i] : 0.f;
-    if (a.bias) y[i] += ok && in_bounds(n0 + i, 1, a.n) ? E::widen(a.bias[n0 + i]) : 0.f;
-  }
-  const int64_t e = m * a.n + n0;
-  const uint32_t lo = E::pack2(y[0], y[1]), hi = E::pack2(y[2], y[3]);
-  if (vec && n0 + 4 <= a.n) {
-    if (in_bounds(e, 4, a.m * a.n)) *reinterpret_cast<uint2*>(a.out + e) = make_uint2(lo, hi);
+  const int64_t e = m * a.n + n0, size = a.m * a.n;
+  const uint32_t d[2] = {E::pack2(finish<E>(a, sum[0], sx, n0), finish<E>(a, sum[1], sx, n0 + 1)),
+                         E::pack2(finish<E>(a, sum[2], sx, n0 + 2), finish<E>(a, sum[3], sx, n0 + 3))};
+  if (n0 + 4 <= a.n) {
+    if (in_bounds(e, 4, size)) *reinterpret_cast<Un8*>(a.out + e) = Un8{d[0], d[1]};
   } else {
-    const uint32_t d[2] = {lo, hi};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (n0 + i < a.n && in_bounds(e + i, 1, a.m * a.n)) a.out[e + i] = (uint16_t)(d[i >> 1] >> (16 * (i & 1)));
+      if (n0 + i < a.n && in_bounds(e + i, 1, size)) a.out[e + i] = (uint16_t)(d[i >> 1] >> (16 * (i & 1)));
   }
 }
 
-// Tile of 128 outputs x 128 tokens, 4 waves of 64 x 64, operands straight
-// from memory into registers.
-template <typename E>
-__global__ __launch_bounds__(256) void k_int8_gemm(Int8GemmArgs a) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// Hand-off of LDS between waves: this wave's own LDS operations are done,
+// then the barrier.  Global loads stay in flight (a __syncthreads would wait
+// for them).
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// XCD-aware tile order: workgroups are dealt round-robin to the 8 XCDs, so
+// each XCD gets a contiguous run of an order that goes column-major inside
+// bands of 4 token blocks: the 32 tiles an XCD works on at a time share 4
+// token blocks and 8 output blocks in its L2.
+__device__ __forceinline__ void tile_of(uint32_t lin, uint32_t mt, uint32_t nt, uint32_t& tm, uint32_t& tn) {
+  constexpr uint32_t RB = 4;
+  const uint32_t total = mt * nt, whole = total & ~7u;
+  const uint32_t t = lin < whole ? (lin & 7u) * (whole >> 3) + (lin >> 3) : lin;
+  const uint32_t band = t / (RB * nt), rows = min(RB, mt - band * RB), within = t - band * RB * nt;
+  tn = within / rows;
+  tm = band * RB + within % rows;
+}
+
+// Many tokens.  Workgroup tile: 64 WM tokens x 128 WN outputs, one wave for
+// each 64 x 128 of it (8 accumulators of 32 x 32, 128 registers).  A 128-deep
+// step is 4 sub-steps of one 32 x 32 x 32 MFMA per accumulator.
+//
+// The step's W tile goes through LDS (global -> registers -> LDS, double
+// buffered), where the WM waves that share its rows read it; each wave loads
+// its own token rows straight into registers, one step ahead, since only WN
+// waves share them and the first-level cache serves that.  LDS then carries
+// 128 WN x 128 bytes in and WM times that out per step, less than half of
+// what it would with both operands in it, and stays below the matrix cores'
+// time (256 x 256: 32 KB in, 128 KB out, 64 KB through the cache in 2048
+// matrix-core cycles).
+//
+// The barrier of a step stands before its last sub-step: by then the next W
+// tile is written and every wave has this one's last operands in registers,
+// so the MFMAs of the last sub-step run while the next step's operands come.
+//
+// ksplit > 1: workgroup z of a tile sums its own range of steps and stores
+// the int32 sums to part[z]; k_int8_reduce adds them and finishes.
+template <int WM, int WN, typename E>
+__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_int8_gemm(Int8GemmArgs a) {
+  constexpr int kThreads = 64 * WM * WN, BM = 64 * WM, BN = 128 * WN;
+  constexpr int kTile = BN * 128;                     // bytes of a W tile
+  constexpr int kStage = kTile / (16 * kThreads);     // 16-byte pieces of it per thread
+  constexpr int kPitch = 128 + 8;                     // output staging: 16-bit elements per token
+  constexpr int kOut = WM * WN * 32 * kPitch * 2;     // bytes: 32 tokens x 128 outputs per wave
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kTile > kOut ? 2 * kTile : kOut];
+  // uniform across the wave: buffer resources made from it stay scalar
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const uint32_t mt = (uint32_t)((a.m + BM - 1) / BM), nt = (uint32_t)((a.n + BN - 1) / BN);
+  const uint32_t tiles = mt * nt;
+  const int z = blockIdx.x / tiles;
+  uint32_t tm, tn;
+  tile_of(blockIdx.x % tiles, mt, nt, tm, tn);
+  const int64_t m0 = (int64_t)tm * BM + 64 * wm, n0 = (int64_t)tn * BN;
   const int64_t kp = int8_kp(a.k);
-  const int64_t tn = (a.n + 127) / 128;
-  const int64_t n0 = blockIdx.x % tn * 128 + 64 * (wave & 1), m0 = blockIdx.x / tn * 128 + 64 * (wave >> 1);
+  const uint32_t strip = 16u * (uint32_t)kp;
+  const uint32_t steps = (uint32_t)(kp >> 7), per = (steps + a.ksplit - 1) / a.ksplit;
+  const uint32_t s0 = min(z * per, steps), s1 = min(s0 + per, steps);
+
   const __amdgpu_buffer_rsrc_t rw = strips_rsrc(a.w, n0 >> 4, int8_weight_strips(a.n), kp);
   const __amdgpu_buffer_rsrc_t rx = strips_rsrc(a.x, m0 >> 4, int8_row_strips(a.m), kp);
-  // lane l of a 32-row operand: row l & 31, half l >> 5 of 32 columns
-  const uint32_t strip = 16u * (uint32_t)kp;
-  const uint32_t at = (uint32_t)((lane >> 4) & 1) * strip + (uint32_t)(lane >> 5) * 256u + (uint32_t)(lane & 15) * 16u;
-  i32x16 acc[2][2];
+  // a 32 x 32 operand: lane l has row l & 31 and the half l >> 5 of the columns
+  const uint32_t inner = (uint32_t)(lane >> 5) * 256u + (uint32_t)(lane & 15) * 16u;
+  const uint32_t xat = (uint32_t)((lane >> 4) & 1) * strip + inner;
+  const uint32_t wat = (uint32_t)(8 * wn + ((lane >> 4) & 1)) * 2048u + inner;  // in the LDS tile
+
+  uint4 st[kStage], xf[4][2], wf[2][4];
+  auto load_stage = [&](uint32_t s) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+    for (int u = 0; u < kStage; ++u) {
+      const uint32_t i = u * kThreads + tid;
+      st[u] = buf_load16(rw, s < s1 ? (i >> 7) * strip + s * 2048u + (i & 127u) * 16u : kOOB);
+    }
+  };
+  auto write_stage = [&](int buf) {
+#pragma unroll
+    for (int u = 0; u < kStage; ++u)
+      *reinterpret_cast<uint4*>(lds + buf * kTile + (u * kThreads + tid) * 16) = st[u];
+  };
+  auto load_x = [&](uint32_t s, int q) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      xf[q][j] = buf_load16(rx, s < s1 ? xat + 2u * j * strip + s * 2048u + q * 512u : kOOB);
+  };
+  auto read_w = [&](int buf, int q, uint4 (&f)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      f[i] = *reinterpret_cast<const uint4*>(lds + buf * kTile + wat + i * 4096 + q * 512);
+  };
+
+  i32x16 acc[4][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
-  for (uint32_t k = 0; k < (uint32_t)kp; k += 32) {
-    uint4 w[2], x[2];
+
+  load_stage(s0);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) w[i] = buf_load16(rw, at + 2u * i * strip + (k >> 6) * 1024u + ((k >> 5) & 1u) * 512u);
+  for (int q = 0; q < 4; ++q) load_x(s0, q);
+  write_stage(0);
+  load_stage(s0 + 1);
+  lds_barrier();
+  read_w(0, 0, wf[0]);
+  for (uint32_t s = s0; s < s1; ++s) {
+    const int buf = (s - s0) & 1;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) x[i] = buf_load16(rx, at + 2u * i * strip + (k >> 6) * 1024u + ((k >> 5) & 1u) * 512u);
+    for (int q = 0; q < 4; ++q) {
+      if (q == 3) lds_barrier();
+      if (q < 3) read_w(buf, q + 1, wf[(q + 1) & 1]);
+      else read_w(buf ^ 1, 0, wf[0]);
+      if (q == 0) {
+        write_stage(buf ^ 1);
+        load_stage(s + 2);
+      }
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(as_i32x4(w[i]), as_i32x4(x[j]), acc[i][j], 0, 0, 0);
+        for (int j = 0; j < 2; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(as_i32x4(wf[q & 1][i]), as_i32x4(xf[q][j]), acc[i][j], 0, 0, 0);
+      load_x(s + 1, q);
+    }
   }
-  const bool vec = a.n % 4 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 7u) == 0;
+
+  // lane: token (lane & 31) of each half j, outputs 32 i + 16 (lane >> 5) .. + 15
+  const int h = lane >> 5;
+  const int64_t nw = n0 + 128 * wn;
+  if (a.ksplit > 1) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int64_t m = m0 + 32 * j + (lane & 31);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int64_t n = nw + 32 * i + 16 * h + 4 * v, np = (a.n + 3) & ~(int64_t)3;
+          const int64_t e = ((int64_t)z * a.m + m) * np + n;
+          if (m < a.m && n < np && in_bounds(e, 4, (int64_t)a.ksplit * a.m * np))
+            *reinterpret_cast<int4*>(a.part + e) =
+                make_int4(acc[i][j][4 * v], acc[i][j][4 * v + 1], acc[i][j][4 * v + 2], acc[i][j][4 * v + 3]);
+        }
+    }
+    return;
+  }
+  // Through LDS, so that a token's 128 outputs leave as whole lines.
+  lds_barrier();  // every wave has read its last operands
+  uint16_t* so = reinterpret_cast<uint16_t*>(lds) + wave * 32 * kPitch;
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    const int64_t m = m0 + 32 * j + (lane & 31);
-    const float sx = m < a.m && in_bounds(m, 1, a.m) ? a.sx[m] : 0.f;
+    const float sx = token_scale(a, m0 + 32 * j + (lane & 31));
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 4; ++i) {
+      uint32_t d[8];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int v[4] = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-        store4<E>(a, m, n0 + 32 * i + 16 * (lane >> 5) + 4 * q, v, sx, vec);
+      for (int v = 0; v < 8; ++v) {
+        const int64_t n = nw + 32 * i + 16 * h + 2 * v;
+        d[v] = E::pack2(finish<E>(a, acc[i][j][2 * v], sx, n), finish<E>(a, acc[i][j][2 * v + 1], sx, n + 1));
       }
+      uint4* o = reinterpret_cast<uint4*>(so + (lane & 31) * kPitch + 32 * i + 16 * h);
+      o[0] = make_uint4(d[0], d[1], d[2], d[3]);
+      o[1] = make_uint4(d[4], d[5], d[6], d[7]);
+    }
+    // the wave's own region: no other wave touches it
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const int row = 4 * r + (lane >> 4), col = (lane & 15) * 8;
+      const uint4 u = *reinterpret_cast<const uint4*>(so + row * kPitch + col);
+      const int64_t m = m0 + 32 * j + row, n = nw + col, e = m * a.n + n;
+      if (m >= a.m || n >= a.n) continue;
+      if (n + 8 <= a.n) {
+        if (in_bounds(e, 8, a.m * a.n)) *reinterpret_cast<Un16*>(a.out + e) = Un16{u.x, u.y, u.z, u.w};
+      } else {
+        const uint32_t d[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (n + i < a.n && in_bounds(e + i, 1, a.m * a.n)) a.out[e + i] = (uint16_t)(d[i >> 1] >> (16 * (i & 1)));
+      }
+    }
   }
+}
+
+// Few tokens: up to 16 TT of them, every one against every weight row, the
+// weight read once.  A workgroup takes one strip pair (32 outputs) and its NW
+// waves share out the reduction, 64 columns in turn; a wave reads weight
+// tiles and token tiles straight into the MFMA's registers, whole kilobytes
+// at a time, and the waves' sums meet in LDS.  Bound by reading the weight.
+template <int TT, int NW, typename E>
+__global__ __launch_bounds__(64 * NW) void k_int8_few(Int8GemmArgs a) {
+  __shared__ i32x4 s_sum[NW][2 * TT][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t kp = int8_kp(a.k), groups = (a.n + 31) / 32;
+  const int64_t group = blockIdx.x % groups;
+  const int z = blockIdx.x / groups;
+  const uint32_t strip = 16u * (uint32_t)kp;
+  const uint32_t chunks = (uint32_t)(kp >> 6), per = (chunks + a.ksplit - 1) / a.ksplit;
+  const uint32_t c0 = min(z * per, chunks), c1 = min(c0 + per, chunks);
+  const __amdgpu_buffer_rsrc_t rw = strips_rsrc(a.w, 2 * group, int8_weight_strips(a.n), kp);
+  const __amdgpu_buffer_rsrc_t rx = strips_rsrc(a.x, 0, int8_row_strips(a.m), kp);
+  const uint32_t at = lane * 16u;
+  i32x4 acc[2][TT];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) acc[i][t][v] = 0;
+  // token rows past m are not read
+  uint32_t xat[TT];
+#pragma unroll
+  for (int t = 0; t < TT; ++t) xat[t] = 16 * t + (lane & 15) < a.m ? t * strip + at : kOOB;
+  constexpr int U = 4;
+  for (uint32_t c = c0 + wave; c < c1; c += U * NW) {
+    uint4 w[U][2], x[U][TT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t cc = c + u * NW;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) w[u][i] = buf_load16(rw, cc < c1 ? i * strip + cc * 1024u + at : kOOB);
+#pragma unroll
+      for (int t = 0; t < TT; ++t) x[u][t] = buf_load16(rx, cc < c1 && xat[t] != kOOB ? xat[t] + cc * 1024u : kOOB);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+          acc[i][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(as_i32x4(w[u][i]), as_i32x4(x[u][t]), acc[i][t], 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) s_sum[wave][i * TT + t][lane] = acc[i][t];
+  __syncthreads();
+  // D row 4 g + i of strip `half` is output 16 (g & 1) + 4 (2 half + g / 2) + i
+  for (int tile = wave; tile < 2 * TT; tile += NW) {
+    i32x4 sum = s_sum[0][tile][lane];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) sum += s_sum[w][tile][lane];
+    const int half = tile / TT, t = tile % TT, g = lane >> 4;
+    const int64_t m = 16 * t + (lane & 15), n = 32 * group + 16 * (g & 1) + 4 * (2 * half + (g >> 1));
+    if (a.ksplit > 1) {
+      const int64_t np = (a.n + 3) & ~(int64_t)3, e = ((int64_t)z * a.m + m) * np + n;
+      if (m < a.m && n < np && in_bounds(e, 4, (int64_t)a.ksplit * a.m * np))
+        *reinterpret_cast<int4*>(a.part + e) = make_int4(sum[0], sum[1], sum[2], sum[3]);
+    } else {
+      store4<E>(a, m, n, sum, token_scale(a, m));
+    }
+  }
+}
+
+// Adds the splits' int32 sums and finishes: 4 outputs a thread.
+template <typename E>
+__global__ __launch_bounds__(256) void k_int8_reduce(Int8GemmArgs a) {
+  const int64_t np = (a.n + 3) & ~(int64_t)3, per = np / 4, id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (id >= per * a.m) return;
+  const int64_t m = id / per, n = id % per * 4;
+  i32x4 sum = {0, 0, 0, 0};
+  for (int z = 0; z < a.ksplit; ++z) {
+    const int64_t e = ((int64_t)z * a.m + m) * np + n;
+    if (in_bounds(e, 4, (int64_t)a.ksplit * a.m * np)) sum += *reinterpret_cast<const i32x4*>(a.part + e);
+  }
+  store4<E>(a, m, n, sum, token_scale(a, m));
 }
 
 // ---- layouts ----------------------------------------------------------------
@@ -191,14 +420,62 @@ bool aligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p
 
 }  // namespace
 
-size_t int8_part_bytes(int64_t, int64_t, int64_t, int) { return 0; }
+Int8Plan int8_plan(int64_t m, int64_t n, int64_t k, int cus) {
+  Int8Plan p{};
+  const int64_t steps = int8_kp(k) / 128;
+  if (m <= 64) {
+    p.kind = m <= 16 ? kInt8Few1 : m <= 32 ? kInt8Few2 : kInt8Few4;
+    const int64_t groups = (n + 31) / 32;
+    p.ksplit = (int)std::max<int64_t>(1, std::min<int64_t>(cus / std::max<int64_t>(1, groups), steps / 8));
+    return p;
+  }
+  const int64_t big = (m + 255) / 256 * ((n + 255) / 256);
+  if (big >= cus / 2) {
+    p.kind = kInt8Tile256;
+    p.ksplit = 1;
+  } else {
+    p.kind = kInt8Tile128;
+    const int64_t tiles = (m + 127) / 128 * ((n + 127) / 128);
+    p.ksplit = (int)std::max<int64_t>(1, std::min<int64_t>(2 * cus / std::max<int64_t>(1, tiles), steps / 4));
+  }
+  return p;
+}
 
-hipError_t launch_int8_gemm(Int8GemmArgs a, int, hipStream_t st) {
-  const int64_t grid = (a.n + 127) / 128 * ((a.m + 127) / 128);
-  if (grid > INT_MAX) return hipErrorInvalidValue;
-  if (a.f16) k_int8_gemm<F16><<<dim3((uint32_t)grid), 256, 0, st>>>(a);
-  else k_int8_gemm<Bf16><<<dim3((uint32_t)grid), 256, 0, st>>>(a);
+size_t int8_plan_bytes(const Int8Plan& p, int64_t m, int64_t n) {
+  return p.ksplit > 1 ? (size_t)p.ksplit * (size_t)m * (size_t)((n + 3) & ~(int64_t)3) * 4u : 0;
+}
+
+size_t int8_part_bytes(int64_t m, int64_t n, int64_t k, int cus) { return int8_plan_bytes(int8_plan(m, n, k, cus), m, n); }
+
+template <typename E>
+static hipError_t run_plan(Int8GemmArgs a, const Int8Plan& p, hipStream_t st) {
+  a.ksplit = a.part ? p.ksplit : 1;
+  auto grid = [&](int64_t bm, int64_t bn) { return (a.m + bm - 1) / bm * ((a.n + bn - 1) / bn) * a.ksplit; };
+  const bool few = p.kind == kInt8Few1 || p.kind == kInt8Few2 || p.kind == kInt8Few4;
+  const int64_t g = few ? (a.n + 31) / 32 * a.ksplit : p.kind == kInt8Tile256 ? grid(256, 256) : grid(128, 128);
+  if (g > INT_MAX) return hipErrorInvalidValue;
+  const dim3 gr((uint32_t)g);
+  switch (p.kind) {
+    case kInt8Few1: k_int8_few<1, 8, E><<<gr, 512, 0, st>>>(a); break;
+    case kInt8Few2: k_int8_few<2, 8, E><<<gr, 512, 0, st>>>(a); break;
+    case kInt8Few4: k_int8_few<4, 8, E><<<gr, 512, 0, st>>>(a); break;
+    case kInt8Tile256: k_int8_gemm<4, 2, E><<<gr, 512, 0, st>>>(a); break;
+    case kInt8Tile128: k_int8_gemm<2, 1, E><<<gr, 128, 0, st>>>(a); break;
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.ksplit == 1) return e;
+  const int64_t blocks = ((a.n + 3) / 4 * a.m + 255) / 256;
+  if (blocks > INT_MAX) return hipErrorInvalidValue;
+  k_int8_reduce<E><<<dim3((uint32_t)blocks), 256, 0, st>>>(a);
   return hipGetLastError();
+}
+
+hipError_t launch_int8_plan(const Int8GemmArgs& a, const Int8Plan& p, hipStream_t st) {
+  return a.f16 ? run_plan<F16>(a, p, st) : run_plan<Bf16>(a, p, st);
+}
+
+hipError_t launch_int8_gemm(const Int8GemmArgs& a, int cus, hipStream_t st) {
+  return launch_int8_plan(a, int8_plan(a.m, a.n, a.k, cus), st);
 }
 
 hipError_t launch_int8_pack(const int8_t* src, int64_t ld, int64_t n, int64_t k, int8_t* dst, hipStream_t st) {
