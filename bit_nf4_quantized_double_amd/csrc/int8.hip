@@ -33,15 +33,37 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t strips_rsrc(const int8_t* p, i
   return make_rsrc(p + (first < total ? first : 0) * 16 * kp, (uint32_t)min(bytes, (int64_t)0x7fffffff));
 }
 
-// One output value.
-template <typename E>
-__device__ __forceinline__ float finish(const Int8GemmArgs& a, int sum, float sx, int64_t n) {
-  const bool ok = n < a.n && in_bounds(n, 1, a.n);
-  float y = (float)sum * sx;
-  if (a.sw) y *= ok ? a.sw[n] : 0.f;
-  if (a.bias) y += ok ? E::widen(a.bias[n]) : 0.f;
-  return y;
-}
+// The scales and biases of W consecutive outputs n .. n + W - 1 (n a multiple
+// of W; past a.n: zeros).
+template <typename E, int W>
+struct Outs {
+  float s[W], b[W];
+  __device__ __forceinline__ void load(const Int8GemmArgs& a, int64_t n) {
+    if (n + W <= a.n && in_bounds(n, W, a.n)) {
+#pragma unroll
+      for (int i = 0; i < W; i += 4) {
+        const float4 f = a.sw ? *reinterpret_cast<const float4*>(a.sw + n + i) : make_float4(1.f, 1.f, 1.f, 1.f);
+        s[i] = f.x; s[i + 1] = f.y; s[i + 2] = f.z; s[i + 3] = f.w;
+        const uint2 u = a.bias ? *reinterpret_cast<const uint2*>(a.bias + n + i) : make_uint2(0, 0);
+        b[i] = E::widen((uint16_t)u.x);
+        b[i + 1] = E::widen((uint16_t)(u.x >> 16));
+        b[i + 2] = E::widen((uint16_t)u.y);
+        b[i + 3] = E::widen((uint16_t)(u.y >> 16));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        const bool ok = n + i < a.n && in_bounds(n + i, 1, a.n);
+        s[i] = ok ? (a.sw ? a.sw[n + i] : 1.f) : 0.f;
+        b[i] = ok && a.bias ? E::widen(a.bias[n + i]) : 0.f;
+      }
+    }
+  }
+  // E(sum sx s + b), token scale first
+  __device__ __forceinline__ uint32_t pair(int i, int lo, int hi, float sx) const {
+    return E::pack2((float)lo * sx * s[i] + b[i], (float)hi * sx * s[i + 1] + b[i + 1]);
+  }
+};
 
 __device__ __forceinline__ float token_scale(const Int8GemmArgs& a, int64_t m) {
   return m < a.m && in_bounds(m, 1, a.m) ? a.sx[m] : 0.f;
@@ -53,8 +75,9 @@ template <typename E>
 __device__ __forceinline__ void store4(const Int8GemmArgs& a, int64_t m, int64_t n0, i32x4 sum, float sx) {
   if (m >= a.m || n0 >= a.n) return;
   const int64_t e = m * a.n + n0, size = a.m * a.n;
-  const uint32_t d[2] = {E::pack2(finish<E>(a, sum[0], sx, n0), finish<E>(a, sum[1], sx, n0 + 1)),
-                         E::pack2(finish<E>(a, sum[2], sx, n0 + 2), finish<E>(a, sum[3], sx, n0 + 3))};
+  Outs<E, 4> o;
+  o.load(a, n0);
+  const uint32_t d[2] = {o.pair(0, sum[0], sum[1], sx), o.pair(2, sum[2], sum[3], sx)};
   if (n0 + 4 <= a.n) {
     if (in_bounds(e, 4, size)) *reinterpret_cast<Un8*>(a.out + e) = Un8{d[0], d[1]};
   } else {
@@ -107,7 +130,7 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
   constexpr int kTile = BN * 128;                     // bytes of a W tile
   constexpr int kStage = kTile / (16 * kThreads);     // 16-byte pieces of it per thread
   constexpr int kPitch = 128 + 8;                     // output staging: 16-bit elements per token
-  constexpr int kOut = WM * WN * 32 * kPitch * 2;     // bytes: 32 tokens x 128 outputs per wave
+  constexpr int kOut = WM * WN * 64 * kPitch * 2;     // bytes: 64 tokens x 128 outputs per wave
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kTile > kOut ? 2 * kTile : kOut];
   // uniform across the wave: buffer resources made from it stay scalar
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -209,39 +232,43 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
     }
     return;
   }
-  // Through LDS, so that a token's 128 outputs leave as whole lines.
+  // Through LDS, so that a token's 128 outputs leave as whole lines: 32
+  // outputs of both token halves at a time into the wave's own region (no
+  // other wave touches it), two halves after each other out.
   lds_barrier();  // every wave has read its last operands
-  uint16_t* so = reinterpret_cast<uint16_t*>(lds) + wave * 32 * kPitch;
+  uint16_t* so = reinterpret_cast<uint16_t*>(lds) + wave * 64 * kPitch;
+  float sx[2];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const float sx = token_scale(a, m0 + 32 * j + (lane & 31));
+  for (int j = 0; j < 2; ++j) sx[j] = token_scale(a, m0 + 32 * j + (lane & 31));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 4; ++i) {
+    Outs<E, 16> os;
+    os.load(a, nw + 32 * i + 16 * h);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
       uint32_t d[8];
 #pragma unroll
-      for (int v = 0; v < 8; ++v) {
-        const int64_t n = nw + 32 * i + 16 * h + 2 * v;
-        d[v] = E::pack2(finish<E>(a, acc[i][j][2 * v], sx, n), finish<E>(a, acc[i][j][2 * v + 1], sx, n + 1));
-      }
-      uint4* o = reinterpret_cast<uint4*>(so + (lane & 31) * kPitch + 32 * i + 16 * h);
+      for (int v = 0; v < 8; ++v) d[v] = os.pair(2 * v, acc[i][j][2 * v], acc[i][j][2 * v + 1], sx[j]);
+      uint4* o = reinterpret_cast<uint4*>(so + (32 * j + (lane & 31)) * kPitch + 32 * i + 16 * h);
       o[0] = make_uint4(d[0], d[1], d[2], d[3]);
       o[1] = make_uint4(d[4], d[5], d[6], d[7]);
     }
-    // the wave's own region: no other wave touches it
+  }
+  const int col = (lane & 15) * 8;
+  const int64_t n = nw + col;
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      const int row = 4 * r + (lane >> 4), col = (lane & 15) * 8;
-      const uint4 u = *reinterpret_cast<const uint4*>(so + row * kPitch + col);
-      const int64_t m = m0 + 32 * j + row, n = nw + col, e = m * a.n + n;
-      if (m >= a.m || n >= a.n) continue;
-      if (n + 8 <= a.n) {
-        if (in_bounds(e, 8, a.m * a.n)) *reinterpret_cast<Un16*>(a.out + e) = Un16{u.x, u.y, u.z, u.w};
-      } else {
-        const uint32_t d[4] = {u.x, u.y, u.z, u.w};
+  for (int r = 0; r < 16; ++r) {
+    const int row = 4 * r + (lane >> 4);
+    const uint4 u = *reinterpret_cast<const uint4*>(so + row * kPitch + col);
+    const int64_t m = m0 + row, e = m * a.n + n;
+    if (m >= a.m || n >= a.n) continue;
+    if (n + 8 <= a.n) {
+      if (in_bounds(e, 8, a.m * a.n)) *reinterpret_cast<Un16*>(a.out + e) = Un16{u.x, u.y, u.z, u.w};
+    } else {
+      const uint32_t d[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (n + i < a.n && in_bounds(e + i, 1, a.m * a.n)) a.out[e + i] = (uint16_t)(d[i >> 1] >> (16 * (i & 1)));
-      }
+      for (int i = 0; i < 8; ++i)
+        if (n + i < a.n && in_bounds(e + i, 1, a.m * a.n)) a.out[e + i] = (uint16_t)(d[i >> 1] >> (16 * (i & 1)));
     }
   }
 }
@@ -452,7 +479,7 @@ static hipError_t run_plan(Int8GemmArgs a, const Int8Plan& p, hipStream_t st) {
   a.ksplit = a.part ? p.ksplit : 1;
   auto grid = [&](int64_t bm, int64_t bn) { return (a.m + bm - 1) / bm * ((a.n + bn - 1) / bn) * a.ksplit; };
   const bool few = p.kind == kInt8Few1 || p.kind == kInt8Few2 || p.kind == kInt8Few4;
-  const int64_t g = few ? (a.n + 31) / 32 * a.ksplit : p.kind == kInt8Tile256 ? grid(256, 256) : grid(128, 128);
+  const int64_t g = few ? (a.n + 31) / 32 * a.ksplit : p.kind == kInt8Tile256 ? grid(256, 256) : p.kind == kInt8Tile256x128 ? grid(256, 128) : grid(128, 128);
   if (g > INT_MAX) return hipErrorInvalidValue;
   const dim3 gr((uint32_t)g);
   switch (p.kind) {
@@ -460,6 +487,7 @@ static hipError_t run_plan(Int8GemmArgs a, const Int8Plan& p, hipStream_t st) {
     case kInt8Few2: k_int8_few<2, 8, E><<<gr, 512, 0, st>>>(a); break;
     case kInt8Few4: k_int8_few<4, 8, E><<<gr, 512, 0, st>>>(a); break;
     case kInt8Tile256: k_int8_gemm<4, 2, E><<<gr, 512, 0, st>>>(a); break;
+    case kInt8Tile256x128: k_int8_gemm<4, 1, E><<<gr, 256, 0, st>>>(a); break;
     case kInt8Tile128: k_int8_gemm<2, 1, E><<<gr, 128, 0, st>>>(a); break;
   }
   hipError_t e = hipGetLastError();

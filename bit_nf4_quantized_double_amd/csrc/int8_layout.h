@@ -106,7 +106,7 @@ struct Int8GemmArgs {  // out[m][n] = E(sx[m] sw[n] sum_k x[m][k] w[n][k] + bias
 };
 // Which kernel a product takes, and over how many workgroups a tile's
 // reduction is split (needs `part`; without it one).
-enum Int8Kind { kInt8Few1, kInt8Few2, kInt8Few4, kInt8Tile256, kInt8Tile128 };
+enum Int8Kind { kInt8Few1, kInt8Few2, kInt8Few4, kInt8Tile256, kInt8Tile128, kInt8Tile256x128 };
 struct Int8Plan {
   Int8Kind kind;
   int ksplit;

@@ -23,12 +23,20 @@ DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # QLORA_BF16 /
 MAX_NORM_WIDTH = 32768
 
 
+# The current device and its current stream as plain numbers: the same as
+# torch.cuda.current_device() and current_stream().cuda_stream, without the
+# Stream object whose making costs as much as a small call's whole checks.
+_device_index = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _stream(device) -> int:
     """The current stream of the device the tensors are on, which has to be
     the current device: the library launches there."""
-    if device.index is not None and device.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
-    return torch.cuda.current_stream().cuda_stream
+    index = _device_index()
+    if device.index != index:
+        raise ValueError(f"the tensors are on {device}, the current device is cuda:{index}")
+    return _raw_stream(index)
 
 
 def _mat(t, dtype, shape, name: str, device=None):
