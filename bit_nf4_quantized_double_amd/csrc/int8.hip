@@ -16,11 +16,9 @@ namespace qlora {
 namespace {
 
 typedef __attribute__((ext_vector_type(4))) int i32x4;
-typedef __attribute__((ext_vector_type(16))) int i32x16;
 
 // Stores that need no more than their elements' alignment (the hardware takes
 // any; rows of an odd number of outputs start anywhere).
-struct __attribute__((packed, aligned(2))) Un8 { uint32_t x, y; };
 struct __attribute__((packed, aligned(2))) Un16 { uint32_t x, y, z, w; };
 
 __device__ __forceinline__ i32x4 as_i32x4(uint4 u) { return __builtin_bit_cast(i32x4, u); }
@@ -63,27 +61,40 @@ struct Outs {
   __device__ __forceinline__ uint32_t pair(int i, int lo, int hi, float sx) const {
     return E::pack2((float)lo * sx * s[i] + b[i], (float)hi * sx * s[i + 1] + b[i + 1]);
   }
+  __device__ __forceinline__ uint4 eight(i32x4 lo, i32x4 hi, float sx) const {
+    return make_uint4(pair(0, lo[0], lo[1], sx), pair(2, lo[2], lo[3], sx), pair(4, hi[0], hi[1], sx),
+                      pair(6, hi[2], hi[3], sx));
+  }
 };
 
 __device__ __forceinline__ float token_scale(const Int8GemmArgs& a, int64_t m) {
   return m < a.m && in_bounds(m, 1, a.m) ? a.sx[m] : 0.f;
 }
 
-// 4 consecutive outputs n0 .. n0 + 3 of token m, as far as they exist (n0 a
-// multiple of 4).
-template <typename E>
-__device__ __forceinline__ void store4(const Int8GemmArgs& a, int64_t m, int64_t n0, i32x4 sum, float sx) {
-  if (m >= a.m || n0 >= a.n) return;
-  const int64_t e = m * a.n + n0, size = a.m * a.n;
-  Outs<E, 4> o;
-  o.load(a, n0);
-  const uint32_t d[2] = {o.pair(0, sum[0], sum[1], sx), o.pair(2, sum[2], sum[3], sx)};
-  if (n0 + 4 <= a.n) {
-    if (in_bounds(e, 4, size)) *reinterpret_cast<Un8*>(a.out + e) = Un8{d[0], d[1]};
+// 8 consecutive outputs n .. n + 7 of token m, as far as they exist, packed.
+__device__ __forceinline__ void store8(const Int8GemmArgs& a, int64_t m, int64_t n, uint4 u) {
+  if (m >= a.m || n >= a.n) return;
+  const int64_t e = m * a.n + n, size = a.m * a.n;
+  if (n + 8 <= a.n) {
+    if (in_bounds(e, 8, size)) *reinterpret_cast<Un16*>(a.out + e) = Un16{u.x, u.y, u.z, u.w};
   } else {
+    const uint32_t d[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (n0 + i < a.n && in_bounds(e + i, 1, size)) a.out[e + i] = (uint16_t)(d[i >> 1] >> (16 * (i & 1)));
+    for (int i = 0; i < 8; ++i)
+      if (n + i < a.n && in_bounds(e + i, 1, size)) a.out[e + i] = (uint16_t)(d[i >> 1] >> (16 * (i & 1)));
+  }
+}
+
+// The split sums of 8 consecutive outputs of token m (rows of `part` are
+// padded to 8 outputs).
+__device__ __forceinline__ int64_t part_at(const Int8GemmArgs& a, int64_t z, int64_t m, int64_t n) {
+  return (z * a.m + m) * ((a.n + 7) & ~(int64_t)7) + n;
+}
+__device__ __forceinline__ void store_part8(const Int8GemmArgs& a, int64_t z, int64_t m, int64_t n, i32x4 lo, i32x4 hi) {
+  const int64_t e = part_at(a, z, m, n);
+  if (m < a.m && n < a.n && in_bounds(e, 8, part_at(a, a.ksplit, 0, 0))) {
+    *reinterpret_cast<i32x4*>(a.part + e) = lo;
+    *reinterpret_cast<i32x4*>(a.part + e + 4) = hi;
   }
 }
 
@@ -106,8 +117,9 @@ __device__ __forceinline__ void tile_of(uint32_t lin, uint32_t mt, uint32_t nt, 
 }
 
 // Many tokens.  Workgroup tile: 64 WM tokens x 128 WN outputs, one wave for
-// each 64 x 128 of it (8 accumulators of 32 x 32, 128 registers).  A 128-deep
-// step is 4 sub-steps of one 32 x 32 x 32 MFMA per accumulator.
+// each 64 x 128 of it (32 accumulators of 16 x 16, 128 registers).  A 128-deep
+// step is 4 sub-steps of 16 MFMAs (16 x 16 x 64): 64 of the step's columns by
+// half of the wave's outputs.
 //
 // The step's W tile goes through LDS (global -> registers -> LDS, double
 // buffered), where the WM waves that share its rows read it; each wave loads
@@ -148,12 +160,10 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
 
   const __amdgpu_buffer_rsrc_t rw = strips_rsrc(a.w, n0 >> 4, int8_weight_strips(a.n), kp);
   const __amdgpu_buffer_rsrc_t rx = strips_rsrc(a.x, m0 >> 4, int8_row_strips(a.m), kp);
-  // a 32 x 32 operand: lane l has row l & 31 and the half l >> 5 of the columns
-  const uint32_t inner = (uint32_t)(lane >> 5) * 256u + (uint32_t)(lane & 15) * 16u;
-  const uint32_t xat = (uint32_t)((lane >> 4) & 1) * strip + inner;
-  const uint32_t wat = (uint32_t)(8 * wn + ((lane >> 4) & 1)) * 2048u + inner;  // in the LDS tile
+  const uint32_t at = (uint32_t)lane * 16u;
+  const uint32_t wat = (uint32_t)(8 * wn) * 2048u + at;  // in the LDS tile
 
-  uint4 st[kStage], xf[4][2], wf[2][4];
+  uint4 st[kStage], xf[2][4], wf[2][4];
   auto load_stage = [&](uint32_t s) {
 #pragma unroll
     for (int u = 0; u < kStage; ++u) {
@@ -166,28 +176,28 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
     for (int u = 0; u < kStage; ++u)
       *reinterpret_cast<uint4*>(lds + buf * kTile + (u * kThreads + tid) * 16) = st[u];
   };
-  auto load_x = [&](uint32_t s, int q) {
+  auto load_x = [&](uint32_t s, int c) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      xf[q][j] = buf_load16(rx, s < s1 ? xat + 2u * j * strip + s * 2048u + q * 512u : kOOB);
+    for (int t = 0; t < 4; ++t) xf[c][t] = buf_load16(rx, s < s1 ? at + t * strip + s * 2048u + c * 1024u : kOOB);
   };
+  // sub-step q: columns 64 (q / 2) .., strips 4 (q % 2) ..
   auto read_w = [&](int buf, int q, uint4 (&f)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      f[i] = *reinterpret_cast<const uint4*>(lds + buf * kTile + wat + i * 4096 + q * 512);
+      f[i] = *reinterpret_cast<const uint4*>(lds + buf * kTile + wat + (4 * (q & 1) + i) * 2048 + (q >> 1) * 1024);
   };
 
-  i32x16 acc[4][2];
+  i32x4 acc[8][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 8; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
+      for (int v = 0; v < 4; ++v) acc[i][t][v] = 0;
 
   load_stage(s0);
-#pragma unroll
-  for (int q = 0; q < 4; ++q) load_x(s0, q);
+  load_x(s0, 0);
+  load_x(s0, 1);
   write_stage(0);
   load_stage(s0 + 1);
   lds_barrier();
@@ -206,70 +216,43 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(as_i32x4(wf[q & 1][i]), as_i32x4(xf[q][j]), acc[i][j], 0, 0, 0);
-      load_x(s + 1, q);
+        for (int t = 0; t < 4; ++t)
+          acc[4 * (q & 1) + i][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(as_i32x4(wf[q & 1][i]), as_i32x4(xf[q >> 1][t]),
+                                                                          acc[4 * (q & 1) + i][t], 0, 0, 0);
+      if (q & 1) load_x(s + 1, q >> 1);
     }
   }
 
-  // lane: token (lane & 31) of each half j, outputs 32 i + 16 (lane >> 5) .. + 15
-  const int h = lane >> 5;
+  // lane 16 g + c: token 16 t + c, outputs 32 p + 8 g .. + 7 in strips 2 p and 2 p + 1
+  const int g = lane >> 4, c = lane & 15;
   const int64_t nw = n0 + 128 * wn;
   if (a.ksplit > 1) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int64_t m = m0 + 32 * j + (lane & 31);
+    for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int64_t n = nw + 32 * i + 16 * h + 4 * v, np = (a.n + 3) & ~(int64_t)3;
-          const int64_t e = ((int64_t)z * a.m + m) * np + n;
-          if (m < a.m && n < np && in_bounds(e, 4, (int64_t)a.ksplit * a.m * np))
-            *reinterpret_cast<int4*>(a.part + e) =
-                make_int4(acc[i][j][4 * v], acc[i][j][4 * v + 1], acc[i][j][4 * v + 2], acc[i][j][4 * v + 3]);
-        }
-    }
+      for (int p = 0; p < 4; ++p)
+        store_part8(a, z, m0 + 16 * t + c, nw + 32 * p + 8 * g, acc[2 * p][t], acc[2 * p + 1][t]);
     return;
   }
-  // Through LDS, so that a token's 128 outputs leave as whole lines: 32
-  // outputs of both token halves at a time into the wave's own region (no
-  // other wave touches it), two halves after each other out.
+  // Through LDS, so that a token's 128 outputs leave as whole lines: each
+  // wave in its own region (no other wave touches it).
   lds_barrier();  // every wave has read its last operands
   uint16_t* so = reinterpret_cast<uint16_t*>(lds) + wave * 64 * kPitch;
-  float sx[2];
+  float sx[4];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) sx[j] = token_scale(a, m0 + 32 * j + (lane & 31));
+  for (int t = 0; t < 4; ++t) sx[t] = token_scale(a, m0 + 16 * t + c);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    Outs<E, 16> os;
-    os.load(a, nw + 32 * i + 16 * h);
+  for (int p = 0; p < 4; ++p) {
+    Outs<E, 8> os;
+    os.load(a, nw + 32 * p + 8 * g);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      uint32_t d[8];
-#pragma unroll
-      for (int v = 0; v < 8; ++v) d[v] = os.pair(2 * v, acc[i][j][2 * v], acc[i][j][2 * v + 1], sx[j]);
-      uint4* o = reinterpret_cast<uint4*>(so + (32 * j + (lane & 31)) * kPitch + 32 * i + 16 * h);
-      o[0] = make_uint4(d[0], d[1], d[2], d[3]);
-      o[1] = make_uint4(d[4], d[5], d[6], d[7]);
-    }
+    for (int t = 0; t < 4; ++t)
+      *reinterpret_cast<uint4*>(so + (16 * t + c) * kPitch + 32 * p + 8 * g) = os.eight(acc[2 * p][t], acc[2 * p + 1][t], sx[t]);
   }
-  const int col = (lane & 15) * 8;
-  const int64_t n = nw + col;
 #pragma unroll
   for (int r = 0; r < 16; ++r) {
-    const int row = 4 * r + (lane >> 4);
-    const uint4 u = *reinterpret_cast<const uint4*>(so + row * kPitch + col);
-    const int64_t m = m0 + row, e = m * a.n + n;
-    if (m >= a.m || n >= a.n) continue;
-    if (n + 8 <= a.n) {
-      if (in_bounds(e, 8, a.m * a.n)) *reinterpret_cast<Un16*>(a.out + e) = Un16{u.x, u.y, u.z, u.w};
-    } else {
-      const uint32_t d[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (n + i < a.n && in_bounds(e + i, 1, a.m * a.n)) a.out[e + i] = (uint16_t)(d[i >> 1] >> (16 * (i & 1)));
-    }
+    const int row = 4 * r + g, col = c * 8;
+    store8(a, m0 + row, nw + col, *reinterpret_cast<const uint4*>(so + row * kPitch + col));
   }
 }
 
@@ -326,35 +309,41 @@ __global__ __launch_bounds__(64 * NW) void k_int8_few(Int8GemmArgs a) {
 #pragma unroll
     for (int t = 0; t < TT; ++t) s_sum[wave][i * TT + t][lane] = acc[i][t];
   __syncthreads();
-  // D row 4 g + i of strip `half` is output 16 (g & 1) + 4 (2 half + g / 2) + i
-  for (int tile = wave; tile < 2 * TT; tile += NW) {
-    i32x4 sum = s_sum[0][tile][lane];
+  for (int t = wave; t < TT; t += NW) {
+    i32x4 lo = s_sum[0][t][lane], hi = s_sum[0][TT + t][lane];
 #pragma unroll
-    for (int w = 1; w < NW; ++w) sum += s_sum[w][tile][lane];
-    const int half = tile / TT, t = tile % TT, g = lane >> 4;
-    const int64_t m = 16 * t + (lane & 15), n = 32 * group + 16 * (g & 1) + 4 * (2 * half + (g >> 1));
+    for (int w = 1; w < NW; ++w) {
+      lo += s_sum[w][t][lane];
+      hi += s_sum[w][TT + t][lane];
+    }
+    const int64_t m = 16 * t + (lane & 15), n = 32 * group + 8 * (lane >> 4);
     if (a.ksplit > 1) {
-      const int64_t np = (a.n + 3) & ~(int64_t)3, e = ((int64_t)z * a.m + m) * np + n;
-      if (m < a.m && n < np && in_bounds(e, 4, (int64_t)a.ksplit * a.m * np))
-        *reinterpret_cast<int4*>(a.part + e) = make_int4(sum[0], sum[1], sum[2], sum[3]);
+      store_part8(a, z, m, n, lo, hi);
     } else {
-      store4<E>(a, m, n, sum, token_scale(a, m));
+      Outs<E, 8> o;
+      o.load(a, n);
+      store8(a, m, n, o.eight(lo, hi, token_scale(a, m)));
     }
   }
 }
 
-// Adds the splits' int32 sums and finishes: 4 outputs a thread.
+// Adds the splits' int32 sums and finishes: 8 outputs a thread.
 template <typename E>
 __global__ __launch_bounds__(256) void k_int8_reduce(Int8GemmArgs a) {
-  const int64_t np = (a.n + 3) & ~(int64_t)3, per = np / 4, id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t per = (a.n + 7) / 8, id = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (id >= per * a.m) return;
-  const int64_t m = id / per, n = id % per * 4;
-  i32x4 sum = {0, 0, 0, 0};
+  const int64_t m = id / per, n = id % per * 8;
+  i32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
   for (int z = 0; z < a.ksplit; ++z) {
-    const int64_t e = ((int64_t)z * a.m + m) * np + n;
-    if (in_bounds(e, 4, (int64_t)a.ksplit * a.m * np)) sum += *reinterpret_cast<const i32x4*>(a.part + e);
+    const int64_t e = part_at(a, z, m, n);
+    if (in_bounds(e, 8, part_at(a, a.ksplit, 0, 0))) {
+      lo += *reinterpret_cast<const i32x4*>(a.part + e);
+      hi += *reinterpret_cast<const i32x4*>(a.part + e + 4);
+    }
   }
-  store4<E>(a, m, n, sum, token_scale(a, m));
+  Outs<E, 8> o;
+  o.load(a, n);
+  store8(a, m, n, o.eight(lo, hi, token_scale(a, m)));
 }
 
 // ---- layouts ----------------------------------------------------------------
@@ -469,7 +458,7 @@ Int8Plan int8_plan(int64_t m, int64_t n, int64_t k, int cus) {
 }
 
 size_t int8_plan_bytes(const Int8Plan& p, int64_t m, int64_t n) {
-  return p.ksplit > 1 ? (size_t)p.ksplit * (size_t)m * (size_t)((n + 3) & ~(int64_t)3) * 4u : 0;
+  return p.ksplit > 1 ? (size_t)p.ksplit * (size_t)m * (size_t)((n + 7) & ~(int64_t)7) * 4u : 0;
 }
 
 size_t int8_part_bytes(int64_t m, int64_t n, int64_t k, int cus) { return int8_plan_bytes(int8_plan(m, n, k, cus), m, n); }
@@ -492,7 +481,7 @@ static hipError_t run_plan(Int8GemmArgs a, const Int8Plan& p, hipStream_t st) {
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.ksplit == 1) return e;
-  const int64_t blocks = ((a.n + 3) / 4 * a.m + 255) / 256;
+  const int64_t blocks = ((a.n + 7) / 8 * a.m + 255) / 256;
   if (blocks > INT_MAX) return hipErrorInvalidValue;
   k_int8_reduce<E><<<dim3((uint32_t)blocks), 256, 0, st>>>(a);
   return hipGetLastError();

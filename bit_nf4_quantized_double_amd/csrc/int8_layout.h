@@ -6,16 +6,16 @@
 // loads a tile with one 16-byte load per lane holds what one operand of
 // v_mfma_i32_16x16x64_i8 wants: row r, a quarter g of the 64 reduction
 // columns.  (Which columns of the tile the instruction pairs up does not
-// matter: both operands are stored alike, and a sum has no order.)  Two
-// strips give the two halves of a v_mfma_i32_32x32x32_i8 operand the same
-// way.  The tiles of a strip follow each other along K, which is padded to a
-// multiple of 128 with zero codes; a strip is contiguous, so both products
-// read memory in runs of whole kilobytes and LDS without bank conflicts.
+// matter: both operands are stored alike, and a sum has no order.)  The tiles
+// of a strip follow each other along K, which is padded to a multiple of 128
+// with zero codes; a strip is contiguous, so both products read memory in
+// runs of whole kilobytes and LDS without bank conflicts.
 //
-// A weight is the A operand, so its rows are the rows of D: D's lane half h
-// holds rows 8 j + 4 h + i (j, i = 0 .. 3) of a 32-row group.  Weight rows are
-// stored so that those are outputs 16 h + 4 j + i: a lane then holds 16
-// consecutive outputs of one token.  The last group is padded to 32 rows.
+// A weight is the A operand, so its rows are the rows of D, of which lane
+// 16 g + c holds rows 4 g + i (i = 0 .. 3) of column c.  Weight rows are stored
+// so that row 4 g + i of strip s of a pair is output 8 g + 4 s + i of the
+// pair's 32: a lane then holds 8 consecutive outputs of one token.  The last
+// pair is padded.
 #pragma once
 
 #include <stddef.h>
@@ -38,7 +38,7 @@ constexpr size_t int8_weight_bytes(int64_t n, int64_t k) {
 
 // Stored row of weight row n (see above); activation rows keep their order.
 __host__ __device__ constexpr int64_t int8_weight_row(int64_t n) {
-  return (n & ~(int64_t)31) | (((n >> 2) & 3) << 3) | (((n >> 4) & 1) << 2) | (n & 3);
+  return (n & ~(int64_t)31) | (((n >> 2) & 1) << 4) | (((n >> 3) & 3) << 2) | (n & 3);
 }
 
 // Byte offset of 16-column piece `piece` (columns 16 piece ..) of stored row `row`.
