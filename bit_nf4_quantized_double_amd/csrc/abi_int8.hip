@@ -170,7 +170,8 @@ size_t qlora_int8_rows_workspace_bytes(int64_t M, int64_t n_out, int64_t k_in) {
 
 size_t qlora_rms_norm_bwd_workspace_bytes(int64_t M, int64_t K) {
   if (M <= 0 || K <= 0 || M > INT_MAX || K > QLORA_MAX_NORM_WIDTH) return 0;
-  return (size_t)qlora::norm_bwd_groups(M, K, qlora::device_compute_units()) * (size_t)K * 4u;
+  // rows of partial sums are padded to 16 values
+  return (size_t)qlora::norm_bwd_groups(M, K, qlora::device_compute_units()) * (size_t)((K + 15) / 16 * 16) * 4u;
 }
 
 int qlora_int8_quantize_weight(const void* W, int dtype, int64_t ldw, int64_t n_out, int64_t k_in, int8_t* codes,
@@ -380,9 +381,9 @@ static int swiglu_args(const void* G, int64_t ldg, const void* U, int64_t ldu, i
   if ((st = check_dim(M, "M")) || (st = check_dim(K, "K")) || (st = check_type(dtype, false)) ||
       (st = check_rows_in(G, ldg, M, K, dtype, "gate")) || (st = check_rows_in(U, ldu, M, K, dtype, "up")))
     return st;
-  // the elementwise kernels count pieces of 8 values in 32 bits
-  if (elementwise && M > 0 && (K + 7) / 8 > ((int64_t)UINT32_MAX - 256) / M)
-    return fail(QLORA_ERR_SHAPE, "M * K exceeds 2^35 elements");
+  // the elementwise kernels count pieces of 16 values in 32 bits
+  if (elementwise && M > 0 && (K + 15) / 16 > ((int64_t)UINT32_MAX - 256) / M)
+    return fail(QLORA_ERR_SHAPE, "M * K exceeds 2^36 elements");
   a->g = G; a->u = U; a->type = dtype; a->ldg = ldg; a->ldu = ldu; a->m = M; a->k = K;
   return QLORA_OK;
 }

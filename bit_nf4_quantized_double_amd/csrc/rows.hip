@@ -28,8 +28,6 @@ constexpr float kAmaxFloor = 1e-30f;
 struct F32 {};
 template <typename T> struct Elem { typedef uint16_t type; };
 template <> struct Elem<F32> { typedef float type; };
-template <typename T> __device__ __forceinline__ float widen(uint16_t b) { return T::widen(b); }
-template <typename T> __device__ __forceinline__ float widen(float f) { return f; }
 
 // 16 bytes at any element's address: rows that are not 16-byte aligned (an odd
 // width, a slice of a wider matrix) are still loaded and stored 16 bytes at a
@@ -57,59 +55,99 @@ Mat<T> mat(const void* p, int64_t ld, int64_t m, int64_t k) {
   return a;
 }
 
-// Elements c .. c + W - 1 of a row as fp32, zeros from k on.
-template <int W, typename T>
-__device__ __forceinline__ void load_row(const Mat<T>& a, int64_t row, int64_t c, int64_t k, float (&v)[W]) {
-  typedef typename Elem<T>::type E;
-  const int64_t e = row * a.ld + c;
-  if (c + W <= k) {
-    constexpr int PER = 16 / sizeof(E);
-    Bytes16 u[W / PER];
+// The first nd (< DW) dwords at p, at any 2-byte boundary; zeros after them.
+// By the bits of nd: a load of DW/2 dwords, of DW/4 ..., each to its place.
+// (A load for each element would keep 16 addresses and masks alive and make
+// the kernels spill.  The places are picked with masks: as selects the compiler
+// makes an indexed array of them, puts it into LDS, and for that reads the
+// launch's dimensions from host memory, 10 us a launch.)
+__device__ __forceinline__ uint32_t only_if(bool b) { return b ? ~0u : 0u; }
+
+template <int B, int DW>
+__device__ __forceinline__ void load_some_from(const uint8_t* p, int nd, uint32_t (&d)[DW]) {
+  if (nd & B) {
+    const int at = nd & ~(2 * B - 1);
+    uint32_t v[B];
+    __builtin_memcpy(v, p + 4 * at, 4 * B);
 #pragma unroll
-    for (int j = 0; j < W / PER; ++j)
-      u[j] = in_bounds(e + j * PER, PER, a.n) ? *reinterpret_cast<const Bytes16*>(a.p + e + j * PER)
-                                              : Bytes16{0, 0, 0, 0};
+    for (int o = 0; o + 2 * B <= DW; o += 2 * B)
 #pragma unroll
-    for (int j = 0; j < W / PER; ++j) {
-      const uint32_t d[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        if constexpr (sizeof(E) == 2) v[j * PER + i] = widen<T>((uint16_t)(d[i >> 1] >> (16 * (i & 1))));
-        else v[j * PER + i] = __builtin_bit_cast(float, d[i]);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < W; ++i) v[i] = c + i < k && in_bounds(e + i, 1, a.n) ? widen<T>(a.p[e + i]) : 0.f;
+      for (int i = 0; i < B; ++i) d[o + i] |= v[i] & only_if(at == o);
   }
+  if constexpr (B > 1) load_some_from<B / 2>(p, nd, d);
+}
+template <int DW>
+__device__ __forceinline__ void load_some(const uint8_t* p, int nd, uint32_t (&d)[DW]) {
+#pragma unroll
+  for (int i = 0; i < DW; ++i) d[i] = 0;
+  load_some_from<DW / 2>(p, nd, d);
+}
+template <int B, int DW>
+__device__ __forceinline__ void store_some_from(uint8_t* p, int nd, const uint32_t (&d)[DW]) {
+  if (nd & B) {
+    const int at = nd & ~(2 * B - 1);
+    uint32_t v[B];
+#pragma unroll
+    for (int i = 0; i < B; ++i) v[i] = 0;
+#pragma unroll
+    for (int o = 0; o + 2 * B <= DW; o += 2 * B)
+#pragma unroll
+      for (int i = 0; i < B; ++i) v[i] |= d[o + i] & only_if(at == o);
+    __builtin_memcpy(p + 4 * at, v, 4 * B);
+  }
+  if constexpr (B > 1) store_some_from<B / 2>(p, nd, d);
+}
+template <int DW>
+__device__ __forceinline__ void store_some(uint8_t* p, int nd, const uint32_t (&d)[DW]) {
+  store_some_from<DW / 2>(p, nd, d);
 }
 
-// The same 16 elements of a 16-bit row, packed in pairs.
+// Elements c .. c + 15 of a row, as 16-byte parts: 8 dwords of pairs of a
+// 16-bit type or 16 dwords of fp32.  WHOLE: all of them are there; otherwise
+// (the end of a row whose length is no multiple of 16) n = k - c are, and
+// zeros follow.
 template <typename T>
-__device__ __forceinline__ void load_packed(const Mat<T>& a, int64_t row, int64_t c, int64_t k, uint32_t (&d)[8]) {
-  const int64_t e = row * a.ld + c;
-  if (c + 16 <= k) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const Bytes16 u = in_bounds(e + 8 * j, 8, a.n) ? *reinterpret_cast<const Bytes16*>(a.p + e + 8 * j)
-                                                     : Bytes16{0, 0, 0, 0};
-      d[4 * j] = u.x;
-      d[4 * j + 1] = u.y;
-      d[4 * j + 2] = u.z;
-      d[4 * j + 3] = u.w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) d[i] = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (c + i < k && in_bounds(e + i, 1, a.n)) d[i >> 1] |= (uint32_t)a.p[e + i] << (16 * (i & 1));
+struct Piece {
+  static constexpr int kDw = sizeof(typename Elem<T>::type) * 4;
+  uint32_t d[kDw];
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (kDw == 8) return T::widen((uint16_t)(d[i >> 1] >> (16 * (i & 1))));
+    else return __builtin_bit_cast(float, d[i]);
   }
-}
-template <typename T>
-__device__ __forceinline__ float unpack(const uint32_t (&d)[8], int i) {
-  return T::widen((uint16_t)(d[i >> 1] >> (16 * (i & 1))));
-}
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kDw; ++i) d[i] = 0;
+  }
+  template <bool WHOLE>
+  __device__ __forceinline__ void load(const Mat<T>& a, int64_t row, int64_t c, int64_t k) {
+    const int64_t e = row * a.ld + c;
+    const uint8_t* p = reinterpret_cast<const uint8_t*>(a.p + e);
+    constexpr int PER = 16 / sizeof(typename Elem<T>::type);
+    if constexpr (WHOLE) {
+#pragma unroll
+      for (int j = 0; j < kDw / 4; ++j) {
+        const Bytes16 u = in_bounds(e + j * PER, PER, a.n) ? *reinterpret_cast<const Bytes16*>(p + 16 * j)
+                                                           : Bytes16{0, 0, 0, 0};
+        d[4 * j] = u.x;
+        d[4 * j + 1] = u.y;
+        d[4 * j + 2] = u.z;
+        d[4 * j + 3] = u.w;
+      }
+    } else {
+      int n = (int)(k - c);
+      if (!in_bounds(e, n, a.n)) n = 0;
+      load_some(p, kDw == 8 ? n >> 1 : n, d);
+      if (kDw == 8 && (n & 1)) {
+        const uint32_t last = a.p[e + n - 1];
+#pragma unroll
+        for (int i = 0; i < kDw; ++i) d[i] |= last & only_if(i == n >> 1);
+      }
+    }
+  }
+};
+
+// Floats in a row of dgamma's partial sums: whole 16-byte pieces.
+__host__ __device__ constexpr int64_t part_pitch(int64_t k) { return (k + 15) / 16 * 16; }
 
 // A row-major contiguous 16-bit output of n elements.
 struct Out16 {
@@ -118,48 +156,56 @@ struct Out16 {
 };
 Out16 out16(uint16_t* p, int64_t m, int64_t k) { return Out16{p, k, m * k}; }
 
-template <typename T, int W>
-__device__ __forceinline__ void store_row(const Out16& o, int64_t row, int64_t c, int64_t k, const float (&v)[W]) {
+template <typename T>
+__device__ __forceinline__ void store_row(const Out16& o, int64_t row, int64_t c, int64_t k, const float (&v)[16]) {
   const int64_t e = row * o.ld + c;
-  if (c + W <= k) {
+  uint8_t* p = reinterpret_cast<uint8_t*>(o.p + e);
+  uint32_t d[8];
 #pragma unroll
-    for (int j = 0; j < W; j += 8)
-      if (in_bounds(e + j, 8, o.n))
-        *reinterpret_cast<Bytes16*>(o.p + e + j) =
-            Bytes16{T::pack2(v[j], v[j + 1]), T::pack2(v[j + 2], v[j + 3]), T::pack2(v[j + 4], v[j + 5]),
-                    T::pack2(v[j + 6], v[j + 7])};
+  for (int i = 0; i < 8; ++i) d[i] = T::pack2(v[2 * i], v[2 * i + 1]);
+  if (c + 16 <= k) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (in_bounds(e + 8 * j, 8, o.n))
+        *reinterpret_cast<Bytes16*>(p + 16 * j) = Bytes16{d[4 * j], d[4 * j + 1], d[4 * j + 2], d[4 * j + 3]};
   } else {
+    int n = (int)(k - c);
+    if (!in_bounds(e, n, o.n)) n = 0;
+    store_some(p, n >> 1, d);
+    if (n & 1) {
+      uint32_t last = 0;
 #pragma unroll
-    for (int i = 0; i < W; ++i)
-      if (c + i < k && in_bounds(e + i, 1, o.n)) o.p[e + i] = (uint16_t)T::pack2(v[i], 0.f);
+      for (int i = 0; i < 8; ++i) last |= d[i] & only_if(i == n >> 1);
+      o.p[e + n - 1] = (uint16_t)last;
+    }
   }
 }
 
 // Sum and maximum (of non-negative fp32 bit patterns, so that a NaN or an
-// infinity wins) over the TPR threads of a row; every thread gets both.
-// `lds` has two words for each wave of the workgroup.
-template <int TPR>
+// infinity wins) over the threads that share a row; each of them gets both.
+// RW rows lie side by side in a wave (row = lane % RW), NW consecutive waves
+// share them; `lds` has 2 RW words for each wave of the workgroup.
+template <int NW, int RW>
 __device__ __forceinline__ void row_reduce(float& sum, uint32_t& top, uint32_t* lds) {
 #pragma unroll
-  for (int d = 32; d > 0; d >>= 1) {
+  for (int d = 32; d >= RW; d >>= 1) {
     sum += __shfl_xor(sum, d);
     top = max(top, (uint32_t)__shfl_xor((int)top, d));
   }
-  if constexpr (TPR > 64) {
-    constexpr int NW = TPR / 64;
-    const int wave = threadIdx.x >> 6, first = wave & ~(NW - 1);
+  if constexpr (NW > 1) {
+    const int wave = threadIdx.x >> 6, first = wave / NW * NW, lane = threadIdx.x & 63, r = lane % RW;
     __syncthreads();  // an earlier reduction's reads are done
-    if ((threadIdx.x & 63) == 0) {
-      lds[2 * wave] = __builtin_bit_cast(uint32_t, sum);
-      lds[2 * wave + 1] = top;
+    if (lane < RW) {
+      lds[2 * (RW * wave + r)] = __builtin_bit_cast(uint32_t, sum);
+      lds[2 * (RW * wave + r) + 1] = top;
     }
     __syncthreads();
     sum = 0.f;
     top = 0;
 #pragma unroll
-    for (int i = 0; i < NW; ++i) {
-      sum += __builtin_bit_cast(float, lds[2 * (first + i)]);
-      top = max(top, lds[2 * (first + i) + 1]);
+    for (int w = 0; w < NW; ++w) {
+      sum += __builtin_bit_cast(float, lds[2 * (RW * (first + w) + r)]);
+      top = max(top, lds[2 * (RW * (first + w) + r) + 1]);
     }
   }
 }
@@ -219,15 +265,24 @@ __device__ __forceinline__ void store_codes(const Out8& o, int64_t row, int64_t 
 }
 
 // ---- what a row is made of --------------------------------------------------
-// load(): 16 values of a row as fp32.
+// Raw: what is loaded for a piece; load(): the loads alone, so that those of
+// all a thread's pieces are in flight together; value(): 16 fp32 values.
 
 template <typename T>
 struct QuantSrc {
   static constexpr bool kNorm = false;
   Mat<T> x;
   const float* col_scale;
-  __device__ __forceinline__ void load(int64_t row, int64_t c, int64_t k, float (&v)[16], float&) const {
-    load_row<16>(x, row, c, k, v);
+  struct Raw {
+    Piece<T> x;
+  };
+  template <bool WHOLE>
+  __device__ __forceinline__ void load(int64_t row, int64_t c, int64_t k, Raw& r) const {
+    r.x.template load<WHOLE>(x, row, c, k);
+  }
+  __device__ __forceinline__ void value(const Raw& r, int64_t, int64_t c, int64_t k, float (&v)[16], float&) const {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = r.x.at(i);
     if (col_scale) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] *= c + i < k && in_bounds(c + i, 1, k) ? col_scale[c + i] : 0.f;
@@ -241,16 +296,21 @@ template <typename T>
 struct SwigluSrc {
   static constexpr bool kNorm = false;
   Mat<T> g, u;
-  __device__ __forceinline__ void load(int64_t row, int64_t c, int64_t k, float (&v)[16], float&) const {
-    float w[16];
-    load_row<16>(g, row, c, k, v);
-    load_row<16>(u, row, c, k, w);
+  struct Raw {
+    Piece<T> g, u;
+  };
+  template <bool WHOLE>
+  __device__ __forceinline__ void load(int64_t row, int64_t c, int64_t k, Raw& r) const {
+    r.g.template load<WHOLE>(g, row, c, k);
+    r.u.template load<WHOLE>(u, row, c, k);
+  }
+  __device__ __forceinline__ void value(const Raw& r, int64_t, int64_t, int64_t, float (&v)[16], float&) const {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = v[i] * sigmoid(v[i]) * w[i];
+    for (int i = 0; i < 16; ++i) v[i] = r.g.at(i) * sigmoid(r.g.at(i)) * r.u.at(i);
   }
 };
 
-// load() gives h gamma and adds up h^2: y is that times rstd, whose factor
+// value() gives h gamma and adds up h^2: y is that times rstd, whose factor
 // the codes do not see and the scale gets at the end, so that one reduction
 // serves both.
 template <typename T, typename G>
@@ -260,67 +320,106 @@ struct NormSrc {
   Mat<G> gamma;
   Out16 h;
   float eps;
-  __device__ __forceinline__ void load(int64_t row, int64_t c, int64_t k, float (&v)[16], float& sum) const {
-    float w[16];
-    load_row<16>(x, row, c, k, v);
+  struct Raw {
+    Piece<T> x, r;
+    Piece<G> g;
+  };
+  template <bool WHOLE>
+  __device__ __forceinline__ void load(int64_t row, int64_t c, int64_t k, Raw& w) const {
+    w.x.template load<WHOLE>(x, row, c, k);
+    if (r.p) w.r.template load<WHOLE>(r, row, c, k);
+    else w.r.zero();
+    w.g.template load<WHOLE>(gamma, 0, c, k);
+  }
+  __device__ __forceinline__ void value(const Raw& w, int64_t row, int64_t c, int64_t k, float (&v)[16],
+                                        float& sum) const {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = w.x.at(i);
     if (r.p) {
-      load_row<16>(r, row, c, k, w);
 #pragma unroll
       for (int i = 0; i < 16; i += 2) {
         // what is normalised is the hidden state as it is stored, in 16 bits
-        const uint32_t b = T::pack2(v[i] + w[i], v[i + 1] + w[i + 1]);
+        const uint32_t b = T::pack2(v[i] + w.r.at(i), v[i + 1] + w.r.at(i + 1));
         v[i] = T::widen((uint16_t)b);
         v[i + 1] = T::widen((uint16_t)(b >> 16));
       }
       store_row<T>(h, row, c, k, v);
     }
-    load_row<16>(gamma, 0, c, k, w);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       sum = __builtin_fmaf(v[i], v[i], sum);
-      v[i] *= w[i];
+      v[i] *= w.g.at(i);
     }
   }
 };
 
-// One row per TPR threads, blockDim.x / TPR rows per workgroup.  A thread
-// holds NCH pieces of 16 values (piece j: TPR j + its index in the row);
-// NCH == 0 (rows too long for that) reads the row a second time instead, from
-// the cache.
-template <typename Src, int TPR, int NCH, bool Y16, typename T>
-__global__ __launch_bounds__(1024) void k_rows(Src src, Out8 o8, Out16 o16, float* rstd_out, int64_t m, int64_t k) {
-  __shared__ uint32_t s_red[32];
-  const int t = threadIdx.x & (TPR - 1);
-  const int64_t row = (int64_t)blockIdx.x * (blockDim.x / TPR) + threadIdx.x / TPR;
+// One piece by itself, whole or not (c < k).
+template <typename Src>
+__device__ __forceinline__ void piece(const Src& src, int64_t row, int64_t c, int64_t k, float (&v)[16], float& sum) {
+  typename Src::Raw r;
+  if (c + 16 <= k) src.template load<true>(row, c, k, r);
+  else src.template load<false>(row, c, k, r);
+  src.value(r, row, c, k, v, sum);
+}
+
+// TPR threads share a row, RW rows lie side by side in a wave, and a
+// workgroup of kBlock threads takes kBlock / TPR rows.  A thread holds NCH
+// pieces of 16 values (piece j: TPR j + its index in the row); NCH == 0 (rows
+// too long for that) reads the row a second time instead, from the cache.
+//
+// WHOLE: k is a multiple of 16, so that no piece is partly filled and all of
+// a thread's loads go out together, with no branch between them.
+//
+// RW = 4 for 8-bit output of many rows: a piece's codes are 16 bytes of a
+// strip whose neighbours are the next rows', so one row alone scatters its
+// stores, 64 cache lines an instruction; four rows side by side store runs of
+// 64 bytes.  8192 x 14336 in bf16, SwiGLU: TODO.
+template <int TPR, int RW> constexpr int kBlock = TPR * RW < 256 ? 256 : TPR * RW;
+
+template <typename Src, int TPR, int RW, int NCH, bool WHOLE, bool Y16, typename T>
+__global__ __launch_bounds__((kBlock<TPR, RW>)) void k_rows(Src src, Out8 o8, Out16 o16, float* rstd_out, int64_t m,
+                                                           int64_t k) {
+  constexpr int NW = TPR * RW / 64;  // waves that share RW rows
+  __shared__ uint32_t s_red[2 * RW * kBlock<TPR, RW> / 64];
+  const int t = threadIdx.x % (TPR * RW) / RW;
+  const int64_t row = ((int64_t)blockIdx.x * (kBlock<TPR, RW> / (TPR * RW)) + threadIdx.x / (TPR * RW)) * RW + threadIdx.x % RW;
   const bool live = row < m;
   const int64_t npieces = Y16 ? (k + 15) / 16 : o8.kp / 16;
   float sum = 0.f;
   uint32_t top = 0;
   constexpr int NV = NCH ? NCH : 1;
   float v[NV][16];
-  if (live) {
-    if constexpr (NCH > 0) {
+  if constexpr (NCH > 0) {
+    typename Src::Raw raw[NCH];
+    if constexpr (WHOLE) {
+      // every load at once; a thread past the row's end reads its start
 #pragma unroll
       for (int j = 0; j < NCH; ++j) {
-        const int64_t p = t + (int64_t)j * TPR;
-        if (p * 16 < k) {
-          src.load(row, p * 16, k, v[j], sum);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[j][i] = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) top = max(top, abs_bits(v[j][i]));
-      }
-    } else {
-      for (int64_t p = t; p * 16 < k; p += TPR) {
-        src.load(row, p * 16, k, v[0], sum);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) top = max(top, abs_bits(v[0][i]));
+        const int64_t c = (t + (int64_t)j * TPR) * 16;
+        src.template load<true>(live ? row : m - 1, c < k ? c : 0, k, raw[j]);
       }
     }
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+      const int64_t c = (t + (int64_t)j * TPR) * 16;
+      if (live && c < k) {
+        if constexpr (WHOLE) src.value(raw[j], row, c, k, v[j], sum);
+        else piece(src, row, c, k, v[j], sum);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[j][i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = max(top, abs_bits(v[j][i]));
+    }
+  } else if (live) {
+    for (int64_t p = t; p * 16 < k; p += TPR) {
+      piece(src, row, p * 16, k, v[0], sum);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = max(top, abs_bits(v[0][i]));
+    }
   }
-  row_reduce<TPR>(sum, top, s_red);
+  row_reduce<NW, RW>(sum, top, s_red);
   if (!live) return;
   float rstd = 1.f;
   // 1 / sqrt in full: it is once a row, and every value of the row has it
@@ -350,7 +449,7 @@ __global__ __launch_bounds__(1024) void k_rows(Src src, Out8 o8, Out16 o16, floa
       for (int64_t p = t; p < npieces; p += TPR) {
         float again = 0.f;
         if (p * 16 < k) {
-          src.load(row, p * 16, k, v[0], again);
+          piece(src, row, p * 16, k, v[0], again);
         } else {
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[0][i] = 0.f;
@@ -365,28 +464,48 @@ __global__ __launch_bounds__(1024) void k_rows(Src src, Out8 o8, Out16 o16, floa
   }
 }
 
-// Threads for a row: enough that two pieces each hold it, as many as there
-// are for few rows; then as many rows in a workgroup as keep one for each
-// compute unit, at most a strip of 16 (whose codes share cache lines).
 template <typename Src, bool Y16, typename T>
 hipError_t launch_rows(const Src& src, const Out8& o8, const Out16& o16, float* rstd, int64_t m, int64_t k, int cus,
                        hipStream_t st) {
   const int64_t pieces = Y16 ? (k + 15) / 16 : o8.kp / 16;
-  auto go = [&](auto tpr, auto nch) {
-    constexpr int TPR = decltype(tpr)::value, NCH = decltype(nch)::value;
-    int64_t r = 1;
-    while (r * 2 * TPR <= 1024 && r < 16 && r * 2 * cus <= m) r *= 2;
-    const int64_t grid = (m + r - 1) / r;
-    k_rows<Src, TPR, NCH, Y16, T><<<dim3((uint32_t)grid), dim3((uint32_t)(TPR * r)), 0, st>>>(src, o8, o16, rstd, m, k);
+  auto go = [&](auto tpr, auto rw, auto nch) {
+    constexpr int TPR = decltype(tpr)::value, RW = decltype(rw)::value, NCH = decltype(nch)::value;
+    constexpr int per = kBlock<TPR, RW> / TPR;
+    const dim3 grid((uint32_t)((m + per - 1) / per)), block(kBlock<TPR, RW>);
+    if (NCH > 0 && k % 16 == 0 && k > 0)
+      k_rows<Src, TPR, RW, NCH, (NCH > 0), Y16, T><<<grid, block, 0, st>>>(src, o8, o16, rstd, m, k);
+    else
+      k_rows<Src, TPR, RW, NCH, false, Y16, T><<<grid, block, 0, st>>>(src, o8, o16, rstd, m, k);
     return hipGetLastError();
   };
-  if (pieces <= 64) return go(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
-  if (pieces <= 128) return go(std::integral_constant<int, 128>{}, std::integral_constant<int, 1>{});
-  if (pieces <= 256) return go(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
-  if (pieces <= 512) return go(std::integral_constant<int, 512>{}, std::integral_constant<int, 1>{});
-  if (pieces <= 1024) return go(std::integral_constant<int, 512>{}, std::integral_constant<int, 2>{});
-  if (pieces <= 2048) return go(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
-  if constexpr (!Src::kNorm) return go(std::integral_constant<int, 1024>{}, std::integral_constant<int, 0>{});
+  using std::integral_constant;
+  constexpr integral_constant<int, 0> c0{};
+  constexpr integral_constant<int, 1> c1{};
+  constexpr integral_constant<int, 2> c2{};
+  constexpr integral_constant<int, 4> c4{};
+  constexpr integral_constant<int, 64> c64{};
+  constexpr integral_constant<int, 128> c128{};
+  constexpr integral_constant<int, 256> c256{};
+  constexpr integral_constant<int, 512> c512{};
+  constexpr integral_constant<int, 1024> c1024{};
+  if constexpr (!Y16) {
+    // four rows side by side where that still leaves each compute unit some
+    if (m >= 4 * cus) {
+      if (pieces <= 64) return go(c64, c4, c1);
+      if (pieces <= 128) return go(c128, c4, c1);
+      if (pieces <= 256) return go(c128, c4, c2);
+      if (pieces <= 512) return go(c256, c4, c2);
+      if (pieces <= 768) return go(c256, c4, integral_constant<int, 3>{});
+      if (pieces <= 1024) return go(c256, c4, c4);
+    }
+  }
+  if (pieces <= 64) return go(c64, c1, c1);
+  if (pieces <= 128) return go(c128, c1, c1);
+  if (pieces <= 256) return go(c256, c1, c1);
+  if (pieces <= 512) return go(c512, c1, c1);
+  if (pieces <= 1024) return go(c512, c1, c2);
+  if (pieces <= 2048) return go(c1024, c1, c2);
+  if constexpr (!Src::kNorm) return go(c1024, c1, c0);
   return hipErrorInvalidValue;  // the entry points refuse norms of longer rows
 }
 
@@ -408,92 +527,164 @@ hipError_t norm_typed(const NormArgs& a, int cus, hipStream_t st) {
 }
 
 // ---- RMS norm, backward -----------------------------------------------------
-// Workgroup b takes rows b, b + groups, ...; a thread keeps its columns
-// throughout, so the dgamma of its rows adds up in registers (in row order)
-// and leaves once, as one row of partial sums; k_norm_dgamma adds the groups
-// up in a fixed order.  No atomics: the same inputs give the same bits.
-template <typename T, typename G, int TPR, int NCH>
-__global__ __launch_bounds__(TPR) void k_norm_bwd(Mat<T> dy, Mat<T> h, Mat<T> dh, Mat<G> gamma, const float* rstd,
-                                                  Out16 dx, float* part, int64_t m, int64_t k) {
-  __shared__ uint32_t s_red[32];
-  const int t = threadIdx.x;
+// A workgroup has SUB teams of TPR threads.  Team i of all of them takes rows
+// i, i + teams, ...; a thread keeps its columns throughout, so the dgamma of
+// its rows adds up in registers (in row order), the teams' sums meet in LDS
+// (in team order), and one row of partial sums leaves each workgroup;
+// k_norm_dgamma adds those up in a fixed order.  No atomics: the same inputs
+// give the same bits.  The next row's h and dY are loaded before the current
+// row's reduction, whose latency would otherwise bound the kernel; they stay
+// packed in pairs.
+template <typename T, typename G, int TPR, int NCH, bool WHOLE>
+__global__ __launch_bounds__(1024) void k_norm_bwd(Mat<T> dy, Mat<T> h, Mat<T> dh, Mat<G> gamma, const float* rstd,
+                                                   Out16 dx, float* part, int64_t m, int64_t k) {
+  constexpr int SUB = 1024 / TPR, NW = TPR / 64;
+  __shared__ uint32_t s_red[2 * 16];
+  __shared__ __attribute__((aligned(16))) float s_acc[SUB > 1 ? SUB * TPR * 16 : 4];
+  const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  const int64_t step = (int64_t)gridDim.x * SUB;
+  auto col = [&](int j) { return ((int64_t)j * TPR + t) * 16; };
+  // one piece of a row (zeros past k; rows past the last read the last)
+  auto get = [&](auto& p, const auto& a, int64_t r, int64_t c) {
+    r = r < m ? r : m - 1;
+    if constexpr (WHOLE) {
+      p.template load<true>(a, r, c < k ? c : 0, k);
+    } else {
+      if (c + 16 <= k) p.template load<true>(a, r, c, k);
+      else if (c < k) p.template load<false>(a, r, c, k);
+      else p.zero();
+    }
+  };
   float acc[NCH][16];
+  Piece<G> gm[NCH];
 #pragma unroll
-  for (int j = 0; j < NCH; ++j)
+  for (int j = 0; j < NCH; ++j) {
+    get(gm[j], gamma, 0, col(j));
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[j][i] = 0.f;
-  for (int64_t row = blockIdx.x; row < m; row += gridDim.x) {
-    const float rs = in_bounds(row, 1, m) ? rstd[row] : 0.f;
-    // the row's values stay packed across the reduction: half the registers
-    uint32_t hp[NCH][8], dp[NCH][8];
+  }
+  Piece<T> hp[NCH], dp[NCH], hn[NCH], dn[NCH], ep[NCH];
+  int64_t row = (int64_t)blockIdx.x * SUB + sub;
+#pragma unroll
+  for (int j = 0; j < NCH; ++j) {
+    get(hp[j], h, row, col(j));
+    get(dp[j], dy, row, col(j));
+  }
+  // every team makes the same number of turns: they share the barriers
+  for (int64_t first = (int64_t)blockIdx.x * SUB; first < m; first += step, row += step) {
+    const bool live = row < m;
+    const float rs = live && in_bounds(row, 1, m) ? rstd[row] : 0.f;
+    if (!live) {  // a row past the last adds nothing
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) hp[j].zero();
+    }
+    if (dh.p) {
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) get(ep[j], dh, row, col(j));
+    }
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+      get(hn[j], h, row + step, col(j));
+      get(dn[j], dy, row + step, col(j));
+    }
     float dot = 0.f;
     uint32_t none = 0;
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
-      const int64_t c = ((int64_t)j * TPR + t) * 16;
-      load_packed(h, row, c, k, hp[j]);
-      load_packed(dy, row, c, k, dp[j]);
-    }
-#pragma unroll
-    for (int j = 0; j < NCH; ++j) {
-      float gm[16];
-      load_row<16>(gamma, 0, ((int64_t)j * TPR + t) * 16, k, gm);
+      float part_dot = 0.f;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const float hat = unpack<T>(hp[j], i) * rs, d = unpack<T>(dp[j], i);
+        const float hat = hp[j].at(i) * rs, d = dp[j].at(i);
         acc[j][i] = __builtin_fmaf(d, hat, acc[j][i]);
-        dot = __builtin_fmaf(d * gm[i], hat, dot);
+        part_dot = __builtin_fmaf(d * gm[j].at(i), hat, part_dot);
       }
+      dot += col(j) < k ? part_dot : 0.f;
     }
-    row_reduce<TPR>(dot, none, s_red);
-    dot /= (float)k;
+    row_reduce<NW, 1>(dot, none, s_red);
+    const float mean = dot / (float)k;
+    // unpack again rather than keep 48 unpacked values across the reduction:
+    // the compiler would find them equal, and spill
+#pragma unroll
+    for (int j = 0; j < NCH; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        asm volatile("" : "+v"(hp[j].d[i]), "+v"(dp[j].d[i]));
+        if constexpr (Piece<G>::kDw == 8) asm volatile("" : "+v"(gm[j].d[i]));
+      }
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
-      const int64_t c = ((int64_t)j * TPR + t) * 16;
-      if (c >= k) continue;
-      float g[16];
-      load_row<16>(gamma, 0, c, k, g);
+      const int64_t c = col(j);
+      if (live && c < k) {
+        float g[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        g[i] = rs * __builtin_fmaf(-(unpack<T>(hp[j], i) * rs), dot, unpack<T>(dp[j], i) * g[i]);
-      if (dh.p) {
-        uint32_t e[8];
-        load_packed(dh, row, c, k, e);
+        for (int i = 0; i < 16; ++i)
+          g[i] = rs * __builtin_fmaf(-(hp[j].at(i) * rs), mean, dp[j].at(i) * gm[j].at(i));
+        if (dh.p) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) g[i] += unpack<T>(e, i);
+          for (int i = 0; i < 16; ++i) g[i] += ep[j].at(i);
+        }
+        store_row<T>(dx, row, c, k, g);
       }
-      store_row<T>(dx, row, c, k, g);
+      hp[j] = hn[j];
+      dp[j] = dn[j];
     }
+  }
+  if constexpr (SUB > 1) {
+    // [team][4-column group][thread]: conflict-free both ways
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<float4*>(s_acc + ((sub * 4 + i) * TPR + t) * 4) =
+          make_float4(acc[0][4 * i], acc[0][4 * i + 1], acc[0][4 * i + 2], acc[0][4 * i + 3]);
+    __syncthreads();
+    if (sub > 0) return;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[0][i] = 0.f;
+#pragma unroll 2
+    for (int w = 0; w < SUB; ++w)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 f = *reinterpret_cast<const float4*>(s_acc + ((w * 4 + i) * TPR + t) * 4);
+        acc[0][4 * i] += f.x;
+        acc[0][4 * i + 1] += f.y;
+        acc[0][4 * i + 2] += f.z;
+        acc[0][4 * i + 3] += f.w;
+      }
   }
 #pragma unroll
   for (int j = 0; j < NCH; ++j) {
     const int64_t c = ((int64_t)j * TPR + t) * 16;
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (c + i < k && in_bounds((int64_t)blockIdx.x * k + c + i, 1, (int64_t)gridDim.x * k))
-        part[(int64_t)blockIdx.x * k + c + i] = acc[j][i];
+    for (int i = 0; i < 16; i += 4) {
+      const int64_t e = (int64_t)blockIdx.x * part_pitch(k) + c + i;
+      if (c + i < k && in_bounds(e, 4, (int64_t)gridDim.x * part_pitch(k)))
+        *reinterpret_cast<float4*>(part + e) = make_float4(acc[j][i], acc[j][i + 1], acc[j][i + 2], acc[j][i + 3]);
+    }
   }
 }
 
-// dgamma[c] = sum over the groups of part[g][c]: 64 columns a workgroup, 16
-// waves that each add every 16th group, then the waves in order.
+// dgamma[c] = sum over the groups of part[g][c]: 32 columns a workgroup, 32
+// partial sums of every 32nd group each, then those in order.
 __global__ __launch_bounds__(1024) void k_norm_dgamma(const float* part, int groups, float* dgamma, int64_t k) {
-  __shared__ float s[16][64];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+  __shared__ float s[32][32];
+  const int col = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.x * 32 + col, pitch = part_pitch(k);
   float v = 0.f;
-  if (c < k)
-    for (int g = w; g < groups; g += 16)
-      v += in_bounds(g * k + c, 1, groups * k) ? part[g * k + c] : 0.f;
-  s[w][lane] = v;
+  if (c < k) {
+#pragma unroll 8
+    for (int g = w; g < groups; g += 32) v += in_bounds(g * pitch + c, 1, groups * pitch) ? part[g * pitch + c] : 0.f;
+  }
+  s[w][col] = v;
   __syncthreads();
   if (w == 0 && c < k) {
     v = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v += s[i][lane];
+    for (int i = 0; i < 32; ++i) v += s[i][col];
     if (in_bounds(c, 1, k)) dgamma[c] = v;
   }
 }
+
+// Threads for a row of the backward.
+int norm_bwd_threads(int64_t k) { return k <= 1024 ? 64 : k <= 2048 ? 128 : k <= 4096 ? 256 : k <= 8192 ? 512 : 1024; }
 
 template <typename T, typename G>
 hipError_t norm_bwd_typed(const NormBwdArgs& a, int cus, hipStream_t st) {
@@ -504,53 +695,64 @@ hipError_t norm_bwd_typed(const NormBwdArgs& a, int cus, hipStream_t st) {
   const int groups = a.m > 0 ? norm_bwd_groups(a.m, a.k, cus) : 0;
   auto go = [&](auto tpr, auto nch) {
     constexpr int TPR = decltype(tpr)::value, NCH = decltype(nch)::value;
-    k_norm_bwd<T, G, TPR, NCH><<<dim3(groups), dim3(TPR), 0, st>>>(dy, h, dh, gamma, a.rstd, dx, a.part, a.m, a.k);
+    if (a.k % 16 == 0)
+      k_norm_bwd<T, G, TPR, NCH, true><<<dim3(groups), dim3(1024), 0, st>>>(dy, h, dh, gamma, a.rstd, dx, a.part, a.m, a.k);
+    else
+      k_norm_bwd<T, G, TPR, NCH, false><<<dim3(groups), dim3(1024), 0, st>>>(dy, h, dh, gamma, a.rstd, dx, a.part, a.m, a.k);
     return hipGetLastError();
   };
-  const int64_t pieces = (a.k + 15) / 16;
+  using std::integral_constant;
+  constexpr integral_constant<int, 1> c1{};
   hipError_t e = hipSuccess;
-  if (groups == 0) {  // no rows: dgamma is an empty sum
-  } else if (pieces <= 64) e = go(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
-  else if (pieces <= 256) e = go(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
-  else if (pieces <= 512) e = go(std::integral_constant<int, 512>{}, std::integral_constant<int, 1>{});
-  else if (pieces <= 1024) e = go(std::integral_constant<int, 1024>{}, std::integral_constant<int, 1>{});
-  else e = go(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
+  if (groups > 0) {  // without rows dgamma is an empty sum
+    switch (norm_bwd_threads(a.k)) {
+      case 64: e = go(integral_constant<int, 64>{}, c1); break;
+      case 128: e = go(integral_constant<int, 128>{}, c1); break;
+      case 256: e = go(integral_constant<int, 256>{}, c1); break;
+      case 512: e = go(integral_constant<int, 512>{}, c1); break;
+      default:
+        e = a.k <= 16384 ? go(integral_constant<int, 1024>{}, c1)
+                         : go(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+    }
+  }
   if (e != hipSuccess) return e;
-  k_norm_dgamma<<<dim3((uint32_t)((a.k + 63) / 64)), dim3(1024), 0, st>>>(a.part, groups, a.dgamma, a.k);
+  k_norm_dgamma<<<dim3((uint32_t)((a.k + 31) / 32)), dim3(1024), 0, st>>>(a.part, groups, a.dgamma, a.k);
   return hipGetLastError();
 }
 
 // ---- SwiGLU in 16 bits, elementwise -----------------------------------------
-// 8 values a thread; `per` pieces of 8 in a row.
+// 16 values a thread; `per` pieces in a row.
 template <typename T>
-__global__ __launch_bounds__(256) void k_swiglu(Mat<T> g, Mat<T> u, Out16 y, uint32_t per, uint32_t total, int64_t k) {
+__global__ __launch_bounds__(256) void k_swiglu(SwigluSrc<T> s, Out16 y, uint32_t per, uint32_t total, int64_t k) {
   const uint32_t id = blockIdx.x * 256u + threadIdx.x;
   if (id >= total) return;
-  const int64_t row = id / per, c = (int64_t)(id % per) * 8;
-  float a[8], b[8];
-  load_row<8>(g, row, c, k, a);
-  load_row<8>(u, row, c, k, b);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) a[i] = a[i] * sigmoid(a[i]) * b[i];
-  store_row<T>(y, row, c, k, a);
+  const int64_t row = id / per, c = (int64_t)(id % per) * 16;
+  float v[16], none = 0.f;
+  piece(s, row, c, k, v, none);
+  store_row<T>(y, row, c, k, v);
 }
 
 template <typename T>
-__global__ __launch_bounds__(256) void k_swiglu_bwd(Mat<T> dy, Mat<T> g, Mat<T> u, Out16 dg, Out16 du, uint32_t per,
+__global__ __launch_bounds__(256) void k_swiglu_bwd(Mat<T> dy, SwigluSrc<T> s, Out16 dg, Out16 du, uint32_t per,
                                                     uint32_t total, int64_t k) {
   const uint32_t id = blockIdx.x * 256u + threadIdx.x;
   if (id >= total) return;
-  const int64_t row = id / per, c = (int64_t)(id % per) * 8;
-  float d[8], a[8], b[8];
-  load_row<8>(dy, row, c, k, d);
-  load_row<8>(g, row, c, k, a);
-  load_row<8>(u, row, c, k, b);
+  const int64_t row = id / per, c = (int64_t)(id % per) * 16;
+  typename SwigluSrc<T>::Raw r;
+  Piece<T> d;
+  if (c + 16 <= k) {
+    s.template load<true>(row, c, k, r);
+    d.template load<true>(dy, row, c, k);
+  } else {
+    s.template load<false>(row, c, k, r);
+    d.template load<false>(dy, row, c, k);
+  }
+  float a[16], b[16];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float s = sigmoid(a[i]);
-    const float dup = d[i] * a[i] * s;
-    a[i] = d[i] * b[i] * s * (1.f + a[i] * (1.f - s));
-    b[i] = dup;
+  for (int i = 0; i < 16; ++i) {
+    const float g = r.g.at(i), sg = sigmoid(g), dyi = d.at(i);
+    a[i] = dyi * r.u.at(i) * sg * (1.f + g * (1.f - sg));
+    b[i] = dyi * g * sg;
   }
   store_row<T>(dg, row, c, k, a);
   store_row<T>(du, row, c, k, b);
@@ -573,11 +775,10 @@ hipError_t launch_norm(const NormArgs& a, int cus, hipStream_t st) {
   return a.type == kRowF16 ? norm_typed<F16, F16>(a, cus, st) : norm_typed<Bf16, Bf16>(a, cus, st);
 }
 
-// Two workgroups a compute unit where there are rows for them: more partial
-// sums would cost more than the rows they spread.
+// One workgroup of 1024 threads a compute unit, where there are rows for them.
 int norm_bwd_groups(int64_t m, int64_t k, int cus) {
-  const int64_t per = k > 8192 ? 1 : 2;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(m, per * cus));
+  const int64_t sub = 1024 / norm_bwd_threads(k);
+  return (int)std::max<int64_t>(1, std::min<int64_t>((m + sub - 1) / sub, cus));
 }
 
 hipError_t launch_norm_bwd(const NormBwdArgs& a, int cus, hipStream_t st) {
@@ -597,23 +798,23 @@ hipError_t launch_swiglu_rows(const SwigluArgs& a, int cus, hipStream_t st) {
 }
 
 hipError_t launch_swiglu(const SwigluArgs& a, hipStream_t st) {
-  const uint32_t per = (uint32_t)((a.k + 7) / 8), total = (uint32_t)(per * a.m);
+  const uint32_t per = (uint32_t)((a.k + 15) / 16), total = (uint32_t)(per * a.m);
   auto go = [&](auto type) {
     typedef decltype(type) T;
-    k_swiglu<T><<<dim3((total + 255u) / 256u), dim3(256), 0, st>>>(
-        mat<T>(a.g, a.ldg, a.m, a.k), mat<T>(a.u, a.ldu, a.m, a.k), out16(a.y, a.m, a.k), per, total, a.k);
+    const SwigluSrc<T> s{mat<T>(a.g, a.ldg, a.m, a.k), mat<T>(a.u, a.ldu, a.m, a.k)};
+    k_swiglu<T><<<dim3((total + 255u) / 256u), dim3(256), 0, st>>>(s, out16(a.y, a.m, a.k), per, total, a.k);
     return hipGetLastError();
   };
   return a.type == kRowF16 ? go(F16{}) : go(Bf16{});
 }
 
 hipError_t launch_swiglu_bwd(const SwigluArgs& a, hipStream_t st) {
-  const uint32_t per = (uint32_t)((a.k + 7) / 8), total = (uint32_t)(per * a.m);
+  const uint32_t per = (uint32_t)((a.k + 15) / 16), total = (uint32_t)(per * a.m);
   auto go = [&](auto type) {
     typedef decltype(type) T;
+    const SwigluSrc<T> s{mat<T>(a.g, a.ldg, a.m, a.k), mat<T>(a.u, a.ldu, a.m, a.k)};
     k_swiglu_bwd<T><<<dim3((total + 255u) / 256u), dim3(256), 0, st>>>(
-        mat<T>(a.dy, a.lddy, a.m, a.k), mat<T>(a.g, a.ldg, a.m, a.k), mat<T>(a.u, a.ldu, a.m, a.k),
-        out16(a.dg, a.m, a.k), out16(a.du, a.m, a.k), per, total, a.k);
+        mat<T>(a.dy, a.lddy, a.m, a.k), s, out16(a.dg, a.m, a.k), out16(a.du, a.m, a.k), per, total, a.k);
     return hipGetLastError();
   };
   return a.type == kRowF16 ? go(F16{}) : go(Bf16{});
