@@ -39,7 +39,7 @@ FLAGS = [
 # written explicitly).
 # Elsewhere products accumulate on the matrix cores and contraction is free.
 CONTRACT = {"codec.hip": "-ffp-contract=off", "merge.hip": "-ffp-contract=off",
-            "rows.hip": "-ffp-contract=off"}
+            "rows.hip": "-ffp-contract=off", "int8.hip": "-ffp-contract=off"}
 
 
 def _compile(src: str, obj: str, checked: bool = False) -> None:

@@ -120,6 +120,7 @@ struct Int8Ws {
 };
 Int8Ws int8_ws(int64_t m, int64_t n, int64_t k) {
   Int8Ws L{};
+  if (qlora::int8_fuses_rows(m, k)) return L;
   L.scale = round_up(qlora::int8_rows_bytes(m, k));
   L.part = L.req = L.scale + round_up((size_t)m * 4u);
   L.total = L.part + round_up(qlora::int8_part_bytes(m, n, k, qlora::device_compute_units()));
@@ -129,12 +130,19 @@ Int8Ws int8_ws(int64_t m, int64_t n, int64_t k) {
 int quantized_product(const int8_t* wcodes, const float* wscale, const float* col_scale, int64_t n, int64_t k,
                       const void* X, int64_t ldx, int64_t m, const uint16_t* bias, uint16_t* out, int dtype, void* ws,
                       size_t ws_bytes, hipStream_t stream) {
+  qlora::QuantArgs q{};
+  q.x = X; q.type = dtype; q.ldx = ldx; q.m = m; q.k = k; q.col_scale = col_scale;
+  if (qlora::int8_fuses_rows(m, k)) {
+    qlora::Int8GemmArgs g{};
+    g.w = wcodes; g.sw = wscale; g.bias = bias; g.out = out;
+    g.m = m; g.n = n; g.k = k;
+    g.f16 = dtype == QLORA_F16;
+    return done(qlora::launch_int8_fused(g, q, stream), "int8 product launch");
+  }
   const Int8Ws L = int8_ws(m, n, k);
   if (!ws || ws_bytes < L.req) return fail(QLORA_ERR_WORKSPACE, "int8 product workspace too small");
   if (!aligned16(ws)) return fail(QLORA_ERR_ALIGN, "workspace must be 16-byte aligned");
   char* base = static_cast<char*>(ws);
-  qlora::QuantArgs q{};
-  q.x = X; q.type = dtype; q.ldx = ldx; q.m = m; q.k = k; q.col_scale = col_scale;
   q.codes = reinterpret_cast<int8_t*>(base);
   q.scale = reinterpret_cast<float*>(base + L.scale);
   const hipError_t e = qlora::launch_quant_rows(q, qlora::device_compute_units(), stream);

@@ -12,6 +12,7 @@
 
 #include "common.h"
 #include "int8_layout.h"
+#include "rows_common.h"
 
 namespace qlora {
 namespace {
@@ -60,7 +61,7 @@ struct Outs {
   }
   // E(sum sx s + b), token scale first
   __device__ __forceinline__ uint32_t pair(int i, int lo, int hi, float sx) const {
-    return E::pack2((float)lo * sx * s[i] + b[i], (float)hi * sx * s[i + 1] + b[i + 1]);
+    return E::pack2(__builtin_fmaf((float)lo * sx, s[i], b[i]), __builtin_fmaf((float)hi * sx, s[i + 1], b[i + 1]));
   }
   __device__ __forceinline__ uint4 eight(i32x4 lo, i32x4 hi, float sx) const {
     return make_uint4(pair(0, lo[0], lo[1], sx), pair(2, lo[2], lo[3], sx), pair(4, hi[0], hi[1], sx),
@@ -117,19 +118,24 @@ __device__ __forceinline__ void tile_of(uint32_t lin, uint32_t mt, uint32_t nt, 
   tm = band * RB + within % rows;
 }
 
-// Many tokens.  Workgroup tile: 64 WM tokens x 128 WN outputs, one wave for
-// each 64 x 128 of it (32 accumulators of 16 x 16, 128 registers).  A 128-deep
-// step is 4 sub-steps of 16 MFMAs (16 x 16 x 64): 64 of the step's columns by
-// half of the wave's outputs.
+// Many tokens.  Workgroup tile: 256 tokens x 128 outputs, 4 waves of 64 x 128
+// (32 accumulators of 16 x 16, 128 registers), two workgroups a compute unit.
+// A 128-deep step is 4 sub-steps of 16 MFMAs (16 x 16 x 64): 64 of the step's
+// columns by half of the wave's outputs.
 //
 // The step's W tile goes through LDS (global -> registers two steps ahead ->
-// LDS, double buffered), where the WM waves that share its rows read it; each wave loads
-// its own token rows straight into registers, one step ahead, since only WN
-// waves share them and the first-level cache serves that.  LDS then carries
-// 128 WN x 128 bytes in and WM times that out per step, less than half of
-// what it would with both operands in it, and stays below the matrix cores'
-// time (256 x 256: 32 KB in, 128 KB out, 64 KB through the cache in 2048
-// matrix-core cycles).
+// LDS, double buffered), where the four waves read it; each wave loads its own
+// token rows, which no other wave needs, straight into registers, one step
+// ahead.  The two workgroups of a compute unit move 96 KB a step through the
+// cache and 160 KB through LDS (32 in, 128 out) in 2048 matrix-core cycles:
+// neither is the bound.
+//
+// Power is: 8192 x 14336 x 4096 runs at 1.9 to 2.0 GHz with the matrix cores
+// busy 61 % of the cycles (392 us, 2.46 PFLOP/s).  The loop without any loads
+// takes 237 us, and 307 us with 32 x 32 x 32 MFMAs, whose accumulators move
+// twice the registers for the same products.  Tiles of 256 x 256 (8 waves, one
+// workgroup a compute unit) take 402 us: less traffic, but nothing runs beside
+// their epilogue.  128 x 128: 448 us.
 //
 // The barrier of a step stands before its last sub-step: by then the next W
 // tile is written and every wave has this one's last operands in registers,
@@ -137,23 +143,22 @@ __device__ __forceinline__ void tile_of(uint32_t lin, uint32_t mt, uint32_t nt, 
 //
 // ksplit > 1: workgroup z of a tile sums its own range of steps and stores
 // the int32 sums to part[z]; k_int8_reduce adds them and finishes.
-template <int WM, int WN, typename E>
-__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_int8_gemm(Int8GemmArgs a) {
-  constexpr int kThreads = 64 * WM * WN, BM = 64 * WM, BN = 128 * WN;
+template <typename E>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_int8_gemm(Int8GemmArgs a) {
+  constexpr int kThreads = 256, BM = 256, BN = 128;
   constexpr int kTile = BN * 128;                     // bytes of a W tile
   constexpr int kStage = kTile / (16 * kThreads);     // 16-byte pieces of it per thread
   constexpr int kPitch = 128 + 8;                     // output staging: 16-bit elements per token
-  constexpr int kOut = WM * WN * 64 * kPitch * 2;     // bytes: 64 tokens x 128 outputs per wave
+  constexpr int kOut = 4 * 64 * kPitch * 2;           // bytes: 64 tokens x 128 outputs per wave
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kTile > kOut ? 2 * kTile : kOut];
   // uniform across the wave: buffer resources made from it stay scalar
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave / WN, wn = wave % WN;
   const uint32_t mt = (uint32_t)((a.m + BM - 1) / BM), nt = (uint32_t)((a.n + BN - 1) / BN);
   const uint32_t tiles = mt * nt;
   const int z = blockIdx.x / tiles;
   uint32_t tm, tn;
   tile_of(blockIdx.x % tiles, mt, nt, tm, tn);
-  const int64_t m0 = (int64_t)tm * BM + 64 * wm, n0 = (int64_t)tn * BN;
+  const int64_t m0 = (int64_t)tm * BM + 64 * wave, n0 = (int64_t)tn * BN;
   const int64_t kp = int8_kp(a.k);
   const uint32_t strip = 16u * (uint32_t)kp;
   const uint32_t steps = (uint32_t)(kp >> 7), per = (steps + a.ksplit - 1) / a.ksplit;
@@ -162,7 +167,6 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
   const __amdgpu_buffer_rsrc_t rw = strips_rsrc(a.w, n0 >> 4, int8_weight_strips(a.n), kp);
   const __amdgpu_buffer_rsrc_t rx = strips_rsrc(a.x, m0 >> 4, int8_row_strips(a.m), kp);
   const uint32_t at = (uint32_t)lane * 16u;
-  const uint32_t wat = (uint32_t)(8 * wn) * 2048u + at;  // in the LDS tile
 
   uint4 st[2][kStage], xf[2][4], wf[2][4];
   auto load_stage = [&](uint32_t s, int d) {
@@ -185,7 +189,7 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
   auto read_w = [&](int buf, int q, uint4 (&f)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      f[i] = *reinterpret_cast<const uint4*>(lds + buf * kTile + wat + (4 * (q & 1) + i) * 2048 + (q >> 1) * 1024);
+      f[i] = *reinterpret_cast<const uint4*>(lds + buf * kTile + at + (4 * (q & 1) + i) * 2048 + (q >> 1) * 1024);
   };
 
   i32x4 acc[8][4];
@@ -236,13 +240,12 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
 
   // lane 16 g + c: token 16 t + c, outputs 32 p + 8 g .. + 7 in strips 2 p and 2 p + 1
   const int g = lane >> 4, c = lane & 15;
-  const int64_t nw = n0 + 128 * wn;
   if (a.ksplit > 1) {
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
       for (int p = 0; p < 4; ++p)
-        store_part8(a, z, m0 + 16 * t + c, nw + 32 * p + 8 * g, acc[2 * p][t], acc[2 * p + 1][t]);
+        store_part8(a, z, m0 + 16 * t + c, n0 + 32 * p + 8 * g, acc[2 * p][t], acc[2 * p + 1][t]);
     return;
   }
   // Through LDS, so that a token's 128 outputs leave as whole lines: each
@@ -255,7 +258,7 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
     Outs<E, 8> os;
-    os.load(a, nw + 32 * p + 8 * g);
+    os.load(a, n0 + 32 * p + 8 * g);
 #pragma unroll
     for (int t = 0; t < 4; ++t)
       *reinterpret_cast<uint4*>(so + (16 * t + c) * kPitch + 32 * p + 8 * g) = os.eight(acc[2 * p][t], acc[2 * p + 1][t], sx[t]);
@@ -263,28 +266,86 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2,
 #pragma unroll
   for (int r = 0; r < 16; ++r) {
     const int row = 4 * r + g, col = c * 8;
-    store8(a, m0 + row, nw + col, *reinterpret_cast<const uint4*>(so + row * kPitch + col));
+    store8(a, m0 + row, n0 + col, *reinterpret_cast<const uint4*>(so + row * kPitch + col));
   }
 }
 
-// Few tokens: up to 16 TT of them, every one against every weight row, the
-// weight read once.  A workgroup takes one strip pair (32 outputs) and its NW
-// waves share out the reduction, 64 columns in turn; a wave reads weight
-// tiles and token tiles straight into the MFMA's registers, whole kilobytes
-// at a time, and the waves' sums meet in LDS.  Bound by reading the weight.
-template <int TT, int NW, typename E>
-__global__ __launch_bounds__(64 * NW) void k_int8_few(Int8GemmArgs a) {
+// Few tokens, or little of everything: 16 TT tokens against 32 outputs (a
+// strip pair) a workgroup, whose 8 waves share out the reduction, 64 columns
+// in turn.  A wave reads weight tiles and token tiles straight into the
+// MFMA's registers, whole kilobytes at a time, four of its turns in flight, and
+// the waves' sums meet in LDS.  Up to 64 tokens the weight is read once, and
+// reading it is the bound (28672 x 8192 for one token: 44 us, 5.3 TB/s).
+//
+// FUSED (TT = 1, at most kFusedTokens tokens): x is not quantized yet.  Every
+// workgroup quantizes all of it into LDS, after its first weight tiles are on
+// their way: the rows are a few kilobytes in the second-level cache, and a
+// launch of its own for them costs more than the repetition.
+constexpr int kFusedTokens = 4;
+constexpr int kFewWaves = 8;
+constexpr int kFewAhead = 4;  // turns in flight
+__host__ __device__ constexpr int64_t fused_pitch(int64_t k) { return int8_kp(k) + 16; }  // of a token's codes in LDS
+
+template <int TT, bool FUSED, typename E>
+__global__ __launch_bounds__(64 * kFewWaves) void k_int8_few(Int8GemmArgs a, QuantSrc<E> src) {
+  constexpr int NW = kFewWaves, U = kFewAhead;
   __shared__ i32x4 s_sum[NW][2 * TT][64];
+  __shared__ float s_scale[kFusedTokens];
+  __shared__ uint32_t s_top[NW][kFusedTokens];
+  extern __shared__ __attribute__((aligned(16))) uint8_t s_codes[];  // FUSED: [m][fused_pitch]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t kp = int8_kp(a.k), groups = (a.n + 31) / 32;
-  const int64_t group = blockIdx.x % groups;
-  const int z = blockIdx.x / groups;
+  const int64_t kp = int8_kp(a.k);
+  const uint32_t groups = (uint32_t)((a.n + 31) / 32), blocks = (uint32_t)((a.m + 16 * TT - 1) / (16 * TT));
+  // token blocks of one group follow each other, then the groups, then the splits
+  const uint32_t tb = blockIdx.x % blocks, group = blockIdx.x / blocks % groups, z = blockIdx.x / blocks / groups;
   const uint32_t strip = 16u * (uint32_t)kp;
   const uint32_t chunks = (uint32_t)(kp >> 6), per = (chunks + a.ksplit - 1) / a.ksplit;
   const uint32_t c0 = min(z * per, chunks), c1 = min(c0 + per, chunks);
-  const __amdgpu_buffer_rsrc_t rw = strips_rsrc(a.w, 2 * group, int8_weight_strips(a.n), kp);
-  const __amdgpu_buffer_rsrc_t rx = strips_rsrc(a.x, 0, int8_row_strips(a.m), kp);
+  const __amdgpu_buffer_rsrc_t rw = strips_rsrc(a.w, 2 * (int64_t)group, int8_weight_strips(a.n), kp);
   const uint32_t at = lane * 16u;
+  uint4 w[U][2];
+  auto load_w = [&](uint32_t c) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) w[u][i] = buf_load16(rw, c + u * NW < c1 ? i * strip + (c + u * NW) * 1024u + at : kOOB);
+  };
+  if constexpr (FUSED) {
+    load_w(c0 + wave);
+    for (int m = 0; m < a.m; ++m) {
+      float none = 0.f, v[16];
+      uint32_t top = 0;
+      for (int64_t p = threadIdx.x; p * 16 < a.k; p += 64 * NW) {
+        piece(src, m, p * 16, a.k, v, none);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = max(top, abs_bits(v[i]));
+      }
+#pragma unroll
+      for (int d = 32; d > 0; d >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
+      if (lane == 0) s_top[wave][m] = top;
+    }
+    lds_barrier();
+    for (int m = 0; m < a.m; ++m) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < NW; ++i) top = max(top, s_top[i][m]);
+      const float amax = fmaxf(__builtin_bit_cast(float, top), kAmaxFloor);
+      const bool finite = top < 0x7f800000u;
+      const RowQuant q = row_quant(finite ? amax : 1.f);
+      for (int64_t p = threadIdx.x; p * 16 < kp; p += 64 * NW) {
+        float none = 0.f, v[16];
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (p * 16 < a.k && finite) {
+          piece(src, m, p * 16, a.k, v, none);
+          u = codes16(q, v);
+        }
+        *reinterpret_cast<uint4*>(s_codes + m * fused_pitch(a.k) + p * 16) = u;
+      }
+      if (threadIdx.x == 0) s_scale[m] = finite ? amax / 127.f : __builtin_nanf("");
+    }
+    lds_barrier();
+  }
+  const __amdgpu_buffer_rsrc_t rx = strips_rsrc(FUSED ? a.w : a.x, (int64_t)tb * TT, FUSED ? 0 : int8_row_strips(a.m), kp);
   i32x4 acc[2][TT];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
@@ -294,18 +355,25 @@ __global__ __launch_bounds__(64 * NW) void k_int8_few(Int8GemmArgs a) {
       for (int v = 0; v < 4; ++v) acc[i][t][v] = 0;
   // token rows past m are not read
   uint32_t xat[TT];
+  const int64_t m0 = (int64_t)tb * (16 * TT);
 #pragma unroll
-  for (int t = 0; t < TT; ++t) xat[t] = 16 * t + (lane & 15) < a.m ? t * strip + at : kOOB;
-  constexpr int U = 4;
+  for (int t = 0; t < TT; ++t) xat[t] = m0 + 16 * t + (lane & 15) < a.m ? t * strip + at : kOOB;
   for (uint32_t c = c0 + wave; c < c1; c += U * NW) {
-    uint4 w[U][2], x[U][TT];
+    uint4 x[U][TT];
+    if (!FUSED || c != c0 + wave) load_w(c);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const uint32_t cc = c + u * NW;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) w[u][i] = buf_load16(rw, cc < c1 ? i * strip + cc * 1024u + at : kOOB);
-#pragma unroll
-      for (int t = 0; t < TT; ++t) x[u][t] = buf_load16(rx, cc < c1 && xat[t] != kOOB ? xat[t] + cc * 1024u : kOOB);
+      for (int t = 0; t < TT; ++t) {
+        if constexpr (FUSED) {
+          x[u][t] = make_uint4(0, 0, 0, 0);
+          if ((lane & 15) < a.m && cc < c1)
+            x[u][t] = *reinterpret_cast<const uint4*>(s_codes + (lane & 15) * fused_pitch(a.k) + cc * 64 + (lane >> 4) * 16);
+        } else {
+          x[u][t] = buf_load16(rx, cc < c1 && xat[t] != kOOB ? xat[t] + cc * 1024u : kOOB);
+        }
+      }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -323,17 +391,18 @@ __global__ __launch_bounds__(64 * NW) void k_int8_few(Int8GemmArgs a) {
   for (int t = wave; t < TT; t += NW) {
     i32x4 lo = s_sum[0][t][lane], hi = s_sum[0][TT + t][lane];
 #pragma unroll
-    for (int w = 1; w < NW; ++w) {
-      lo += s_sum[w][t][lane];
-      hi += s_sum[w][TT + t][lane];
+    for (int v = 1; v < NW; ++v) {
+      lo += s_sum[v][t][lane];
+      hi += s_sum[v][TT + t][lane];
     }
-    const int64_t m = 16 * t + (lane & 15), n = 32 * group + 8 * (lane >> 4);
+    const int64_t m = m0 + 16 * t + (lane & 15), n = 32 * (int64_t)group + 8 * (lane >> 4);
     if (a.ksplit > 1) {
       store_part8(a, z, m, n, lo, hi);
     } else {
-      Outs<E, 8> o;
-      o.load(a, n);
-      store8(a, m, n, o.eight(lo, hi, token_scale(a, m)));
+      Outs<E, 8> os;
+      os.load(a, n);
+      const float sx = !FUSED ? token_scale(a, m) : m < a.m ? s_scale[m & (kFusedTokens - 1)] : 0.f;
+      store8(a, m, n, os.eight(lo, hi, sx));
     }
   }
 }
@@ -447,25 +516,49 @@ bool aligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p
 
 }  // namespace
 
+// Which kernel, and how many splits: the least by a model of their times, in
+// microseconds on 256 compute units, fitted to sweeps over 40 to 2048 tokens,
+// 1000 to 28672 outputs and reductions of 2500 to 28672 (it is within 15 % of
+// most and picks the fastest or one within 10 % of it).
+//   few     a workgroup makes one turn of its loads for each 2048 columns, at
+//           1.0, 1.2 or 2.0 us a turn for 16, 32 or 64 tokens; all of them
+//           together run at no more than 850 TOP/s (operands from the cache)
+//           and read the weight at no more than 5.3 TB/s.
+//           72 x 4096 x 4096: 8 us, as tiles 28 us (15 us with 4 splits).
+//   tiles   256 x 128, two workgroups a compute unit: 1.72 us a step of 128
+//           columns with two, 0.82 us with one.  8192 x 14336 x 4096: 392 us;
+//           1024 x 11008 x 4096: 50 us, few tokens' kernel 101 us.
+//   split   a launch more (3 us), and the int32 sums written and read at
+//           5 TB/s.  512 x 4096 x 11008 as tiles: 67, 45, 37 us in 1, 2, 4.
 Int8Plan int8_plan(int64_t m, int64_t n, int64_t k, int cus) {
-  Int8Plan p{};
+  Int8Plan best{};
+  double least = 0;
+  const double scale = 256.0 / cus, ops = 2e-6 * (double)n * (double)int8_kp(k);
   const int64_t steps = int8_kp(k) / 128;
-  if (m <= 64) {
-    p.kind = m <= 16 ? kInt8Few1 : m <= 32 ? kInt8Few2 : kInt8Few4;
-    const int64_t groups = (n + 31) / 32;
-    p.ksplit = (int)std::max<int64_t>(1, std::min<int64_t>(cus / std::max<int64_t>(1, groups), steps / 8));
-    return p;
+  auto consider = [&](Int8Kind kind, int split, double us) {
+    if (split > 1) us += 3.0 + 8e-6 * split * (double)m * (double)n / 5.0;
+    if (best.ksplit == 0 || us < least) {
+      best = Int8Plan{kind, split};
+      least = us;
+    }
+  };
+  const Int8Kind few = m <= 16 ? kInt8Few16 : m <= 32 ? kInt8Few32 : kInt8Few64;
+  const int64_t rows = m <= 16 ? 16 : m <= 32 ? 32 : 64, blocks = (m + rows - 1) / rows;
+  const double turn = m <= 16 ? 1.0 : m <= 32 ? 1.2 : 2.0;
+  const int64_t groups = blocks * ((n + 31) / 32), tiles = (m + 255) / 256 * ((n + 127) / 128);
+  for (int split = 1; split <= 8; split *= 2) {
+    if (split == 1 || groups * split <= cus) {
+      const double turns = (double)((steps + 16 * split - 1) / (16 * split));
+      const double bulk = scale * std::max(ops * (double)(blocks * rows) / 850.0, (double)n * (double)k / 5.3e6);
+      consider(few, split, 2.7 + std::max(turns * turn, bulk));
+    }
+    if (m > 64 && (split == 1 || tiles * split <= 2 * cus)) {
+      const int64_t wgs = tiles * split, full = wgs / (2 * cus), rest = wgs % (2 * cus);
+      const double step = 1.72 * (double)full + (rest > cus ? 1.6 : rest > 0 ? 0.82 : 0.0);
+      consider(kInt8Tile, split, 3.0 + step * (double)((steps + split - 1) / split));
+    }
   }
-  const int64_t big = (m + 255) / 256 * ((n + 255) / 256);
-  if (big >= cus / 2) {
-    p.kind = kInt8Tile256;
-    p.ksplit = 1;
-  } else {
-    p.kind = kInt8Tile128;
-    const int64_t tiles = (m + 127) / 128 * ((n + 127) / 128);
-    p.ksplit = (int)std::max<int64_t>(1, std::min<int64_t>(2 * cus / std::max<int64_t>(1, tiles), steps / 4));
-  }
-  return p;
+  return best;
 }
 
 size_t int8_plan_bytes(const Int8Plan& p, int64_t m, int64_t n) {
@@ -474,21 +567,27 @@ size_t int8_plan_bytes(const Int8Plan& p, int64_t m, int64_t n) {
 
 size_t int8_part_bytes(int64_t m, int64_t n, int64_t k, int cus) { return int8_plan_bytes(int8_plan(m, n, k, cus), m, n); }
 
+bool int8_fuses_rows(int64_t m, int64_t k) { return m <= kFusedTokens && m * fused_pitch(k) <= 32768; }
+
 template <typename E>
-static hipError_t run_plan(Int8GemmArgs a, const Int8Plan& p, hipStream_t st) {
+static hipError_t run_plan(Int8GemmArgs a, const Int8Plan& p, const QuantArgs* rows, hipStream_t st) {
   a.ksplit = a.part ? p.ksplit : 1;
-  auto grid = [&](int64_t bm, int64_t bn) { return (a.m + bm - 1) / bm * ((a.n + bn - 1) / bn) * a.ksplit; };
-  const bool few = p.kind == kInt8Few1 || p.kind == kInt8Few2 || p.kind == kInt8Few4;
-  const int64_t g = few ? (a.n + 31) / 32 * a.ksplit : p.kind == kInt8Tile256 ? grid(256, 256) : p.kind == kInt8Tile256x128 ? grid(256, 128) : grid(128, 128);
-  if (g > INT_MAX) return hipErrorInvalidValue;
-  const dim3 gr((uint32_t)g);
-  switch (p.kind) {
-    case kInt8Few1: k_int8_few<1, 8, E><<<gr, 512, 0, st>>>(a); break;
-    case kInt8Few2: k_int8_few<2, 8, E><<<gr, 512, 0, st>>>(a); break;
-    case kInt8Few4: k_int8_few<4, 8, E><<<gr, 512, 0, st>>>(a); break;
-    case kInt8Tile256: k_int8_gemm<4, 2, E><<<gr, 512, 0, st>>>(a); break;
-    case kInt8Tile256x128: k_int8_gemm<4, 1, E><<<gr, 256, 0, st>>>(a); break;
-    case kInt8Tile128: k_int8_gemm<2, 1, E><<<gr, 128, 0, st>>>(a); break;
+  const bool tile = p.kind == kInt8Tile;
+  const int64_t bm = tile ? 256 : p.kind == kInt8Few16 ? 16 : p.kind == kInt8Few32 ? 32 : 64, bn = tile ? 128 : 32;
+  const int64_t tiles = (a.m + bm - 1) / bm * ((a.n + bn - 1) / bn);
+  if (tiles * a.ksplit > INT_MAX) return hipErrorInvalidValue;
+  const dim3 gr((uint32_t)(tiles * a.ksplit));
+  QuantSrc<E> src{};
+  if (rows) {
+    src = QuantSrc<E>{mat<E>(rows->x, rows->ldx, rows->m, rows->k), rows->col_scale};
+    k_int8_few<1, true, E><<<gr, 64 * kFewWaves, (size_t)(a.m * fused_pitch(a.k)), st>>>(a, src);
+  } else {
+    switch (p.kind) {
+      case kInt8Few16: k_int8_few<1, false, E><<<gr, 64 * kFewWaves, 0, st>>>(a, src); break;
+      case kInt8Few32: k_int8_few<2, false, E><<<gr, 64 * kFewWaves, 0, st>>>(a, src); break;
+      case kInt8Few64: k_int8_few<4, false, E><<<gr, 64 * kFewWaves, 0, st>>>(a, src); break;
+      case kInt8Tile: k_int8_gemm<E><<<gr, 256, 0, st>>>(a); break;
+    }
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.ksplit == 1) return e;
@@ -499,11 +598,18 @@ static hipError_t run_plan(Int8GemmArgs a, const Int8Plan& p, hipStream_t st) {
 }
 
 hipError_t launch_int8_plan(const Int8GemmArgs& a, const Int8Plan& p, hipStream_t st) {
-  return a.f16 ? run_plan<F16>(a, p, st) : run_plan<Bf16>(a, p, st);
+  return a.f16 ? run_plan<F16>(a, p, nullptr, st) : run_plan<Bf16>(a, p, nullptr, st);
 }
 
 hipError_t launch_int8_gemm(const Int8GemmArgs& a, int cus, hipStream_t st) {
   return launch_int8_plan(a, int8_plan(a.m, a.n, a.k, cus), st);
+}
+
+hipError_t launch_int8_fused(const Int8GemmArgs& a, const QuantArgs& rows, hipStream_t st) {
+  Int8Plan p{};
+  p.kind = kInt8Few16;
+  p.ksplit = 1;
+  return a.f16 ? run_plan<F16>(a, p, &rows, st) : run_plan<Bf16>(a, p, &rows, st);
 }
 
 hipError_t launch_int8_pack(const int8_t* src, int64_t ld, int64_t n, int64_t k, int8_t* dst, hipStream_t st) {

@@ -106,7 +106,7 @@ struct Int8GemmArgs {  // out[m][n] = E(sx[m] sw[n] sum_k x[m][k] w[n][k] + bias
 };
 // Which kernel a product takes, and over how many workgroups a tile's
 // reduction is split (needs `part`; without it one).
-enum Int8Kind { kInt8Few1, kInt8Few2, kInt8Few4, kInt8Tile256, kInt8Tile128, kInt8Tile256x128 };
+enum Int8Kind { kInt8Few16, kInt8Few32, kInt8Few64, kInt8Tile };
 struct Int8Plan {
   Int8Kind kind;
   int ksplit;
@@ -116,6 +116,10 @@ size_t int8_plan_bytes(const Int8Plan& p, int64_t m, int64_t n);
 size_t int8_part_bytes(int64_t m, int64_t n, int64_t k, int cus);
 hipError_t launch_int8_plan(const Int8GemmArgs& a, const Int8Plan& p, hipStream_t st);
 hipError_t launch_int8_gemm(const Int8GemmArgs& a, int cus, hipStream_t st);
+// Few enough tokens for a product that quantizes its 16-bit rows itself, in one
+// launch (a.x, a.sx and a.part are then not used).
+bool int8_fuses_rows(int64_t m, int64_t k);
+hipError_t launch_int8_fused(const Int8GemmArgs& a, const QuantArgs& rows, hipStream_t st);
 hipError_t launch_int8_pack(const int8_t* src, int64_t ld, int64_t n, int64_t k, int8_t* dst, hipStream_t st);
 hipError_t launch_int8_transpose(const int8_t* src, int64_t n, int64_t k, int8_t* dst, hipStream_t st);
 hipError_t launch_int8_dequant(const int8_t* codes, const float* scale, int64_t m, int64_t k, bool weight, bool f16,

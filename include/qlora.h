@@ -450,8 +450,9 @@ int qlora_int8_dequant_rows(const int8_t *codes, const float *scale, int64_t M, 
  *                           dY[m][n] scale[n]: the gradient of the forward with its rounding to 8 bits passed
  *                           straight through.  Needs codes_t.  There is no dW: the weight is frozen.
  * Workspace: qlora_int8_workspace_bytes(QLORA_OP_FWD / _BWD, M, n_out, k_in),
- * and qlora_int8_rows_workspace_bytes for _rows; the part for split sums is
- * optional (without room the product runs unsplit, with the same result).
+ * and qlora_int8_rows_workspace_bytes for _rows; 0 for few tokens, which need
+ * none.  The part for split sums is optional (without room the product runs
+ * unsplit, with the same result).
  */
 size_t qlora_int8_workspace_bytes(int op, int64_t M, int64_t n_out, int64_t k_in);
 size_t qlora_int8_rows_workspace_bytes(int64_t M, int64_t n_out, int64_t k_in);
