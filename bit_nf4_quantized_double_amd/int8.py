@@ -66,7 +66,7 @@ def quantize_weight(W: torch.Tensor, transposed: bool = False) -> Int8Weight:
     """fp32, bf16 or fp16 [n_out, k_in] -> Int8Weight.  ``transposed``: also
     lay out the transpose, which linear_bwd reads."""
     dt, (n, k), dev = _first(W, "W", tuple(DTYPES))
-    p, ld = _mat(W, dt, (n, k), "W")
+    p, ld = _mat(W, dt, W.shape, "W", dev)
     w = Int8Weight(torch.empty(weight_bytes(n, k), dtype=torch.uint8, device=dev),
                    torch.empty(n, dtype=torch.float32, device=dev), n, k)
     st = qlora.lib().qlora_int8_quantize_weight(p, DTYPES[dt], ld, n, k, w.codes.data_ptr(), w.scale.data_ptr(),
@@ -79,7 +79,7 @@ def weight_from_codes(codes: torch.Tensor, scale: torch.Tensor, transposed: bool
     """int8 codes [n_out, k_in] and fp32 scales [n_out] from elsewhere (a
     checkpoint) -> Int8Weight with W = scale[:, None] * codes."""
     dt, (n, k), dev = _first(codes, "codes", (torch.int8,))
-    p, ld = _mat(codes, dt, (n, k), "codes")
+    p, ld = _mat(codes, dt, codes.shape, "codes", dev)
     _vec(scale, (torch.float32,), n, "scale", dev)
     w = Int8Weight(torch.empty(weight_bytes(n, k), dtype=torch.uint8, device=dev), scale.clone(), n, k)
     st = qlora.lib().qlora_int8_pack_weight(p, ld, n, k, w.codes.data_ptr(), _stream(dev))

@@ -39,17 +39,36 @@ def _stream(device) -> int:
     return _raw_stream(index)
 
 
-def _mat(t, dtype, shape, name: str, device=None):
+# Small calls are bound by the host: each check below passes on its first
+# line for the usual argument, and only says what is wrong when that fails.
+
+def _first(t, name: str, types=(torch.bfloat16, torch.float16)):
+    """(dtype, shape, device) that a call's other matrices have to match."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    dtype, shape = t.dtype, t.shape
+    if dtype not in types:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in types)}, got {dtype}")
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D, got {len(shape)} dimensions")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor (there is no CPU path)")
+    return dtype, shape, t.device
+
+
+def _mat(t, dtype, shape, name: str, device):
     """(pointer, row stride) of a matrix with contiguous rows."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr(), shape[1]
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor (there is no CPU path)")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if device is not None and t.device != device:
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
         raise ValueError(f"{name} must be on {device}")
     m, k = shape
     if k > 1 and t.stride(1) != 1:
@@ -60,40 +79,32 @@ def _mat(t, dtype, shape, name: str, device=None):
     return t.data_ptr(), ld
 
 
-def _first(t, name: str, types=(torch.bfloat16, torch.float16)):
-    """(dtype, shape, device) that a call's other matrices have to match."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in types:
-        raise TypeError(f"{name} must be {' or '.join(str(d) for d in types)}, got {t.dtype}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D, got {t.dim()} dimensions")
-    return t.dtype, tuple(t.shape), t.device
-
-
 def _vec(t, types, n: int, name: str, device) -> int:
     """Pointer of a contiguous vector of n elements."""
+    if isinstance(t, torch.Tensor) and t.dtype in types and t.shape == (n,) and t.device == device and t.is_contiguous():
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in types:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in types)}, got {t.dtype}")
-    if not t.is_cuda or t.device != device:
+    if t.device != device:
         raise ValueError(f"{name} must be on {device}")
-    if tuple(t.shape) != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous vector of {n} elements, got {tuple(t.shape)}")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous vector of {n} elements, got {tuple(t.shape)}")
 
 
-def _out(t, shape, dtype, name: str, device):
-    """A caller's output buffer (checked), or a new one."""
+def _out(t, shape, dtype, name: str, device, like=None):
+    """A caller's output buffer (checked), or a new one (`like`: a tensor of
+    that shape, type and device, to make it from sooner)."""
     if t is None:
+        if like is not None and like.is_contiguous():
+            return torch.empty_like(like)
         return torch.empty(shape, dtype=dtype, device=device)
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
     return t
 
 
-@dataclass
+@dataclass(slots=True)
 class Int8Rows:
     """Rows in 8 bits, a scale each, in the layout the int8 product reads."""
     codes: torch.Tensor  # uint8 [qlora_int8_rows_bytes(m, k)], opaque
@@ -127,7 +138,7 @@ def quantize_rows(X: torch.Tensor, col_scale: torch.Tensor | None = None) -> Int
     """bf16, fp16 or fp32 [M, K] -> Int8Rows; col_scale (fp32 [K]) multiplies
     the columns first."""
     dt, (m, k), dev = _first(X, "X", tuple(DTYPES))
-    p, ld = _mat(X, dt, (m, k), "X")
+    p, ld = _mat(X, dt, X.shape, "X", dev)
     c = None if col_scale is None else _vec(col_scale, (torch.float32,), k, "col_scale", dev)
     q = _new_rows(m, k, torch.bfloat16 if dt == torch.float32 else dt, dev)
     st = qlora.lib().qlora_int8_quantize_rows(p, DTYPES[dt], ld, m, k, c, q.codes.data_ptr(), q.scale.data_ptr(),
@@ -154,14 +165,14 @@ def dequant_rows(q: Int8Rows, out: torch.Tensor | None = None, dtype=None) -> to
 def _norm_args(X, gamma, residual, H):
     dt, shape, dev = _first(X, "X")
     m, k = shape
-    p, ld = _mat(X, dt, shape, "X")
+    p, ld = _mat(X, dt, shape, "X", dev)
     g = _vec(gamma, (dt, torch.float32), k, "gamma", dev)
     if residual is None:
         if H is not None:
             raise ValueError("H is written only with a residual (without one it is X)")
         return dt, m, k, dev, (p, ld, None, 0, g, DTYPES[gamma.dtype], m, k), X
     r, ldr = _mat(residual, dt, shape, "residual", dev)
-    return dt, m, k, dev, (p, ld, r, ldr, g, DTYPES[gamma.dtype], m, k), _out(H, shape, dt, "H", dev)
+    return dt, m, k, dev, (p, ld, r, ldr, g, DTYPES[gamma.dtype], m, k), _out(H, shape, dt, "H", dev, X)
 
 
 def rms_norm_fwd(X: torch.Tensor, gamma: torch.Tensor, eps: float, residual: torch.Tensor | None = None, *,
@@ -170,7 +181,7 @@ def rms_norm_fwd(X: torch.Tensor, gamma: torch.Tensor, eps: float, residual: tor
     (Y, h, rstd); without a residual h is X itself.  ``H`` may be X or the
     residual (updated in place)."""
     dt, m, k, dev, args, h = _norm_args(X, gamma, residual, H)
-    Y = _out(Y, (m, k), dt, "Y", dev)
+    Y = _out(Y, (m, k), dt, "Y", dev, X)
     rstd = torch.empty(m, dtype=torch.float32, device=dev)
     st = qlora.lib().qlora_rms_norm_fwd(*args, eps, None if residual is None else h.data_ptr(), Y.data_ptr(),
                                         rstd.data_ptr(), DTYPES[dt], _stream(dev))
@@ -196,12 +207,12 @@ def rms_norm_bwd(dY: torch.Tensor, H: torch.Tensor, rstd: torch.Tensor, gamma: t
     ``dH``: the gradient that reaches h by itself, added to dX."""
     dt, shape, dev = _first(dY, "dY")
     m, k = shape
-    dy, lddy = _mat(dY, dt, shape, "dY")
+    dy, lddy = _mat(dY, dt, shape, "dY", dev)
     h, ldh = _mat(H, dt, shape, "H", dev)
     dh, lddh = (None, 0) if dH is None else _mat(dH, dt, shape, "dH", dev)
     g = _vec(gamma, (dt, torch.float32), k, "gamma", dev)
     rs = _vec(rstd, (torch.float32,), m, "rstd", dev)
-    dX = _out(dX, shape, dt, "dX", dev)
+    dX = _out(dX, shape, dt, "dX", dev, dY)
     dgamma = _out(dgamma, (k,), torch.float32, "dgamma", dev)
     L = qlora.lib()
     wst, wsn = qlora._ws(L.qlora_rms_norm_bwd_workspace_bytes(m, k), dev, ws)
@@ -214,7 +225,7 @@ def rms_norm_bwd(dY: torch.Tensor, H: torch.Tensor, rstd: torch.Tensor, gamma: t
 
 def _swiglu_args(G, U):
     dt, shape, dev = _first(G, "gate")
-    g, ldg = _mat(G, dt, shape, "gate")
+    g, ldg = _mat(G, dt, shape, "gate", dev)
     u, ldu = _mat(U, dt, shape, "up", dev)
     return dt, shape, dev, (g, ldg, u, ldu, *shape)
 
@@ -222,7 +233,7 @@ def _swiglu_args(G, U):
 def swiglu_fwd(G: torch.Tensor, U: torch.Tensor, *, Y: torch.Tensor | None = None) -> torch.Tensor:
     """silu(G) * U in 16 bits."""
     dt, shape, dev, args = _swiglu_args(G, U)
-    Y = _out(Y, shape, dt, "Y", dev)
+    Y = _out(Y, shape, dt, "Y", dev, G)
     qlora._check(qlora.lib().qlora_swiglu_fwd(*args, Y.data_ptr(), DTYPES[dt], _stream(dev)), "qlora_swiglu_fwd")
     return Y
 
@@ -241,7 +252,7 @@ def swiglu_bwd(dY: torch.Tensor, G: torch.Tensor, U: torch.Tensor, *, dG: torch.
     """Returns (dG, dU)."""
     dt, shape, dev, args = _swiglu_args(G, U)
     dy, lddy = _mat(dY, dt, shape, "dY", dev)
-    dG, dU = _out(dG, shape, dt, "dG", dev), _out(dU, shape, dt, "dU", dev)
+    dG, dU = _out(dG, shape, dt, "dG", dev, G), _out(dU, shape, dt, "dU", dev, G)
     st = qlora.lib().qlora_swiglu_bwd(dy, lddy, *args, dG.data_ptr(), dU.data_ptr(), DTYPES[dt], _stream(dev))
     qlora._check(st, "qlora_swiglu_bwd")
     return dG, dU
