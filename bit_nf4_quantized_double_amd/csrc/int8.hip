@@ -121,14 +121,15 @@ __device__ __forceinline__ void tile_of(uint32_t lin, uint32_t mt, uint32_t nt, 
   tm = band * RB + within % rows;
 }
 
-// Many tokens.  Workgroup tile: 256 tokens x 128 outputs, 4 waves of 64 x 128
-// (32 accumulators of 16 x 16, 128 registers), two workgroups a compute unit.
-// A 128-deep step is 4 sub-steps of 16 MFMAs (16 x 16 x 64): 64 of the step's
-// columns by half of the wave's outputs.
+// Many tokens.  Workgroup tile: 256 tokens x 128 outputs.  WN = 1: 4 waves of
+// 64 x 128 (32 accumulators of 16 x 16, 128 registers), two workgroups a
+// compute unit, for more tiles than those; WN = 2: 8 waves of 64 x 64, so that
+// one workgroup alone gives each SIMD two waves.  A 128-deep step is sub-steps
+// of 16 MFMAs (16 x 16 x 64): 64 of its columns by 64 outputs.
 //
 // The step's W tile goes through LDS (global -> registers two steps ahead ->
-// LDS, double buffered), where the four waves read it; each wave loads its own
-// token rows, which no other wave needs, straight into registers, one step
+// LDS, double buffered), where the waves read it; each wave loads its token
+// rows, which at most one other wave needs, straight into registers, one step
 // ahead.  The two workgroups of a compute unit move 96 KB a step through the
 // cache and 160 KB through LDS (32 in, 128 out) in 2048 matrix-core cycles:
 // neither is the bound.
@@ -146,37 +147,42 @@ __device__ __forceinline__ void tile_of(uint32_t lin, uint32_t mt, uint32_t nt, 
 //
 // ksplit > 1: workgroup z of a tile sums its own range of steps and stores
 // the int32 sums to part[z]; k_int8_reduce adds them and finishes.
-template <typename E>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_int8_gemm(Int8GemmArgs a) {
-  constexpr int kThreads = 256, BM = 256, BN = 128;
-  constexpr int kTile = BN * 128;                     // bytes of a W tile
+template <int WN, typename E>
+__global__ __launch_bounds__(256 * WN) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_int8_gemm(Int8GemmArgs a) {
+  constexpr int kThreads = 256 * WN, BM = 256, BN = 128;
+  constexpr int KC = 2;                               // chunks of 64 columns in a step
+  constexpr int NS = 8 / WN;                          // weight strips of a wave
+  constexpr int kTile = BN * 64 * KC;                 // bytes of a W tile
   constexpr int kStage = kTile / (16 * kThreads);     // 16-byte pieces of it per thread
-  constexpr int kPitch = 128 + 8;                     // output staging: 16-bit elements per token
-  constexpr int kOut = 4 * 64 * kPitch * 2;           // bytes: 64 tokens x 128 outputs per wave
+  constexpr int kPitch = 16 * NS + 8;                 // output staging: 16-bit elements per token
+  constexpr int kOut = 4 * WN * 64 * kPitch * 2;      // bytes: 64 tokens x 16 NS outputs per wave
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kTile > kOut ? 2 * kTile : kOut];
   // uniform across the wave: buffer resources made from it stay scalar
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
   const uint32_t mt = (uint32_t)((a.m + BM - 1) / BM), nt = (uint32_t)((a.n + BN - 1) / BN);
   const uint32_t tiles = mt * nt;
   const int z = blockIdx.x / tiles;
   uint32_t tm, tn;
   tile_of(blockIdx.x % tiles, mt, nt, tm, tn);
-  const int64_t m0 = (int64_t)tm * BM + 64 * wave, n0 = (int64_t)tn * BN;
+  const int64_t m0 = (int64_t)tm * BM + 64 * wm, n0 = (int64_t)tn * BN;
   const int64_t kp = int8_kp(a.k);
   const uint32_t strip = 16u * (uint32_t)kp;
-  const uint32_t steps = (uint32_t)(kp >> 7), per = (steps + a.ksplit - 1) / a.ksplit;
-  const uint32_t s0 = min(z * per, steps), s1 = min(s0 + per, steps);
+  // this split's columns, in chunks of 64: [c0, c1)
+  const uint32_t chunks = (uint32_t)(kp >> 6), per = (chunks + a.ksplit - 1) / a.ksplit;
+  const uint32_t c0 = min(z * per, chunks), c1 = min(c0 + per, chunks), steps = (c1 - c0 + KC - 1) / KC;
 
   const __amdgpu_buffer_rsrc_t rw = strips_rsrc(a.w, n0 >> 4, int8_weight_strips(a.n), kp);
   const __amdgpu_buffer_rsrc_t rx = strips_rsrc(a.x, m0 >> 4, int8_row_strips(a.m), kp);
   const uint32_t at = (uint32_t)lane * 16u;
+  const uint32_t wat = (uint32_t)(wn * NS * KC) * 1024u + at;  // the wave's strips in the LDS tile
 
-  uint4 st[2][kStage], xf[2][4], wf[2][4];
+  uint4 st[2][kStage], xf[KC][4], wf[2][4];
   auto load_stage = [&](uint32_t s, int d) {
 #pragma unroll
     for (int u = 0; u < kStage; ++u) {
-      const uint32_t i = u * kThreads + tid;
-      st[d][u] = buf_load16(rw, s < s1 ? (i >> 7) * strip + s * 2048u + (i & 127u) * 16u : kOOB);
+      const uint32_t i = u * kThreads + tid, c = c0 + s * KC + i % (64 * KC) / 64;
+      st[d][u] = buf_load16(rw, c < c1 ? i / (64 * KC) * strip + c * 1024u + i % 64 * 16u : kOOB);
     }
   };
   auto write_stage = [&](int buf, int d) {
@@ -184,92 +190,96 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     for (int u = 0; u < kStage; ++u)
       *reinterpret_cast<uint4*>(lds + buf * kTile + (u * kThreads + tid) * 16) = st[d][u];
   };
-  auto load_x = [&](uint32_t s, int c) {
+  auto load_x = [&](uint32_t s, int j) {
+    const uint32_t c = c0 + s * KC + j;
 #pragma unroll
-    for (int t = 0; t < 4; ++t) xf[c][t] = buf_load16(rx, s < s1 ? at + t * strip + s * 2048u + c * 1024u : kOOB);
+    for (int t = 0; t < 4; ++t) xf[j][t] = buf_load16(rx, c < c1 ? at + t * strip + c * 1024u : kOOB);
   };
-  // sub-step q: columns 64 (q / 2) .., strips 4 (q % 2) ..
+  // sub-step q: columns 64 (q / P) .., strips 4 (q % P) .. of the wave's
+  constexpr int P = NS / 4, Q = KC * P;  // sub-steps for 64 columns, and in a step
   auto read_w = [&](int buf, int q, uint4 (&f)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      f[i] = *reinterpret_cast<const uint4*>(lds + buf * kTile + at + (4 * (q & 1) + i) * 2048 + (q >> 1) * 1024);
+      f[i] = *reinterpret_cast<const uint4*>(lds + buf * kTile + wat + ((4 * (q % P) + i) * KC + q / P) * 1024);
   };
 
-  i32x4 acc[8][4];
+  i32x4 acc[NS][4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < NS; ++i)
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
       for (int v = 0; v < 4; ++v) acc[i][t][v] = 0;
 
-  load_stage(s0, 0);
-  load_x(s0, 0);
-  load_x(s0, 1);
+  load_stage(0, 0);
+#pragma unroll
+  for (int j = 0; j < KC; ++j) load_x(0, j);
   write_stage(0, 0);
-  load_stage(s0 + 1, 1);
-  load_stage(s0 + 2, 0);
+  load_stage(1, 1);
+  load_stage(2, 0);
   lds_barrier();
   read_w(0, 0, wf[0]);
-  // step s, P = (s - s0) % 2: W tile s is in LDS buffer P, s + 1 in st[P ^ 1], s + 2 on its way to st[P]
+  // step s, B = s % 2: W tile s is in LDS buffer B, s + 1 in st[B ^ 1], s + 2 on its way to st[B]
   auto step = [&](uint32_t s, auto parity) {
-    constexpr int P = decltype(parity)::value;
+    constexpr int B = decltype(parity)::value;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (q == 3) lds_barrier();
-      if (q < 3) read_w(P, q + 1, wf[(q + 1) & 1]);
-      else read_w(P ^ 1, 0, wf[0]);
+    for (int q = 0; q < Q; ++q) {
       if (q == 0) {
-        write_stage(P ^ 1, P ^ 1);
-        load_stage(s + 3, P ^ 1);
+        write_stage(B ^ 1, B ^ 1);
+        load_stage(s + 3, B ^ 1);
       }
+      if (q == Q - 1) lds_barrier();
+      if (q < Q - 1) read_w(B, q + 1, wf[(q + 1) & 1]);
+      else read_w(B ^ 1, 0, wf[0]);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int t = 0; t < 4; ++t)
-          acc[4 * (q & 1) + i][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(as_i32x4(wf[q & 1][i]), as_i32x4(xf[q >> 1][t]),
-                                                                          acc[4 * (q & 1) + i][t], 0, 0, 0);
-      if (q & 1) load_x(s + 1, q >> 1);
+          acc[4 * (q % P) + i][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(as_i32x4(wf[q & 1][i]), as_i32x4(xf[q / P][t]),
+                                                                          acc[4 * (q % P) + i][t], 0, 0, 0);
+      if (q % P == P - 1) load_x(s + 1, q / P);
       // the scheduler keeps each sub-step's loads ahead of its MFMAs only if
       // it cannot move them across (408 us for the 8192 x 14336 x 4096
       // product without this, 390 with it)
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  for (uint32_t s = s0; s < s1; s += 2) {
+  for (uint32_t s = 0; s < steps; s += 2) {
     step(s, std::integral_constant<int, 0>{});
-    if (s + 1 < s1) step(s + 1, std::integral_constant<int, 1>{});
+    if (s + 1 < steps) step(s + 1, std::integral_constant<int, 1>{});
   }
 
   // lane 16 g + c: token 16 t + c, outputs 32 p + 8 g .. + 7 in strips 2 p and 2 p + 1
   const int g = lane >> 4, c = lane & 15;
+  const int64_t nw = n0 + 16 * NS * wn;
   if (a.ksplit > 1) {
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int p = 0; p < 4; ++p)
-        store_part8(a, z, m0 + 16 * t + c, n0 + 32 * p + 8 * g, acc[2 * p][t], acc[2 * p + 1][t]);
+      for (int p = 0; p < NS / 2; ++p)
+        store_part8(a, z, m0 + 16 * t + c, nw + 32 * p + 8 * g, acc[2 * p][t], acc[2 * p + 1][t]);
     return;
   }
-  // Through LDS, so that a token's 128 outputs leave as whole lines: each
-  // wave in its own region (no other wave touches it).
+  // Through LDS, so that a token's outputs leave as whole lines: each wave in
+  // its own region (no other wave touches it).
   lds_barrier();  // every wave has read its last operands
   uint16_t* so = reinterpret_cast<uint16_t*>(lds) + wave * 64 * kPitch;
   float sx[4];
 #pragma unroll
   for (int t = 0; t < 4; ++t) sx[t] = token_scale(a, m0 + 16 * t + c);
 #pragma unroll
-  for (int p = 0; p < 4; ++p) {
+  for (int p = 0; p < NS / 2; ++p) {
     Outs<E, 8> os;
-    os.load(a, n0 + 32 * p + 8 * g);
+    os.load(a, nw + 32 * p + 8 * g);
 #pragma unroll
     for (int t = 0; t < 4; ++t)
       *reinterpret_cast<uint4*>(so + (16 * t + c) * kPitch + 32 * p + 8 * g) = os.eight(acc[2 * p][t], acc[2 * p + 1][t], sx[t]);
   }
+  constexpr int kAcross = 2 * NS;  // 16-byte pieces of a token's outputs
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const int row = 4 * r + g, col = c * 8;
-    store8(a, m0 + row, n0 + col, *reinterpret_cast<const uint4*>(so + row * kPitch + col));
+  for (int r = 0; r < kAcross; ++r) {
+    const int row = (64 / kAcross) * r + lane / kAcross, col = lane % kAcross * 8;
+    store8(a, m0 + row, nw + col, *reinterpret_cast<const uint4*>(so + row * kPitch + col));
   }
 }
 
@@ -531,9 +541,10 @@ bool aligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p
 //           together run at no more than 850 TOP/s (operands from the cache)
 //           and read the weight at no more than 5.3 TB/s.
 //           72 x 4096 x 4096: 8 us, as tiles 28 us (15 us with 4 splits).
-//   tiles   256 x 128, two workgroups a compute unit: 1.72 us a step of 128
-//           columns with two, 0.82 us with one.  8192 x 14336 x 4096: 392 us;
-//           1024 x 11008 x 4096: 50 us, few tokens' kernel 101 us.
+//   tiles   256 x 128: 1.72 us a step of 128 columns with two workgroups a
+//           compute unit (4 waves), 0.8 us with one (8 waves: 80 us for 2048 x
+//           4096 x 11008, 88 us with 4).  8192 x 14336 x 4096: 377 us; 1024 x
+//           11008 x 4096: 50 us, few tokens' kernel 101 us.
 //   split   a launch more (3 us), and the int32 sums written and read at
 //           5 TB/s.  512 x 4096 x 11008 as tiles: 67, 45, 37 us in 1, 2, 4.
 Int8Plan int8_plan(int64_t m, int64_t n, int64_t k, int cus) {
@@ -560,8 +571,8 @@ Int8Plan int8_plan(int64_t m, int64_t n, int64_t k, int cus) {
     }
     if (m > 64 && (split == 1 || tiles * split <= 2 * cus)) {
       const int64_t wgs = tiles * split, full = wgs / (2 * cus), rest = wgs % (2 * cus);
-      const double step = 1.72 * (double)full + (rest > cus ? 1.6 : rest > 0 ? 0.82 : 0.0);
-      consider(kInt8Tile, split, 3.0 + step * (double)((steps + split - 1) / split));
+      const double step = 1.72 * (double)full + (rest > cus ? 1.6 : rest > 0 ? 0.8 : 0.0);
+      consider(wgs <= cus ? kInt8Tile8 : kInt8Tile4, split, 3.0 + step * (double)((steps + split - 1) / split));
     }
   }
   return best;
@@ -578,7 +589,7 @@ bool int8_fuses_rows(int64_t m, int64_t k) { return m <= kFusedTokens && m * fus
 template <typename E>
 static hipError_t run_plan(Int8GemmArgs a, const Int8Plan& p, const QuantArgs* rows, hipStream_t st) {
   a.ksplit = a.part ? p.ksplit : 1;
-  const bool tile = p.kind == kInt8Tile;
+  const bool tile = p.kind == kInt8Tile4 || p.kind == kInt8Tile8;
   const int64_t bm = tile ? 256 : p.kind == kInt8Few16 ? 16 : p.kind == kInt8Few32 ? 32 : 64, bn = tile ? 128 : 32;
   const int64_t tiles = (a.m + bm - 1) / bm * ((a.n + bn - 1) / bn);
   if (tiles * a.ksplit > INT_MAX) return hipErrorInvalidValue;
@@ -592,7 +603,8 @@ static hipError_t run_plan(Int8GemmArgs a, const Int8Plan& p, const QuantArgs* r
       case kInt8Few16: k_int8_few<1, false, E><<<gr, 64 * kFewWaves, 0, st>>>(a, src); break;
       case kInt8Few32: k_int8_few<2, false, E><<<gr, 64 * kFewWaves, 0, st>>>(a, src); break;
       case kInt8Few64: k_int8_few<4, false, E><<<gr, 64 * kFewWaves, 0, st>>>(a, src); break;
-      case kInt8Tile: k_int8_gemm<E><<<gr, 256, 0, st>>>(a); break;
+      case kInt8Tile4: k_int8_gemm<1, E><<<gr, 256, 0, st>>>(a); break;
+      case kInt8Tile8: k_int8_gemm<2, E><<<gr, 512, 0, st>>>(a); break;
     }
   }
   hipError_t e = hipGetLastError();
