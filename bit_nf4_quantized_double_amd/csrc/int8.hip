@@ -19,9 +19,10 @@ namespace {
 
 typedef __attribute__((ext_vector_type(4))) int i32x4;
 
-// 16 bytes at any 16-bit element's address (the hardware takes any; rows of an
-// odd number of outputs start anywhere).
+// 16 bytes at any element's address (the hardware takes any; rows of an odd
+// number of elements start anywhere).
 typedef __attribute__((ext_vector_type(4), aligned(2))) uint32_t u32x4u;
+typedef __attribute__((ext_vector_type(4), aligned(1))) uint32_t u32x4b;
 
 __device__ __forceinline__ i32x4 as_i32x4(uint4 u) { return __builtin_bit_cast(i32x4, u); }
 
@@ -443,15 +444,18 @@ __global__ __launch_bounds__(256) void k_int8_reduce(Int8GemmArgs a) {
 // Row-major codes into weight tiles: one 16-byte piece a thread, rows past n
 // and columns past k zero.
 __global__ __launch_bounds__(256) void k_int8_pack(const int8_t* src, int64_t ld, int64_t n, int64_t k, int8_t* dst,
-                                                   int64_t rows, bool vec) {
+                                                   int64_t rows) {
   const int64_t kp = int8_kp(k);
   const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x & 15), piece = (int64_t)blockIdx.y * 16 + (threadIdx.x >> 4);
   if (row >= rows || piece * 16 >= kp) return;
   const int64_t c = piece * 16, e = row * ld + c, size = (n - 1) * ld + k;
   uint4 u = make_uint4(0, 0, 0, 0);
   if (row < n) {
-    if (vec && c + 16 <= k) {
-      if (in_bounds(e, 16, size)) u = *reinterpret_cast<const uint4*>(src + e);
+    if (c + 16 <= k) {
+      if (in_bounds(e, 16, size)) {
+        const u32x4b b = *reinterpret_cast<const u32x4b*>(src + e);
+        u = make_uint4(b.x, b.y, b.z, b.w);
+      }
     } else {
       uint32_t d[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -495,7 +499,7 @@ __global__ __launch_bounds__(256) void k_int8_transpose(const int8_t* src, int64
 // Tiles back to a row-major 16-bit matrix of the values they stand for.
 template <typename E>
 __global__ __launch_bounds__(256) void k_int8_dequant(const int8_t* codes, const float* scale, int64_t m, int64_t k,
-                                                      bool weight, uint16_t* out, bool vec) {
+                                                      bool weight, uint16_t* out) {
   const int64_t kp = int8_kp(k), rows = (weight ? int8_weight_strips(m) : int8_row_strips(m)) * 16;
   // a strip's columns first: its 16 rows fill up together
   const uint32_t across = (uint32_t)((k + 255) / 256);
@@ -515,11 +519,11 @@ __global__ __launch_bounds__(256) void k_int8_dequant(const int8_t* codes, const
     o[i] = E::pack2((float)(int8_t)w * s, (float)(int8_t)(w >> 8) * s);
   }
   const int64_t e = row * k + c;
-  if (vec && c + 16 <= k) {
+  if (c + 16 <= k) {
     if (in_bounds(e, 16, m * k)) {
-      uint4* q = reinterpret_cast<uint4*>(out + e);
-      q[0] = make_uint4(o[0], o[1], o[2], o[3]);
-      q[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      u32x4u* q = reinterpret_cast<u32x4u*>(out + e);
+      q[0] = u32x4u{o[0], o[1], o[2], o[3]};
+      q[1] = u32x4u{o[4], o[5], o[6], o[7]};
     }
   } else {
 #pragma unroll
@@ -527,8 +531,6 @@ __global__ __launch_bounds__(256) void k_int8_dequant(const int8_t* codes, const
       if (c + i < k && in_bounds(e + i, 1, m * k)) out[e + i] = (uint16_t)(o[i >> 1] >> (16 * (i & 1)));
   }
 }
-
-bool aligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
 
 }  // namespace
 
@@ -633,7 +635,7 @@ hipError_t launch_int8_fused(const Int8GemmArgs& a, const QuantArgs& rows, hipSt
 hipError_t launch_int8_pack(const int8_t* src, int64_t ld, int64_t n, int64_t k, int8_t* dst, hipStream_t st) {
   const int64_t rows = int8_weight_strips(n) * 16;
   const dim3 grid((uint32_t)(rows / 16), (uint32_t)((int8_kp(k) / 16 + 15) / 16));
-  k_int8_pack<<<grid, 256, 0, st>>>(src, ld, n, k, dst, rows, aligned(src, 16) && (n <= 1 || ld % 16 == 0));
+  k_int8_pack<<<grid, 256, 0, st>>>(src, ld, n, k, dst, rows);
   return hipGetLastError();
 }
 
@@ -648,9 +650,8 @@ hipError_t launch_int8_dequant(const int8_t* codes, const float* scale, int64_t 
   const int64_t blocks = (m + 15) / 16 * ((k + 255) / 256);
   if (blocks > INT_MAX) return hipErrorInvalidValue;
   const dim3 grid((uint32_t)blocks);
-  const bool vec = aligned(out, 16) && (m <= 1 || k % 8 == 0);
-  if (f16) k_int8_dequant<F16><<<grid, 256, 0, st>>>(codes, scale, m, k, weight, out, vec);
-  else k_int8_dequant<Bf16><<<grid, 256, 0, st>>>(codes, scale, m, k, weight, out, vec);
+  if (f16) k_int8_dequant<F16><<<grid, 256, 0, st>>>(codes, scale, m, k, weight, out);
+  else k_int8_dequant<Bf16><<<grid, 256, 0, st>>>(codes, scale, m, k, weight, out);
   return hipGetLastError();
 }
 

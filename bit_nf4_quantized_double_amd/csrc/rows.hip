@@ -60,19 +60,19 @@ __device__ __forceinline__ void store_row(const Out16& o, int64_t row, int64_t c
 
 // Sum and maximum (of non-negative fp32 bit patterns, so that a NaN or an
 // infinity wins) over the threads that share a row; each of them gets both.
-// RW rows lie side by side in a wave (row = lane % RW), NW consecutive waves
-// share them; `lds` has 2 RW words for each wave of the workgroup.
+// RW rows share a wave (64 / RW lanes each, one after another), NW consecutive
+// waves share them; `lds` has 2 RW words for each wave of the workgroup.
 template <int NW, int RW>
 __device__ __forceinline__ void row_reduce(float& sum, uint32_t& top, uint32_t* lds) {
 #pragma unroll
-  for (int d = 32; d >= RW; d >>= 1) {
+  for (int d = 32 / RW; d > 0; d >>= 1) {
     sum += __shfl_xor(sum, d);
     top = max(top, (uint32_t)__shfl_xor((int)top, d));
   }
   if constexpr (NW > 1) {
-    const int wave = threadIdx.x >> 6, first = wave / NW * NW, lane = threadIdx.x & 63, r = lane % RW;
+    const int wave = threadIdx.x >> 6, first = wave / NW * NW, lane = threadIdx.x & 63, r = lane / (64 / RW);
     __syncthreads();  // an earlier reduction's reads are done
-    if (lane < RW) {
+    if (lane % (64 / RW) == 0) {
       lds[2 * (RW * wave + r)] = __builtin_bit_cast(uint32_t, sum);
       lds[2 * (RW * wave + r) + 1] = top;
     }
@@ -95,12 +95,9 @@ struct Out8 {
   bool weight;
 };
 
-__device__ __forceinline__ void store_codes(const Out8& o, int64_t row, int64_t piece, bool finite, const RowQuant& q,
-                                            const float (&v)[16]) {
-  if (piece * 16 >= o.kp) return;
+__device__ __forceinline__ void store_codes(const Out8& o, int64_t row, int64_t piece, uint4 u) {
+  if (row >= o.nscale || piece * 16 >= o.kp) return;
   const int64_t at = int8_piece(o.weight ? int8_weight_row(row) : row, piece, o.kp);
-  uint4 u = codes16(q, v);
-  if (!finite) u = make_uint4(0, 0, 0, 0);
   if (in_bounds(at, 16, o.bytes)) *reinterpret_cast<uint4*>(o.codes + at) = u;
 }
 
@@ -110,10 +107,14 @@ __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf
 
 template <typename T>
 struct SwigluSrc {
-  static constexpr bool kNorm = false;
+  static constexpr bool kNorm = false, kHeavy = false;
   Mat<T> g, u;
   struct Raw {
     Piece<T> g, u;
+    __device__ __forceinline__ void shift(int n) {
+      g.shift(n);
+      u.shift(n);
+    }
   };
   template <bool WHOLE>
   __device__ __forceinline__ void load(int64_t row, int64_t c, int64_t k, Raw& r) const {
@@ -131,7 +132,7 @@ struct SwigluSrc {
 // serves both.
 template <typename T, typename G>
 struct NormSrc {
-  static constexpr bool kNorm = true;
+  static constexpr bool kNorm = true, kHeavy = Piece<G>::kDw == 16;  // heavy: 32 registers a piece in flight
   Mat<T> x, r;
   Mat<G> gamma;
   Out16 h;
@@ -139,6 +140,11 @@ struct NormSrc {
   struct Raw {
     Piece<T> x, r;
     Piece<G> g;
+    __device__ __forceinline__ void shift(int n) {
+      x.shift(n);
+      r.shift(n);
+      g.shift(n);
+    }
   };
   template <bool WHOLE>
   __device__ __forceinline__ void load(int64_t row, int64_t c, int64_t k, Raw& w) const {
@@ -169,27 +175,33 @@ struct NormSrc {
   }
 };
 
-// TPR threads share a row, RW rows lie side by side in a wave, and a
-// workgroup of kBlock threads takes kBlock / TPR rows.  A thread holds NCH
-// pieces of 16 values (piece j: TPR j + its index in the row); NCH == 0 (rows
-// too long for that) reads the row a second time instead, from the cache.
+// TPR threads share a row, RW rows share a wave, and a workgroup of kBlock
+// threads takes kBlock / TPR rows.  A thread holds NCH pieces of 16 values
+// (piece j: TPR j + its index in the row); NCH == 0 (rows too long for that)
+// reads the row a second time instead, from the cache.
 //
-// WHOLE: k is a multiple of 16, so that no piece is partly filled and all of
-// a thread's loads go out together, with no branch between them.
+// WIDE: k is at least 16.  All of a thread's loads then go out together, with
+// no branch between them: where a row's length is no multiple of 16 its last
+// piece is made from the 16 values before its end.
 //
 // RW = 4 for 8-bit output of many rows: a piece's codes are 16 bytes of a
 // strip whose neighbours are the next rows', so one row alone scatters its
-// stores, 64 cache lines an instruction; four rows side by side store runs of
-// 64 bytes.  8192 x 14336 in bf16, SwiGLU: TODO.
+// stores, 64 cache lines an instruction.  With four rows in a wave the codes
+// change lanes before they are stored, so that neighbouring lanes hold
+// neighbouring rows and store runs of 64 bytes, while the loads stay runs of
+// 512 bytes of one row.  TODO
 template <int TPR, int RW> constexpr int kBlock = TPR * RW < 256 ? 256 : TPR * RW;
 
-template <typename Src, int TPR, int RW, int NCH, bool WHOLE, bool Y16, typename T>
+template <typename Src, int TPR, int RW, int NCH, bool WIDE, bool Y16, typename T>
 __global__ __launch_bounds__((kBlock<TPR, RW>)) void k_rows(Src src, Out8 o8, Out16 o16, float* rstd_out, int64_t m,
                                                            int64_t k) {
   constexpr int NW = TPR * RW / 64;  // waves that share RW rows
   __shared__ uint32_t s_red[2 * RW * kBlock<TPR, RW> / 64];
-  const int t = threadIdx.x % (TPR * RW) / RW;
-  const int64_t row = ((int64_t)blockIdx.x * (kBlock<TPR, RW> / (TPR * RW)) + threadIdx.x / (TPR * RW)) * RW + threadIdx.x % RW;
+  constexpr int LR = 64 / RW;  // lanes of a row in a wave
+  const int lane = threadIdx.x & 63, wave = threadIdx.x % (TPR * RW) / 64;
+  const int t = wave * LR + lane % LR;
+  const int64_t row0 = ((int64_t)blockIdx.x * (kBlock<TPR, RW> / (TPR * RW)) + threadIdx.x / (TPR * RW)) * RW;
+  const int64_t row = row0 + lane / LR;
   const bool live = row < m;
   const int64_t npieces = Y16 ? (k + 15) / 16 : o8.kp / 16;
   float sum = 0.f;
@@ -198,20 +210,22 @@ __global__ __launch_bounds__((kBlock<TPR, RW>)) void k_rows(Src src, Out8 o8, Ou
   float v[NV][16];
   if constexpr (NCH > 0) {
     typename Src::Raw raw[NCH];
-    if constexpr (WHOLE) {
-      // every load at once; a thread past the row's end reads its start
+    if constexpr (WIDE) {
+      // a thread past the row's end reads its last 16 values and drops them
 #pragma unroll
-      for (int j = 0; j < NCH; ++j) {
-        const int64_t c = (t + (int64_t)j * TPR) * 16;
-        src.template load<true>(live ? row : m - 1, c < k ? c : 0, k, raw[j]);
-      }
+      for (int j = 0; j < NCH; ++j)
+        src.template load<true>(live ? row : m - 1, min((t + (int64_t)j * TPR) * 16, k - 16), k, raw[j]);
     }
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
       const int64_t c = (t + (int64_t)j * TPR) * 16;
       if (live && c < k) {
-        if constexpr (WHOLE) src.value(raw[j], row, c, k, v[j], sum);
-        else piece(src, row, c, k, v[j], sum);
+        if constexpr (WIDE) {
+          if (c + 16 > k) raw[j].shift((int)(c + 16 - k));
+          src.value(raw[j], row, c, k, v[j], sum);
+        } else {
+          piece(src, row, c, k, v[j], sum);
+        }
       } else {
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[j][i] = 0.f;
@@ -227,7 +241,7 @@ __global__ __launch_bounds__((kBlock<TPR, RW>)) void k_rows(Src src, Out8 o8, Ou
     }
   }
   row_reduce<NW, RW>(sum, top, s_red);
-  if (!live) return;
+  if (RW == 1 && !live) return;
   float rstd = 1.f;
   // 1 / sqrt in full: it is once a row, and every value of the row has it
   if constexpr (Src::kNorm) rstd = 1.f / sqrtf(sum / (float)k + src.eps);
@@ -249,9 +263,22 @@ __global__ __launch_bounds__((kBlock<TPR, RW>)) void k_rows(Src src, Out8 o8, Ou
     else amax = fmaxf(amax, kAmaxFloor);
     const bool finite = top < 0x7f800000u && amax < __builtin_inff();
     const RowQuant q = row_quant(finite ? amax : 1.f);
-    if constexpr (NCH > 0) {
+    if constexpr (RW > 1) {
 #pragma unroll
-      for (int j = 0; j < NCH; ++j) store_codes(o8, row, t + (int64_t)j * TPR, finite, q, v[j]);
+      for (int j = 0; j < NCH; ++j) {
+        // lane RW i + r takes row r's piece i from lane LR r + i
+        uint4 u = finite ? codes16(q, v[j]) : make_uint4(0, 0, 0, 0);
+        const int from = (lane % RW * LR + lane / RW) * 4;
+        u.x = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)u.x);
+        u.y = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)u.y);
+        u.z = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)u.z);
+        u.w = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)u.w);
+        store_codes(o8, row0 + lane % RW, wave * LR + lane / RW + (int64_t)j * TPR, u);
+      }
+    } else if constexpr (NCH > 0) {
+#pragma unroll
+      for (int j = 0; j < NCH; ++j)
+        store_codes(o8, row, t + (int64_t)j * TPR, finite ? codes16(q, v[j]) : make_uint4(0, 0, 0, 0));
     } else {
       for (int64_t p = t; p < npieces; p += TPR) {
         float again = 0.f;
@@ -261,12 +288,12 @@ __global__ __launch_bounds__((kBlock<TPR, RW>)) void k_rows(Src src, Out8 o8, Ou
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[0][i] = 0.f;
         }
-        store_codes(o8, row, p, finite, q, v[0]);
+        store_codes(o8, row, p, finite ? codes16(q, v[0]) : make_uint4(0, 0, 0, 0));
       }
     }
     // a row with an infinity or a NaN: zero codes and a NaN scale, so that
     // every value and product of it is NaN
-    if (t == 0 && in_bounds(row, 1, o8.nscale))
+    if (live && t == 0 && in_bounds(row, 1, o8.nscale))
       o8.scale[row] = finite ? amax * rstd / 127.f : __builtin_nanf("");
   }
 }
@@ -279,10 +306,13 @@ hipError_t launch_rows(const Src& src, const Out8& o8, const Out16& o16, float* 
     constexpr int TPR = decltype(tpr)::value, RW = decltype(rw)::value, NCH = decltype(nch)::value;
     constexpr int per = kBlock<TPR, RW> / TPR;
     const dim3 grid((uint32_t)((m + per - 1) / per)), block(kBlock<TPR, RW>);
-    if (NCH > 0 && k % 16 == 0 && k > 0)
-      k_rows<Src, TPR, RW, NCH, (NCH > 0), Y16, T><<<grid, block, 0, st>>>(src, o8, o16, rstd, m, k);
-    else
-      k_rows<Src, TPR, RW, NCH, false, Y16, T><<<grid, block, 0, st>>>(src, o8, o16, rstd, m, k);
+    if constexpr (TPR == 64 && RW == 1) {
+      if (k < 16) {
+        k_rows<Src, TPR, RW, NCH, false, Y16, T><<<grid, block, 0, st>>>(src, o8, o16, rstd, m, k);
+        return hipGetLastError();
+      }
+    }
+    k_rows<Src, TPR, RW, NCH, (NCH > 0), Y16, T><<<grid, block, 0, st>>>(src, o8, o16, rstd, m, k);
     return hipGetLastError();
   };
   using std::integral_constant;
@@ -297,13 +327,16 @@ hipError_t launch_rows(const Src& src, const Out8& o8, const Out16& o16, float* 
   constexpr integral_constant<int, 1024> c1024{};
   if constexpr (!Y16) {
     // four rows side by side where that still leaves each compute unit some
-    if (m >= 4 * cus) {
+    if (m >= 4 * cus && k >= 16) {
       if (pieces <= 64) return go(c64, c4, c1);
       if (pieces <= 128) return go(c128, c4, c1);
       if (pieces <= 256) return go(c128, c4, c2);
       if (pieces <= 512) return go(c256, c4, c2);
       if (pieces <= 768) return go(c256, c4, integral_constant<int, 3>{});
-      if (pieces <= 1024) return go(c256, c4, c4);
+      if (pieces <= 1024) {
+        if constexpr (Src::kHeavy) return go(c512, c2, c2);  // four pieces of it would spill
+        else return go(c256, c4, c4);
+      }
     }
   }
   if (pieces <= 64) return go(c64, c1, c1);
@@ -342,7 +375,7 @@ hipError_t norm_typed(const NormArgs& a, int cus, hipStream_t st) {
 // give the same bits.  The next row's h and dY are loaded before the current
 // row's reduction, whose latency would otherwise bound the kernel; they stay
 // packed in pairs.
-template <typename T, typename G, int TPR, int NCH, bool WHOLE>
+template <typename T, typename G, int TPR, int NCH, bool WIDE>
 __global__ __launch_bounds__(1024) void k_norm_bwd(Mat<T> dy, Mat<T> h, Mat<T> dh, Mat<G> gamma, const float* rstd,
                                                    Out16 dx, float* part, int64_t m, int64_t k) {
   constexpr int SUB = 1024 / TPR, NW = TPR / 64;
@@ -351,14 +384,21 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(Mat<T> dy, Mat<T> h, Mat<T> d
   const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
   const int64_t step = (int64_t)gridDim.x * SUB;
   auto col = [&](int j) { return ((int64_t)j * TPR + t) * 16; };
-  // one piece of a row (zeros past k; rows past the last read the last)
+  // one piece of a row; rows past the last read the last.  WIDE: as in k_rows,
+  // made good by fix() when it is used, so that nothing waits for it before.
   auto get = [&](auto& p, const auto& a, int64_t r, int64_t c) {
     r = r < m ? r : m - 1;
-    if constexpr (WHOLE) {
-      p.template load<true>(a, r, c < k ? c : 0, k);
+    if constexpr (WIDE) {
+      p.template load<true>(a, r, min(c, k - 16), k);
     } else {
       if (c + 16 <= k) p.template load<true>(a, r, c, k);
       else if (c < k) p.template load<false>(a, r, c, k);
+      else p.zero();
+    }
+  };
+  auto fix = [&](auto& p, int64_t c) {
+    if (WIDE && c + 16 > k) {
+      if (c < k) p.shift((int)(c + 16 - k));
       else p.zero();
     }
   };
@@ -367,13 +407,15 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(Mat<T> dy, Mat<T> h, Mat<T> d
 #pragma unroll
   for (int j = 0; j < NCH; ++j) {
     get(gm[j], gamma, 0, col(j));
+    fix(gm[j], col(j));
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[j][i] = 0.f;
   }
+  constexpr bool AHEAD = NCH == 1;  // two pieces a thread and the next row's would spill
   Piece<T> hp[NCH], dp[NCH], hn[NCH], dn[NCH], ep[NCH];
   int64_t row = (int64_t)blockIdx.x * SUB + sub;
 #pragma unroll
-  for (int j = 0; j < NCH; ++j) {
+  for (int j = 0; j < NCH && AHEAD; ++j) {
     get(hp[j], h, row, col(j));
     get(dp[j], dy, row, col(j));
   }
@@ -381,18 +423,17 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(Mat<T> dy, Mat<T> h, Mat<T> d
   for (int64_t first = (int64_t)blockIdx.x * SUB; first < m; first += step, row += step) {
     const bool live = row < m;
     const float rs = live && in_bounds(row, 1, m) ? rstd[row] : 0.f;
-    if (!live) {  // a row past the last adds nothing
 #pragma unroll
-      for (int j = 0; j < NCH; ++j) hp[j].zero();
-    }
-    if (dh.p) {
-#pragma unroll
-      for (int j = 0; j < NCH; ++j) get(ep[j], dh, row, col(j));
+    for (int j = 0; j < NCH; ++j) {
+      if (live) fix(hp[j], col(j));
+      else hp[j].zero();  // a row past the last adds nothing
+      fix(dp[j], col(j));
     }
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
-      get(hn[j], h, row + step, col(j));
-      get(dn[j], dy, row + step, col(j));
+      if (dh.p && AHEAD) get(ep[j], dh, row, col(j));
+      get(AHEAD ? hn[j] : hp[j], h, AHEAD ? row + step : row, col(j));
+      get(AHEAD ? dn[j] : dp[j], dy, AHEAD ? row + step : row, col(j));
     }
     float dot = 0.f;
     uint32_t none = 0;
@@ -405,7 +446,7 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(Mat<T> dy, Mat<T> h, Mat<T> d
         acc[j][i] = __builtin_fmaf(d, hat, acc[j][i]);
         part_dot = __builtin_fmaf(d * gm[j].at(i), hat, part_dot);
       }
-      dot += col(j) < k ? part_dot : 0.f;
+      dot += part_dot;
     }
     row_reduce<NW, 1>(dot, none, s_red);
     const float mean = dot / (float)k;
@@ -427,13 +468,17 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(Mat<T> dy, Mat<T> h, Mat<T> d
         for (int i = 0; i < 16; ++i)
           g[i] = rs * __builtin_fmaf(-(hp[j].at(i) * rs), mean, dp[j].at(i) * gm[j].at(i));
         if (dh.p) {
+          if (!AHEAD) get(ep[j], dh, row, c);
+          fix(ep[j], c);
 #pragma unroll
           for (int i = 0; i < 16; ++i) g[i] += ep[j].at(i);
         }
         store_row<T>(dx, row, c, k, g);
       }
-      hp[j] = hn[j];
-      dp[j] = dn[j];
+      if (AHEAD) {
+        hp[j] = hn[j];
+        dp[j] = dn[j];
+      }
     }
   }
   if constexpr (SUB > 1) {
@@ -502,10 +547,13 @@ hipError_t norm_bwd_typed(const NormBwdArgs& a, int cus, hipStream_t st) {
   const int groups = a.m > 0 ? norm_bwd_groups(a.m, a.k, cus) : 0;
   auto go = [&](auto tpr, auto nch) {
     constexpr int TPR = decltype(tpr)::value, NCH = decltype(nch)::value;
-    if (a.k % 16 == 0)
-      k_norm_bwd<T, G, TPR, NCH, true><<<dim3(groups), dim3(1024), 0, st>>>(dy, h, dh, gamma, a.rstd, dx, a.part, a.m, a.k);
-    else
-      k_norm_bwd<T, G, TPR, NCH, false><<<dim3(groups), dim3(1024), 0, st>>>(dy, h, dh, gamma, a.rstd, dx, a.part, a.m, a.k);
+    if constexpr (TPR == 64) {
+      if (a.k < 16) {
+        k_norm_bwd<T, G, TPR, NCH, false><<<dim3(groups), dim3(1024), 0, st>>>(dy, h, dh, gamma, a.rstd, dx, a.part, a.m, a.k);
+        return hipGetLastError();
+      }
+    }
+    k_norm_bwd<T, G, TPR, NCH, true><<<dim3(groups), dim3(1024), 0, st>>>(dy, h, dh, gamma, a.rstd, dx, a.part, a.m, a.k);
     return hipGetLastError();
   };
   using std::integral_constant;

@@ -105,6 +105,25 @@ struct Piece {
 #pragma unroll
     for (int i = 0; i < kDw; ++i) d[i] = 0;
   }
+  // Drops the first n (0 .. 15) elements and fills up with zeros: what makes
+  // the end of a row out of the 16 elements before its end.
+  __device__ __forceinline__ void shift(int n) {
+    if constexpr (kDw == 8) {
+      if (n & 1) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[i] = __builtin_amdgcn_alignbit(i + 1 < 8 ? d[i + 1] : 0u, d[i], 16);
+      }
+      n >>= 1;
+    }
+    shift_dwords<kDw / 2>(n);
+  }
+  template <int B>
+  __device__ __forceinline__ void shift_dwords(int n) {
+    const uint32_t yes = only_if(n & B);
+#pragma unroll
+    for (int i = 0; i < kDw; ++i) d[i] = (d[i] & ~yes) | ((i + B < kDw ? d[i + B] : 0u) & yes);
+    if constexpr (B > 1) shift_dwords<B / 2>(n);
+  }
   template <bool WHOLE>
   __device__ __forceinline__ void load(const Mat<T>& a, int64_t row, int64_t c, int64_t k) {
     const int64_t e = row * a.ld + c;
@@ -181,11 +200,12 @@ __device__ __forceinline__ uint4 codes16(const RowQuant& q, const float (&v)[16]
 
 template <typename T>
 struct QuantSrc {
-  static constexpr bool kNorm = false;
+  static constexpr bool kNorm = false, kHeavy = false;
   Mat<T> x;
   const float* col_scale;
   struct Raw {
     Piece<T> x;
+    __device__ __forceinline__ void shift(int n) { x.shift(n); }
   };
   template <bool WHOLE>
   __device__ __forceinline__ void load(int64_t row, int64_t c, int64_t k, Raw& r) const {
