@@ -122,15 +122,14 @@ __device__ __forceinline__ void tile_of(uint32_t lin, uint32_t mt, uint32_t nt, 
   tm = band * RB + within % rows;
 }
 
-// Many tokens.  Workgroup tile: 256 tokens x 128 outputs.  WN = 1: 4 waves of
-// 64 x 128 (32 accumulators of 16 x 16, 128 registers), two workgroups a
-// compute unit, for more tiles than those; WN = 2: 8 waves of 64 x 64, so that
-// one workgroup alone gives each SIMD two waves.  A 128-deep step is sub-steps
-// of 16 MFMAs (16 x 16 x 64): 64 of its columns by 64 outputs.
+// Many tokens.  Workgroup tile: 256 tokens x 128 outputs, 4 waves of 64 x 128
+// (32 accumulators of 16 x 16, 128 registers), two workgroups a compute unit.
+// A 128-deep step is 4 sub-steps of 16 MFMAs (16 x 16 x 64): 64 of its columns
+// by 64 outputs.
 //
 // The step's W tile goes through LDS (global -> registers two steps ahead ->
-// LDS, double buffered), where the waves read it; each wave loads its token
-// rows, which at most one other wave needs, straight into registers, one step
+// LDS, double buffered), where the four waves read it; each wave loads its own
+// token rows, which no other wave needs, straight into registers, one step
 // ahead.  The two workgroups of a compute unit move 96 KB a step through the
 // cache and 160 KB through LDS (32 in, 128 out) in 2048 matrix-core cycles:
 // neither is the bound.
@@ -140,7 +139,8 @@ __device__ __forceinline__ void tile_of(uint32_t lin, uint32_t mt, uint32_t nt, 
 // takes 237 us, and 307 us with 32 x 32 x 32 MFMAs, whose accumulators move
 // twice the registers for the same products.  Tiles of 256 x 256 (8 waves, one
 // workgroup a compute unit) take 402 us where these take 392: less traffic, but
-// nothing runs beside their epilogue.  128 x 128: 448 us.
+// nothing runs beside their epilogue.  128 x 128: 448 us.  8 waves of 64 x 64
+// where a tile has its compute unit to itself: 4 % less or more, by the shape.
 //
 // The barrier of a step stands before its last sub-step: by then the next W
 // tile is written and every wave has this one's last operands in registers,
@@ -148,25 +148,24 @@ __device__ __forceinline__ void tile_of(uint32_t lin, uint32_t mt, uint32_t nt, 
 //
 // ksplit > 1: workgroup z of a tile sums its own range of steps and stores
 // the int32 sums to part[z]; k_int8_reduce adds them and finishes.
-template <int WN, typename E>
-__global__ __launch_bounds__(256 * WN) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_int8_gemm(Int8GemmArgs a) {
-  constexpr int kThreads = 256 * WN, BM = 256, BN = 128;
+template <typename E>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_int8_gemm(Int8GemmArgs a) {
+  constexpr int kThreads = 256, BM = 256, BN = 128;
   constexpr int KC = 2;                               // chunks of 64 columns in a step
-  constexpr int NS = 8 / WN;                          // weight strips of a wave
+  constexpr int NS = BN / 16;                         // weight strips
   constexpr int kTile = BN * 64 * KC;                 // bytes of a W tile
   constexpr int kStage = kTile / (16 * kThreads);     // 16-byte pieces of it per thread
-  constexpr int kPitch = 16 * NS + 8;                 // output staging: 16-bit elements per token
-  constexpr int kOut = 4 * WN * 64 * kPitch * 2;      // bytes: 64 tokens x 16 NS outputs per wave
+  constexpr int kPitch = BN + 8;                      // output staging: 16-bit elements per token
+  constexpr int kOut = 4 * 64 * kPitch * 2;           // bytes: 64 tokens x 128 outputs per wave
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kTile > kOut ? 2 * kTile : kOut];
   // uniform across the wave: buffer resources made from it stay scalar
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave / WN, wn = wave % WN;
   const uint32_t mt = (uint32_t)((a.m + BM - 1) / BM), nt = (uint32_t)((a.n + BN - 1) / BN);
   const uint32_t tiles = mt * nt;
   const int z = blockIdx.x / tiles;
   uint32_t tm, tn;
   tile_of(blockIdx.x % tiles, mt, nt, tm, tn);
-  const int64_t m0 = (int64_t)tm * BM + 64 * wm, n0 = (int64_t)tn * BN;
+  const int64_t m0 = (int64_t)tm * BM + 64 * wave, n0 = (int64_t)tn * BN;
   const int64_t kp = int8_kp(a.k);
   const uint32_t strip = 16u * (uint32_t)kp;
   // this split's columns, in chunks of 64: [c0, c1)
@@ -176,7 +175,6 @@ __global__ __launch_bounds__(256 * WN) __attribute__((amdgpu_waves_per_eu(2, 2))
   const __amdgpu_buffer_rsrc_t rw = strips_rsrc(a.w, n0 >> 4, int8_weight_strips(a.n), kp);
   const __amdgpu_buffer_rsrc_t rx = strips_rsrc(a.x, m0 >> 4, int8_row_strips(a.m), kp);
   const uint32_t at = (uint32_t)lane * 16u;
-  const uint32_t wat = (uint32_t)(wn * NS * KC) * 1024u + at;  // the wave's strips in the LDS tile
 
   uint4 st[2][kStage], xf[KC][4], wf[2][4];
   auto load_stage = [&](uint32_t s, int d) {
@@ -201,7 +199,7 @@ __global__ __launch_bounds__(256 * WN) __attribute__((amdgpu_waves_per_eu(2, 2))
   auto read_w = [&](int buf, int q, uint4 (&f)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      f[i] = *reinterpret_cast<const uint4*>(lds + buf * kTile + wat + ((4 * (q % P) + i) * KC + q / P) * 1024);
+      f[i] = *reinterpret_cast<const uint4*>(lds + buf * kTile + at + ((4 * (q % P) + i) * KC + q / P) * 1024);
   };
 
   i32x4 acc[NS][4];
@@ -252,13 +250,12 @@ __global__ __launch_bounds__(256 * WN) __attribute__((amdgpu_waves_per_eu(2, 2))
 
   // lane 16 g + c: token 16 t + c, outputs 32 p + 8 g .. + 7 in strips 2 p and 2 p + 1
   const int g = lane >> 4, c = lane & 15;
-  const int64_t nw = n0 + 16 * NS * wn;
   if (a.ksplit > 1) {
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
       for (int p = 0; p < NS / 2; ++p)
-        store_part8(a, z, m0 + 16 * t + c, nw + 32 * p + 8 * g, acc[2 * p][t], acc[2 * p + 1][t]);
+        store_part8(a, z, m0 + 16 * t + c, n0 + 32 * p + 8 * g, acc[2 * p][t], acc[2 * p + 1][t]);
     return;
   }
   // Through LDS, so that a token's outputs leave as whole lines: each wave in
@@ -271,7 +268,7 @@ __global__ __launch_bounds__(256 * WN) __attribute__((amdgpu_waves_per_eu(2, 2))
 #pragma unroll
   for (int p = 0; p < NS / 2; ++p) {
     Outs<E, 8> os;
-    os.load(a, nw + 32 * p + 8 * g);
+    os.load(a, n0 + 32 * p + 8 * g);
 #pragma unroll
     for (int t = 0; t < 4; ++t)
       *reinterpret_cast<uint4*>(so + (16 * t + c) * kPitch + 32 * p + 8 * g) = os.eight(acc[2 * p][t], acc[2 * p + 1][t], sx[t]);
@@ -280,7 +277,7 @@ __global__ __launch_bounds__(256 * WN) __attribute__((amdgpu_waves_per_eu(2, 2))
 #pragma unroll
   for (int r = 0; r < kAcross; ++r) {
     const int row = (64 / kAcross) * r + lane / kAcross, col = lane % kAcross * 8;
-    store8(a, m0 + row, nw + col, *reinterpret_cast<const uint4*>(so + row * kPitch + col));
+    store8(a, m0 + row, n0 + col, *reinterpret_cast<const uint4*>(so + row * kPitch + col));
   }
 }
 
@@ -543,10 +540,9 @@ __global__ __launch_bounds__(256) void k_int8_dequant(const int8_t* codes, const
 //           together run at no more than 850 TOP/s (operands from the cache)
 //           and read the weight at no more than 5.3 TB/s.
 //           72 x 4096 x 4096: 8 us, as tiles 28 us (15 us with 4 splits).
-//   tiles   256 x 128: 1.72 us a step of 128 columns with two workgroups a
-//           compute unit (4 waves), 0.8 us with one (8 waves: 80 us for 2048 x
-//           4096 x 11008, 88 us with 4).  8192 x 14336 x 4096: 377 us; 1024 x
-//           11008 x 4096: 50 us, few tokens' kernel 101 us.
+//   tiles   256 x 128, two workgroups a compute unit: 1.72 us a step of 128
+//           columns with two, 0.82 us with one.  8192 x 14336 x 4096: 377 us;
+//           1024 x 11008 x 4096: 50 us, few tokens' kernel 101 us.
 //   split   a launch more (3 us), and the int32 sums written and read at
 //           5 TB/s.  512 x 4096 x 11008 as tiles: 67, 45, 37 us in 1, 2, 4.
 Int8Plan int8_plan(int64_t m, int64_t n, int64_t k, int cus) {
@@ -573,8 +569,8 @@ Int8Plan int8_plan(int64_t m, int64_t n, int64_t k, int cus) {
     }
     if (m > 64 && (split == 1 || tiles * split <= 2 * cus)) {
       const int64_t wgs = tiles * split, full = wgs / (2 * cus), rest = wgs % (2 * cus);
-      const double step = 1.72 * (double)full + (rest > cus ? 1.6 : rest > 0 ? 0.8 : 0.0);
-      consider(wgs <= cus ? kInt8Tile8 : kInt8Tile4, split, 3.0 + step * (double)((steps + split - 1) / split));
+      const double step = 1.72 * (double)full + (rest > cus ? 1.6 : rest > 0 ? 0.82 : 0.0);
+      consider(kInt8Tile, split, 3.0 + step * (double)((steps + split - 1) / split));
     }
   }
   return best;
@@ -591,7 +587,7 @@ bool int8_fuses_rows(int64_t m, int64_t k) { return m <= kFusedTokens && m * fus
 template <typename E>
 static hipError_t run_plan(Int8GemmArgs a, const Int8Plan& p, const QuantArgs* rows, hipStream_t st) {
   a.ksplit = a.part ? p.ksplit : 1;
-  const bool tile = p.kind == kInt8Tile4 || p.kind == kInt8Tile8;
+  const bool tile = p.kind == kInt8Tile;
   const int64_t bm = tile ? 256 : p.kind == kInt8Few16 ? 16 : p.kind == kInt8Few32 ? 32 : 64, bn = tile ? 128 : 32;
   const int64_t tiles = (a.m + bm - 1) / bm * ((a.n + bn - 1) / bn);
   if (tiles * a.ksplit > INT_MAX) return hipErrorInvalidValue;
@@ -605,8 +601,7 @@ static hipError_t run_plan(Int8GemmArgs a, const Int8Plan& p, const QuantArgs* r
       case kInt8Few16: k_int8_few<1, false, E><<<gr, 64 * kFewWaves, 0, st>>>(a, src); break;
       case kInt8Few32: k_int8_few<2, false, E><<<gr, 64 * kFewWaves, 0, st>>>(a, src); break;
       case kInt8Few64: k_int8_few<4, false, E><<<gr, 64 * kFewWaves, 0, st>>>(a, src); break;
-      case kInt8Tile4: k_int8_gemm<1, E><<<gr, 256, 0, st>>>(a); break;
-      case kInt8Tile8: k_int8_gemm<2, E><<<gr, 512, 0, st>>>(a); break;
+      case kInt8Tile: k_int8_gemm<E><<<gr, 256, 0, st>>>(a); break;
     }
   }
   hipError_t e = hipGetLastError();

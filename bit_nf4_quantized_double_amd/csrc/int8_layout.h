@@ -106,7 +106,7 @@ struct Int8GemmArgs {  // out[m][n] = E(sx[m] sw[n] sum_k x[m][k] w[n][k] + bias
 };
 // Which kernel a product takes, and over how many workgroups a tile's
 // reduction is split (needs `part`; without it one).
-enum Int8Kind { kInt8Few16, kInt8Few32, kInt8Few64, kInt8Tile4, kInt8Tile8 };
+enum Int8Kind { kInt8Few16, kInt8Few32, kInt8Few64, kInt8Tile };
 struct Int8Plan {
   Int8Kind kind;
   int ksplit;

@@ -423,18 +423,22 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(Mat<T> dy, Mat<T> h, Mat<T> d
   for (int64_t first = (int64_t)blockIdx.x * SUB; first < m; first += step, row += step) {
     const bool live = row < m;
     const float rs = live && in_bounds(row, 1, m) ? rstd[row] : 0.f;
+    auto mend = [&] {
 #pragma unroll
-    for (int j = 0; j < NCH; ++j) {
-      if (live) fix(hp[j], col(j));
-      else hp[j].zero();  // a row past the last adds nothing
-      fix(dp[j], col(j));
-    }
+      for (int j = 0; j < NCH; ++j) {
+        if (live) fix(hp[j], col(j));
+        else hp[j].zero();  // a row past the last adds nothing
+        fix(dp[j], col(j));
+      }
+    };
+    if (AHEAD) mend();
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
       if (dh.p && AHEAD) get(ep[j], dh, row, col(j));
       get(AHEAD ? hn[j] : hp[j], h, AHEAD ? row + step : row, col(j));
       get(AHEAD ? dn[j] : dp[j], dy, AHEAD ? row + step : row, col(j));
     }
+    if (!AHEAD) mend();
     float dot = 0.f;
     uint32_t none = 0;
 #pragma unroll
