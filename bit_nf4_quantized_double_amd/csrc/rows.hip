@@ -189,7 +189,15 @@ struct NormSrc {
 // stores, 64 cache lines an instruction.  With four rows in a wave the codes
 // change lanes before they are stored, so that neighbouring lanes hold
 // neighbouring rows and store runs of 64 bytes, while the loads stay runs of
-// 512 bytes of one row.  TODO
+// 512 bytes of one row.  SwiGLU at 8192 x 14336: 130 us, 163 us with a row to
+// a workgroup.  Rows interleaved by lanes instead, for loads and stores alike,
+// do as well at aligned widths, and take 107 us for 57 at 8192 x 7167.
+//
+// Measured in bf16 at 8192 x 4096, where a copy of one input takes 24 us (5.6
+// TB/s): quantize 21 us (4.9 TB/s), SwiGLU in 8 bits 31 us (5.5), norm with the
+// residual 45 us (5.9), the same in 8 bits 41 us (5.7).  Rows of 14336 are 1024
+// threads to a workgroup and one of those to a compute unit, so loads and
+// stores take turns: 4.4 to 4.5 TB/s.
 template <int TPR, int RW> constexpr int kBlock = TPR * RW < 256 ? 256 : TPR * RW;
 
 template <typename Src, int TPR, int RW, int NCH, bool WIDE, bool Y16, typename T>
@@ -374,7 +382,8 @@ hipError_t norm_typed(const NormArgs& a, int cus, hipStream_t st) {
 // k_norm_dgamma adds those up in a fixed order.  No atomics: the same inputs
 // give the same bits.  The next row's h and dY are loaded before the current
 // row's reduction, whose latency would otherwise bound the kernel; they stay
-// packed in pairs.
+// packed in pairs.  8192 x 4096: 55 us (4.9 TB/s); without the loads ahead, four
+// rows to a workgroup's turn, 70 us.
 template <typename T, typename G, int TPR, int NCH, bool WIDE>
 __global__ __launch_bounds__(1024) void k_norm_bwd(Mat<T> dy, Mat<T> h, Mat<T> dh, Mat<G> gamma, const float* rstd,
                                                    Out16 dx, float* part, int64_t m, int64_t k) {
@@ -580,7 +589,8 @@ hipError_t norm_bwd_typed(const NormBwdArgs& a, int cus, hipStream_t st) {
 }
 
 // ---- SwiGLU in 16 bits, elementwise -----------------------------------------
-// 16 values a thread; `per` pieces in a row.
+// 16 values a thread; `per` pieces in a row.  8192 x 4096 in bf16: forward 32 us
+// (6.3 TB/s), backward 61 us (5.5).
 template <typename T>
 __global__ __launch_bounds__(256) void k_swiglu(SwigluSrc<T> s, Out16 y, uint32_t per, uint32_t total, int64_t k) {
   const uint32_t id = blockIdx.x * 256u + threadIdx.x;
