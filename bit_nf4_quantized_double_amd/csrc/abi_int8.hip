@@ -43,7 +43,7 @@ int check_dim(int64_t v, const char* name) {
 
 int check_reduction(int64_t v, const char* name) {
   if (v > qlora::kInt8MaxK)
-    return fail(QLORA_ERR_SHAPE, std::string(name) + " exceeds 133144, where an int32 sum of products could overflow");
+    return fail(QLORA_ERR_SHAPE, std::string(name) + " exceeds 132104, where an int32 sum of products could overflow");
   return QLORA_OK;
 }
 

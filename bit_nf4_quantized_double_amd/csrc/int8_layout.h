@@ -25,8 +25,9 @@
 
 namespace qlora {
 
-// The largest reduction whose int32 sum cannot overflow: 2^31 / 127^2.
-constexpr int64_t kInt8MaxK = 133144;
+// The largest reduction whose int32 sum cannot overflow: quantized rows hold
+// codes of -127 .. 127, a weight's codes from elsewhere -128 too.
+constexpr int64_t kInt8MaxK = 132104;
 
 __host__ __device__ constexpr int64_t int8_kp(int64_t k) { return (k + 127) / 128 * 128; }
 __host__ __device__ constexpr int64_t int8_row_strips(int64_t m) { return (m + 15) / 16; }

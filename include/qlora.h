@@ -395,7 +395,7 @@ int qlora_format_table(int format, float out[16]);
  * the matrix cores, an opaque layout of qlora_int8_rows_bytes(M, K) bytes for
  * rows and qlora_int8_weight_bytes(n_out, k_in) for a weight (columns padded
  * to 128, rows to 16 or 32; the two layouts differ); qlora_int8_dequant_rows
- * and _weight read them back.  The reduction of a product is at most 133144
+ * and _weight read them back.  The reduction of a product is at most 132104
  * (QLORA_ERR_SHAPE beyond): its int32 sum is exact.
  */
 enum { QLORA_BF16 = 0, QLORA_F16 = 1, QLORA_F32 = 2 };
@@ -421,7 +421,7 @@ size_t qlora_int8_rows_bytes(int64_t M, int64_t K);
  *   qlora_int8_quantize_weight   W [n_out, k_in] (ldw) in bf16, fp16 or fp32, quantized row by row
  *   qlora_int8_pack_weight       W8 int8 [n_out, k_in] (ldw), codes from elsewhere, into the layout (its scales
  *                                are used as they are: W = scale[n] W8[n][k]; codes of -128 are allowed)
- *   qlora_int8_transpose_weight  the codes of W^T for the backward (n_out <= 133144)
+ *   qlora_int8_transpose_weight  the codes of W^T for the backward (n_out <= 132104)
  *   qlora_int8_dequant_weight    E(scale[n] code) as 16-bit [n_out, k_in]
  */
 int qlora_int8_quantize_weight(const void *W, int dtype, int64_t ldw, int64_t n_out, int64_t k_in,
@@ -499,7 +499,7 @@ int qlora_rms_norm_bwd(const void *dY, int64_t lddy, const void *H, int64_t ldh,
  * SwiGLU: y = g s u with s = 1 / (1 + e^-g), in fp32.  G and U [M, K] (ldg,
  * ldu) may be the halves of one product's output.
  *   qlora_swiglu_fwd   Y 16-bit [M, K]
- *   qlora_swiglu_int8  y quantized by rows from its fp32 values (K <= 133144)
+ *   qlora_swiglu_int8  y quantized by rows from its fp32 values (K <= 132104)
  *   qlora_swiglu_bwd   dG = dY u s (1 + g (1 - s)),  dU = dY g s, 16-bit [M, K]
  */
 int qlora_swiglu_fwd(const void *G, int64_t ldg, const void *U, int64_t ldu, int64_t M, int64_t K,

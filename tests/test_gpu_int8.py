@@ -100,17 +100,40 @@ def test_weight_layouts(n, k):
 
 
 def test_largest_sums():
-    """Every product at its largest magnitude: the int32 sum stays exact up to
-    the longest reduction, at either sign."""
+    """Every product at its largest magnitude (a weight's codes go to -128):
+    the int32 sum stays exact up to the longest reduction, at either sign."""
     need_gpu()
-    k = 133144
-    codes = torch.full((2, k), 127, dtype=torch.int8, device="cuda")
-    codes[1] = -127
-    w = int8.weight_from_codes(codes, torch.ones(2, device="cuda"))
-    for m in (1, 20):
+    k = 132104
+    codes = torch.full((3, k), 127, dtype=torch.int8, device="cuda")
+    codes[1] = -128
+    codes[2, ::2] = -128
+    w = int8.weight_from_codes(codes, torch.ones(3, device="cuda"), transposed=True)
+    for m in (1, 20, 70):
         x = torch.full((m, k), 1.0, dtype=BF16, device="cuda")
-        y = f64(int8.linear_fwd(w, x))
-        np.testing.assert_allclose(y, np.tile([127.0 * k, -127.0 * k], (m, 1)), rtol=2.0 ** -8)
+        x[m - 1] = -1.0
+        y = int8.linear_fwd(w, x)
+        want = np.tile([127.0 * k, -128.0 * k, -0.5 * k], (m, 1)) * np.where(np.arange(m) == m - 1, -1.0, 1.0)[:, None]
+        close16(y, want, np.abs(want))
+    dy = torch.ones((2, 3), dtype=BF16, device="cuda")
+    close16(int8.linear_bwd(w, dy), np.tile(f64(codes).sum(0), (2, 1)), 3 * 128.0)
+
+
+def test_large_offsets():
+    """More than 2^31 elements in and out: the last rows are those of a call of
+    their own."""
+    need_gpu()
+    m, k, n = 270000, 128, 8200
+    _, w = _weight(n, k, 1)
+    x = rand((m, k), 2)
+    y = int8.linear_fwd(w, x)
+    assert y.numel() > 2 ** 31
+    for at in (0, m // 2, m - 100):
+        assert torch.equal(y[at:at + 100], int8.linear_fwd(w, x[at:at + 100].contiguous()))
+    q = rows.quantize_rows(y)
+    v = rows.dequant_rows(q)
+    dx = int8.linear_bwd(w, y)
+    assert torch.equal(v[-100:], rows.dequant_rows(rows.quantize_rows(y[-100:])))
+    assert torch.equal(dx[-100:], int8.linear_bwd(w, y[-100:]))
 
 
 def test_odd_rows():
@@ -194,8 +217,8 @@ def test_refusals():
         int8.linear_fwd(w, x, Y=torch.empty((4, 41), dtype=BF16, device="cuda"))
     with pytest.raises(RuntimeError, match="transposed codes"):
         int8.linear_bwd(int8.quantize_weight(rand((40, 64), 1, F32)), rand((4, 40), 1))
-    with pytest.raises(RuntimeError, match="133144"):
-        int8.quantize_weight(rand((1, 133145), 1, F32))
+    with pytest.raises(RuntimeError, match="132104"):
+        int8.quantize_weight(rand((1, 132105), 1, F32))
     with pytest.raises(ValueError, match="codes"):
         int8.linear_fwd(int8.Int8Weight(w.codes[:-1], w.scale, 40, 64), x)
     with pytest.raises(TypeError, match="codes must be"):

@@ -295,6 +295,26 @@ def test_autograd():
     close16(both.grad.reshape(12, 80)[:, 40:], wu, m)
 
 
+def test_large_offsets():
+    """More than 2^31 elements: the last rows are those of a call of their own."""
+    need_gpu()
+    m, k = 530000, 4096
+    x = rand((m, 64), 1).repeat(1, 64)
+    g = rand((k,), 2)
+    assert x.numel() > 2 ** 31
+    y, h, rstd = rows.rms_norm_fwd(x, g, EPS, x)
+    a, b, c = rows.rms_norm_fwd(x[-50:], g, EPS, x[-50:])
+    assert torch.equal(y[-50:], a) and torch.equal(h[-50:], b) and torch.equal(rstd[-50:], c)
+    dx, _ = rows.rms_norm_bwd(y, h, rstd, g)
+    assert torch.equal(dx[-50:], rows.rms_norm_bwd(a, b, c, g)[0])
+    del dx, h
+    s = rows.swiglu_fwd(x, y)
+    assert torch.equal(s[-50:], rows.swiglu_fwd(x[-50:], a))
+    dg, du = rows.swiglu_bwd(s, x, y)
+    want = rows.swiglu_bwd(s[-50:], x[-50:], a)
+    assert torch.equal(dg[-50:], want[0]) and torch.equal(du[-50:], want[1])
+
+
 def test_refusals():
     need_gpu()
     x, g = rand((4, 64), 1), rand((64,), 2)
@@ -329,8 +349,8 @@ def test_refusals():
         rows.swiglu_fwd(x, x, Y=torch.empty_like(x).t())
     with pytest.raises(RuntimeError, match="QLORA_MAX_NORM_WIDTH"):
         rows.rms_norm_fwd(rand((1, 32769), 1), rand((32769,), 2), EPS)
-    with pytest.raises(RuntimeError, match="133144"):
-        rows.quantize_rows(rand((1, 133145), 1))
+    with pytest.raises(RuntimeError, match="132104"):
+        rows.quantize_rows(rand((1, 132105), 1))
     with pytest.raises(ValueError, match="rstd"):
         rows.rms_norm_bwd(x, h, rstd[:2], g)
     with pytest.raises(ValueError, match="codes"):

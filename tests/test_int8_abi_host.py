@@ -58,17 +58,17 @@ def test_weight_refusals(L):
     assert q(P2, F32, 64, 64, 64, P, P, 0) == ALIGN
     assert q(P, F32, 64, 64, 64, P2, P, 0) == ALIGN
     assert q(P, F32, 64, 64, 64, None, P, 0) == INVALID
-    assert q(P, F32, 133145, 64, 133145, P, P, 0) == SHAPE
+    assert q(P, F32, 132105, 64, 132105, P, P, 0) == SHAPE
     assert q(P, F32, 64, BIG, 64, P, P, 0) == SHAPE
     assert q(P, F32, 1 << 41, 64, 64, P, P, 0) == SHAPE
     assert q(None, F32, 64, 0, 64, None, None, 0) == 0
     p = L.qlora_int8_pack_weight
     assert p(None, 64, 64, 64, P, 0) == INVALID and p(P, 63, 64, 64, P, 0) == INVALID
     assert p(P, 64, 64, 64, P1, 0) == ALIGN and p(P, 1 << 41, 64, 64, P, 0) == SHAPE
-    assert p(P, 64, 64, 133145, P, 0) == SHAPE and p(None, 64, 0, 64, None, 0) == 0
+    assert p(P, 64, 64, 132105, P, 0) == SHAPE and p(None, 64, 0, 64, None, 0) == 0
     assert L.qlora_int8_transpose_weight(None, P, 0) == INVALID
     assert L.qlora_int8_transpose_weight(_w(), None, 0) == INVALID
-    assert L.qlora_int8_transpose_weight(_w(n=133145), P, 0) == SHAPE
+    assert L.qlora_int8_transpose_weight(_w(n=132105), P, 0) == SHAPE
     assert L.qlora_int8_dequant_weight(_w(), P, F32, 0) == INVALID
     assert L.qlora_int8_dequant_weight(_w(scale=None), P, BF16, 0) == INVALID
     assert L.qlora_int8_dequant_weight(_w(), P2, BF16, 0) == ALIGN
@@ -80,7 +80,7 @@ def test_row_refusals(L):
     assert q(P1, BF16, 64, 4, 64, None, P, P, 0) == ALIGN
     assert q(P, BF16, 64, 4, 64, P2, P, P, 0) == ALIGN
     assert q(P, BF16, 64, 4, 64, None, None, P, 0) == INVALID
-    assert q(P, BF16, 133145, 4, 133145, None, P, P, 0) == SHAPE
+    assert q(P, BF16, 132105, 4, 132105, None, P, P, 0) == SHAPE
     assert q(P, BF16, 64, -4, 64, None, P, P, 0) == INVALID
     assert q(None, BF16, 64, 0, 64, None, None, None, 0) == 0
     d = L.qlora_int8_dequant_rows
@@ -105,7 +105,7 @@ def test_product_refusals(L):
     assert r(_w(), P, P, 40, None, P, BF16, P2, 1, 0) == ALIGN
     assert b(_w(codes_t=None), P, 64, 40, P, BF16, P, need, 0) == INVALID
     assert b"transposed" in L.qlora_last_error()
-    assert b(_w(n=133145), P, 133145, 40, P, BF16, P, 1 << 30, 0) == SHAPE
+    assert b(_w(n=132105), P, 132105, 40, P, BF16, P, 1 << 30, 0) == SHAPE
     assert b(_w(), P, 64, 40, P, BF16, None, 0, 0) == WORKSPACE
 
 
@@ -135,7 +135,7 @@ def test_swiglu_refusals(L):
     assert f(None, 64, P, 64, 4, 64, P, BF16, 0) == INVALID and f(P, 64, P1, 64, 4, 64, P, BF16, 0) == ALIGN
     assert f(P, 64, P, 64, 4, 64, None, BF16, 0) == INVALID and f(P, 64, P, 64, 4, 64, P, F32, 0) == INVALID
     assert f(P, 1 << 20, P, 1 << 20, BIG - 1, 1 << 20, P, BF16, 0) == SHAPE
-    assert i(P, 133145, P, 133145, 4, 133145, P, P, BF16, 0) == SHAPE
+    assert i(P, 132105, P, 132105, 4, 132105, P, P, BF16, 0) == SHAPE
     assert i(P, 64, P, 64, 4, 64, P, None, BF16, 0) == INVALID
     assert b(None, 64, P, 64, P, 64, 4, 64, P, P, BF16, 0) == INVALID
     assert b(P, 64, P, 64, P, 64, 4, 64, P, None, BF16, 0) == INVALID
