@@ -57,7 +57,8 @@ def _transposed(w: Int8Weight) -> Int8Weight:
     t = torch.empty(weight_bytes(w.k_in, w.n_out), dtype=torch.uint8, device=w.codes.device)
     cw = w._c()
     st = qlora.lib().qlora_int8_transpose_weight(ctypes.byref(cw), t.data_ptr(), _stream(w.codes.device))
-    qlora._check(st, "qlora_int8_transpose_weight")
+    if st:
+        qlora._check(st, "qlora_int8_transpose_weight")
     w.codes_t = t
     return w
 
@@ -71,7 +72,8 @@ def quantize_weight(W: torch.Tensor, transposed: bool = False) -> Int8Weight:
                    torch.empty(n, dtype=torch.float32, device=dev), n, k)
     st = qlora.lib().qlora_int8_quantize_weight(p, DTYPES[dt], ld, n, k, w.codes.data_ptr(), w.scale.data_ptr(),
                                                 _stream(dev))
-    qlora._check(st, "qlora_int8_quantize_weight")
+    if st:
+        qlora._check(st, "qlora_int8_quantize_weight")
     return _transposed(w) if transposed else w
 
 
@@ -83,7 +85,8 @@ def weight_from_codes(codes: torch.Tensor, scale: torch.Tensor, transposed: bool
     _vec(scale, (torch.float32,), n, "scale", dev)
     w = Int8Weight(torch.empty(weight_bytes(n, k), dtype=torch.uint8, device=dev), scale.clone(), n, k)
     st = qlora.lib().qlora_int8_pack_weight(p, ld, n, k, w.codes.data_ptr(), _stream(dev))
-    qlora._check(st, "qlora_int8_pack_weight")
+    if st:
+        qlora._check(st, "qlora_int8_pack_weight")
     return _transposed(w) if transposed else w
 
 
@@ -96,7 +99,8 @@ def dequant_weight(w: Int8Weight, out: torch.Tensor | None = None, dtype=torch.b
     out = _out(out, (w.n_out, w.k_in), dtype, "out", dev)
     cw = w._c()
     st = qlora.lib().qlora_int8_dequant_weight(ctypes.byref(cw), out.data_ptr(), DTYPES[dtype], _stream(dev))
-    qlora._check(st, "qlora_int8_dequant_weight")
+    if st:
+        qlora._check(st, "qlora_int8_dequant_weight")
     return out
 
 
@@ -127,12 +131,14 @@ def linear_fwd(w: Int8Weight, X, bias: torch.Tensor | None = None, *, Y: torch.T
         wst, wsn = qlora._ws(L.qlora_int8_rows_workspace_bytes(m, w.n_out, w.k_in), dev, ws)
         st = L.qlora_int8_linear_rows(ctypes.byref(cw), X.codes.data_ptr(), X.scale.data_ptr(), m, b, Y.data_ptr(),
                                       DTYPES[dt], None if wst is None else wst.data_ptr(), wsn, _stream(dev))
-        qlora._check(st, "qlora_int8_linear_rows")
+        if st:
+            qlora._check(st, "qlora_int8_linear_rows")
         return Y
     wst, wsn = qlora._ws(L.qlora_int8_workspace_bytes(qlora.QLORA_OP_FWD, m, w.n_out, w.k_in), dev, ws)
     st = L.qlora_int8_linear_fwd(ctypes.byref(cw), p, ld, m, b, Y.data_ptr(), DTYPES[dt],
                                  None if wst is None else wst.data_ptr(), wsn, _stream(dev))
-    qlora._check(st, "qlora_int8_linear_fwd")
+    if st:
+        qlora._check(st, "qlora_int8_linear_fwd")
     return Y
 
 
@@ -150,7 +156,8 @@ def linear_bwd(w: Int8Weight, dY: torch.Tensor, *, dX: torch.Tensor | None = Non
     wst, wsn = qlora._ws(L.qlora_int8_workspace_bytes(qlora.QLORA_OP_BWD, m, w.n_out, w.k_in), dev, ws)
     st = L.qlora_int8_linear_bwd(ctypes.byref(cw), p, ld, m, dX.data_ptr(), DTYPES[dt],
                                  None if wst is None else wst.data_ptr(), wsn, _stream(dev))
-    qlora._check(st, "qlora_int8_linear_bwd")
+    if st:
+        qlora._check(st, "qlora_int8_linear_bwd")
     return dX
 
 

@@ -98,7 +98,7 @@ def _out(t, shape, dtype, name: str, device, like=None):
     if t is None:
         if like is not None and like.is_contiguous():
             return torch.empty_like(like)
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(*shape, dtype=dtype, device=device)  # sooner than with a tuple
     if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
     return t
@@ -127,10 +127,16 @@ def _new_rows(m: int, k: int, dtype, device) -> Int8Rows:
 def check_rows(q, device=None) -> Int8Rows:
     if not isinstance(q, Int8Rows):
         raise TypeError("expected Int8Rows")
-    nbytes = (q.m + 15) // 16 * 16 * ((q.k + 127) // 128 * 128)
-    device = q.codes.device if device is None else device
-    _vec(q.codes, (torch.uint8,), nbytes, "codes", device)
-    _vec(q.scale, (torch.float32,), q.m, "scale", device)
+    codes, scale, m = q.codes, q.scale, q.m
+    if device is None:
+        device = codes.device
+    nbytes = (m + 15) // 16 * 16 * ((q.k + 127) // 128 * 128)
+    if not (codes.dtype is torch.uint8 and codes.shape == (nbytes,) and codes.device == device and codes.is_contiguous()):
+        _vec(codes, (torch.uint8,), nbytes, "codes", device)
+    if not (scale.dtype is torch.float32 and scale.shape == (m,) and scale.device == device and scale.is_contiguous()):
+        _vec(scale, (torch.float32,), m, "scale", device)
+    if not codes.is_cuda:
+        raise ValueError("codes must be GPU tensors (there is no CPU path)")
     return q
 
 
@@ -143,7 +149,8 @@ def quantize_rows(X: torch.Tensor, col_scale: torch.Tensor | None = None) -> Int
     q = _new_rows(m, k, torch.bfloat16 if dt == torch.float32 else dt, dev)
     st = qlora.lib().qlora_int8_quantize_rows(p, DTYPES[dt], ld, m, k, c, q.codes.data_ptr(), q.scale.data_ptr(),
                                               _stream(dev))
-    qlora._check(st, "qlora_int8_quantize_rows")
+    if st:
+        qlora._check(st, "qlora_int8_quantize_rows")
     return q
 
 
@@ -153,12 +160,13 @@ def dequant_rows(q: Int8Rows, out: torch.Tensor | None = None, dtype=None) -> to
     check_rows(q)
     dev = q.codes.device
     dtype = dtype or (q.dtype if out is None else out.dtype)
-    if dtype not in (torch.bfloat16, torch.float16):
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
         raise TypeError("dequant_rows produces bf16 or fp16")
     out = _out(out, (q.m, q.k), dtype, "out", dev)
     st = qlora.lib().qlora_int8_dequant_rows(q.codes.data_ptr(), q.scale.data_ptr(), q.m, q.k, out.data_ptr(),
                                              DTYPES[dtype], _stream(dev))
-    qlora._check(st, "qlora_int8_dequant_rows")
+    if st:
+        qlora._check(st, "qlora_int8_dequant_rows")
     return out
 
 
@@ -185,7 +193,8 @@ def rms_norm_fwd(X: torch.Tensor, gamma: torch.Tensor, eps: float, residual: tor
     rstd = torch.empty(m, dtype=torch.float32, device=dev)
     st = qlora.lib().qlora_rms_norm_fwd(*args, eps, None if residual is None else h.data_ptr(), Y.data_ptr(),
                                         rstd.data_ptr(), DTYPES[dt], _stream(dev))
-    qlora._check(st, "qlora_rms_norm_fwd")
+    if st:
+        qlora._check(st, "qlora_rms_norm_fwd")
     return Y, h, rstd
 
 
@@ -196,7 +205,8 @@ def rms_norm_int8(X: torch.Tensor, gamma: torch.Tensor, eps: float, residual: to
     q = _new_rows(m, k, dt, dev)
     st = qlora.lib().qlora_rms_norm_int8(*args, eps, None if residual is None else h.data_ptr(), q.codes.data_ptr(),
                                          q.scale.data_ptr(), DTYPES[dt], _stream(dev))
-    qlora._check(st, "qlora_rms_norm_int8")
+    if st:
+        qlora._check(st, "qlora_rms_norm_int8")
     return q, h
 
 
@@ -219,7 +229,8 @@ def rms_norm_bwd(dY: torch.Tensor, H: torch.Tensor, rstd: torch.Tensor, gamma: t
     st = L.qlora_rms_norm_bwd(dy, lddy, h, ldh, rs, g, DTYPES[gamma.dtype], dh, lddh, m, k, dX.data_ptr(),
                               dgamma.data_ptr(), DTYPES[dt], None if wst is None else wst.data_ptr(), wsn,
                               _stream(dev))
-    qlora._check(st, "qlora_rms_norm_bwd")
+    if st:
+        qlora._check(st, "qlora_rms_norm_bwd")
     return dX, dgamma
 
 
@@ -234,7 +245,9 @@ def swiglu_fwd(G: torch.Tensor, U: torch.Tensor, *, Y: torch.Tensor | None = Non
     """silu(G) * U in 16 bits."""
     dt, shape, dev, args = _swiglu_args(G, U)
     Y = _out(Y, shape, dt, "Y", dev, G)
-    qlora._check(qlora.lib().qlora_swiglu_fwd(*args, Y.data_ptr(), DTYPES[dt], _stream(dev)), "qlora_swiglu_fwd")
+    st = qlora.lib().qlora_swiglu_fwd(*args, Y.data_ptr(), DTYPES[dt], _stream(dev))
+    if st:
+        qlora._check(st, "qlora_swiglu_fwd")
     return Y
 
 
@@ -243,7 +256,8 @@ def swiglu_int8(G: torch.Tensor, U: torch.Tensor) -> Int8Rows:
     dt, shape, dev, args = _swiglu_args(G, U)
     q = _new_rows(*shape, dt, dev)
     st = qlora.lib().qlora_swiglu_int8(*args, q.codes.data_ptr(), q.scale.data_ptr(), DTYPES[dt], _stream(dev))
-    qlora._check(st, "qlora_swiglu_int8")
+    if st:
+        qlora._check(st, "qlora_swiglu_int8")
     return q
 
 
@@ -254,7 +268,8 @@ def swiglu_bwd(dY: torch.Tensor, G: torch.Tensor, U: torch.Tensor, *, dG: torch.
     dy, lddy = _mat(dY, dt, shape, "dY", dev)
     dG, dU = _out(dG, shape, dt, "dG", dev, G), _out(dU, shape, dt, "dU", dev, G)
     st = qlora.lib().qlora_swiglu_bwd(dy, lddy, *args, dG.data_ptr(), dU.data_ptr(), DTYPES[dt], _stream(dev))
-    qlora._check(st, "qlora_swiglu_bwd")
+    if st:
+        qlora._check(st, "qlora_swiglu_bwd")
     return dG, dU
 
 
