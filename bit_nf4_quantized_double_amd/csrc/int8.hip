@@ -75,14 +75,16 @@ __device__ __forceinline__ float token_scale(const Int8GemmArgs& a, int64_t m) {
 }
 
 // 8 consecutive outputs n .. n + 7 of token m, as far as they exist, packed.
-__device__ __forceinline__ void store8(const Int8GemmArgs& a, int64_t m, int64_t n, uint4 u) {
+// `stream`: not kept in the second-level cache.
+__device__ __forceinline__ void store8(const Int8GemmArgs& a, int64_t m, int64_t n, uint4 u, bool stream = false) {
   if (m >= a.m || n >= a.n) return;
   const int64_t e = m * a.n + n, size = a.m * a.n;
   if (n + 8 <= a.n) {
-    // not kept in the second-level cache, which the operands need (8192 x
-    // 14336 x 4096: 377 us against 396)
     const u32x4u v = {u.x, u.y, u.z, u.w};
-    if (in_bounds(e, 8, size)) __builtin_nontemporal_store(v, reinterpret_cast<u32x4u*>(a.out + e));
+    if (in_bounds(e, 8, size)) {
+      if (stream) __builtin_nontemporal_store(v, reinterpret_cast<u32x4u*>(a.out + e));
+      else *reinterpret_cast<u32x4u*>(a.out + e) = v;
+    }
   } else {
     const uint32_t d[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -111,8 +113,10 @@ __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(
 
 // XCD-aware tile order: workgroups are dealt round-robin to the 8 XCDs, so
 // each XCD gets a contiguous run of an order that goes column-major inside
-// bands of 4 token blocks: the 32 tiles an XCD works on at a time share 4
-// token blocks and 8 output blocks in its L2.
+// bands of 4 token blocks: the 64 tiles an XCD works on at a time share 4
+// token blocks and 16 output blocks in its L2.  (Few tokens' kernel at 6240 x
+// 295 x 7723: 37 us, 44 us in bands of 16, 70 us dealt out token block by token
+// block.)
 __device__ __forceinline__ void tile_of(uint32_t lin, uint32_t mt, uint32_t nt, uint32_t& tm, uint32_t& tn) {
   constexpr uint32_t RB = 4;
   const uint32_t total = mt * nt, whole = total & ~7u;
@@ -274,10 +278,15 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       *reinterpret_cast<uint4*>(so + (16 * t + c) * kPitch + 32 * p + 8 * g) = os.eight(acc[2 * p][t], acc[2 * p + 1][t], sx[t]);
   }
   constexpr int kAcross = 2 * NS;  // 16-byte pieces of a token's outputs
+  // Whole lines are not kept in the second-level cache, which the operands need
+  // (8192 x 14336 x 4096: 373 us against 384); where rows start inside a line,
+  // that cache has to put the parts together (3549 x 26474 x 224: 59 us, 94
+  // without it).
+  const bool stream = a.n % 64 == 0;
 #pragma unroll
   for (int r = 0; r < kAcross; ++r) {
     const int row = (64 / kAcross) * r + lane / kAcross, col = lane % kAcross * 8;
-    store8(a, m0 + row, n0 + col, *reinterpret_cast<const uint4*>(so + row * kPitch + col));
+    store8(a, m0 + row, n0 + col, *reinterpret_cast<const uint4*>(so + row * kPitch + col), stream);
   }
 }
 
@@ -286,9 +295,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 // in turn.  A wave reads weight tiles and token tiles straight into the
 // MFMA's registers, whole kilobytes at a time, four of its turns in flight, and
 // the waves' sums meet in LDS.  Up to 64 tokens the weight is read once, and
-// reading it is the bound: 28672 x 8192 for one token 43 us (5.4 TB/s, a copy's
-// rate is 5.1), 8192 x 28672 for sixteen 41 us (5.7).  More tokens come in
-// blocks of 64, up to 850 TOP/s from the cache: 150 x 1000 x 2500 takes 6.4 us,
+// reading it is the bound: 28672 x 8192 for one token 42 us (5.6 TB/s, a copy's
+// rate is 5.1), 8192 x 28672 for sixteen 42 us.  More tokens come in
+// blocks of 64, up to 940 TOP/s from the cache: 150 x 1000 x 2500 takes 6.1 us,
 // and 13 us as tiles with a split reduction.
 //
 // FUSED (TT = 1, at most kFusedTokens tokens): x is not quantized yet.  Every
@@ -311,8 +320,9 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_int8_few(Int8GemmArgs a, Qua
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t kp = int8_kp(a.k);
   const uint32_t groups = (uint32_t)((a.n + 31) / 32), blocks = (uint32_t)((a.m + 16 * TT - 1) / (16 * TT));
-  // token blocks of one group follow each other, then the groups, then the splits
-  const uint32_t tb = blockIdx.x % blocks, group = blockIdx.x / blocks % groups, z = blockIdx.x / blocks / groups;
+  const uint32_t z = blockIdx.x / (blocks * groups);
+  uint32_t tb, group;
+  tile_of(blockIdx.x % (blocks * groups), blocks, groups, tb, group);
   const uint32_t strip = 16u * (uint32_t)kp;
   const uint32_t chunks = (uint32_t)(kp >> 6), per = (chunks + a.ksplit - 1) / a.ksplit;
   const uint32_t c0 = min(z * per, chunks), c1 = min(c0 + per, chunks);
@@ -537,25 +547,28 @@ __global__ __launch_bounds__(256) void k_int8_dequant(const int8_t* codes, const
 }  // namespace
 
 // Which kernel, and how many splits: the least by a model of their times, in
-// microseconds on 256 compute units, fitted to sweeps over 40 to 2048 tokens,
-// 1000 to 28672 outputs and reductions of 2500 to 28672 (it is within 15 % of
-// most and picks the fastest or one within 10 % of it).
+// microseconds on 256 compute units, fitted to sweeps over 40 to 8192 tokens,
+// 64 to 28672 outputs and reductions of 224 to 28672 (it is within 20 % of
+// nearly all and picks the fastest or one within 10 % of it).
 //   few     a workgroup makes one turn of its loads for each 2048 columns, at
 //           1.0, 1.2 or 2.0 us a turn for 16, 32 or 64 tokens; all of them
-//           together run at no more than 850 TOP/s (operands from the cache)
-//           and read the weight at no more than 5.3 TB/s.
+//           together run at no more than 1000 TOP/s (operands from the cache),
+//           with 2.3 us for each further round of workgroups, and read the
+//           weight at no more than 5.5 TB/s.
 //           72 x 4096 x 4096: 8 us, as tiles 28 us (15 us with 4 splits).
 //   tiles   256 x 128, two workgroups a compute unit: 1.72 us a step of 128
-//           columns with two, 0.82 us with one.  8192 x 14336 x 4096: 377 us;
-//           1024 x 11008 x 4096: 50 us, few tokens' kernel 101 us.
+//           columns with two, 0.82 us with one.  8192 x 14336 x 4096: 373 us;
+//           1024 x 11008 x 4096: 50 us, few tokens' kernel 90 us.
+//   either  writes its output at no more than 3.5 TB/s.
 //   split   a launch more (3 us), and the int32 sums written and read at
 //           5 TB/s.  512 x 4096 x 11008 as tiles: 67, 45, 37 us in 1, 2, 4.
 Int8Plan int8_plan(int64_t m, int64_t n, int64_t k, int cus) {
   Int8Plan best{};
   double least = 0;
-  const double scale = 256.0 / cus, ops = 2e-6 * (double)n * (double)int8_kp(k);
+  const double scale = 256.0 / cus, ops = 2e-6 * (double)n * (double)int8_kp(k), out = 2e-6 * (double)m * (double)n / 3.5;
   const int64_t steps = int8_kp(k) / 128;
   auto consider = [&](Int8Kind kind, int split, double us) {
+    us = std::max(us, out);
     if (split > 1) us += 3.0 + 8e-6 * split * (double)m * (double)n / 5.0;
     if (best.ksplit == 0 || us < least) {
       best = Int8Plan{kind, split};
@@ -566,16 +579,18 @@ Int8Plan int8_plan(int64_t m, int64_t n, int64_t k, int cus) {
   const int64_t rows = m <= 16 ? 16 : m <= 32 ? 32 : 64, blocks = (m + rows - 1) / rows;
   const double turn = m <= 16 ? 1.0 : m <= 32 ? 1.2 : 2.0;
   const int64_t groups = blocks * ((n + 31) / 32), tiles = (m + 255) / 256 * ((n + 127) / 128);
+  const int64_t rounds = (groups + 2 * cus - 1) / (2 * cus);
   for (int split = 1; split <= 8; split *= 2) {
     if (split == 1 || groups * split <= cus) {
       const double turns = (double)((steps + 16 * split - 1) / (16 * split));
-      const double bulk = scale * std::max(ops * (double)(blocks * rows) / 850.0, (double)n * (double)k / 5.3e6);
+      const double bulk = scale * std::max(ops * (double)(blocks * rows) / 1000.0, (double)n * (double)k / 5.5e6) +
+                          2.3 * (double)(rounds - 1);
       consider(few, split, 2.7 + std::max(turns * turn, bulk));
     }
     if (m > 64 && (split == 1 || tiles * split <= 2 * cus)) {
       const int64_t wgs = tiles * split, full = wgs / (2 * cus), rest = wgs % (2 * cus);
       const double step = 1.72 * (double)full + (rest > cus ? 1.6 : rest > 0 ? 0.82 : 0.0);
-      consider(kInt8Tile, split, 3.0 + step * (double)((steps + split - 1) / split));
+      consider(kInt8Tile, split, 5.0 + step * (double)((steps + split - 1) / split));
     }
   }
   return best;

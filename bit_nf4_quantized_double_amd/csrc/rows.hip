@@ -345,6 +345,9 @@ hipError_t launch_rows(const Src& src, const Out8& o8, const Out16& o16, float* 
         if constexpr (Src::kHeavy) return go(c512, c2, c2);  // four pieces of it would spill
         else return go(c256, c4, c4);
       }
+      if constexpr (!Src::kNorm) {
+        if (pieces <= 2048) return go(c512, c2, c4);
+      }
     }
   }
   if (pieces <= 64) return go(c64, c1, c1);
