@@ -120,7 +120,7 @@ struct Int8Ws {
 };
 Int8Ws int8_ws(int64_t m, int64_t n, int64_t k) {
   Int8Ws L{};
-  if (qlora::int8_fuses_rows(m, k)) return L;
+  if (qlora::int8_fuses_rows(m, n, k)) return L;
   L.scale = round_up(qlora::int8_rows_bytes(m, k));
   L.part = L.req = L.scale + round_up((size_t)m * 4u);
   L.total = L.part + round_up(qlora::int8_part_bytes(m, n, k, qlora::device_compute_units()));
@@ -132,7 +132,7 @@ int quantized_product(const int8_t* wcodes, const float* wscale, const float* co
                       size_t ws_bytes, hipStream_t stream) {
   qlora::QuantArgs q{};
   q.x = X; q.type = dtype; q.ldx = ldx; q.m = m; q.k = k; q.col_scale = col_scale;
-  if (qlora::int8_fuses_rows(m, k)) {
+  if (qlora::int8_fuses_rows(m, n, k)) {
     qlora::Int8GemmArgs g{};
     g.w = wcodes; g.sw = wscale; g.bias = bias; g.out = out;
     g.m = m; g.n = n; g.k = k;

@@ -300,22 +300,23 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 // blocks of 64, up to 940 TOP/s from the cache: 150 x 1000 x 2500 takes 6.1 us,
 // and 13 us as tiles with a split reduction.
 //
-// FUSED (TT = 1, at most kFusedTokens tokens): x is not quantized yet.  Every
-// workgroup quantizes all of it into LDS, after its first weight tiles are on
-// their way: the rows are a few kilobytes in the second-level cache, and a
-// launch of its own for them costs more than the repetition (1 x 28672 x 8192:
-// 43.0 us for 47.9).
-constexpr int kFusedTokens = 4;
+// NP > 0 (TT = 1): x is not quantized yet, and is at most 8192 NP values.
+// Every workgroup quantizes all of it into LDS, after its first weight tiles
+// are on their way: the rows are a few kilobytes in the second-level cache, and
+// a launch of its own for them costs more than the repetition (1 x 28672 x
+// 8192: 42.0 us for 47.9).
+constexpr int kFusedValues = 32768;
 constexpr int kFewWaves = 8;
 constexpr int kFewAhead = 4;  // turns in flight
 __host__ __device__ constexpr int64_t fused_pitch(int64_t k) { return int8_kp(k) + 16; }  // of a token's codes in LDS
 
-template <int TT, bool FUSED, typename E>
+template <int TT, int NP, typename E>
 __global__ __launch_bounds__(64 * kFewWaves) void k_int8_few(Int8GemmArgs a, QuantSrc<E> src) {
+  constexpr bool FUSED = NP > 0;
   constexpr int NW = kFewWaves, U = kFewAhead;
   __shared__ i32x4 s_sum[NW][2 * TT][64];
-  __shared__ float s_scale[kFusedTokens];
-  __shared__ uint32_t s_top[NW][kFusedTokens];
+  __shared__ float s_scale[16];
+  __shared__ uint32_t s_top[16];
   extern __shared__ __attribute__((aligned(16))) uint8_t s_codes[];  // FUSED: [m][fused_pitch]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t kp = int8_kp(a.k);
@@ -337,36 +338,62 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_int8_few(Int8GemmArgs a, Qua
   };
   if constexpr (FUSED) {
     load_w(c0 + wave);
-    for (int m = 0; m < a.m; ++m) {
-      float none = 0.f, v[16];
-      uint32_t top = 0;
-      for (int64_t p = threadIdx.x; p * 16 < a.k; p += 64 * NW) {
-        piece(src, m, p * 16, a.k, v, none);
+    // the tokens' pieces of 16 columns, one after another: a thread has NP of
+    // them, and 8 neighbouring threads' are always of one token
+    const uint32_t across = (uint32_t)(kp >> 4);
+    typename QuantSrc<E>::Raw raw[NP];
+    auto value = [&](int i, float (&v)[16]) {
+      const uint32_t id = i * 64 * NW + threadIdx.x, m = id / across;
+      const int64_t c = (int64_t)(id % across) * 16;
+      float none = 0.f;
+      if (m < a.m && c < a.k) {
+        src.value(raw[i], m, c, a.k, v, none);
+      } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) top = max(top, abs_bits(v[i]));
+        for (int j = 0; j < 16; ++j) v[j] = 0.f;
       }
+    };
 #pragma unroll
-      for (int d = 32; d > 0; d >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
-      if (lane == 0) s_top[wave][m] = top;
+    for (int i = 0; i < NP; ++i) {
+      const uint32_t id = i * 64 * NW + threadIdx.x;
+      // past the end of a row or of the tokens: its (their) last values, dropped below
+      src.template load<true>(min((int64_t)(id / across), a.m - 1), min((int64_t)(id % across) * 16, a.k - 16), a.k, raw[i]);
+    }
+    if (threadIdx.x < 16) s_top[threadIdx.x] = 0;
+    lds_barrier();
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const uint32_t id = i * 64 * NW + threadIdx.x, m = id / across;
+      const int64_t c = (int64_t)(id % across) * 16;
+      if (c < a.k && c + 16 > a.k) raw[i].shift((int)(c + 16 - a.k));
+      float v[16];
+      value(i, v);
+      uint32_t top = 0;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) top = max(top, abs_bits(v[j]));
+#pragma unroll
+      for (int d = 4; d > 0; d >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
+      // a maximum of whole numbers: the order does not matter
+      if (lane % 8 == 0 && m < a.m) atomicMax(&s_top[m], top);
     }
     lds_barrier();
-    for (int m = 0; m < a.m; ++m) {
-      uint32_t top = 0;
 #pragma unroll
-      for (int i = 0; i < NW; ++i) top = max(top, s_top[i][m]);
-      const float amax = fmaxf(__builtin_bit_cast(float, top), kAmaxFloor);
-      const bool finite = top < 0x7f800000u;
-      const RowQuant q = row_quant(finite ? amax : 1.f);
-      for (int64_t p = threadIdx.x; p * 16 < kp; p += 64 * NW) {
-        float none = 0.f, v[16];
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (p * 16 < a.k && finite) {
-          piece(src, m, p * 16, a.k, v, none);
-          u = codes16(q, v);
-        }
-        *reinterpret_cast<uint4*>(s_codes + m * fused_pitch(a.k) + p * 16) = u;
+    for (int i = 0; i < NP; ++i) {
+      const uint32_t id = i * 64 * NW + threadIdx.x, m = id / across, p = id % across;
+      // unpacked again: kept across the barrier the values would cost half the
+      // workgroups that fit a compute unit
+      float v[16];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) asm volatile("" : "+v"(raw[i].x.d[j]));
+      value(i, v);
+      if (m < a.m) {
+        const uint32_t top = s_top[m];
+        const float amax = fmaxf(__builtin_bit_cast(float, top), kAmaxFloor);
+        const bool finite = top < 0x7f800000u;
+        const RowQuant q = row_quant(finite ? amax : 1.f);
+        *reinterpret_cast<uint4*>(s_codes + m * fused_pitch(a.k) + p * 16) = finite ? codes16(q, v) : make_uint4(0, 0, 0, 0);
+        if (p == 0) s_scale[m] = finite ? amax / 127.f : __builtin_nanf("");
       }
-      if (threadIdx.x == 0) s_scale[m] = finite ? amax / 127.f : __builtin_nanf("");
     }
     lds_barrier();
   }
@@ -426,7 +453,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_int8_few(Int8GemmArgs a, Qua
     } else {
       Outs<E, 8> os;
       os.load(a, n);
-      const float sx = !FUSED ? token_scale(a, m) : m < a.m ? s_scale[m & (kFusedTokens - 1)] : 0.f;
+      const float sx = !FUSED ? token_scale(a, m) : m < a.m ? s_scale[m & 15] : 0.f;
       store8(a, m, n, os.eight(lo, hi, sx));
     }
   }
@@ -602,7 +629,12 @@ size_t int8_plan_bytes(const Int8Plan& p, int64_t m, int64_t n) {
 
 size_t int8_part_bytes(int64_t m, int64_t n, int64_t k, int cus) { return int8_plan_bytes(int8_plan(m, n, k, cus), m, n); }
 
-bool int8_fuses_rows(int64_t m, int64_t k) { return m <= kFusedTokens && m * fused_pitch(k) <= 32768; }
+// The quantizer inside the product costs each workgroup 2.9 us for 32768 values,
+// and a launch of its own about as much: worth it while the workgroups, one for
+// each 32 outputs, are few or the values are.
+bool int8_fuses_rows(int64_t m, int64_t n, int64_t k) {
+  return m <= 16 && k >= 16 && m * int8_kp(k) <= kFusedValues && (n + 31) / 32 * m * int8_kp(k) <= 256 * kFusedValues;
+}
 
 template <typename E>
 static hipError_t run_plan(Int8GemmArgs a, const Int8Plan& p, const QuantArgs* rows, hipStream_t st) {
@@ -615,12 +647,15 @@ static hipError_t run_plan(Int8GemmArgs a, const Int8Plan& p, const QuantArgs* r
   QuantSrc<E> src{};
   if (rows) {
     src = QuantSrc<E>{mat<E>(rows->x, rows->ldx, rows->m, rows->k), rows->col_scale};
-    k_int8_few<1, true, E><<<gr, 64 * kFewWaves, (size_t)(a.m * fused_pitch(a.k)), st>>>(a, src);
+    const size_t lds = (size_t)(a.m * fused_pitch(a.k));
+    static_assert(kFusedValues == 4 * 16 * 64 * kFewWaves, "values a workgroup quantizes");
+    if (a.m * int8_kp(a.k) <= kFusedValues / 4) k_int8_few<1, 1, E><<<gr, 64 * kFewWaves, lds, st>>>(a, src);
+    else k_int8_few<1, 4, E><<<gr, 64 * kFewWaves, lds, st>>>(a, src);
   } else {
     switch (p.kind) {
-      case kInt8Few16: k_int8_few<1, false, E><<<gr, 64 * kFewWaves, 0, st>>>(a, src); break;
-      case kInt8Few32: k_int8_few<2, false, E><<<gr, 64 * kFewWaves, 0, st>>>(a, src); break;
-      case kInt8Few64: k_int8_few<4, false, E><<<gr, 64 * kFewWaves, 0, st>>>(a, src); break;
+      case kInt8Few16: k_int8_few<1, 0, E><<<gr, 64 * kFewWaves, 0, st>>>(a, src); break;
+      case kInt8Few32: k_int8_few<2, 0, E><<<gr, 64 * kFewWaves, 0, st>>>(a, src); break;
+      case kInt8Few64: k_int8_few<4, 0, E><<<gr, 64 * kFewWaves, 0, st>>>(a, src); break;
       case kInt8Tile: k_int8_gemm<E><<<gr, 256, 0, st>>>(a); break;
     }
   }

@@ -117,9 +117,9 @@ size_t int8_plan_bytes(const Int8Plan& p, int64_t m, int64_t n);
 size_t int8_part_bytes(int64_t m, int64_t n, int64_t k, int cus);
 hipError_t launch_int8_plan(const Int8GemmArgs& a, const Int8Plan& p, hipStream_t st);
 hipError_t launch_int8_gemm(const Int8GemmArgs& a, int cus, hipStream_t st);
-// Few enough tokens for a product that quantizes its 16-bit rows itself, in one
-// launch (a.x, a.sx and a.part are then not used).
-bool int8_fuses_rows(int64_t m, int64_t k);
+// Whether a product quantizes its 16-bit rows itself, in one launch (a.x, a.sx
+// and a.part are then not used).
+bool int8_fuses_rows(int64_t m, int64_t n, int64_t k);
 hipError_t launch_int8_fused(const Int8GemmArgs& a, const QuantArgs& rows, hipStream_t st);
 hipError_t launch_int8_pack(const int8_t* src, int64_t ld, int64_t n, int64_t k, int8_t* dst, hipStream_t st);
 hipError_t launch_int8_transpose(const int8_t* src, int64_t n, int64_t k, int8_t* dst, hipStream_t st);
