@@ -438,9 +438,12 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(Mat<T> dy, Mat<T> h, Mat<T> d
     auto mend = [&] {
 #pragma unroll
       for (int j = 0; j < NCH; ++j) {
-        if (live) fix(hp[j], col(j));
-        else hp[j].zero();  // a row past the last adds nothing
+        fix(hp[j], col(j));
         fix(dp[j], col(j));
+        if (!live) {  // a row past the last adds nothing, also where the last one's dY is infinite
+          hp[j].zero();
+          dp[j].zero();
+        }
       }
     };
     if (AHEAD) mend();

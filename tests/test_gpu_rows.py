@@ -163,6 +163,22 @@ def test_rms_norm_backward(m, k, stream, dtype, gdtype):
     assert torch.equal(dx, again[0]) and torch.equal(dgamma, again[1])
 
 
+@pytest.mark.parametrize("m,k", [(1, 640), (3, 640), (5, 2048), (3, 8)])
+def test_rms_norm_backward_last_row_infinite(m, k):
+    """An infinite dY in the last row reaches dgamma as that infinity, also
+    where its workgroup has places for rows past it."""
+    need_gpu()
+    h, g, dy = rand((m, k), 1).abs() + 1, rand((k,), 2), rand((m, k), 3)
+    _, _, rstd = rows.rms_norm_fwd(h, g, EPS)
+    _, wg = ref.rms_norm_bwd(f64(dy), f64(h), f64(g), EPS)
+    dy[m - 1, 5] = float("inf")
+    dg = f64(rows.rms_norm_bwd(dy, h, rstd, g)[1])
+    assert dg[5] == np.inf
+    rest = np.arange(k) != 5
+    bound = (E32 + m * 2.0 ** -24) * (np.abs(f64(dy)) * f64(h) * f64(rstd)[:, None]).sum(0)
+    assert (np.abs(dg - wg)[rest] <= bound[rest]).all()
+
+
 def test_rms_norm_in_place():
     """The residual stream updated in its own buffer, and dX in dH's and dY's."""
     need_gpu()
