@@ -389,7 +389,7 @@ hipError_t norm_typed(const NormArgs& a, int cus, hipStream_t st) {
 // rows to a workgroup's turn, 70 us.
 template <typename T, typename G, int TPR, int NCH, bool WIDE>
 __global__ __launch_bounds__(1024) void k_norm_bwd(Mat<T> dy, Mat<T> h, Mat<T> dh, Mat<G> gamma, const float* rstd,
-                                                   Out16 dx, float* part, int64_t m, int64_t k) {
+                                                   Out16 dx, float* part, float* dgamma, int64_t m, int64_t k) {
   constexpr int SUB = 1024 / TPR, NW = TPR / 64;
   __shared__ uint32_t s_red[2 * 16];
   __shared__ __attribute__((aligned(16))) float s_acc[SUB > 1 ? SUB * TPR * 16 : 4];
@@ -521,9 +521,28 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(Mat<T> dy, Mat<T> h, Mat<T> d
         acc[0][4 * i + 3] += f.w;
       }
   }
+  // a workgroup alone has the whole dgamma (two pieces a thread: 4 us slower
+  // at 32768 for the registers that this takes)
+  if constexpr (NCH == 1) {
+    if (gridDim.x == 1) {
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const int64_t c = col(0) + i;
+        if (c + 4 <= k) {
+          if (in_bounds(c, 4, k))
+            *reinterpret_cast<float4*>(dgamma + c) = make_float4(acc[0][i], acc[0][i + 1], acc[0][i + 2], acc[0][i + 3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (c + e < k && in_bounds(c + e, 1, k)) dgamma[c + e] = acc[0][i + e];
+        }
+      }
+      return;
+    }
+  }
 #pragma unroll
   for (int j = 0; j < NCH; ++j) {
-    const int64_t c = ((int64_t)j * TPR + t) * 16;
+    const int64_t c = col(j);
 #pragma unroll
     for (int i = 0; i < 16; i += 4) {
       const int64_t e = (int64_t)blockIdx.x * part_pitch(k) + c + i;
@@ -568,11 +587,13 @@ hipError_t norm_bwd_typed(const NormBwdArgs& a, int cus, hipStream_t st) {
     constexpr int TPR = decltype(tpr)::value, NCH = decltype(nch)::value;
     if constexpr (TPR == 64) {
       if (a.k < 16) {
-        k_norm_bwd<T, G, TPR, NCH, false><<<dim3(groups), dim3(1024), 0, st>>>(dy, h, dh, gamma, a.rstd, dx, a.part, a.m, a.k);
+        k_norm_bwd<T, G, TPR, NCH, false><<<dim3(groups), dim3(1024), 0, st>>>(dy, h, dh, gamma, a.rstd, dx, a.part, a.dgamma,
+                                                                            a.m, a.k);
         return hipGetLastError();
       }
     }
-    k_norm_bwd<T, G, TPR, NCH, true><<<dim3(groups), dim3(1024), 0, st>>>(dy, h, dh, gamma, a.rstd, dx, a.part, a.m, a.k);
+    k_norm_bwd<T, G, TPR, NCH, true><<<dim3(groups), dim3(1024), 0, st>>>(dy, h, dh, gamma, a.rstd, dx, a.part, a.dgamma,
+                                                                            a.m, a.k);
     return hipGetLastError();
   };
   using std::integral_constant;
@@ -589,7 +610,8 @@ hipError_t norm_bwd_typed(const NormBwdArgs& a, int cus, hipStream_t st) {
                          : go(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
     }
   }
-  if (e != hipSuccess) return e;
+  // k_norm_bwd's own condition for having written dgamma
+  if (e != hipSuccess || (groups == 1 && a.k <= 16384)) return e;
   k_norm_dgamma<<<dim3((uint32_t)((a.k + 31) / 32)), dim3(1024), 0, st>>>(a.part, groups, a.dgamma, a.k);
   return hipGetLastError();
 }
@@ -650,9 +672,14 @@ hipError_t launch_norm(const NormArgs& a, int cus, hipStream_t st) {
   return a.type == kRowF16 ? norm_typed<F16, F16>(a, cus, st) : norm_typed<Bf16, Bf16>(a, cus, st);
 }
 
-// One workgroup of 1024 threads a compute unit, where there are rows for them.
+// One workgroup of 1024 threads a compute unit, where there are rows for them;
+// a single one for the rows of two turns, which then needs no second kernel to
+// add up dgamma (on the device 4 x 4096: 6.0 us for 8.9, 8 x 4096: 8.3; at a
+// third turn they are level).  From 8192 values on a row has a turn of its own
+// and a second one costs what the kernel does.
 int norm_bwd_groups(int64_t m, int64_t k, int cus) {
   const int64_t sub = 1024 / norm_bwd_threads(k);
+  if (k <= 4096 && m <= 2 * sub) return 1;
   return (int)std::max<int64_t>(1, std::min<int64_t>((m + sub - 1) / sub, cus));
 }
 

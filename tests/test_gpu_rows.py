@@ -179,6 +179,25 @@ def test_rms_norm_backward_last_row_infinite(m, k):
     assert (np.abs(dg - wg)[rest] <= bound[rest]).all()
 
 
+@pytest.mark.parametrize("m,k", [(1, 7), (16, 645), (33, 640), (2, 8195), (1, 16384), (1, 16400)])
+def test_rms_norm_backward_few_rows(m, k):
+    """Few rows, where one workgroup writes dgamma itself, or its sum for a
+    second kernel: nothing before or past dgamma is written."""
+    need_gpu()
+    x, g, dy = rand((m, k), 1), rand((k,), 2), rand((m, k), 3)
+    _, h, rstd = rows.rms_norm_fwd(x, g, EPS)
+    got = []
+    for off in (0, 4):
+        buf = torch.full((k + 32,), -7.0, device="cuda")
+        rows.rms_norm_bwd(dy, h, rstd, g, dgamma=buf[off : off + k])
+        assert (buf[:off] == -7).all() and (buf[off + k :] == -7).all()
+        got.append(f64(buf[off : off + k]))
+    _, wg = ref.rms_norm_bwd(f64(dy), f64(h), f64(g), EPS)
+    bound = (E32 + m * 2.0 ** -24) * (np.abs(f64(dy) * f64(h)) * f64(rstd)[:, None]).sum(0)
+    for dg in got:
+        assert (np.abs(dg - wg) <= bound).all()
+
+
 def test_rms_norm_in_place():
     """The residual stream updated in its own buffer, and dX in dH's and dY's."""
     need_gpu()
