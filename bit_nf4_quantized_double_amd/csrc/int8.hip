@@ -295,7 +295,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 // in turn.  A wave reads weight tiles and token tiles straight into the
 // MFMA's registers, whole kilobytes at a time, four of its turns in flight, and
 // the waves' sums meet in LDS.  Up to 64 tokens the weight is read once, and
-// reading it is the bound: 28672 x 8192 for one token 42 us (5.6 TB/s, a copy's
+// reading it is the bound: 28672 x 8192 for one token 40 us (5.9 TB/s, a copy's
 // rate is 5.1), 8192 x 28672 for sixteen 42 us.  More tokens come in
 // blocks of 64, up to 940 TOP/s from the cache: 150 x 1000 x 2500 takes 6.1 us,
 // and 13 us as tiles with a split reduction.
@@ -303,8 +303,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 // NP > 0 (TT = 1): x is not quantized yet, and is at most 8192 NP values.
 // Every workgroup quantizes all of it into LDS, after its first weight tiles
 // are on their way: the rows are a few kilobytes in the second-level cache, and
-// a launch of its own for them costs more than the repetition (1 x 28672 x
-// 8192: 42.0 us for 47.9).
+// a launch of its own for them costs more than the repetition (a call of 1 x
+// 28672 x 8192: 41.6 us for 47.9, of 16 x 4096 x 2048: 8.3 for 12.5).
 constexpr int kFusedValues = 32768;
 constexpr int kFewWaves = 8;
 constexpr int kFewAhead = 4;  // turns in flight

@@ -194,10 +194,12 @@ struct NormSrc {
 // do as well at aligned widths, and take 107 us for 57 at 8192 x 7167.
 //
 // Measured in bf16 at 8192 x 4096, where a copy of one input takes 24 us (5.6
-// TB/s): quantize 21 us (4.9 TB/s), SwiGLU in 8 bits 31 us (5.5), norm with the
+// TB/s): quantize 20 us (5.1 TB/s), SwiGLU in 8 bits 31 us (5.5), norm with the
 // residual 45 us (5.9), the same in 8 bits 41 us (5.7).  Rows of 14336 are 1024
 // threads to a workgroup and one of those to a compute unit, so loads and
-// stores take turns: 4.4 to 4.5 TB/s.
+// stores take turns: 4.4 to 4.5 TB/s.  Walking over the rows, with the next
+// ones loaded into the registers that finished pieces leave, spills: SwiGLU
+// 175 us for 131.
 template <int TPR, int RW> constexpr int kBlock = TPR * RW < 256 ? 256 : TPR * RW;
 
 template <typename Src, int TPR, int RW, int NCH, bool WIDE, bool Y16, typename T>
