@@ -166,6 +166,8 @@ class Int8LinearFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, X, bias, w: Int8Weight):
+        if X.shape[-1] != w.k_in:  # a reshape to rows of k_in values could hide it
+            raise ValueError(f"X has {X.shape[-1]} columns, the weight {w.k_in}")
         ctx.w, ctx.xshape = w, X.shape
         ctx.bias_dtype = None if bias is None else bias.dtype
         Y = linear_fwd(w, rows._rows_of(X, w.k_in), bias)

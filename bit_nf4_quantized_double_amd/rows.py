@@ -279,11 +279,22 @@ def _rows_of(t: torch.Tensor, width: int) -> torch.Tensor:
     return t if width <= 1 or t.stride(1) == 1 and (t.shape[0] <= 1 or t.stride(0) >= width) else t.contiguous()
 
 
+def _same_shape(t, shape, name: str) -> None:
+    """Before anything is reshaped to a matrix: afterwards a tensor of another
+    shape may have as many rows, and would be paired up wrongly."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
 class RMSNormFunction(torch.autograd.Function):
     """(X, residual or None, gamma) -> (Y, h)."""
 
     @staticmethod
     def forward(ctx, X, residual, gamma, eps: float):
+        if residual is not None:
+            _same_shape(residual, X.shape, "residual")
         k = X.shape[-1]
         X2 = _rows_of(X, k)
         R2 = None if residual is None else _rows_of(residual, k)
@@ -324,6 +335,7 @@ class SwiGLUFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, G, U):
+        _same_shape(U, G.shape, "up")
         k = G.shape[-1]
         G2, U2 = _rows_of(G, k), _rows_of(U, k)
         ctx.save_for_backward(G2, U2)
