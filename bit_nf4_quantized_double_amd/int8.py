@@ -162,14 +162,17 @@ def linear_bwd(w: Int8Weight, dY: torch.Tensor, *, dX: torch.Tensor | None = Non
 
 
 class Int8LinearFunction(torch.autograd.Function):
-    """Autograd wrapper: gradients for X and the bias; no grad for W."""
+    """Autograd wrapper: gradients for X and the bias; no grad for W.  X may be
+    Int8Rows, through which no gradient passes."""
 
     @staticmethod
     def forward(ctx, X, bias, w: Int8Weight):
+        ctx.w, ctx.bias_dtype = w, None if bias is None else bias.dtype
+        if isinstance(X, Int8Rows):
+            return linear_fwd(w, X, bias)
         if X.shape[-1] != w.k_in:  # a reshape to rows of k_in values could hide it
             raise ValueError(f"X has {X.shape[-1]} columns, the weight {w.k_in}")
-        ctx.w, ctx.xshape = w, X.shape
-        ctx.bias_dtype = None if bias is None else bias.dtype
+        ctx.xshape = X.shape
         Y = linear_fwd(w, rows._rows_of(X, w.k_in), bias)
         return Y.reshape(*X.shape[:-1], w.n_out)
 
@@ -191,8 +194,8 @@ class Int8Linear(torch.nn.Module):
         self.bias = None if bias is None else torch.nn.Parameter(bias)
 
     def forward(self, X):
-        if isinstance(X, Int8Rows):
-            return linear_fwd(self.w, X, self.bias)
+        if isinstance(X, Int8Rows) and not (torch.is_grad_enabled() and self.bias is not None and self.bias.requires_grad):
+            return linear_fwd(self.w, X, self.bias)  # nothing to differentiate: without the wrapper's cost
         return Int8LinearFunction.apply(X, self.bias, self.w)
 
 

@@ -1,0 +1,32 @@
+"""The differentiable forms of norm, SwiGLU and the int8 product on the GPU:
+gradients that go missing, and the smallest widths."""
+
+import numpy as np
+import pytest
+import torch
+
+from bit_nf4_quantized_double_amd import int8, rows
+from rows_util import close16, f64, need_gpu, rand
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+EPS = 1e-5
+
+
+def test_bias_gradient_with_rows_in_8_bits():
+    """Int8Linear on rows that are in 8 bits already: its bias is a parameter
+    there too."""
+    need_gpu()
+    lin = int8.Int8Linear(rand((48, 200), 1, F32, 0.02), rand((48,), 2))
+    x, d = rand((6, 200), 3), rand((6, 48), 4)
+    q = rows.quantize_rows(x)
+    y = lin(q)
+    assert torch.equal(y, int8.linear_fwd(lin.w, q, lin.bias.detach()))
+    y.backward(d)
+    close16(lin.bias.grad, f64(d).sum(0), np.abs(f64(d)).sum(0))
+    with torch.no_grad():
+        assert not lin(q).requires_grad
+    lin.bias.requires_grad_(False)
+    assert not lin(q).requires_grad
+    assert not int8.Int8Linear(rand((48, 200), 1, F32, 0.02))(q).requires_grad
