@@ -177,6 +177,7 @@ class Int8LinearFunction(torch.autograd.Function):
         return Y.reshape(*X.shape[:-1], w.n_out)
 
     @staticmethod
+    @qlora._once
     def backward(ctx, dY):
         dY2 = rows._rows_of(dY, ctx.w.n_out)
         dX = linear_bwd(ctx.w, dY2).reshape(ctx.xshape) if ctx.needs_input_grad[0] else None

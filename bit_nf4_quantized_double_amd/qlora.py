@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -428,6 +429,35 @@ def linear_bwd(w: NF4Weight, X: torch.Tensor, dY: torch.Tensor, A: torch.Tensor 
         st = lib().qlora_linear_bwd(*head, *tail)
         _check(st, "qlora_linear_bwd")
     return dX, dA, dB
+
+
+class _NotTwice(torch.autograd.Function):
+    """The identity on a gradient that cannot be differentiated itself.
+    ``leaf`` requires a gradient, so that the result does too."""
+
+    @staticmethod
+    def forward(ctx, grad, leaf):
+        return grad.view_as(grad)
+
+    @staticmethod
+    def backward(ctx, _):
+        raise RuntimeError("the second derivative of this operator is not available")
+
+
+def _once(backward):
+    """For a Function's backward that calls kernels: gradients made with
+    create_graph=True refuse to be differentiated.  Left as they are they
+    would be constants, and second derivatives silently incomplete."""
+    @functools.wraps(backward)
+    def run(ctx, *grads):
+        if not torch.is_grad_enabled():
+            return backward(ctx, *grads)
+        with torch.no_grad():
+            out = backward(ctx, *grads)
+        leaf = torch.empty(0, requires_grad=True)
+        wrap = lambda g: None if g is None else _NotTwice.apply(g, leaf)
+        return tuple(map(wrap, out)) if isinstance(out, tuple) else wrap(out)
+    return run
 
 
 class QLoRALinearFunction(torch.autograd.Function):

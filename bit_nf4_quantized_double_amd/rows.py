@@ -306,6 +306,7 @@ class RMSNormFunction(torch.autograd.Function):
         return Y.reshape(X.shape), h
 
     @staticmethod
+    @qlora._once
     def backward(ctx, dY, dh):
         H, rstd, gamma = ctx.saved_tensors
         k = H.shape[-1]
@@ -342,6 +343,7 @@ class SwiGLUFunction(torch.autograd.Function):
         return swiglu_fwd(G2, U2).reshape(G.shape)
 
     @staticmethod
+    @qlora._once
     def backward(ctx, dY):
         G, U = ctx.saved_tensors
         dG, dU = swiglu_bwd(_rows_of(dY, G.shape[-1]), G, U)

@@ -30,3 +30,28 @@ def test_bias_gradient_with_rows_in_8_bits():
     lin.bias.requires_grad_(False)
     assert not lin(q).requires_grad
     assert not int8.Int8Linear(rand((48, 200), 1, F32, 0.02))(q).requires_grad
+
+
+def _twice(first, leaves):
+    """Gradients of gradients, beside a term that has them."""
+    leaf = leaves[0]
+    for loss in (first, (first.float().square()).sum(), first.float().sum() + leaf.float().square().sum()):
+        loss = loss.float().sum()
+        g = torch.autograd.grad(loss, leaf, create_graph=True, retain_graph=True)[0]
+        with pytest.raises(RuntimeError, match="second derivative"):
+            (g.float().square().sum() + leaf.float().square().sum()).backward()
+    # a first-order step with the graph kept is as it was
+    want = torch.autograd.grad(first.float().sum(), leaf, retain_graph=True)[0]
+    got = torch.autograd.grad(first.float().sum(), leaf, retain_graph=True, create_graph=True)[0]
+    assert torch.equal(want, got)
+
+
+def test_no_second_derivatives():
+    """They have no formula here: asked for, they are refused, not left out."""
+    need_gpu()
+    x, r = rand((6, 64), 1).requires_grad_(), rand((6, 64), 2).requires_grad_()
+    _twice(rows.swiglu(x, r), (x, r))
+    _twice(rows.RMSNorm(64, EPS)(x), (x,))
+    y, h = rows.RMSNorm(64, EPS)(x, r)
+    _twice(y + h, (r,))
+    _twice(int8.Int8Linear(rand((32, 64), 3, F32, 0.02), rand((32,), 4), transposed=True)(x), (x,))
