@@ -473,6 +473,7 @@ class QLoRALinearFunction(torch.autograd.Function):
         return Y.reshape(*X.shape[:-1], w.n_out)
 
     @staticmethod
+    @_once
     def backward(ctx, dY):
         X2, A, B, U = ctx.saved_tensors
         # the gradient arrives in the output's dtype, which is X's (bf16 or fp16)

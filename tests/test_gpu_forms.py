@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from bit_nf4_quantized_double_amd import int8, rows
+from bit_nf4_quantized_double_amd import int8, qlora, rows
 from rows_util import close16, f64, need_gpu, rand
 
 pytestmark = pytest.mark.gpu
@@ -55,3 +55,13 @@ def test_no_second_derivatives():
     y, h = rows.RMSNorm(64, EPS)(x, r)
     _twice(y + h, (r,))
     _twice(int8.Int8Linear(rand((32, 64), 3, F32, 0.02), rand((32,), 4), transposed=True)(x), (x,))
+
+
+def test_no_second_derivatives_of_the_nf4_linear():
+    need_gpu()
+    lin = qlora.QLoRALinear(rand((64, 128), 1, F32, 0.02), r=8, alpha=16.0)
+    with torch.no_grad():
+        lin.B.copy_(rand((64, 8), 2, scale=0.1))
+    x = rand((6, 128), 3).requires_grad_()
+    _twice(lin(x), (x,))
+    _twice(lin(x), (lin.A,))
