@@ -301,6 +301,8 @@ class RMSNormFunction(torch.autograd.Function):
         Y, H, rstd = rms_norm_fwd(X2, gamma, eps, R2)
         ctx.save_for_backward(H, rstd, gamma)
         ctx.has_residual = residual is not None
+        # an output that nothing reads has no gradient: it comes as None, not as a tensor of zeros
+        ctx.set_materialize_grads(False)
         # without a residual h is X: a view of it would be an input returned as an output
         h = H.reshape(X.shape) if residual is not None else None
         return Y.reshape(X.shape), h
@@ -310,11 +312,11 @@ class RMSNormFunction(torch.autograd.Function):
     def backward(ctx, dY, dh):
         H, rstd, gamma = ctx.saved_tensors
         k = H.shape[-1]
-        dY2 = torch.zeros_like(H) if dY is None else _rows_of(dY, k)
-        dX, dgamma = rms_norm_bwd(dY2, H, rstd, gamma, None if dh is None else _rows_of(dh, k))
-        shape = (dY if dY is not None else dh).shape
-        dX = dX.reshape(shape)
-        return dX, (dX if ctx.has_residual else None), dgamma.to(gamma.dtype), None
+        if dY is None:  # h alone is read: its gradient passes through
+            return dh, (dh if ctx.has_residual else None), (torch.zeros_like(gamma) if ctx.needs_input_grad[2] else None), None
+        dX, dgamma = rms_norm_bwd(_rows_of(dY, k), H, rstd, gamma, None if dh is None else _rows_of(dh, k))
+        dX = dX.reshape(dY.shape)
+        return dX, (dX if ctx.has_residual else None), (dgamma.to(gamma.dtype) if ctx.needs_input_grad[2] else None), None
 
 
 class RMSNorm(torch.nn.Module):
