@@ -276,7 +276,7 @@ def swiglu_bwd(dY: torch.Tensor, G: torch.Tensor, U: torch.Tensor, *, dG: torch.
 def _rows_of(t: torch.Tensor, width: int) -> torch.Tensor:
     """[..., width] as a matrix with contiguous rows."""
     t = t.reshape(-1, width)
-    return t if width <= 1 or t.stride(1) == 1 and (t.shape[0] <= 1 or t.stride(0) >= width) else t.contiguous()
+    return t if (width <= 1 or t.stride(1) == 1) and (t.shape[0] <= 1 or t.stride(0) >= width) else t.contiguous()
 
 
 def _same_shape(t, shape, name: str) -> None:

@@ -65,3 +65,21 @@ def test_no_second_derivatives_of_the_nf4_linear():
     x = rand((6, 128), 3).requires_grad_()
     _twice(lin(x), (x,))
     _twice(lin(x), (lin.A,))
+
+
+@pytest.mark.parametrize("m", [1, 5])
+def test_rows_of_one_value(m):
+    """Also where a gradient or an input is one value seen m times."""
+    need_gpu()
+    g, u = rand((m, 1), 1).requires_grad_(), rand((m, 1), 2).requires_grad_()
+    rows.swiglu(g, u).sum().backward()
+    dg, du = rows.swiglu_bwd(torch.ones((m, 1), dtype=BF16, device="cuda"), g.detach(), u.detach())
+    assert torch.equal(g.grad, dg) and torch.equal(u.grad, du)
+    one = rand((1, 1), 3).expand(m, 1)
+    assert torch.equal(rows.swiglu(one, u.detach()), rows.swiglu(one.contiguous(), u.detach()))
+    x = rand((m, 1), 4).requires_grad_()
+    norm = rows.RMSNorm(1, EPS)
+    norm(x).sum().backward()
+    _, h, rstd = rows.rms_norm_fwd(x.detach(), norm.weight.detach(), EPS)
+    dx, dgamma = rows.rms_norm_bwd(torch.ones((m, 1), dtype=BF16, device="cuda"), h, rstd, norm.weight.detach())
+    assert torch.equal(x.grad, dx) and torch.equal(norm.weight.grad, dgamma.to(BF16))
