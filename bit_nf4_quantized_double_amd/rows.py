@@ -13,6 +13,7 @@ rows may be further apart (a slice of a wider matrix).
 from __future__ import annotations
 
 import ctypes
+import math
 from dataclasses import dataclass
 
 import torch
@@ -275,7 +276,7 @@ def swiglu_bwd(dY: torch.Tensor, G: torch.Tensor, U: torch.Tensor, *, dG: torch.
 
 def _rows_of(t: torch.Tensor, width: int) -> torch.Tensor:
     """[..., width] as a matrix with contiguous rows."""
-    t = t.reshape(-1, width)
+    t = t.reshape(math.prod(t.shape[:-1]), width)  # not -1, which rows of no values leave open
     return t if (width <= 1 or t.stride(1) == 1) and (t.shape[0] <= 1 or t.stride(0) >= width) else t.contiguous()
 
 

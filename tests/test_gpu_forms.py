@@ -83,3 +83,22 @@ def test_rows_of_one_value(m):
     _, h, rstd = rows.rms_norm_fwd(x.detach(), norm.weight.detach(), EPS)
     dx, dgamma = rows.rms_norm_bwd(torch.ones((m, 1), dtype=BF16, device="cuda"), h, rstd, norm.weight.detach())
     assert torch.equal(x.grad, dx) and torch.equal(norm.weight.grad, dgamma.to(BF16))
+
+
+def test_no_rows_and_rows_of_no_values():
+    need_gpu()
+    for shape in ((0, 64), (2, 0, 64), (3, 0), (2, 3, 0)):
+        x, r = (torch.empty(shape, dtype=BF16, device="cuda", requires_grad=True) for _ in range(2))
+        norm = rows.RMSNorm(shape[-1], EPS)
+        y, h = norm(x, r)
+        s = rows.swiglu(y, h)
+        assert y.shape == h.shape == s.shape == shape
+        s.sum().backward()
+        assert x.grad.shape == r.grad.shape == shape and (norm.weight.grad == 0).all()
+        lin = int8.Int8Linear(rand((40, shape[-1]), 1, F32, 0.02), rand((40,), 2), transposed=True)
+        x.grad = None
+        out = lin(x)
+        out.sum().backward()
+        rows_in = out.numel() // 40
+        assert out.shape == (*shape[:-1], 40) and x.grad.shape == shape
+        assert torch.equal(out, lin.bias.detach().expand(out.shape)) and (lin.bias.grad == rows_in).all()
