@@ -323,8 +323,8 @@ int qlora_rms_norm_fwd(const void* X, int64_t ldx, const void* residual, int64_t
         (st = check_gamma(gamma, gamma_dtype, dtype, K)))
       return st;
     if (residual && (st = check_rows_in(residual, ldr, M, K, dtype, "residual"))) return st;
-    if (M == 0 || K == 0) return (int)QLORA_OK;
-    if ((st = check_buffer(H, residual != nullptr, "H")) || (st = check_buffer(Y, true, "Y")) ||
+    if (M == 0 || (K == 0 && !rstd)) return (int)QLORA_OK;
+    if ((st = check_buffer(H, residual && K > 0, "H")) || (st = check_buffer(Y, K > 0, "Y")) ||
         (st = check_buffer(rstd, true, "rstd")))
       return st;
     qlora::NormArgs a{};
@@ -345,8 +345,8 @@ int qlora_rms_norm_int8(const void* X, int64_t ldx, const void* residual, int64_
         (st = check_gamma(gamma, gamma_dtype, dtype, K)))
       return st;
     if (residual && (st = check_rows_in(residual, ldr, M, K, dtype, "residual"))) return st;
-    if (M == 0 || K == 0) return (int)QLORA_OK;
-    if ((st = check_buffer(H, residual != nullptr, "H")) || (st = check_buffer(codes, true, "codes")) ||
+    if (M == 0 || (K == 0 && !scale)) return (int)QLORA_OK;
+    if ((st = check_buffer(H, residual && K > 0, "H")) || (st = check_buffer(codes, K > 0, "codes")) ||
         (st = check_buffer(scale, true, "scale")))
       return st;
     qlora::NormArgs a{};

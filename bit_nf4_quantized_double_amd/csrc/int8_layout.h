@@ -65,8 +65,8 @@ struct NormArgs {
   int64_t ldx, ldr, m, k;
   float eps;
   uint16_t* h;     // NULL without a residual
-  uint16_t* y;     // 16-bit output, or NULL:
-  float* rstd;     // with y
+  uint16_t* y;     // 16-bit output,
+  float* rstd;     // with y; NULL for
   int8_t* codes;   // 8-bit output
   float* scale;
 };

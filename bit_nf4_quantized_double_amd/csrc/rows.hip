@@ -253,8 +253,9 @@ __global__ __launch_bounds__((kBlock<TPR, RW>)) void k_rows(Src src, Out8 o8, Ou
   row_reduce<NW, RW>(sum, top, s_red);
   if (RW == 1 && !live) return;
   float rstd = 1.f;
-  // 1 / sqrt in full: it is once a row, and every value of the row has it
-  if constexpr (Src::kNorm) rstd = 1.f / sqrtf(sum / (float)k + src.eps);
+  // 1 / sqrt in full: it is once a row, and every value of the row has it (a
+  // row of no values has the mean 0)
+  if constexpr (Src::kNorm) rstd = 1.f / sqrtf(sum / (float)max(k, (int64_t)1) + src.eps);
   if constexpr (Y16) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -374,7 +375,8 @@ hipError_t norm_typed(const NormArgs& a, int cus, hipStream_t st) {
   s.gamma = mat<G>(a.gamma, a.k, 1, a.k);
   s.h = out16(a.h, a.m, a.k);
   s.eps = a.eps;
-  if (a.y) return launch_rows<NormSrc<T, G>, true, T>(s, Out8{}, out16(a.y, a.m, a.k), a.rstd, a.m, a.k, cus, st);
+  // (y is NULL where rows have no values)
+  if (a.rstd) return launch_rows<NormSrc<T, G>, true, T>(s, Out8{}, out16(a.y, a.m, a.k), a.rstd, a.m, a.k, cus, st);
   return launch_rows<NormSrc<T, G>, false, T>(s, out8(a.codes, a.scale, a.m, a.k, false), Out16{}, nullptr, a.m, a.k,
                                               cus, st);
 }

@@ -473,7 +473,8 @@ int qlora_int8_linear_bwd(const qlora_int8_weight *w, const void *dY, int64_t ld
  * stored values.  gamma: [K], of the rows' type or fp32 (gamma_dtype).  eps
  * at least 1e-12.  K <= QLORA_MAX_NORM_WIDTH.  H may be X or the residual
  * itself (same pointer and stride K).  A row whose sum of squares passes fp32
- * gives rstd = 0 (y = 0) or, in 8 bits, a NaN row.
+ * gives rstd = 0 (y = 0) or, in 8 bits, a NaN row.  A row of no values has the
+ * mean square 0, and in 8 bits the scale of a row of zeros.
  *   qlora_rms_norm_fwd   Y 16-bit [M, K], rstd fp32 [M] (for the backward)
  *   qlora_rms_norm_int8  y quantized by rows from its fp32 values
  *   qlora_rms_norm_bwd   from dY, H (X without a residual), rstd: with hat = h rstd and g = dY gamma,

@@ -149,3 +149,12 @@ def test_cpu_tensors_are_refused():
                  lambda: rows.rms_norm_fwd(x, x[0], 1e-5), lambda: int8.quantize_weight(x)):
         with pytest.raises(ValueError, match="GPU"):
             call()
+
+
+def test_norm_of_no_values_writes_nothing_without_a_place(L):
+    """K = 0: nothing to write but rstd or the scales, and not even those when
+    the caller has no place for them."""
+    assert L.qlora_rms_norm_fwd(None, 0, None, 0, None, BF16, 4, 0, 1e-5, None, None, None, BF16, 0) == 0
+    assert L.qlora_rms_norm_int8(None, 0, None, 0, None, BF16, 4, 0, 1e-5, None, None, None, BF16, 0) == 0
+    assert L.qlora_rms_norm_fwd(None, 0, None, 0, None, BF16, 4, 0, 1e-5, None, None, P2, BF16, 0) == ALIGN
+    assert L.qlora_rms_norm_int8(None, 0, None, 0, None, BF16, 4, 0, 1e-5, None, None, P2, BF16, 0) == ALIGN
