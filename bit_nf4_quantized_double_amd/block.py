@@ -53,7 +53,8 @@ class Int8MLPBlock:
     one product, whose output's halves SwiGLU reads."""
 
     def __init__(self, block: MLPBlock):
-        self.gamma, self.eps = block.norm.weight.detach(), block.norm.eps
+        # a copy, as the merged weights are: training that goes on does not reach it
+        self.gamma, self.eps = block.norm.weight.detach().clone(), block.norm.eps
         self.hidden = block.gate.w.n_out
         self.gate_up = int8.quantize_weight(torch.cat([_merged(block.gate), _merged(block.up)]))
         self.down = int8.quantize_weight(_merged(block.down))
