@@ -334,8 +334,16 @@ def _ws(nbytes: int, device, ws: torch.Tensor | None):
     """The caller's workspace when it is big enough, else a fresh one."""
     if nbytes == 0:
         return None, 0
-    if ws is not None and ws.numel() >= nbytes:
-        return ws, ws.numel()
+    if ws is not None:
+        if not isinstance(ws, torch.Tensor):
+            raise TypeError("ws must be a torch.Tensor")
+        have = ws.numel() * ws.element_size()
+        if have >= nbytes:  # kernels write to all of these bytes
+            if ws.device != device:
+                raise ValueError(f"ws must be on {device}")
+            if not ws.is_contiguous():
+                raise ValueError("ws must be contiguous")
+            return ws, have
     t = torch.empty(nbytes, dtype=torch.uint8, device=device)
     return t, nbytes
 
