@@ -103,7 +103,12 @@ __device__ __forceinline__ void store_codes(const Out8& o, int64_t row, int64_t 
 
 // ---- sources of rows (QuantSrc: rows_common.h) -------------------------------
 
-__device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.f + __expf(-g)); }
+// 1 / (1 + e^-g).  The reciprocal instruction flushes results below 2^-126, so
+// it is taken of 2^-32 (1 + e^-g) and scaled back: powers of two, which change
+// no other result.
+__device__ __forceinline__ float sigmoid(float g) {
+  return __builtin_amdgcn_rcpf(__builtin_fmaf(__expf(-g), 0x1p-32f, 0x1p-32f)) * 0x1p-32f;
+}
 
 template <typename T>
 struct SwigluSrc {

@@ -1,11 +1,13 @@
-"""Corners of the row-wise operators on the GPU: rows of no values."""
+"""Corners of the row-wise operators on the GPU: rows of no values,
+gates far out."""
 
 import numpy as np
 import pytest
 import torch
 
+import oracle.rows as ref
 from bit_nf4_quantized_double_amd import int8, rows
-from rows_util import f64, need_gpu, rand
+from rows_util import E32, TINY, U, f64, need_gpu, rand
 
 pytestmark = pytest.mark.gpu
 
@@ -33,3 +35,25 @@ def test_norm_in_8_bits_of_no_values(m):
         del stale
         _, _, rstd = rows.rms_norm_fwd(x, g, EPS, residual)
         np.testing.assert_allclose(f64(rstd), EPS ** -0.5, rtol=2.0 ** -21)
+
+
+def test_swiglu_gates_whose_sigmoid_is_subnormal():
+    """1 / (1 + e^-g) below 2^-126 is a number still, and its products with a
+    large u or dY are ordinary ones.  The bound: half a spacing of the
+    output's type and that of s, whose spacing there is 2^-149."""
+    need_gpu()
+    g = torch.tensor([[-86.0, -87.0, -87.5, -88.0, -88.5]], dtype=BF16, device="cuda")
+    for c in (1.0, 1e4, 1e30):
+        u = torch.full_like(g, c)
+        G, C = f64(g), f64(u)
+        s = ref.sigmoid(G)
+        # e^-g through 2^(-g log2 e) in fp32: |g| 2^-24 and a few roundings
+        def near(got, want, slope):
+            err = np.abs(want) * (U[BF16] + (1 + np.abs(G)) * E32) + slope * 2.0 ** -149 + TINY[BF16]
+            assert (np.abs(f64(got) - want) <= err).all(), (f64(got), want)
+        near(rows.swiglu_fwd(g, u), ref.swiglu_fwd(G, C), np.abs(G) * C)
+        dg, du = rows.swiglu_bwd(u, g, u)
+        wg, wu = ref.swiglu_bwd(C, G, C)
+        if c * c < 1e38:
+            near(dg, wg, C * C * (1 + np.abs(G)))
+        near(du, wu, np.abs(G) * C)
