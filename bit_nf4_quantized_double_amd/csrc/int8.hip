@@ -321,9 +321,10 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_int8_few(Int8GemmArgs a, Qua
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t kp = int8_kp(a.k);
   const uint32_t groups = (uint32_t)((a.n + 31) / 32), blocks = (uint32_t)((a.m + 16 * TT - 1) / (16 * TT));
-  const uint32_t z = blockIdx.x / (blocks * groups);
+  const uint32_t lin = (uint32_t)block_of(blockIdx.x, blockIdx.y), z = lin / (blocks * groups);
+  if (z >= (uint32_t)a.ksplit) return;
   uint32_t tb, group;
-  tile_of(blockIdx.x % (blocks * groups), blocks, groups, tb, group);
+  tile_of(lin % (blocks * groups), blocks, groups, tb, group);
   const uint32_t strip = 16u * (uint32_t)kp;
   const uint32_t chunks = (uint32_t)(kp >> 6), per = (chunks + a.ksplit - 1) / a.ksplit;
   const uint32_t c0 = min(z * per, chunks), c1 = min(c0 + per, chunks);
@@ -484,7 +485,8 @@ __global__ __launch_bounds__(256) void k_int8_reduce(Int8GemmArgs a) {
 __global__ __launch_bounds__(256) void k_int8_pack(const int8_t* src, int64_t ld, int64_t n, int64_t k, int8_t* dst,
                                                    int64_t rows) {
   const int64_t kp = int8_kp(k);
-  const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x & 15), piece = (int64_t)blockIdx.y * 16 + (threadIdx.x >> 4);
+  const int64_t row = block_of(blockIdx.x, blockIdx.z) * 16 + (threadIdx.x & 15),
+                piece = (int64_t)blockIdx.y * 16 + (threadIdx.x >> 4);
   if (row >= rows || piece * 16 >= kp) return;
   const int64_t c = piece * 16, e = row * ld + c, size = (n - 1) * ld + k;
   uint4 u = make_uint4(0, 0, 0, 0);
@@ -542,8 +544,9 @@ __global__ __launch_bounds__(256) void k_int8_dequant(const int8_t* codes, const
   const int64_t kp = int8_kp(k), rows = (weight ? int8_weight_strips(m) : int8_row_strips(m)) * 16;
   // a strip's columns first: its 16 rows fill up together
   const uint32_t across = (uint32_t)((k + 255) / 256);
-  const int64_t row = (int64_t)(blockIdx.x / across) * 16 + (threadIdx.x & 15),
-                piece = (int64_t)(blockIdx.x % across) * 16 + (threadIdx.x >> 4);
+  const uint32_t lin = (uint32_t)block_of(blockIdx.x, blockIdx.y);
+  const int64_t row = (int64_t)(lin / across) * 16 + (threadIdx.x & 15),
+                piece = (int64_t)(lin % across) * 16 + (threadIdx.x >> 4);
   const int64_t c = piece * 16;
   if (row >= m || c >= k) return;
   const int64_t at = int8_piece(weight ? int8_weight_row(row) : row, piece, kp);
@@ -642,8 +645,9 @@ static hipError_t run_plan(Int8GemmArgs a, const Int8Plan& p, const QuantArgs* r
   const bool tile = p.kind == kInt8Tile;
   const int64_t bm = tile ? 256 : p.kind == kInt8Few16 ? 16 : p.kind == kInt8Few32 ? 32 : 64, bn = tile ? 128 : 32;
   const int64_t tiles = (a.m + bm - 1) / bm * ((a.n + bn - 1) / bn);
-  if (tiles * a.ksplit > INT_MAX) return hipErrorInvalidValue;
-  const dim3 gr((uint32_t)(tiles * a.ksplit));
+  // tiles count in one dimension, of 2^32 threads: past that lie outputs of 0.5 TB
+  if (tiles * a.ksplit > (tile ? (int64_t)INT_MAX / 128 : INT_MAX)) return hipErrorInvalidValue;
+  const dim3 gr = tile ? dim3((uint32_t)(tiles * a.ksplit)) : grid_of(tiles * a.ksplit);
   QuantSrc<E> src{};
   if (rows) {
     src = QuantSrc<E>{mat<E>(rows->x, rows->ldx, rows->m, rows->k), rows->col_scale};
@@ -662,7 +666,7 @@ static hipError_t run_plan(Int8GemmArgs a, const Int8Plan& p, const QuantArgs* r
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.ksplit == 1) return e;
   const int64_t blocks = ((a.n + 7) / 8 * a.m + 255) / 256;
-  if (blocks > INT_MAX) return hipErrorInvalidValue;
+  if (blocks >= (int64_t)1 << 24) return hipErrorInvalidValue;  // of 256 threads; plans split only small outputs
   k_int8_reduce<E><<<dim3((uint32_t)blocks), 256, 0, st>>>(a);
   return hipGetLastError();
 }
@@ -684,7 +688,7 @@ hipError_t launch_int8_fused(const Int8GemmArgs& a, const QuantArgs& rows, hipSt
 
 hipError_t launch_int8_pack(const int8_t* src, int64_t ld, int64_t n, int64_t k, int8_t* dst, hipStream_t st) {
   const int64_t rows = int8_weight_strips(n) * 16;
-  const dim3 grid((uint32_t)(rows / 16), (uint32_t)((int8_kp(k) / 16 + 15) / 16));
+  const dim3 strips = grid_of(rows / 16), grid(strips.x, (uint32_t)((int8_kp(k) / 16 + 15) / 16), strips.y);
   k_int8_pack<<<grid, 256, 0, st>>>(src, ld, n, k, dst, rows);
   return hipGetLastError();
 }
@@ -699,7 +703,7 @@ hipError_t launch_int8_dequant(const int8_t* codes, const float* scale, int64_t 
                                uint16_t* out, hipStream_t st) {
   const int64_t blocks = (m + 15) / 16 * ((k + 255) / 256);
   if (blocks > INT_MAX) return hipErrorInvalidValue;
-  const dim3 grid((uint32_t)blocks);
+  const dim3 grid = grid_of(blocks);
   if (f16) k_int8_dequant<F16><<<grid, 256, 0, st>>>(codes, scale, m, k, weight, out);
   else k_int8_dequant<Bf16><<<grid, 256, 0, st>>>(codes, scale, m, k, weight, out);
   return hipGetLastError();

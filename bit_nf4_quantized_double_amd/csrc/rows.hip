@@ -215,7 +215,7 @@ __global__ __launch_bounds__((kBlock<TPR, RW>)) void k_rows(Src src, Out8 o8, Ou
   constexpr int LR = 64 / RW;  // lanes of a row in a wave
   const int lane = threadIdx.x & 63, wave = threadIdx.x % (TPR * RW) / 64;
   const int t = wave * LR + lane % LR;
-  const int64_t row0 = ((int64_t)blockIdx.x * (kBlock<TPR, RW> / (TPR * RW)) + threadIdx.x / (TPR * RW)) * RW;
+  const int64_t row0 = (block_of(blockIdx.x, blockIdx.y) * (kBlock<TPR, RW> / (TPR * RW)) + threadIdx.x / (TPR * RW)) * RW;
   const int64_t row = row0 + lane / LR;
   const bool live = row < m;
   const int64_t npieces = Y16 ? (k + 15) / 16 : o8.kp / 16;
@@ -321,7 +321,7 @@ hipError_t launch_rows(const Src& src, const Out8& o8, const Out16& o16, float* 
   auto go = [&](auto tpr, auto rw, auto nch) {
     constexpr int TPR = decltype(tpr)::value, RW = decltype(rw)::value, NCH = decltype(nch)::value;
     constexpr int per = kBlock<TPR, RW> / TPR;
-    const dim3 grid((uint32_t)((m + per - 1) / per)), block(kBlock<TPR, RW>);
+    const dim3 grid = grid_of((m + per - 1) / per), block(kBlock<TPR, RW>);
     if constexpr (TPR == 64 && RW == 1) {
       if (k < 16) {
         k_rows<Src, TPR, RW, NCH, false, Y16, T><<<grid, block, 0, st>>>(src, o8, o16, rstd, m, k);

@@ -11,6 +11,15 @@ namespace {
 
 constexpr float kAmaxFloor = 1e-30f;
 
+// A launch has fewer than 2^32 threads in a dimension: workgroups (of up to
+// 1024 threads) past kGridX go on in the second one, whose last line is filled
+// up with workgroups that have nothing to do.
+constexpr int64_t kGridX = 1 << 21;
+inline dim3 grid_of(int64_t blocks) {
+  return dim3((uint32_t)(blocks < kGridX ? blocks : kGridX), (uint32_t)((blocks + kGridX - 1) / kGridX));
+}
+__device__ __forceinline__ int64_t block_of(uint32_t x, uint32_t y) { return (int64_t)y * kGridX + x; }
+
 // One fp32 of a 16- or 32-bit element type.
 struct F32 {};
 template <typename T> struct Elem { typedef uint16_t type; };

@@ -1,5 +1,5 @@
 """Corners of the row-wise operators on the GPU: rows of no values,
-gates far out."""
+gates far out, and more rows than a launch has in one dimension."""
 
 import numpy as np
 import pytest
@@ -57,3 +57,46 @@ def test_swiglu_gates_whose_sigmoid_is_subnormal():
         if c * c < 1e38:
             near(dg, wg, C * C * (1 + np.abs(G)))
         near(du, wu, np.abs(G) * C)
+
+
+def _same(a, b):
+    for x, y in zip(a, b):
+        assert torch.equal(x, y)
+
+
+def test_more_rows_than_a_launch_dimension():
+    """A row takes 64 threads or more, and a dimension of a launch fewer than
+    2^32 threads: the rows around that edge and the last ones are those of
+    calls of their own."""
+    need_gpu()
+    m, k = (1 << 26) + 70, 16
+    x, g = rand((4099, k), 1).repeat(m // 4099 + 1, 1)[:m], rand((k,), 2)
+    parts = [slice(0, 100), slice((1 << 26) - 50, (1 << 26) + 50), slice(m - 70, m)]
+    y, _, rstd = rows.rms_norm_fwd(x, g, EPS)
+    for p in parts:
+        a, _, c = rows.rms_norm_fwd(x[p], g, EPS)
+        _same((y[p], rstd[p]), (a, c))
+    del rstd
+    for call in (lambda t: rows.rms_norm_int8(t, g, EPS)[0], rows.quantize_rows, lambda t: rows.swiglu_int8(t, t)):
+        q = call(x)
+        v = rows.dequant_rows(q)
+        for p in parts:
+            few = call(x[p])
+            assert torch.equal(v[p], rows.dequant_rows(few))
+            assert torch.equal(q.scale[p], few.scale)
+        del q, v
+
+
+def test_more_8_bit_rows_and_outputs_than_a_launch_dimension():
+    """Reading rows back, packing a weight and the product of few tokens take
+    fewer threads a row; the values are exact, so all of them are compared."""
+    need_gpu()
+    m = (1 << 28) + 40
+    x = (torch.arange(1, 252, device="cuda") - 126).to(BF16).repeat(m // 251 + 1)[:m].reshape(m, 1)
+    assert torch.equal(rows.dequant_rows(rows.quantize_rows(x)), x)
+    codes = x.to(torch.int8)
+    w = int8.weight_from_codes(codes, torch.ones(m, device="cuda"))
+    assert torch.equal(int8.dequant_weight(w), x)
+    one = torch.tensor([[1.0], [-2.0]], dtype=BF16, device="cuda")
+    y = int8.linear_fwd(w, one)
+    assert torch.equal(y[0], x[:, 0]) and torch.equal(y[1], -2 * x[:, 0])
