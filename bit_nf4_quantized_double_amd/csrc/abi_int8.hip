@@ -100,18 +100,38 @@ int check_int8_weight(const qlora_int8_weight* w) {
   return check_buffer(w->scale, w->n_out > 0, "weight scale");
 }
 
+qlora::Int8GemmArgs product_args(const int8_t* wcodes, const float* wscale, int64_t n, int64_t k, const int8_t* xcodes,
+                                 const float* xscale, int64_t m, const uint16_t* bias, uint16_t* out, int dtype) {
+  qlora::Int8GemmArgs g{};
+  g.w = wcodes; g.x = xcodes; g.sw = wscale; g.sx = xscale; g.bias = bias; g.out = out;
+  g.m = m; g.n = n; g.k = k;
+  g.f16 = dtype == QLORA_F16;
+  return g;
+}
+
 // The product of quantized rows with a weight's tiles, `n` outputs from a
 // reduction over `k`.
 int product(const int8_t* wcodes, const float* wscale, int64_t n, int64_t k, const int8_t* xcodes, const float* xscale,
             int64_t m, const uint16_t* bias, uint16_t* out, int dtype, void* part, size_t part_bytes,
             hipStream_t stream) {
   const int cus = qlora::device_compute_units();
-  qlora::Int8GemmArgs g{};
-  g.w = wcodes; g.x = xcodes; g.sw = wscale; g.sx = xscale; g.bias = bias; g.out = out;
-  g.m = m; g.n = n; g.k = k;
-  g.f16 = dtype == QLORA_F16;
+  qlora::Int8GemmArgs g = product_args(wcodes, wscale, n, k, xcodes, xscale, m, bias, out, dtype);
   if (part && part_bytes >= qlora::int8_part_bytes(m, n, k, cus)) g.part = static_cast<int32_t*>(part);
   return done(qlora::launch_int8_gemm(g, cus, stream), "int8 product launch");
+}
+
+// The arguments of a product whose rows are quantized already.
+int check_rows_product(const qlora_int8_weight* w, const int8_t* codes, const float* scale, int64_t M,
+                       const uint16_t* bias, const uint16_t* Y, int dtype, const void* ws) {
+  int st;
+  if ((st = check_int8_weight(w)) || (st = check_dim(M, "M")) || (st = check_type(dtype, false))) return st;
+  if (M == 0 || w->n_out == 0) return QLORA_OK;
+  if ((st = check_buffer(codes, w->k_in > 0, "codes")) || (st = check_buffer(scale, true, "scale")) ||
+      (st = check_buffer(Y, true, "Y")))
+    return st;
+  if (bias && (st = check_buffer(bias, true, "bias"))) return st;
+  if (ws && !aligned16(ws)) return fail(QLORA_ERR_ALIGN, "workspace must be 16-byte aligned");
+  return QLORA_OK;
 }
 
 // Workspace of a product that quantizes its rows: [codes][scales][split sums].
@@ -285,13 +305,8 @@ int qlora_int8_linear_rows(const qlora_int8_weight* w, const int8_t* codes, cons
                            hipStream_t stream) {
   return guarded([&] {
     int st;
-    if ((st = check_int8_weight(w)) || (st = check_dim(M, "M")) || (st = check_type(dtype, false))) return st;
+    if ((st = check_rows_product(w, codes, scale, M, bias, Y, dtype, ws))) return st;
     if (M == 0 || w->n_out == 0) return (int)QLORA_OK;
-    if ((st = check_buffer(codes, w->k_in > 0, "codes")) || (st = check_buffer(scale, true, "scale")) ||
-        (st = check_buffer(Y, true, "Y")))
-      return st;
-    if (bias && (st = check_buffer(bias, true, "bias"))) return st;
-    if (ws && !aligned16(ws)) return fail(QLORA_ERR_ALIGN, "workspace must be 16-byte aligned");
     return product(w->codes, w->scale, w->n_out, w->k_in, codes, scale, M, bias, Y, dtype, ws, ws_bytes, stream);
   });
 }
@@ -310,6 +325,42 @@ int qlora_int8_linear_bwd(const qlora_int8_weight* w, const void* dY, int64_t ld
     // the channels' scales belong to the reduction here: they go into dY
     return quantized_product(w->codes_t, nullptr, w->scale, w->k_in, w->n_out, dY, lddy, M, nullptr, dX, dtype, ws,
                              ws_bytes, stream);
+  });
+}
+
+int qlora_int8_plan(int op, int64_t M, int64_t n_out, int64_t k_in, int compute_units, int64_t out[3]) {
+  return guarded([&] {
+    if (!out) return fail(QLORA_ERR_INVALID_ARG, "out is NULL");
+    if (op != QLORA_OP_FWD && op != QLORA_OP_BWD) return fail(QLORA_ERR_INVALID_ARG, "unknown op");
+    int st;
+    if ((st = check_dim(M, "M")) || (st = check_dim(n_out, "n_out")) || (st = check_dim(k_in, "k_in"))) return st;
+    const int64_t n = op == QLORA_OP_FWD ? n_out : k_in, k = op == QLORA_OP_FWD ? k_in : n_out;
+    const qlora::Int8Plan p =
+        qlora::int8_plan(M, n, k, compute_units > 0 ? compute_units : qlora::device_compute_units());
+    out[0] = qlora::int8_tokens(p.kind);
+    out[1] = p.ksplit;
+    out[2] = qlora::int8_fuses_rows(M, n, k);
+    return (int)QLORA_OK;
+  });
+}
+
+int qlora_debug_int8_linear_rows(const qlora_int8_weight* w, const int8_t* codes, const float* scale, int64_t M,
+                                 const uint16_t* bias, uint16_t* Y, int dtype, int tokens, int splits, void* ws,
+                                 size_t ws_bytes, hipStream_t stream) {
+  return guarded([&] {
+    int st;
+    if ((st = check_rows_product(w, codes, scale, M, bias, Y, dtype, ws))) return st;
+    qlora::Int8Plan p{};
+    for (const qlora::Int8Kind kind : {qlora::kInt8Few16, qlora::kInt8Few32, qlora::kInt8Few64, qlora::kInt8Tile})
+      if (qlora::int8_tokens(kind) == tokens) p = qlora::Int8Plan{kind, splits};
+    if (p.ksplit == 0 || splits < 1 || splits > 64)
+      return fail(QLORA_ERR_INVALID_ARG, "tokens must be 16, 32, 64 or 256, splits 1 to 64");
+    if (M == 0 || w->n_out == 0) return (int)QLORA_OK;
+    if (splits > 1 && (!ws || ws_bytes < qlora::int8_plan_bytes(p, M, w->n_out)))
+      return fail(QLORA_ERR_WORKSPACE, "int8 product workspace too small");
+    qlora::Int8GemmArgs g = product_args(w->codes, w->scale, w->n_out, w->k_in, codes, scale, M, bias, Y, dtype);
+    if (splits > 1) g.part = static_cast<int32_t*>(ws);
+    return done(qlora::launch_int8_plan(g, p, stream), "int8 product launch");
   });
 }
 

@@ -643,7 +643,7 @@ template <typename E>
 static hipError_t run_plan(Int8GemmArgs a, const Int8Plan& p, const QuantArgs* rows, hipStream_t st) {
   a.ksplit = a.part ? p.ksplit : 1;
   const bool tile = p.kind == kInt8Tile;
-  const int64_t bm = tile ? 256 : p.kind == kInt8Few16 ? 16 : p.kind == kInt8Few32 ? 32 : 64, bn = tile ? 128 : 32;
+  const int64_t bm = int8_tokens(p.kind), bn = tile ? 128 : 32;
   const int64_t tiles = (a.m + bm - 1) / bm * ((a.n + bn - 1) / bn);
   // tiles count in one dimension, of 2^32 threads: past that lie outputs of 0.5 TB
   if (tiles * a.ksplit > (tile ? (int64_t)INT_MAX / 128 : INT_MAX)) return hipErrorInvalidValue;

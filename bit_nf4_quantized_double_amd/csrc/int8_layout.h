@@ -108,6 +108,9 @@ struct Int8GemmArgs {  // out[m][n] = E(sx[m] sw[n] sum_k x[m][k] w[n][k] + bias
 // Which kernel a product takes, and over how many workgroups a tile's
 // reduction is split (needs `part`; without it one).
 enum Int8Kind { kInt8Few16, kInt8Few32, kInt8Few64, kInt8Tile };
+constexpr int int8_tokens(Int8Kind kind) {  // of a workgroup
+  return kind == kInt8Few16 ? 16 : kind == kInt8Few32 ? 32 : kind == kInt8Few64 ? 64 : 256;
+}
 struct Int8Plan {
   Int8Kind kind;
   int ksplit;

@@ -109,6 +109,13 @@ def workspace_bytes(op: int, m: int, n_out: int, k_in: int) -> int:
     return int(qlora.lib().qlora_int8_workspace_bytes(op, m, n_out, k_in))
 
 
+def plan(op: int, m: int, n_out: int, k_in: int, compute_units: int = 0) -> dict:
+    """How the library runs a product (qlora_int8_plan)."""
+    out = (ctypes.c_int64 * 3)()
+    qlora._check(qlora.lib().qlora_int8_plan(op, m, n_out, k_in, compute_units, out), "qlora_int8_plan")
+    return {"kernel": "tile" if out[0] == 256 else f"few{out[0]}", "splits": out[1], "quantizes_rows": bool(out[2])}
+
+
 def linear_fwd(w: Int8Weight, X, bias: torch.Tensor | None = None, *, Y: torch.Tensor | None = None,
                ws: torch.Tensor | None = None) -> torch.Tensor:
     """Y = X W^T + bias.  X: a bf16 or fp16 matrix [M, k_in], quantized on the
@@ -213,6 +220,8 @@ def _bind(L: ctypes.CDLL) -> None:
         "qlora_int8_dequant_weight": (i32, [W, vp, i32, vp]),
         "qlora_int8_linear_fwd": (i32, [W, vp, i64, i64, vp, vp, i32, vp, sz, vp]),
         "qlora_int8_linear_rows": (i32, [W, vp, vp, i64, vp, vp, i32, vp, sz, vp]),
+        "qlora_int8_plan": (i32, [i32, i64, i64, i64, i32, ctypes.POINTER(i64)]),
+        "qlora_debug_int8_linear_rows": (i32, [W, vp, vp, i64, vp, vp, i32, i32, i32, vp, sz, vp]),
         "qlora_int8_linear_bwd": (i32, [W, vp, i64, i64, vp, i32, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():

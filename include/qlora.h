@@ -466,6 +466,28 @@ int qlora_int8_linear_bwd(const qlora_int8_weight *w, const void *dY, int64_t ld
                           uint16_t *dX, int dtype, void *ws, size_t ws_bytes, hipStream_t stream);
 
 /*
+ * Host function: how the library runs the product of op (QLORA_OP_FWD, or
+ * QLORA_OP_BWD for dX) on a device with `compute_units` compute units (<= 0:
+ * the current device's).  out[0] = the tokens of a workgroup, which name the
+ * kernel: 16, 32 or 64 (few tokens) or 256 (tiles); out[1] = over how many
+ * workgroups a tile's reduction is split (1: unsplit; more need the workspace's
+ * room for split sums).  out[2] = 1 where a call on 16-bit rows quantizes them
+ * inside the product instead, with 16 tokens to a workgroup and unsplit.
+ * QLORA_ERR_INVALID_ARG for an unknown op, negative sizes or out == NULL.
+ */
+int qlora_int8_plan(int op, int64_t M, int64_t n_out, int64_t k_in, int compute_units, int64_t out[3]);
+
+/*
+ * Diagnostic: qlora_int8_linear_rows by a named kernel and split instead of
+ * the plan's.  `tokens` as out[0] above, 1 <= splits <= 64; with splits > 1 the
+ * workspace holds splits * M * (n_out rounded up to 8) int32.  The result is the
+ * same bit for bit whichever is named.
+ */
+int qlora_debug_int8_linear_rows(const qlora_int8_weight *w, const int8_t *codes, const float *scale,
+                                 int64_t M, const uint16_t *bias, uint16_t *Y, int dtype, int tokens,
+                                 int splits, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/*
  * RMS norm with the residual's addition:
  *     h = E(x + residual)  (h = x without a residual: H is then not written)
  *     y = h gamma rstd,  rstd = 1 / sqrt(mean_k h^2 + eps), in fp32
