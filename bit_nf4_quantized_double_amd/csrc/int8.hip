@@ -136,12 +136,15 @@ __device__ __forceinline__ void tile_of(uint32_t lin, uint32_t mt, uint32_t nt, 
 // token rows, which no other wave needs, straight into registers, one step
 // ahead.  The two workgroups of a compute unit move 96 KB a step through the
 // cache and 160 KB through LDS (32 in, 128 out) in 2048 matrix-core cycles:
-// neither is the bound.
+// neither is the bound by its rate.
 //
-// Power is: 8192 x 14336 x 4096 runs at 1.9 to 2.0 GHz with the matrix cores
-// busy 61 % of the cycles (377 us, 2.55 PFLOP/s).  The loop without any loads
-// takes 237 us, and 307 us with 32 x 32 x 32 MFMAs, whose accumulators move
-// twice the registers for the same products.  Tiles of 256 x 256 (8 waves, one
+// 8192 x 14336 x 4096 takes 384 us (2.5 PFLOP/s): 734 thousand cycles at 1.91
+// GHz, the matrix cores busy 62 % of them.  The loop without any loads takes 237
+// us at 2.18 GHz, so two things cost: waves that wait for an operand or for
+// their turn to issue (about 100 us; half of all wave cycles), and the clock,
+// which the power limit lowers under this load (about 45 us).  With 32 x 32 x 32
+// MFMAs, whose accumulators move twice the registers for the same products, the
+// loop without loads takes 307 us.  Tiles of 256 x 256 (8 waves, one
 // workgroup a compute unit) take 402 us where these take 392: less traffic, but
 // nothing runs beside their epilogue.  128 x 128: 448 us.  8 waves of 64 x 64
 // where a tile has its compute unit to itself: 4 % less or more, by the shape.
@@ -279,7 +282,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   }
   constexpr int kAcross = 2 * NS;  // 16-byte pieces of a token's outputs
   // Whole lines are not kept in the second-level cache, which the operands need
-  // (8192 x 14336 x 4096: 373 us against 384); where rows start inside a line,
+  // (8192 x 14336 x 4096: 3 % less time); where rows start inside a line,
   // that cache has to put the parts together (3549 x 26474 x 224: 59 us, 94
   // without it).
   const bool stream = a.n % 64 == 0;
@@ -537,7 +540,8 @@ __global__ __launch_bounds__(256) void k_int8_transpose(const int8_t* src, int64
 }
 
 // Tiles back to a row-major 16-bit matrix of the values they stand for; bound by
-// memory (8192 x 4096: 18 us, 5.5 TB/s).
+// memory (8192 x 4096: 20 to 22 us, 4.7 to 5.0 TB/s; 18 us on codes that were just
+// written).
 template <typename E>
 __global__ __launch_bounds__(256) void k_int8_dequant(const int8_t* codes, const float* scale, int64_t m, int64_t k,
                                                       bool weight, uint16_t* out) {
@@ -587,7 +591,7 @@ __global__ __launch_bounds__(256) void k_int8_dequant(const int8_t* codes, const
 //           weight at no more than 5.5 TB/s.
 //           72 x 4096 x 4096: 8 us, as tiles 28 us (15 us with 4 splits).
 //   tiles   256 x 128, two workgroups a compute unit: 1.72 us a step of 128
-//           columns with two, 0.82 us with one.  8192 x 14336 x 4096: 373 us;
+//           columns with two, 0.82 us with one.  8192 x 14336 x 4096: 384 us;
 //           1024 x 11008 x 4096: 50 us, few tokens' kernel 90 us.
 //   either  writes its output at no more than 3.5 TB/s.
 //   split   a launch more (3 us), and the int32 sums written and read at
@@ -634,7 +638,10 @@ size_t int8_part_bytes(int64_t m, int64_t n, int64_t k, int cus) { return int8_p
 
 // The quantizer inside the product costs each workgroup 2.9 us for 32768 values,
 // and a launch of its own about as much: worth it while the workgroups, one for
-// each 32 outputs, are few or the values are.
+// each 32 outputs, are few or the values are.  This form has no split, and needs
+// none: one token, 1024 outputs and a reduction of 28672 take 12.9 us on the GPU,
+// quantizer, product split 4 ways and their sum 13.3 (4.1 + 6.5 + 2.7), and a
+// call 12.6 us for 19.9.
 bool int8_fuses_rows(int64_t m, int64_t n, int64_t k) {
   return m <= 16 && k >= 16 && m * int8_kp(k) <= kFusedValues && (n + 31) / 32 * m * int8_kp(k) <= 256 * kFusedValues;
 }

@@ -195,16 +195,19 @@ struct NormSrc {
 // change lanes before they are stored, so that neighbouring lanes hold
 // neighbouring rows and store runs of 64 bytes, while the loads stay runs of
 // 512 bytes of one row.  SwiGLU at 8192 x 14336: 130 us, 163 us with a row to
-// a workgroup.  Rows interleaved by lanes instead, for loads and stores alike,
-// do as well at aligned widths, and take 107 us for 57 at 8192 x 7167.
+// a workgroup (two sets of inputs in turn, in part from the last-level cache).
+// Rows interleaved by lanes instead, for loads and stores alike, do as well at
+// aligned widths, and take 107 us for 57 at 8192 x 7167.
 //
-// Measured in bf16 at 8192 x 4096, where a copy of one input takes 24 us (5.6
-// TB/s): quantize 20 us (5.1 TB/s), SwiGLU in 8 bits 31 us (5.5), norm with the
-// residual 45 us (5.9), the same in 8 bits 41 us (5.7).  Rows of 14336 are 1024
-// threads to a workgroup and one of those to a compute unit, so loads and
-// stores take turns: 4.4 to 4.5 TB/s.  Walking over the rows, with the next
-// ones loaded into the registers that finished pieces leave, spills: SwiGLU
-// 175 us for 131.
+// Measured in bf16 at 8192 x 4096 on fresh inputs, median times of the kernel:
+// quantize 19 us (5.2 TB/s), SwiGLU in 8 bits 32 us (5.2), norm with the
+// residual 45 us (5.9), the same in 8 bits 42 us (5.6; 47 us with the values
+// read back between the calls).  Rows of 14336 are 1024 threads to a workgroup
+// and one of those to a compute unit, so loads and stores take turns: SwiGLU at
+// 8192 x 14336 144 to 150 us (4.0 TB/s).  Walking over the rows, with the next
+// ones loaded into the registers that finished pieces leave, spills: 175 us for
+// 131 under the conditions of the 130 above.  The norm with four pieces a
+// thread spills 3 registers as it is: 2048 x 16384 56 us, in 16 bits 46 us.
 template <int TPR, int RW> constexpr int kBlock = TPR * RW < 256 ? 256 : TPR * RW;
 
 template <typename Src, int TPR, int RW, int NCH, bool WIDE, bool Y16, typename T>
@@ -394,8 +397,11 @@ hipError_t norm_typed(const NormArgs& a, int cus, hipStream_t st) {
 // k_norm_dgamma adds those up in a fixed order.  No atomics: the same inputs
 // give the same bits.  The next row's h and dY are loaded before the current
 // row's reduction, whose latency would otherwise bound the kernel; they stay
-// packed in pairs.  8192 x 4096: 55 us (4.9 TB/s); without the loads ahead, four
-// rows to a workgroup's turn, 70 us.
+// packed in pairs.  8192 x 4096: 56 us (4.8 TB/s); without the loads ahead, four
+// rows to a workgroup's turn, 70 us.  Every instance is short of registers: with
+// one piece a thread 8 to 13 of them are spilled, 12 to 20 with gamma in fp32,
+// most of them reloaded once a turn (8192 x 4096 with gamma in fp32: 62 us; 2048
+// x 16384: 61 and 73 us); with two pieces 61 and 123.
 template <typename T, typename G, int TPR, int NCH, bool WIDE>
 __global__ __launch_bounds__(1024) void k_norm_bwd(Mat<T> dy, Mat<T> h, Mat<T> dh, Mat<G> gamma, const float* rstd,
                                                    Out16 dx, float* part, float* dgamma, int64_t m, int64_t k) {
@@ -432,7 +438,7 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(Mat<T> dy, Mat<T> h, Mat<T> d
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[j][i] = 0.f;
   }
-  constexpr bool AHEAD = NCH == 1;  // two pieces a thread and the next row's would spill
+  constexpr bool AHEAD = NCH == 1;  // two pieces a thread and the next row's would spill far more
   Piece<T> hp[NCH], dp[NCH], hn[NCH], dn[NCH], ep[NCH];
   int64_t row = (int64_t)blockIdx.x * SUB + sub;
 #pragma unroll
@@ -627,7 +633,7 @@ hipError_t norm_bwd_typed(const NormBwdArgs& a, int cus, hipStream_t st) {
 
 // ---- SwiGLU in 16 bits, elementwise -----------------------------------------
 // 16 values a thread; `per` pieces in a row.  8192 x 4096 in bf16: forward 32 us
-// (6.3 TB/s), backward 61 us (5.5).
+// (6.3 TB/s), backward 57 us (5.9).
 template <typename T>
 __global__ __launch_bounds__(256) void k_swiglu(SwigluSrc<T> s, Out16 y, uint32_t per, uint32_t total, int64_t k) {
   const uint32_t id = blockIdx.x * 256u + threadIdx.x;

@@ -383,8 +383,10 @@ int qlora_format_table(int format, float out[16]);
  * `dtype` is the element type of 16-bit inputs and outputs (QLORA_BF16 or
  * QLORA_F16; QLORA_F32 where said).  Inputs marked [M, K] (ld) are row-major
  * with rows `ld` elements apart (ld >= K) and need only be aligned to their
- * element size; rows that are 16-byte aligned are read faster.  Outputs are
- * contiguous and 16-byte aligned.  Any M and K from 0 on; sizes that leave
+ * element size; rows that are 16-byte aligned are read faster.  gamma and
+ * col_scale are aligned to their element size too.  Outputs, codes and the other
+ * vectors (scales, rstd, bias) are contiguous and 16-byte aligned.  Any M and K
+ * from 0 on (M ceil(K / 16) below 2^32 - 256 for 16-bit SwiGLU); sizes that leave
  * nothing to do are no-ops.
  *
  * Quantized rows.  A row x of K values becomes int8 codes and one fp32 scale:
@@ -450,9 +452,12 @@ int qlora_int8_dequant_rows(const int8_t *codes, const float *scale, int64_t M, 
  *                           dY[m][n] scale[n]: the gradient of the forward with its rounding to 8 bits passed
  *                           straight through.  Needs codes_t.  There is no dW: the weight is frozen.
  * Workspace: qlora_int8_workspace_bytes(QLORA_OP_FWD / _BWD, M, n_out, k_in),
- * and qlora_int8_rows_workspace_bytes for _rows; 0 for few tokens, which need
- * none.  The part for split sums is optional (without room the product runs
- * unsplit, with the same result).
+ * and qlora_int8_rows_workspace_bytes for _rows.  It is 0 only where nothing is
+ * needed: for _fwd and _bwd where the rows are quantized inside the product
+ * (some calls of up to 16 tokens, not all), for _rows where the reduction is not
+ * split.  Its part for split sums, all of it for _rows, is optional (without
+ * room the product runs unsplit, with the same result); the rest is not
+ * (QLORA_ERR_WORKSPACE).
  */
 size_t qlora_int8_workspace_bytes(int op, int64_t M, int64_t n_out, int64_t k_in);
 size_t qlora_int8_rows_workspace_bytes(int64_t M, int64_t n_out, int64_t k_in);
@@ -490,7 +495,7 @@ int qlora_debug_int8_linear_rows(const qlora_int8_weight *w, const int8_t *codes
 /*
  * RMS norm with the residual's addition:
  *     h = E(x + residual)  (h = x without a residual: H is then not written)
- *     y = h gamma rstd,  rstd = 1 / sqrt(mean_k h^2 + eps), in fp32
+ *     y = h gamma rstd,  rstd = 1 / sqrt(mean_k h^2 + eps), in fp32, h gamma first
  * h is rounded to 16 bits because it is stored so, and the norm is of the
  * stored values.  gamma: [K], of the rows' type or fp32 (gamma_dtype).  eps
  * at least 1e-12.  K <= QLORA_MAX_NORM_WIDTH.  H may be X or the residual

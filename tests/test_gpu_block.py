@@ -94,6 +94,8 @@ def test_refusals():
         block.MLPBlock(rand((64, 128), 1, torch.float32), rand((64, 128), 1, torch.float32), rand((64, 128), 1, torch.float32))
 
 
+# At these sizes all three numbers of tokens take the few tokens' kernel, on rows
+# that the norm and SwiGLU wrote; tiles in a graph: test_gpu_int8_plans.py.
 def test_served_block_in_a_graph():
     """Captured once, replayed on new inputs: every replay is the eager result,
     with eager work in between (1 token: quantized inside the product; 40: its

@@ -17,7 +17,9 @@ pytestmark = pytest.mark.gpu
 BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
 
 # (M, n_out, k_in): one of each; ragged tiles of outputs, tokens and the
-# reduction; each kernel and its edges (16, 17, 64, 65 tokens); splits
+# reduction; the few tokens' kernels and their edges (16, 17, 64, 65 tokens),
+# which the plan takes for all of these forwards (tiles and splits:
+# test_gpu_int8_plans.py)
 SHAPES = [(1, 1, 1), (1, 33, 64), (2, 31, 100), (5, 130, 129), (16, 256, 256), (17, 64, 128), (16, 1000, 2500),
           (33, 96, 1000), (64, 520, 4096), (65, 520, 512), (100, 260, 300), (128, 128, 128), (150, 1000, 2500),
           (257, 513, 640), (300, 4096, 1024), (512, 256, 8192), (1, 8192, 4096), (3, 256, 28672), (700, 130, 65)]

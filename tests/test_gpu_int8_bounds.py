@@ -1,6 +1,8 @@
 """The row-wise operators and the int8 product through the bounds-checked
 build (libqlora_checked.so): the same bits as the normal build, and no access
-outside a buffer.  Shapes: every kernel at ragged and at whole tiles."""
+outside a buffer.  Shapes: ragged ones and whole tiles of the few tokens'
+kernels (tiles and splits: test_gpu_int8_plans.py), and rows of each width class
+in small numbers (many rows: test_gpu_rows_many.py)."""
 
 import pytest
 import torch
