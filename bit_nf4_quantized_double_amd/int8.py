@@ -180,8 +180,9 @@ class Int8LinearFunction(torch.autograd.Function):
         if X.shape[-1] != w.k_in:  # a reshape to rows of k_in values could hide it
             raise ValueError(f"X has {X.shape[-1]} columns, the weight {w.k_in}")
         ctx.xshape = X.shape
-        Y = linear_fwd(w, rows._rows_of(X, w.k_in), bias)
-        return Y.reshape(*X.shape[:-1], w.n_out)
+        Y = rows._new((*X.shape[:-1], w.n_out), X)
+        linear_fwd(w, rows._rows_of(X, w.k_in), bias, Y=rows._rows_of(Y, w.n_out))
+        return Y
 
     @staticmethod
     @qlora._once

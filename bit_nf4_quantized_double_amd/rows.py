@@ -280,6 +280,10 @@ def _rows_of(t: torch.Tensor, width: int) -> torch.Tensor:
     return t if (width <= 1 or t.stride(1) == 1) and (t.shape[0] <= 1 or t.stride(0) >= width) else t.contiguous()
 
 
+def _new(shape, like: torch.Tensor) -> torch.Tensor:
+    return torch.empty(shape, dtype=like.dtype, device=like.device)
+
+
 def _same_shape(t, shape, name: str) -> None:
     """Before anything is reshaped to a matrix: afterwards a tensor of another
     shape may have as many rows, and would be paired up wrongly."""
@@ -299,23 +303,24 @@ class RMSNormFunction(torch.autograd.Function):
         k = X.shape[-1]
         X2 = _rows_of(X, k)
         R2 = None if residual is None else _rows_of(residual, k)
-        Y, H, rstd = rms_norm_fwd(X2, gamma, eps, R2)
-        ctx.save_for_backward(H, rstd, gamma)
+        # outputs are made in their own shape: views of others could not be modified in place
+        Y = _new(X.shape, X)
+        h = None if residual is None else _new(X.shape, X)
+        _, H, rstd = rms_norm_fwd(X2, gamma, eps, R2, H=None if h is None else _rows_of(h, k), Y=_rows_of(Y, k))
+        ctx.save_for_backward(H if h is None else h, rstd, gamma)
         ctx.has_residual = residual is not None
         # an output that nothing reads has no gradient: it comes as None, not as a tensor of zeros
         ctx.set_materialize_grads(False)
-        # without a residual h is X: a view of it would be an input returned as an output
-        h = H.reshape(X.shape) if residual is not None else None
-        return Y.reshape(X.shape), h
+        return Y, h  # without a residual h is X, which is not returned as an output
 
     @staticmethod
     @qlora._once
     def backward(ctx, dY, dh):
-        H, rstd, gamma = ctx.saved_tensors
-        k = H.shape[-1]
+        h, rstd, gamma = ctx.saved_tensors
+        k = h.shape[-1]
         if dY is None:  # h alone is read: its gradient passes through
             return dh, (dh if ctx.has_residual else None), (torch.zeros_like(gamma) if ctx.needs_input_grad[2] else None), None
-        dX, dgamma = rms_norm_bwd(_rows_of(dY, k), H, rstd, gamma, None if dh is None else _rows_of(dh, k))
+        dX, dgamma = rms_norm_bwd(_rows_of(dY, k), _rows_of(h, k), rstd, gamma, None if dh is None else _rows_of(dh, k))
         dX = dX.reshape(dY.shape)
         return dX, (dX if ctx.has_residual else None), (dgamma.to(gamma.dtype) if ctx.needs_input_grad[2] else None), None
 
@@ -343,7 +348,9 @@ class SwiGLUFunction(torch.autograd.Function):
         k = G.shape[-1]
         G2, U2 = _rows_of(G, k), _rows_of(U, k)
         ctx.save_for_backward(G2, U2)
-        return swiglu_fwd(G2, U2).reshape(G.shape)
+        Y = _new(G.shape, G)
+        swiglu_fwd(G2, U2, Y=_rows_of(Y, k))
+        return Y
 
     @staticmethod
     @qlora._once

@@ -102,3 +102,23 @@ def test_no_rows_and_rows_of_no_values():
         rows_in = out.numel() // 40
         assert out.shape == (*shape[:-1], 40) and x.grad.shape == shape
         assert torch.equal(out, lin.bias.detach().expand(out.shape)) and (lin.bias.grad == rows_in).all()
+
+
+@pytest.mark.parametrize("shape", [(6, 64), (2, 3, 64)])
+def test_outputs_modified_in_place(shape):
+    """What a form returns is a tensor of its own: it can be changed in place
+    where no gradient needs it, and where one does (h) the backward says so."""
+    need_gpu()
+    x, r = rand(shape, 1).requires_grad_(), rand(shape, 2).requires_grad_()
+    norm = rows.RMSNorm(64, EPS)
+    lin = int8.Int8Linear(rand((64, 64), 3, F32, 0.02), rand((64,), 4), transposed=True)
+    d = rand(shape, 5)
+    for call in (lambda: norm(x), lambda: norm(x, r)[0], lambda: rows.swiglu(x, r), lambda: lin(x)):
+        want = torch.autograd.grad(call(), x, 2 * d)[0]
+        y = call()
+        y.mul_(2)
+        assert torch.equal(torch.autograd.grad(y, x, d)[0], want)
+    y, h = norm(x, r)
+    h.add_(1)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward(d)
