@@ -331,21 +331,23 @@ def _plain_loss(s):
 # ---- through the package ---------------------------------------------------------------------------------------
 
 def _run_own(s):
-    from bit_nf4_quantized_double_amd import attention, cross_entropy, rotary
     op = s["op"]
     if op in ("rotate", "rotate_train"):
+        from bit_nf4_quantized_double_amd import rotary
         q, k = rotary.rotate(s["q"], s["k"], s["positions"], s["freqs"], interleaved=s["interleaved"])
         if op == "rotate":
             return {"q": q, "k": k}
         dq, dk = rotary.rotate_bwd(s["dq"], s["dk"], s["positions"], s["freqs"], interleaved=s["interleaved"])
         return {"q": q, "k": k, "dq": dq, "dk": dk}
-    if op == "score":
-        loss, lse = cross_entropy.linear_cross_entropy_fwd(s["x"], s["w"], s["targets"], ignore_index=IGNORE)
-        return {"loss": loss, "lse": lse}
-    if op == "loss_train":
+    if op in ("score", "loss_train"):
+        from bit_nf4_quantized_double_amd import cross_entropy
+        if op == "score":
+            loss, lse = cross_entropy.linear_cross_entropy_fwd(s["x"], s["w"], s["targets"], ignore_index=IGNORE)
+            return {"loss": loss, "lse": lse}
         loss, lse, dx = cross_entropy.linear_cross_entropy_grad(s["x"], s["w"], s["targets"], s["dloss"],
                                                                 ignore_index=IGNORE)
         return {"loss": loss, "lse": lse, "dx": dx}
+    from bit_nf4_quantized_double_amd import attention
     o, lse = attention.attention_fwd(s["q"], s["k"], s["v"], s["cu_q"], s["cu_k"], lengths_k=s.get("lengths_k"),
                                      causal=s["causal"])
     if op != "attend_train":
