@@ -1,0 +1,229 @@
+// extern "C" entry points of rotary positions, attention and the head's loss:
+// argument checks on the host, workspace layout and the launch sequence on
+// the caller's stream.  Declarations and contracts: include/qlora.h.
+#include <climits>
+#include <cmath>
+#include <exception>
+
+#include "../../include/qlora.h"
+#include "abi.h"
+#include "common.h"
+#include "decoder.h"
+
+namespace {
+
+using qlora::aligned16;
+using qlora::fail;
+using qlora::hip_fail;
+using qlora::round_up;
+
+// No exception leaves a C entry point (building a message can run out of memory).
+template <typename F>
+int guarded(F f) noexcept {
+  try {
+    return f();
+  } catch (...) {
+    return QLORA_ERR_HIP;
+  }
+}
+
+int done(hipError_t e, const char* where) { return e == hipSuccess ? QLORA_OK : hip_fail(e, where); }
+
+int check_range(int64_t v, int64_t most, const char* name) {
+  if (v < 0) return fail(QLORA_ERR_INVALID_ARG, std::string(name) + " is negative");
+  if (v > most) return fail(QLORA_ERR_SHAPE, std::string(name) + " exceeds " + std::to_string(most));
+  return QLORA_OK;
+}
+
+int check_type16(int dtype) {
+  if (dtype == QLORA_BF16 || dtype == QLORA_F16) return QLORA_OK;
+  return fail(QLORA_ERR_INVALID_ARG, "unsupported element type");
+}
+
+constexpr int64_t kMostStride = (int64_t)1 << 40;
+
+// [tokens, heads, d]: there, aligned to `align` bytes, its strides multiples of
+// that, and for an output without two elements in one place.
+int check_heads(const qlora_heads* x, int64_t tokens, int64_t heads, int64_t d, int align, bool out, const char* name) {
+  if (tokens == 0 || heads == 0 || d == 0) return QLORA_OK;
+  if (!x || !x->p) return fail(QLORA_ERR_INVALID_ARG, std::string(name) + " is NULL");
+  const int64_t t = tokens > 1 ? x->token_stride : 0, h = heads > 1 ? x->head_stride : 0;
+  if (t < 0 || h < 0) return fail(QLORA_ERR_INVALID_ARG, std::string(name) + ": negative stride");
+  if (t > kMostStride || h > kMostStride) return fail(QLORA_ERR_SHAPE, std::string(name) + ": a stride exceeds 2^40 elements");
+  if (reinterpret_cast<uintptr_t>(x->p) % align || t * 2 % align || h * 2 % align)
+    return fail(QLORA_ERR_ALIGN, std::string(name) + " and its strides must be multiples of " + std::to_string(align) + " bytes");
+  if (out) {
+    const bool by_token = (heads == 1 || h >= d) && (tokens == 1 || t >= (heads - 1) * h + d);
+    const bool by_head = (tokens == 1 || t >= d) && (heads == 1 || h >= (tokens - 1) * t + d);
+    if (!by_token && !by_head) return fail(QLORA_ERR_INVALID_ARG, std::string(name) + ": an output's elements overlap");
+  }
+  return QLORA_OK;
+}
+
+qlora::Heads heads_arg(const qlora_heads* x, int64_t tokens, int64_t heads, int64_t d) {
+  if (tokens == 0 || heads == 0 || d == 0) return qlora::Heads{nullptr, 0, 0, 0};
+  return qlora::heads_of(x->p, tokens > 1 ? x->token_stride : 0, heads > 1 ? x->head_stride : 0, tokens, heads, d);
+}
+
+int check_attention(const qlora_attention* a) {
+  if (!a) return fail(QLORA_ERR_INVALID_ARG, "attention descriptor is NULL");
+  const int64_t most = INT_MAX - 255;
+  int st;
+  if ((st = check_range(a->tokens_q, most, "tokens_q")) || (st = check_range(a->tokens_k, most, "tokens_k")) ||
+      (st = check_range(a->batch, 1 << 24, "batch")) || (st = check_range(a->heads, 65536, "heads")) ||
+      (st = check_range(a->kv_heads, 65536, "kv_heads")) ||
+      (st = check_range(a->head_dim, QLORA_MAX_HEAD_DIM, "head_dim")) || (st = check_type16(a->dtype)))
+    return st;
+  if (a->head_dim % 8 || a->head_dim == 0) return fail(QLORA_ERR_SHAPE, "head_dim must be a positive multiple of 8");
+  if (a->kv_heads == 0 ? a->heads != 0 : a->heads % a->kv_heads != 0)
+    return fail(QLORA_ERR_SHAPE, "heads must be a multiple of kv_heads");
+  if (!(a->scale > 0.f) || !std::isfinite(a->scale)) return fail(QLORA_ERR_INVALID_ARG, "scale must be positive and finite");
+  if (!a->cu_q || !a->cu_k) return fail(QLORA_ERR_INVALID_ARG, "cu_q or cu_k is NULL");
+  for (const int32_t* p : {a->cu_q, a->cu_k, a->len_q, a->len_k})
+    if (reinterpret_cast<uintptr_t>(p) % 4) return fail(QLORA_ERR_ALIGN, "cu_q, cu_k, len_q and len_k must be 4-byte aligned");
+  if (a->heads) {
+    const int64_t group = a->heads / a->kv_heads;
+    if (a->tokens_q > most / group) return fail(QLORA_ERR_SHAPE, "tokens_q * heads / kv_heads exceeds 2^31 - 256");
+    // workgroups of a launch: fewer than 2^24
+    if (((a->tokens_q * group + 31) / 32 + a->batch + 2) * a->kv_heads >= (1 << 24) ||
+        ((a->tokens_k + 127) / 128 + a->batch + 2) * a->kv_heads >= (1 << 24))
+      return fail(QLORA_ERR_SHAPE, "too many rows for one launch");
+  }
+  return QLORA_OK;
+}
+
+qlora::AttnArgs attention_args(const qlora_attention* a) {
+  qlora::AttnArgs g{};
+  g.cu_q = a->cu_q; g.cu_k = a->cu_k; g.len_q = a->len_q; g.len_k = a->len_k;
+  g.tq = a->tokens_q; g.tk = a->tokens_k; g.batch = (int32_t)a->batch;
+  g.heads = (int32_t)a->heads; g.kv_heads = (int32_t)a->kv_heads; g.group = (int32_t)(a->heads / a->kv_heads);
+  g.d = (int32_t)a->head_dim; g.splits = 1;
+  g.scale = a->scale; g.causal = a->causal != 0; g.zero_rest = a->zero_rest != 0; g.f16 = a->dtype == QLORA_F16;
+  return g;
+}
+
+bool nothing(const qlora_attention* a) { return a->heads == 0 || a->tokens_q + a->tokens_k == 0; }
+
+qlora::AttnPlan plan_of(const qlora_attention* a, int cus) {
+  return qlora::attn_plan(a->tokens_q, a->tokens_k, a->batch, a->heads, a->kv_heads, cus);
+}
+
+size_t delta_bytes(const qlora_attention* a) { return round_up((size_t)a->tokens_q * (size_t)a->heads * 4u); }
+
+}  // namespace
+
+extern "C" {
+
+int qlora_rope(const qlora_heads* Q, int64_t heads, const qlora_heads* K, int64_t kv_heads, int64_t tokens,
+               int64_t head_dim, int64_t rot, int interleaved, const void* positions, int positions64,
+               const uint64_t* turns, float factor, int inverse, const qlora_heads* Qo, const qlora_heads* Ko, int dtype,
+               hipStream_t stream) {
+  return guarded([&] {
+    int st;
+    if ((st = check_range(heads, 65536, "heads")) || (st = check_range(kv_heads, 65536, "kv_heads")) ||
+        (st = check_range(tokens, INT_MAX, "tokens")) || (st = check_range(head_dim, 65536, "head_dim")) ||
+        (st = check_type16(dtype)))
+      return st;
+    if (rot < 0 || rot % 2 || rot > head_dim) return fail(QLORA_ERR_SHAPE, "rot must be even and at most head_dim");
+    if (!std::isfinite(factor)) return fail(QLORA_ERR_INVALID_ARG, "factor must be finite");
+    if ((st = check_heads(Q, tokens, heads, head_dim, 2, false, "Q")) ||
+        (st = check_heads(K, tokens, kv_heads, head_dim, 2, false, "K")) ||
+        (st = check_heads(Qo, tokens, heads, head_dim, 2, true, "Qo")) ||
+        (st = check_heads(Ko, tokens, kv_heads, head_dim, 2, true, "Ko")))
+      return st;
+    if (tokens == 0 || heads + kv_heads == 0 || head_dim == 0) return (int)QLORA_OK;
+    if (rot > 0) {
+      if (!positions || !turns) return fail(QLORA_ERR_INVALID_ARG, "positions or turns is NULL");
+      if (reinterpret_cast<uintptr_t>(positions) % (positions64 ? 8 : 4) || reinterpret_cast<uintptr_t>(turns) % 8)
+        return fail(QLORA_ERR_ALIGN, "positions and turns must be aligned to their element size");
+    }
+    qlora::RopeArgs a{};
+    a.q = heads_arg(Q, tokens, heads, head_dim); a.qo = heads_arg(Qo, tokens, heads, head_dim);
+    a.k = heads_arg(K, tokens, kv_heads, head_dim); a.ko = heads_arg(Ko, tokens, kv_heads, head_dim);
+    a.t = tokens; a.heads = (int32_t)heads; a.kv_heads = (int32_t)kv_heads; a.d = (int32_t)head_dim; a.rot = (int32_t)rot;
+    a.positions = positions; a.turns = turns; a.factor = factor;
+    a.pos64 = positions64 != 0; a.interleaved = interleaved != 0; a.inverse = inverse != 0; a.f16 = dtype == QLORA_F16;
+    return done(qlora::launch_rope(a, stream), "rotary positions launch");
+  });
+}
+
+size_t qlora_attention_workspace_bytes(int op, const qlora_attention* a) {
+  size_t n = 0;
+  guarded([&] {
+    if (check_attention(a) != QLORA_OK || nothing(a)) return (int)QLORA_OK;
+    if (op == QLORA_OP_FWD)
+      n = qlora::attn_part_bytes(plan_of(a, qlora::device_compute_units()), a->tokens_q, a->heads, a->head_dim);
+    else if (op == QLORA_OP_BWD)
+      n = delta_bytes(a) + 2 * qlora::kAttnTops * 4u;
+    return (int)QLORA_OK;
+  });
+  return n;
+}
+
+int qlora_attention_plan(const qlora_attention* a, int compute_units, int64_t out[2]) {
+  return guarded([&] {
+    if (!out) return fail(QLORA_ERR_INVALID_ARG, "out is NULL");
+    int st;
+    if ((st = check_attention(a))) return st;
+    const qlora::AttnPlan p = plan_of(a, compute_units > 0 ? compute_units : qlora::device_compute_units());
+    out[0] = p.rows;
+    out[1] = p.splits;
+    return (int)QLORA_OK;
+  });
+}
+
+int qlora_attention_fwd(const qlora_attention* a, const qlora_heads* Q, const qlora_heads* K, const qlora_heads* V,
+                        const qlora_heads* O, float* lse, void* ws, size_t ws_bytes, hipStream_t stream) {
+  return guarded([&] {
+    int st;
+    if ((st = check_attention(a))) return st;
+    const int64_t d = a->head_dim;
+    if ((st = check_heads(Q, a->tokens_q, a->heads, d, 16, false, "Q")) ||
+        (st = check_heads(K, a->tokens_k, a->kv_heads, d, 16, false, "K")) ||
+        (st = check_heads(V, a->tokens_k, a->kv_heads, d, 16, false, "V")) ||
+        (st = check_heads(O, a->tokens_q, a->heads, d, 16, true, "O")))
+      return st;
+    if (nothing(a) || a->tokens_q == 0) return (int)QLORA_OK;
+    if (!lse) return fail(QLORA_ERR_INVALID_ARG, "lse is NULL");
+    if (!aligned16(lse)) return fail(QLORA_ERR_ALIGN, "lse must be 16-byte aligned");
+    if (ws && !aligned16(ws)) return fail(QLORA_ERR_ALIGN, "workspace must be 16-byte aligned");
+    qlora::AttnArgs g = attention_args(a);
+    g.q = heads_arg(Q, a->tokens_q, a->heads, d); g.k = heads_arg(K, a->tokens_k, a->kv_heads, d);
+    g.v = heads_arg(V, a->tokens_k, a->kv_heads, d); g.o = heads_arg(O, a->tokens_q, a->heads, d);
+    g.lse = lse;
+    qlora::AttnPlan p = plan_of(a, qlora::device_compute_units());
+    if (!ws || ws_bytes < qlora::attn_part_bytes(p, a->tokens_q, a->heads, d)) p.splits = 1;
+    g.part = static_cast<float*>(ws);
+    return done(qlora::launch_attn_fwd(g, p, stream), "attention launch");
+  });
+}
+
+int qlora_attention_bwd(const qlora_attention* a, const qlora_heads* dO, const qlora_heads* Q, const qlora_heads* K,
+                        const qlora_heads* V, const qlora_heads* O, const float* lse, const qlora_heads* dQ,
+                        const qlora_heads* dK, const qlora_heads* dV, void* ws, size_t ws_bytes, hipStream_t stream) {
+  return guarded([&] {
+    int st;
+    if ((st = check_attention(a))) return st;
+    const int64_t d = a->head_dim, tq = a->tokens_q, tk = a->tokens_k, h = a->heads, hk = a->kv_heads;
+    if ((st = check_heads(dO, tq, h, d, 16, false, "dO")) || (st = check_heads(Q, tq, h, d, 16, false, "Q")) ||
+        (st = check_heads(K, tk, hk, d, 16, false, "K")) || (st = check_heads(V, tk, hk, d, 16, false, "V")) ||
+        (st = check_heads(O, tq, h, d, 16, false, "O")) || (st = check_heads(dQ, tq, h, d, 16, true, "dQ")) ||
+        (st = check_heads(dK, tk, hk, d, 16, true, "dK")) || (st = check_heads(dV, tk, hk, d, 16, true, "dV")))
+      return st;
+    if (nothing(a)) return (int)QLORA_OK;
+    if (tq > 0 && !lse) return fail(QLORA_ERR_INVALID_ARG, "lse is NULL");
+    if (!aligned16(lse)) return fail(QLORA_ERR_ALIGN, "lse must be 16-byte aligned");
+    if (!ws || ws_bytes < qlora_attention_workspace_bytes(QLORA_OP_BWD, a))
+      return fail(QLORA_ERR_WORKSPACE, "attention backward workspace too small");
+    if (!aligned16(ws)) return fail(QLORA_ERR_ALIGN, "workspace must be 16-byte aligned");
+    qlora::AttnArgs g = attention_args(a);
+    g.dout = heads_arg(dO, tq, h, d); g.q = heads_arg(Q, tq, h, d); g.k = heads_arg(K, tk, hk, d);
+    g.v = heads_arg(V, tk, hk, d); g.o = heads_arg(O, tq, h, d); g.lse = const_cast<float*>(lse);
+    g.dq = heads_arg(dQ, tq, h, d); g.dk = heads_arg(dK, tk, hk, d); g.dv = heads_arg(dV, tk, hk, d);
+    float* delta = static_cast<float*>(ws);
+    float* top = reinterpret_cast<float*>(static_cast<char*>(ws) + delta_bytes(a));
+    return done(qlora::launch_attn_bwd(g, delta, top, stream), "attention backward launch");
+  });
+}
+
+}  // extern "C"

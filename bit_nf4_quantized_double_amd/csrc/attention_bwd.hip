@@ -1,0 +1,484 @@
+// Attention of packed sequences, backward.  With P = exp(scale Q K^T - lse) at
+// the keys a row sees (0 elsewhere) and delta = sum_d dO O:
+//
+//   dV = P^T dO,  dS = P (dO V^T - delta),  dQ = scale dS K,  dK = scale dS^T Q,
+//
+// dK and dV summed over the query heads of a key head.  P is made again from
+// the log-sums.  Two kernels: one goes over the queries for a tile of keys (dK,
+// dV), one over the keys for a tile of queries (dQ).  That computes the scores
+// and dO V^T twice (7 products instead of 5), but every sum has one owner: no
+// atomics, the same bits every time.
+//
+// P and dS are matrix operands in 16 bits.  In fp16 their small values would
+// fall below its range, so P is kept times 2^12, and dS times a power of two
+// from a bound on it: |dS| <= 2 d max|dO| max|V|, taken to 2^14 at most.  The
+// maxima are of the finite values (over the row for dQ, over all for dK).
+//
+// Masked places: P and dS are set to zero there, whatever the values are; in
+// tiles that some rows see only in part, infinities and NaNs of the second
+// products' other operand are left out and added where they are seen.
+#include <algorithm>
+#include <type_traits>
+
+#include "attention_common.h"
+
+namespace qlora {
+namespace {
+
+constexpr int kDeltaTokens = 16;  // tokens of a delta tile
+constexpr float kPShift = 12.f;   // fp16: P times 2^12
+
+template <typename E>
+struct IsF16 { static constexpr bool value = false; };
+template <>
+struct IsF16<F16> { static constexpr bool value = true; };
+
+template <typename E>
+__device__ __forceinline__ float finite_max(const uint4& u) {
+  const uint4 f = finite_part<E>(u);
+  const uint32_t d[4] = {f.x, f.y, f.z, f.w};
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(E::widen((uint16_t)d[i])), fabsf(E::widen((uint16_t)(d[i] >> 16)))));
+  return m;
+}
+
+__device__ __forceinline__ int tops_of(int64_t tokens, int64_t batch) {
+  const int64_t n = attn_tiles(tokens, 1, batch, kDeltaTokens);
+  return (int)(n < kAttnTops ? n : kAttnTops);
+}
+
+// delta = sum_d dO O, 16 lanes a row; in fp16 (blockIdx.y: dO, V) also the
+// largest finite magnitude of each workgroup's rows.
+template <typename E>
+__global__ __launch_bounds__(256) void k_attn_delta(AttnArgs a, float* delta, float* top) {
+  const bool isv = blockIdx.y == 1;
+  const Heads& x = isv ? a.v : a.dout;
+  const int32_t heads = isv ? a.kv_heads : a.heads;
+  const int64_t tokens = isv ? a.tk : a.tq, tiles = attn_tiles(tokens, 1, a.batch, kDeltaTokens);
+  const int sub = threadIdx.x >> 4, l16 = threadIdx.x & 15;
+  float most = 0.f;
+  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const Region rg = find_region(isv ? a.cu_k : a.cu_q, a.batch, tokens, 1, kDeltaTokens, t);
+    if (rg.tile < 0) continue;
+    const int32_t n = seq_length(isv ? a.len_k : a.len_q, rg.seq, a.batch, rg.size), first = rg.tile * kDeltaTokens;
+    const int32_t rows = max(0, min(n - first, kDeltaTokens)) * heads;
+    for (int32_t r = sub; r < rows; r += 16) {
+      const int64_t tok = rg.start + first + r / heads, head = r % heads;
+      float sum = 0.f;
+      for (int c = 8 * l16; c < a.d; c += 128) {
+        const uint4 u = load16(x, tok * x.token + head * x.head + c, true);
+        if (IsF16<E>::value) most = fmaxf(most, finite_max<E>(u));
+        if (!isv) {
+          const uint4 v = load16(a.o, tok * a.o.token + head * a.o.head + c, true);
+          const uint32_t p[4] = {u.x, u.y, u.z, u.w}, q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            sum += E::widen((uint16_t)p[i]) * E::widen((uint16_t)q[i]);
+            sum += E::widen((uint16_t)(p[i] >> 16)) * E::widen((uint16_t)(q[i] >> 16));
+          }
+        }
+      }
+#pragma unroll
+      for (int s = 8; s > 0; s >>= 1) sum += __shfl_xor(sum, s, 16);
+      if (!isv && l16 == 0 && in_bounds(tok * heads + head, 1, a.tq * heads)) delta[tok * heads + head] = sum;
+    }
+  }
+  if constexpr (IsF16<E>::value) {
+    __shared__ float s_top[4];
+#pragma unroll
+    for (int s = 32; s > 0; s >>= 1) most = fmaxf(most, __shfl_xor(most, s));
+    if ((threadIdx.x & 63) == 0) s_top[threadIdx.x >> 6] = most;
+    __syncthreads();
+    const int at = (isv ? kAttnTops : 0) + blockIdx.x;
+    if (threadIdx.x == 0 && in_bounds(at, 1, 2 * kAttnTops))
+      top[at] = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
+  }
+}
+
+// The largest of the partial maxima, in every thread.  All threads take part.
+__device__ __forceinline__ float all_tops(const float* top, int n, float* s_top) {
+  float m = 0.f;
+  for (int i = threadIdx.x; i < n; i += 256) m = fmaxf(m, in_bounds(i, 1, kAttnTops) ? top[i] : 0.f);
+#pragma unroll
+  for (int s = 32; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor(m, s));
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) s_top[threadIdx.x >> 6] = m;
+  __syncthreads();
+  return fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
+}
+
+// A power of two that takes values up to `bound` to 2^14 at most.
+__device__ __forceinline__ float to_range(float bound) {
+  const int e = (int)(__builtin_bit_cast(uint32_t, bound) >> 23) - 126;  // bound < 2^e
+  return __builtin_bit_cast(float, (uint32_t)(max(-100, min(100, 14 - e)) + 127) << 23);
+}
+
+// dQ: 128 rows a workgroup, 32 a wave, tiles of 64 keys.
+template <typename E, int DB>
+__global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
+  constexpr int BN = 64, BM = 128;
+  constexpr int CH = TileLayout<DB>::kChunks, PER = BN * CH / 256, BYTES = BN * TileLayout<DB>::kPitch;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[4 * BYTES];
+  __shared__ int s_bad[2];
+  __shared__ float s_top[4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = lane >> 5;
+  const int32_t kv_head = blockIdx.x % a.kv_heads;
+  const int64_t t = attn_tiles(a.tq, a.group, a.batch, BM) - 1 - blockIdx.x / a.kv_heads;
+  const Region rg = find_region(a.cu_q, a.batch, a.tq, a.group, BM, t);
+  if (rg.tile < 0 || (int64_t)rg.tile * BM >= rg.size * a.group) return;
+  const int32_t nq = seq_length(a.len_q, rg.seq, a.batch, rg.size);
+  const Keys ks = keys_of(a, rg.seq);
+  const int32_t rows = nq * a.group, first = rg.tile * BM, wfirst = first + wave * 32, row = wfirst + (lane & 31);
+  const bool live = row < rows;
+  const int32_t tok = row / a.group, head = kv_head * a.group + row % a.group;
+  const int64_t at = (rg.start + tok) * a.dq.token + head * a.dq.head;
+  if (a.zero_rest && !live && row < rg.size * a.group)
+    for (int c = 8 * half; c < a.d; c += 16)
+      if (in_bounds(at + c, 8, a.dq.n))
+        *reinterpret_cast<uint4*>(const_cast<uint16_t*>(a.dq.p) + at + c) = make_uint4(0, 0, 0, 0);
+  if (first >= rows) return;
+
+  const int32_t off = ks.n - nq;
+  const int32_t last = !live ? -1 : a.causal ? min(ks.n - 1, tok + off) : ks.n - 1;
+  const int32_t end = a.causal ? max(0, min(ks.n, (min(first + BM, rows) - 1) / a.group + off + 1)) : ks.n;
+  const int32_t whole = a.causal ? min(ks.n, first / a.group + off + 1) : ks.n;
+  const int32_t wwhole = a.causal ? min(ks.n, wfirst / a.group + off + 1) : ks.n;
+  const int32_t wend = a.causal ? min(ks.n, (min(wfirst + 32, rows) - 1) / a.group + off + 1) : ks.n;
+  const int32_t k1 = (end + BN - 1) / BN;
+
+  typename E::v8 qf[2 * DB], df[2 * DB];
+  float most = 0.f;
+#pragma unroll
+  for (int s = 0; s < 2 * DB; ++s) {
+    const int c = 16 * s + 8 * half;
+    qf[s] = E::vec(load16(a.q, (rg.start + tok) * a.q.token + head * a.q.head + c, live && c < a.d));
+    const uint4 u = load16(a.dout, (rg.start + tok) * a.dout.token + head * a.dout.head + c, live && c < a.d);
+    df[s] = E::vec(u);
+    if (IsF16<E>::value) most = fmaxf(most, finite_max<E>(u));
+  }
+  const int64_t r_at = (rg.start + tok) * a.heads + head;
+  float lse = INFINITY, delta = 0.f;  // a row that sees nothing: P = 0
+  if (live && in_bounds(r_at, 1, a.tq * a.heads)) {
+    lse = a.lse[r_at] * kLog2e;
+    delta = a.delta[r_at];
+    if (lse == -INFINITY) lse = INFINITY;
+  }
+  float up = 1.f;
+  if constexpr (IsF16<E>::value) {
+    const float vtop = all_tops(a.top + kAttnTops, tops_of(a.tk, a.batch), s_top);
+    up = to_range(2.f * a.d * half_max(most) * vtop);
+  }
+  const float c2 = a.scale * kLog2e;
+
+  uint4 st[2][PER];
+  auto load = [&](int32_t kt) {
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+      const int c = u * 256 + tid, ch = c % CH;
+      const int32_t key = kt * BN + c / CH;
+      const bool ok = kt < k1 && key < ks.n && ch * 8 < a.d;
+      st[0][u] = load16(a.k, (ks.start + key) * a.k.token + kv_head * a.k.head + ch * 8, ok);
+      st[1][u] = load16(a.v, (ks.start + key) * a.v.token + kv_head * a.v.head + ch * 8, ok);
+    }
+  };
+  auto store = [&](int32_t kt, int buf) {
+    uint8_t* const to = lds + buf * 2 * BYTES;
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+      const int c = u * 256 + tid;
+      *reinterpret_cast<uint4*>(to + TileLayout<DB>::at(c / CH, c % CH)) = st[0][u];
+      *reinterpret_cast<uint4*>(to + BYTES + TileLayout<DB>::at(c / CH, c % CH)) = st[1][u];
+    }
+    if ((kt + 1) * BN > whole) {
+      uint32_t nf = 0;
+#pragma unroll
+      for (int u = 0; u < PER; ++u) nf |= not_finite<E>(st[0][u]);
+      if (nf) s_bad[buf] = kt + 1;
+    }
+  };
+
+  f32x16 dq[DB];
+#pragma unroll
+  for (int b = 0; b < DB; ++b) dq[b] = (f32x16)(0.f);
+  auto tile = [&](int32_t kt, const uint8_t* kb, bool bad) {
+    const uint8_t* vb = kb + BYTES;
+    const bool masked = (kt + 1) * BN > wwhole;
+#pragma unroll
+    for (int u = 0; u < BN / 32; ++u) {
+      f32x16 s = (f32x16)(0.f), dp = (f32x16)(0.f);
+#pragma unroll
+      for (int i = 0; i < 2 * DB; ++i) s = E::mfma32(frag_rows<E, DB>(kb, 32 * u, i, lane), qf[i], s);
+#pragma unroll
+      for (int i = 0; i < 2 * DB; ++i) dp = E::mfma32(frag_rows<E, DB>(vb, 32 * u, i, lane), df[i], dp);
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], c2, -lse)) * ((dp[r] - delta) * up);
+      if (masked) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (kt * BN + 32 * u + 8 * (r / 4) + 4 * half + r % 4 > last) s[r] = 0.f;
+      }
+      typename E::v8 p[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) p[i] = pack8<E>(s, 8 * i);
+      if (!bad) {
+#pragma unroll
+        for (int b = 0; b < DB; ++b)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) dq[b] = E::mfma32(E::vec(frag_cols<DB>(kb, 32 * u + 16 * i, b, lane)), p[i], dq[b]);
+      } else {
+#pragma unroll
+        for (int b = 0; b < DB; ++b) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            dq[b] = E::mfma32(E::vec(finite_part<E>(frag_cols<DB>(kb, 32 * u + 16 * i, b, lane))), p[i], dq[b]);
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+#pragma unroll 1
+            for (int j = 0; j < 32; ++j) {
+              const float x = tile_value<E, DB>(kb, 32 * u + j, 32 * b + 8 * (r / 4) + 4 * half + r % 4);
+              if (kt * BN + 32 * u + j <= last && !(fabsf(x) < INFINITY)) dq[b][r] += x * 0.f;
+            }
+        }
+      }
+    }
+  };
+
+  if (tid < 2) s_bad[tid] = 0;
+  __syncthreads();
+  load(0);
+  store(0, 0);
+  load(1);
+  __syncthreads();
+  for (int32_t kt = 0; kt < k1; ++kt) {
+    const int buf = kt & 1;
+    if (kt + 1 < k1) {
+      store(kt + 1, buf ^ 1);
+      load(kt + 2);
+    }
+    if (kt * BN < wend) tile(kt, lds + buf * 2 * BYTES, s_bad[buf] == kt + 1);
+    __syncthreads();
+  }
+  const float f = a.scale / up;
+#pragma unroll
+  for (int b = 0; b < DB; ++b) store_block<E>(a.dq, at, live, b, a.d, dq[b], f, lane);
+}
+
+// dK and dV: 128 keys a workgroup, 32 a wave, tiles of 32 rows of queries.
+template <typename E, int DB>
+__global__ __launch_bounds__(256, 2) void k_attn_bwd_kv(AttnArgs a) {
+  constexpr int BQ = 32, BK = 128;
+  constexpr int CH = TileLayout<DB>::kChunks, PER = BQ * CH / 256, BYTES = BQ * TileLayout<DB>::kPitch;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[4 * BYTES];
+  __shared__ __attribute__((aligned(16))) float s_lse[2][BQ], s_delta[2][BQ];
+  __shared__ __attribute__((aligned(16))) int s_last[2][BQ];
+  __shared__ int s_bad[2];
+  __shared__ float s_top[4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = lane >> 5;
+  const int32_t kv_head = blockIdx.x % a.kv_heads;
+  const Region rg = find_region(a.cu_k, a.batch, a.tk, 1, BK, blockIdx.x / a.kv_heads);
+  if (rg.tile < 0 || (int64_t)rg.tile * BK >= rg.size) return;
+  const int32_t nk = seq_length(a.len_k, rg.seq, a.batch, rg.size);
+  const int32_t key0 = rg.tile * BK, wkey0 = key0 + wave * 32, key = wkey0 + (lane & 31);
+  const bool live = key < nk;
+  const int64_t k_at = (rg.start + key) * a.dk.token + kv_head * a.dk.head;
+  const int64_t v_at = (rg.start + key) * a.dv.token + kv_head * a.dv.head;
+  if (a.zero_rest && !live && key < rg.size)
+    for (int c = 8 * half; c < a.d; c += 16) {
+      if (in_bounds(k_at + c, 8, a.dk.n))
+        *reinterpret_cast<uint4*>(const_cast<uint16_t*>(a.dk.p) + k_at + c) = make_uint4(0, 0, 0, 0);
+      if (in_bounds(v_at + c, 8, a.dv.n))
+        *reinterpret_cast<uint4*>(const_cast<uint16_t*>(a.dv.p) + v_at + c) = make_uint4(0, 0, 0, 0);
+    }
+  if (key0 >= nk) return;
+
+  // the sequence's queries
+  const int64_t q0 = region_start(a.cu_q, a.batch, a.tq, rg.seq + 1);
+  const int64_t qsize = clampl(region_start(a.cu_q, a.batch, a.tq, rg.seq + 2), q0, a.tq) - q0;
+  const int32_t nq = seq_length(a.len_q, rg.seq, a.batch, qsize), rows = nq * a.group, off = nk - nq;
+  const int32_t t0 = a.causal ? max(0, key0 - off) : 0;  // the first query that sees the first key
+  const int32_t r0 = (int32_t)min((int64_t)t0 * a.group, (int64_t)rows) / BQ, r1 = (rows + BQ - 1) / BQ;
+
+  typename E::v8 kf[2 * DB], vf[2 * DB];
+#pragma unroll
+  for (int s = 0; s < 2 * DB; ++s) {
+    const int c = 16 * s + 8 * half;
+    kf[s] = E::vec(load16(a.k, (rg.start + key) * a.k.token + kv_head * a.k.head + c, live && c < a.d));
+    vf[s] = E::vec(load16(a.v, (rg.start + key) * a.v.token + kv_head * a.v.head + c, live && c < a.d));
+  }
+  float up = 1.f;
+  if constexpr (IsF16<E>::value) {
+    const float dtop = all_tops(a.top, tops_of(a.tq, a.batch), s_top);
+    up = to_range(2.f * a.d * dtop * all_tops(a.top + kAttnTops, tops_of(a.tk, a.batch), s_top));
+  }
+  constexpr float kShift = IsF16<E>::value ? kPShift : 0.f;
+  const float ups = up * __builtin_amdgcn_exp2f(-kShift);
+  const float c2 = a.scale * kLog2e;
+
+  uint4 st[2][PER];
+  float st_lse, st_delta;
+  int st_last;
+  auto load = [&](int32_t rt) {
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+      const int c = u * 256 + tid, ch = c % CH;
+      const int32_t r = rt * BQ + c / CH, tok = r / a.group, head = kv_head * a.group + r % a.group;
+      const bool ok = rt < r1 && r < rows && ch * 8 < a.d;
+      st[0][u] = load16(a.q, (q0 + tok) * a.q.token + head * a.q.head + ch * 8, ok);
+      st[1][u] = load16(a.dout, (q0 + tok) * a.dout.token + head * a.dout.head + ch * 8, ok);
+    }
+    if (tid < BQ) {
+      const int32_t r = rt * BQ + tid, tok = r / a.group, head = kv_head * a.group + r % a.group;
+      const int64_t at = (q0 + tok) * a.heads + head;
+      st_lse = INFINITY;
+      st_delta = 0.f;
+      st_last = -1;
+      if (rt < r1 && r < rows && in_bounds(at, 1, a.tq * a.heads)) {
+        st_lse = a.lse[at] * kLog2e;
+        if (st_lse == -INFINITY) st_lse = INFINITY;  // a row that sees nothing: P = 0
+        st_lse -= kShift;
+        st_delta = a.delta[at];
+        st_last = a.causal ? min(nk - 1, tok + off) : nk - 1;
+      }
+    }
+  };
+  auto store = [&](int32_t rt, int buf) {
+    uint8_t* const to = lds + buf * 2 * BYTES;
+    uint32_t nf = 0;
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+      const int c = u * 256 + tid;
+      *reinterpret_cast<uint4*>(to + TileLayout<DB>::at(c / CH, c % CH)) = st[0][u];
+      *reinterpret_cast<uint4*>(to + BYTES + TileLayout<DB>::at(c / CH, c % CH)) = st[1][u];
+      nf |= not_finite<E>(st[0][u]) | not_finite<E>(st[1][u]);
+    }
+    if (nf) s_bad[buf] = rt + 1;
+    if (tid < BQ) {
+      s_lse[buf][tid] = st_lse;
+      s_delta[buf][tid] = st_delta;
+      s_last[buf][tid] = st_last;
+    }
+  };
+
+  f32x16 dk[DB], dv[DB];
+#pragma unroll
+  for (int b = 0; b < DB; ++b) dk[b] = dv[b] = (f32x16)(0.f);
+  auto tile = [&](int32_t rt, int buf) {
+    const uint8_t *qb = lds + buf * 2 * BYTES, *db = qb + BYTES;
+    f32x16 s = (f32x16)(0.f), dp = (f32x16)(0.f);
+#pragma unroll
+    for (int i = 0; i < 2 * DB; ++i) s = E::mfma32(frag_rows<E, DB>(qb, 0, i, lane), kf[i], s);
+#pragma unroll
+    for (int i = 0; i < 2 * DB; ++i) dp = E::mfma32(frag_rows<E, DB>(db, 0, i, lane), vf[i], dp);
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const float4 l = *reinterpret_cast<const float4*>(&s_lse[buf][8 * g + 4 * half]);
+      const float4 e = *reinterpret_cast<const float4*>(&s_delta[buf][8 * g + 4 * half]);
+      const float ls[4] = {l.x, l.y, l.z, l.w}, es[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = 4 * g + j;
+        s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], c2, -ls[j]));
+        dp[r] = s[r] * ((dp[r] - es[j]) * ups);
+      }
+    }
+    // the first row sees the fewest keys
+    const bool masked = (rt + 1) * BQ > rows || wkey0 + 31 > s_last[buf][0];
+    if (masked) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (key > s_last[buf][8 * (r / 4) + 4 * half + r % 4]) s[r] = dp[r] = 0.f;
+    }
+    typename E::v8 p[2], ds[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      p[i] = pack8<E>(s, 8 * i);
+      ds[i] = pack8<E>(dp, 8 * i);
+    }
+    if (!(masked && s_bad[buf] == rt + 1)) {
+#pragma unroll
+      for (int b = 0; b < DB; ++b)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          dv[b] = E::mfma32(E::vec(frag_cols<DB>(db, 16 * i, b, lane)), p[i], dv[b]);
+          dk[b] = E::mfma32(E::vec(frag_cols<DB>(qb, 16 * i, b, lane)), ds[i], dk[b]);
+        }
+    } else {
+#pragma unroll
+      for (int b = 0; b < DB; ++b) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          dv[b] = E::mfma32(E::vec(finite_part<E>(frag_cols<DB>(db, 16 * i, b, lane))), p[i], dv[b]);
+          dk[b] = E::mfma32(E::vec(finite_part<E>(frag_cols<DB>(qb, 16 * i, b, lane))), ds[i], dk[b]);
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+#pragma unroll 1
+          for (int j = 0; j < BQ; ++j) {
+            if (key > s_last[buf][j]) continue;
+            const int c = 32 * b + 8 * (r / 4) + 4 * half + r % 4;
+            const float x = tile_value<E, DB>(db, j, c), y = tile_value<E, DB>(qb, j, c);
+            if (!(fabsf(x) < INFINITY)) dv[b][r] += x;
+            if (!(fabsf(y) < INFINITY)) dk[b][r] += y * 0.f;
+          }
+      }
+    }
+  };
+
+  if (tid < 2) s_bad[tid] = 0;
+  __syncthreads();
+  load(r0);
+  store(r0, 0);
+  load(r0 + 1);
+  __syncthreads();
+  for (int32_t rt = r0; rt < r1; ++rt) {
+    const int buf = (rt - r0) & 1;
+    if (rt + 1 < r1) {
+      store(rt + 1, buf ^ 1);
+      load(rt + 2);
+    }
+    tile(rt, buf);
+    __syncthreads();
+  }
+  const float fk = a.scale / up, fv = __builtin_amdgcn_exp2f(-kShift);
+#pragma unroll
+  for (int b = 0; b < DB; ++b) {
+    store_block<E>(a.dk, k_at, live, b, a.d, dk[b], fk, lane);
+    store_block<E>(a.dv, v_at, live, b, a.d, dv[b], fv, lane);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_attn_bwd(const AttnArgs& args, float* delta, float* top, hipStream_t stream) {
+  AttnArgs a = args;
+  a.delta = delta;
+  a.top = top;
+  const auto run = [&](auto e, auto db) {
+    using E = decltype(e);
+    constexpr int DB = decltype(db)::value;
+    const int64_t dt = attn_tiles(a.tq, 1, a.batch, kDeltaTokens), vt = attn_tiles(a.tk, 1, a.batch, kDeltaTokens);
+    if (a.f16) {
+      // as many workgroups as partial maxima, the same for dO and V
+      k_attn_delta<E><<<dim3((uint32_t)std::min<int64_t>(std::max(dt, vt), kAttnTops), 2), 256, 0, stream>>>(a, delta, top);
+    } else if (a.tq > 0) {
+      k_attn_delta<E><<<(uint32_t)std::min<int64_t>(dt, 1 << 20), 256, 0, stream>>>(a, delta, top);
+    }
+    if (a.tk > 0)
+      k_attn_bwd_kv<E, DB><<<(uint32_t)(attn_tiles(a.tk, 1, a.batch, 128) * a.kv_heads), 256, 0, stream>>>(a);
+    if (a.tq > 0)
+      k_attn_bwd_q<E, DB><<<(uint32_t)(attn_tiles(a.tq, a.group, a.batch, 128) * a.kv_heads), 256, 0, stream>>>(a);
+  };
+  const auto typed = [&](auto e) {
+    if (a.d <= 64) run(e, std::integral_constant<int, 2>{});
+    else run(e, std::integral_constant<int, 4>{});
+  };
+  if (a.f16) typed(F16{});
+  else typed(Bf16{});
+  return hipGetLastError();
+}
+
+QLORA_OOB_READER(oob_count_attention_bwd)
+
+}  // namespace qlora

@@ -1,0 +1,210 @@
+// Shared by the attention kernels: which sequence a workgroup's rows belong
+// to, operand tiles in LDS, and matrix-core fragments of them.
+//
+// Rows.  The queries of a key head's `group` heads are packed: row r of a
+// sequence is token r / group, head r % group of the group.  They share their
+// keys, so a tile of rows needs one pass over the keys whatever the group is.
+//
+// Tiles.  Lengths are on the device only, so the host cannot list the tiles.
+// Sequences s_0 <= s_1 <= ... take tile numbers from floor(s_i group / rows) + i
+// on: no two overlap, since ceil(n / b) <= floor((s + n) / b) - floor(s / b) + 1,
+// and about one number a sequence has nothing to do.  The tokens before the
+// first sequence and behind the last count as a sequence each (0 and batch + 1),
+// whose rows are zeroed or left alone.
+#pragma once
+
+#include "common.h"
+#include "decoder.h"
+
+namespace qlora {
+namespace {
+
+constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
+
+__device__ __forceinline__ int64_t clampl(int64_t x, int64_t lo, int64_t hi) { return x < lo ? lo : x > hi ? hi : x; }
+
+// Numbers of tiles of `rows` rows that the launch needs.
+__host__ __device__ inline int64_t attn_tiles(int64_t tokens, int64_t group, int64_t batch, int64_t rows) {
+  return tokens * group / rows + batch + 2;
+}
+
+// Start of region i (0: before the first sequence, batch + 1: behind the last).
+__device__ __forceinline__ int64_t region_start(const int32_t* cu, int32_t batch, int64_t tokens, int32_t i) {
+  if (i <= 0 || !in_bounds(i - 1, 1, batch + 1)) return 0;
+  return clampl(cu[i - 1], 0, tokens);
+}
+
+struct Region {
+  int64_t start, size;  // tokens
+  int32_t tile;         // of the region; < 0: none
+  int32_t seq;          // -1: no sequence's
+};
+
+// The region of tile number t.  All lanes of the wave take part and get the same.
+__device__ __forceinline__ Region find_region(const int32_t* cu, int32_t batch, int64_t tokens, int32_t group, int32_t rows,
+                                              int64_t t) {
+  const int lane = threadIdx.x & 63;
+  int32_t n = 0;  // regions that start at tile t or before
+  for (int32_t i0 = 0; i0 < batch + 2; i0 += 64) {
+    const int32_t i = i0 + lane;
+    const bool yes = i < batch + 2 && region_start(cu, batch, tokens, i) * group / rows + i <= t;
+    n += __popcll(__ballot(yes));
+  }
+  const int32_t i = __builtin_amdgcn_readfirstlane(n - 1);
+  Region r;
+  r.start = region_start(cu, batch, tokens, i);
+  r.size = (i > batch ? tokens : clampl(region_start(cu, batch, tokens, i + 1), r.start, tokens)) - r.start;
+  r.tile = (int32_t)(t - (r.start * group / rows + i));
+  r.seq = i >= 1 && i <= batch ? i - 1 : -1;
+  return r;
+}
+
+// Tokens of a sequence: its region, or fewer where lengths are given.
+__device__ __forceinline__ int32_t seq_length(const int32_t* len, int32_t seq, int32_t batch, int64_t size) {
+  if (seq < 0) return 0;
+  if (!len) return (int32_t)size;
+  return in_bounds(seq, 1, batch) ? (int32_t)clampl(len[seq], 0, size) : 0;
+}
+
+// Keys of a sequence: [start, start + n).
+struct Keys {
+  int64_t start;
+  int32_t n;
+};
+__device__ __forceinline__ Keys keys_of(const AttnArgs& a, int32_t seq) {
+  if (seq < 0) return Keys{0, 0};
+  const int64_t s = region_start(a.cu_k, a.batch, a.tk, seq + 1);
+  const int64_t e = clampl(region_start(a.cu_k, a.batch, a.tk, seq + 2), s, a.tk);
+  return Keys{s, seq_length(a.len_k, seq, a.batch, e - s)};
+}
+
+// 16-byte chunks of a tile's row in LDS are permuted by chunk ^ spread(row): the
+// 8 (16) rows that a wave's b128 reads of one column touch at a time, and the 4
+// rows by 32 (64) bytes of its transposing reads, fall into different banks.
+template <int DB>
+__device__ __forceinline__ uint32_t spread(uint32_t r) {
+  const uint32_t f = (((r ^ (r >> 3)) & 1) << 3) | ((r & 3) << 1 & 4) | ((r & 1) << 1) | ((r >> 2) & 1);
+  return DB >= 4 ? f : f & 7;
+}
+
+// A tile: rows of DB * 32 16-bit values (chunks past d are zeros).
+template <int DB>
+struct TileLayout {
+  static constexpr int kPitch = DB * 64;   // bytes of a row
+  static constexpr int kChunks = DB * 4;   // 16-byte chunks of a row
+  static __device__ __forceinline__ uint32_t at(uint32_t row, uint32_t chunk) {
+    return row * kPitch + ((chunk ^ spread<DB>(row)) << 4);
+  }
+};
+
+// MFMA operand (32 x 16): row r0 + lane % 32, columns 16 step + 8 (lane / 32) .. + 7.
+template <typename E, int DB>
+__device__ __forceinline__ typename E::v8 frag_rows(const uint8_t* tile, int r0, int step, int lane) {
+  return E::vec(*reinterpret_cast<const uint4*>(tile + TileLayout<DB>::at(r0 + (lane & 31), 2 * step + (lane >> 5))));
+}
+
+typedef __attribute__((ext_vector_type(4))) short s16x4;
+
+// The transposed operand (32 x 16): column 32 block + lane % 32 of rows r0 ..
+// r0 + 15, in the order in which the accumulators of a 32 x 32 product hold
+// their rows: element e of lane half h is row r0 + 8 (e / 4) + 4 h + e % 4.
+// (ds_read_b64_tr_b16: 16 lanes give the addresses of 4 rows of 16 values, 4 a
+// lane, and each gets one column of them.)
+template <int DB>
+__device__ __forceinline__ uint4 frag_cols(const uint8_t* tile, int r0, int block, int lane) {
+  uint2 u[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t row = r0 + 8 * i + 4 * (lane >> 5) + ((lane & 15) >> 2);
+    const uint32_t chunk = 4 * block + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+    const uint8_t* p = tile + TileLayout<DB>::at(row, chunk) + 8 * (lane & 1);
+    const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
+    u[i] = __builtin_bit_cast(uint2, v);
+  }
+  return make_uint4(u[0].x, u[0].y, u[1].x, u[1].y);
+}
+
+// Halves of d that are infinite or NaN: their top bits.
+template <typename E>
+__device__ __forceinline__ uint32_t not_finite(uint32_t d);
+template <>
+__device__ __forceinline__ uint32_t not_finite<Bf16>(uint32_t d) {
+  return ~((~d & 0x7f807f80u) + 0x7fff7fffu) & 0x80008000u;
+}
+template <>
+__device__ __forceinline__ uint32_t not_finite<F16>(uint32_t d) {
+  return ~((~d & 0x7c007c00u) + 0x7fff7fffu) & 0x80008000u;
+}
+template <typename E>
+__device__ __forceinline__ uint32_t not_finite(const uint4& u) {
+  return not_finite<E>(u.x) | not_finite<E>(u.y) | not_finite<E>(u.z) | not_finite<E>(u.w);
+}
+// d with such halves zeroed
+template <typename E>
+__device__ __forceinline__ uint32_t finite_part(uint32_t d) {
+  return d & ~((not_finite<E>(d) >> 15) * 0xffffu);
+}
+template <typename E>
+__device__ __forceinline__ uint4 finite_part(const uint4& u) {
+  return make_uint4(finite_part<E>(u.x), finite_part<E>(u.y), finite_part<E>(u.z), finite_part<E>(u.w));
+}
+// value (row, column) of a tile
+template <typename E, int DB>
+__device__ __forceinline__ float tile_value(const uint8_t* tile, int row, int col) {
+  return E::widen(*reinterpret_cast<const uint16_t*>(tile + TileLayout<DB>::at(row, col >> 3) + 2 * (col & 7)));
+}
+
+// Between a wave's own writes to LDS and other lanes' reads of them, or the
+// reverse: the hardware keeps a wave's LDS operations in order, the compiler has to.
+__device__ __forceinline__ void own_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// The largest of both halves of the wave, lane by lane % 32; and the sum.
+__device__ __forceinline__ float half_max(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, x), false, false);
+  return fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
+}
+__device__ __forceinline__ float half_sum(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, x), false, false);
+  return __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
+}
+
+// A 32 x 32 accumulator block, whose columns (lane % 32) are rows of the
+// tensor: values 32 block + 0 .. 31 of the lane's row at element `at`, as far
+// as they are below d, times f, rounded.  The halves of the wave trade parts so
+// that each lane stores 16 bytes twice.
+template <typename E>
+__device__ __forceinline__ void store_block(const Heads& o, int64_t at, bool ok, int block, int d, const f32x16& acc, float f,
+                                            int lane) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t lo = E::pack2(acc[8 * i + 2 * j] * f, acc[8 * i + 2 * j + 1] * f);
+      const uint32_t hi = E::pack2(acc[8 * i + 4 + 2 * j] * f, acc[8 * i + 5 + 2 * j] * f);
+      const auto r = __builtin_amdgcn_permlane32_swap(lo, hi, false, false);
+      w[j] = r[0];
+      w[2 + j] = r[1];
+    }
+    const int c = 32 * block + 16 * i + 8 * (lane >> 5);
+    if (ok && c < d && in_bounds(at + c, 8, o.n))
+      *reinterpret_cast<uint4*>(const_cast<uint16_t*>(o.p) + at + c) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+__device__ __forceinline__ uint4 load16(const Heads& x, int64_t at, bool ok) {
+  return ok && in_bounds(at, 8, x.n) ? *reinterpret_cast<const uint4*>(x.p + at) : make_uint4(0, 0, 0, 0);
+}
+
+template <typename E, typename A>
+__device__ __forceinline__ typename E::v8 pack8(const A& p, int i, float f = 1.f) {
+  return E::vec(make_uint4(E::pack2(p[i] * f, p[i + 1] * f), E::pack2(p[i + 2] * f, p[i + 3] * f),
+                           E::pack2(p[i + 4] * f, p[i + 5] * f), E::pack2(p[i + 6] * f, p[i + 7] * f)));
+}
+
+}  // namespace
+}  // namespace qlora

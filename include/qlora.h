@@ -538,6 +538,96 @@ int qlora_swiglu_bwd(const void *dY, int64_t lddy, const void *G, int64_t ldg, c
                      int64_t ldu, int64_t M, int64_t K, uint16_t *dG, uint16_t *dU, int dtype,
                      hipStream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Between a decoder's linears and at its end: rotary positions, attention of
+ * packed sequences, and the loss under a frozen output head.
+ *
+ * A qlora_heads is a 16-bit tensor [tokens, heads, head_dim] whose values of a
+ * head are contiguous; the strides (in elements) of its tokens and heads are
+ * free, so that it may be a part of a projection's output or of a cache.  A
+ * stride of 0 reads a broadcast input.  Outputs' elements must not overlap.
+ */
+typedef struct {
+  void *p;
+  int64_t token_stride, head_stride;
+} qlora_heads;
+
+/*
+ * Rotary positions.  For token t and pair i of the first `rot` values of each
+ * head, with the angle 2 pi turns[i] positions[t] / 2^64,
+ *     (a, b) -> factor (a cos - b sin, b cos + a sin),
+ * and values rot .. head_dim - 1 unchanged.  Pairs are (i, i + rot/2), or
+ * (2i, 2i + 1) where `interleaved`.  `inverse` turns by the negative angle: the
+ * backward.  The sines are made in fp32 from the angle modulo a turn, which is
+ * exact for every position (turns wraps), and a result is rounded once.
+ *   Q, K        in; K->p may be NULL with kv_heads 0
+ *   Qo, Ko      out; may be Q and K themselves (same pointer and strides)
+ *   positions   int32 [tokens], or int64 where `positions64`; negative ones too
+ *   turns       device uint64 [rot / 2], 8-byte aligned
+ * Any sizes, strides and 2-byte alignment; heads that can be read 16 bytes at a
+ * time (rot a multiple of 16, head_dim and strides of 8, 16-byte aligned) are
+ * faster.  rot is even, at most head_dim (QLORA_ERR_SHAPE otherwise).
+ */
+int qlora_rope(const qlora_heads *Q, int64_t heads, const qlora_heads *K, int64_t kv_heads,
+               int64_t tokens, int64_t head_dim, int64_t rot, int interleaved, const void *positions,
+               int positions64, const uint64_t *turns, float factor, int inverse,
+               const qlora_heads *Qo, const qlora_heads *Ko, int dtype, hipStream_t stream);
+
+/*
+ * Attention of packed sequences.  Sequence b has the queries at tokens
+ * cu_q[b] .. cu_q[b+1] - 1 of Q and the keys at cu_k[b] .. cu_k[b+1] - 1 of K
+ * and V, or the first len_q[b], len_k[b] of them where lengths are given (a
+ * padded batch, a cache with room).  Query head h reads key head
+ * h / (heads / kv_heads).  With n queries and m keys, query i sees keys
+ * 0 .. i + m - n where `causal` (the last query sees all; a single new token of a
+ * sequence in a cache is n = 1), otherwise all:
+ *     O = E(sum_j p_j V_j),  p = softmax(scale Q K^T) over the keys it sees,
+ *     lse = log sum_j exp(scale Q K_j)     (fp32 [tokens_q, heads])
+ * A query that sees no key gets O = 0 and lse = -inf, and no gradient.  Masked
+ * keys have no effect, whatever they hold: infinities and NaNs as well.
+ * Scores, sums and lse are fp32; p is rounded to 16 bits for the product with V.
+ *   cu_q, cu_k  device int32 [batch + 1], ascending; values outside the tensors
+ *               are taken to their ends (no access goes outside)
+ *   len_q, len_k  device int32 [batch] or NULL
+ *   zero_rest   nonzero: tokens of O (backward: dQ, dK, dV) that belong to no
+ *               sequence become zeros (lse: -inf); zero: they are left as they are
+ *   head_dim    a multiple of 8, at most 128.  Pointers are 16-byte aligned and
+ *               strides multiples of 8 (QLORA_ERR_ALIGN); scale is positive.
+ *               tokens_q * heads / kv_heads and tokens_k at most 2^31 - 256.
+ * Backward, from dO, O, lse (as the forward wrote them):
+ *     dV = sum P dO, dS = P (dO V - sum dO O), dQ = scale dS K, dK = scale sum dS Q,
+ * dK and dV summed over the heads that share them.  P and dS are rounded to 16
+ * bits for the products.  Same inputs, same bits: no atomics.  fp16: dS is kept
+ * in range by a power of two from the largest finite |dO| and |V|, of the row for
+ * dQ and of the whole batch for dK; what is 2^-30 below these bounds is lost.
+ * Workspace: qlora_attention_workspace_bytes(op, ...).  The forward's is for keys
+ * split over workgroups and optional (without room it runs unsplit, as right);
+ * the backward's is needed (QLORA_ERR_WORKSPACE).
+ */
+#define QLORA_MAX_HEAD_DIM 128
+typedef struct {
+  int64_t tokens_q, tokens_k, batch, heads, kv_heads, head_dim;
+  const int32_t *cu_q, *cu_k, *len_q, *len_k;
+  float scale;
+  int causal, zero_rest, dtype;
+} qlora_attention;
+
+size_t qlora_attention_workspace_bytes(int op, const qlora_attention *a);
+int qlora_attention_fwd(const qlora_attention *a, const qlora_heads *Q, const qlora_heads *K,
+                        const qlora_heads *V, const qlora_heads *O, float *lse, void *ws,
+                        size_t ws_bytes, hipStream_t stream);
+int qlora_attention_bwd(const qlora_attention *a, const qlora_heads *dO, const qlora_heads *Q,
+                        const qlora_heads *K, const qlora_heads *V, const qlora_heads *O,
+                        const float *lse, const qlora_heads *dQ, const qlora_heads *dK,
+                        const qlora_heads *dV, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* Host function: how a forward of these sizes runs.  out[0] = rows (tokens times
+ * heads / kv_heads) of a workgroup: 128, or 32 with the keys shared out among its
+ * waves; out[1] = over how many workgroups a row's keys are split.
+ * `compute_units` <= 0: the current device's. */
+int qlora_attention_plan(const qlora_attention *a, int compute_units, int64_t out[2]);
+
 /* Host function: static description of a status code. */
 const char *qlora_status_string(int status);
 
