@@ -22,7 +22,8 @@ LIB = os.path.join(PKG, "libqlora.so")
 # counted when outside its buffer; qlora_debug_oob_count reads the count).
 LIB_CHECKED = os.path.join(PKG, "libqlora_checked.so")
 SOURCES = ["nf4_table.cpp", "codec.hip", "gemm.hip", "skinny.hip", "lora.hip", "adapter.hip", "merge.hip", "rows.hip", "int8.hip",
-           "rope.hip", "attention.hip", "attention_bwd.hip", "abi.hip", "abi_int8.hip", "abi_decoder.hip"]
+           "rope.hip", "attention.hip", "attention_bwd.hip", "cross_entropy.hip", "abi.hip", "abi_int8.hip",
+           "abi_decoder.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

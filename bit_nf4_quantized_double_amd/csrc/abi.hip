@@ -46,6 +46,7 @@ uint64_t oob_count_int8(bool reset);
 uint64_t oob_count_rope(bool reset);
 uint64_t oob_count_attention(bool reset);
 uint64_t oob_count_attention_bwd(bool reset);
+uint64_t oob_count_cross_entropy(bool reset);
 hipError_t launch_lora_down(const uint16_t* X, int M, int K, const uint16_t* A, int r, float s, uint16_t* U,
                             float* part, DropMask drop, bool f16, hipStream_t st);
 size_t rowdot_part_bytes(int64_t M, int64_t Kd, int r);
@@ -236,7 +237,8 @@ int qlora_debug_oob_count(uint64_t* count, int reset) {
   const uint64_t c[] = {qlora::oob_count_codec(rs), qlora::oob_count_gemm(rs), qlora::oob_count_skinny(rs),
                         qlora::oob_count_lora(rs), qlora::oob_count_adapter(rs), qlora::oob_count_merge(rs),
                         qlora::oob_count_rows(rs), qlora::oob_count_int8(rs), qlora::oob_count_rope(rs),
-                        qlora::oob_count_attention(rs), qlora::oob_count_attention_bwd(rs)};
+                        qlora::oob_count_attention(rs), qlora::oob_count_attention_bwd(rs),
+                        qlora::oob_count_cross_entropy(rs)};
   uint64_t total = 0;
   for (uint64_t v : c) {
     if (v == ~(uint64_t)0) return fail(QLORA_ERR_HIP, "reading the out-of-bounds counters failed");

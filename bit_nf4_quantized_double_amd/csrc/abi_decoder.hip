@@ -110,6 +110,22 @@ qlora::AttnPlan plan_of(const qlora_attention* a, int cus) {
 
 size_t delta_bytes(const qlora_attention* a) { return round_up((size_t)a->tokens_q * (size_t)a->heads * 4u); }
 
+int check_ce_sizes(int64_t M, int64_t K, int64_t V) {
+  int st;
+  if ((st = check_range(M, INT_MAX, "M")) || (st = check_range(K, 1 << 20, "K")) || (st = check_range(V, 1 << 24, "V")))
+    return st;
+  if (K < 8 || K % 8) return fail(QLORA_ERR_SHAPE, "K must be a positive multiple of 8");
+  if (V < 1) return fail(QLORA_ERR_SHAPE, "V must be at least 1");
+  return QLORA_OK;
+}
+
+int check_aligned(const void* p, int align, const char* name) {
+  if (!p) return fail(QLORA_ERR_INVALID_ARG, std::string(name) + " is NULL");
+  if (reinterpret_cast<uintptr_t>(p) % align)
+    return fail(QLORA_ERR_ALIGN, std::string(name) + " must be " + std::to_string(align) + "-byte aligned");
+  return QLORA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -223,6 +239,58 @@ int qlora_attention_bwd(const qlora_attention* a, const qlora_heads* dO, const q
     float* delta = static_cast<float*>(ws);
     float* top = reinterpret_cast<float*>(static_cast<char*>(ws) + delta_bytes(a));
     return done(qlora::launch_attn_bwd(g, delta, top, stream), "attention backward launch");
+  });
+}
+
+size_t qlora_cross_entropy_workspace_bytes(int64_t M, int64_t K, int64_t V, int with_gradient) {
+  size_t n = 0;
+  guarded([&] {
+    if (check_ce_sizes(M, K, V) == QLORA_OK && M > 0)
+      n = qlora::ce_workspace_bytes(M, K, V, with_gradient != 0, qlora::device_compute_units());
+    return (int)QLORA_OK;
+  });
+  return n;
+}
+
+int qlora_cross_entropy(const void* X, int64_t ldx, const void* W, int64_t ldw, const int64_t* targets, int64_t M,
+                        int64_t K, int64_t V, int64_t ignore_index, const float* dloss, float* loss, float* lse,
+                        uint16_t* dX, int dtype, void* ws, size_t ws_bytes, hipStream_t stream) {
+  return guarded([&] {
+    int st;
+    if ((st = check_ce_sizes(M, K, V)) || (st = check_type16(dtype))) return st;
+    if (M == 0) return (int)QLORA_OK;
+    if ((st = check_aligned(X, 2, "X")) || (st = check_aligned(W, 16, "W")) || (st = check_aligned(targets, 8, "targets")) ||
+        (st = check_aligned(loss, 4, "loss")) || (st = check_aligned(lse, 4, "lse")))
+      return st;
+    if (dloss && (st = check_aligned(dloss, 4, "dloss"))) return st;
+    if (dX && (st = check_aligned(dX, 16, "dX"))) return st;
+    if (M == 1) ldx = K;
+    if (V == 1) ldw = K;
+    if (ldx < K || ldw < K) return fail(QLORA_ERR_INVALID_ARG, "a row stride is below the row length");
+    if (ldx > kMostStride || ldw > (1 << 22)) return fail(QLORA_ERR_SHAPE, "a row stride is too large");
+    if (ldw % 8) return fail(QLORA_ERR_ALIGN, "ldw must be a multiple of 8");
+    if ((const void*)dX == X && ldx != K) return fail(QLORA_ERR_INVALID_ARG, "dX may be X only where its rows are contiguous");
+    const int cus = qlora::device_compute_units();
+    if (!ws || ws_bytes < qlora::ce_workspace_bytes(M, K, V, dX != nullptr, cus))
+      return fail(QLORA_ERR_WORKSPACE, "cross entropy workspace too small");
+    if (!aligned16(ws)) return fail(QLORA_ERR_ALIGN, "workspace must be 16-byte aligned");
+    qlora::CeArgs a{};
+    a.x = static_cast<const uint16_t*>(X); a.w = static_cast<const uint16_t*>(W);
+    a.ldx = ldx; a.ldw = ldw; a.m = M; a.k = K; a.v = V;
+    a.targets = targets; a.ignore = ignore_index; a.dloss = dloss;
+    a.loss = loss; a.lse = lse; a.dx = dX; a.f16 = dtype == QLORA_F16;
+    return done(qlora::launch_ce(a, ws, cus, stream), "cross entropy launch");
+  });
+}
+
+int qlora_scale_rows(const uint16_t* X, const float* g, int64_t M, int64_t K, uint16_t* Y, int dtype, hipStream_t stream) {
+  return guarded([&] {
+    int st;
+    if ((st = check_range(M, INT_MAX, "M")) || (st = check_range(K, 1 << 20, "K")) || (st = check_type16(dtype))) return st;
+    if (K % 8) return fail(QLORA_ERR_SHAPE, "K must be a multiple of 8");
+    if (M == 0 || K == 0) return (int)QLORA_OK;
+    if ((st = check_aligned(X, 16, "X")) || (st = check_aligned(g, 4, "g")) || (st = check_aligned(Y, 16, "Y"))) return st;
+    return done(qlora::launch_scale_rows(X, g, M, K, Y, dtype == QLORA_F16, stream), "row scale launch");
   });
 }
 

@@ -58,4 +58,20 @@ size_t attn_part_bytes(const AttnPlan& p, int64_t tq, int64_t heads, int64_t d);
 hipError_t launch_attn_fwd(const AttnArgs& a, const AttnPlan& p, hipStream_t stream);
 hipError_t launch_attn_bwd(const AttnArgs& a, float* delta, float* top, hipStream_t stream);
 
+// ---- the head's cross entropy (cross_entropy.hip) ----
+struct CeArgs {
+  const uint16_t *x, *w;  // [m, k] (ldx), [v, k] (ldw)
+  int64_t ldx, ldw, m, k, v;
+  const int64_t* targets;  // [m]
+  int64_t ignore;
+  const float* dloss;      // [m] or NULL (ones)
+  float *loss, *lse;       // [m]
+  uint16_t* dx;            // [m, k] contiguous, or NULL: no gradient
+  bool f16;
+};
+size_t ce_workspace_bytes(int64_t m, int64_t k, int64_t v, bool grad, int compute_units);
+hipError_t launch_ce(const CeArgs& a, void* ws, int compute_units, hipStream_t stream);
+hipError_t launch_scale_rows(const uint16_t* x, const float* g, int64_t m, int64_t k, uint16_t* out, bool f16,
+                             hipStream_t stream);
+
 }  // namespace qlora

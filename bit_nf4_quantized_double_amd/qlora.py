@@ -125,8 +125,8 @@ def _load(path: str) -> ctypes.CDLL:
         fn = getattr(L, name)
         fn.restype = res
         fn.argtypes = args
-    from . import attention, int8, rotary, rows  # their own entry points of the same library
-    for part in (rows, int8, rotary, attention):
+    from . import attention, cross_entropy, int8, rotary, rows  # their own entry points of the same library
+    for part in (rows, int8, rotary, attention, cross_entropy):
         part._bind(L)
     _loaded[path] = L
     return L

@@ -628,6 +628,37 @@ int qlora_attention_bwd(const qlora_attention *a, const qlora_heads *dO, const q
  * `compute_units` <= 0: the current device's. */
 int qlora_attention_plan(const qlora_attention *a, int compute_units, int64_t out[2]);
 
+/*
+ * Softmax cross entropy of hidden states X [M, K] (ldx) under a frozen output
+ * head W [V, K] (ldw), without its logits:
+ *     z = X W^T in fp32,  lse[m] = log sum_v exp z[m][v],
+ *     loss[m] = lse[m] - z[m][targets[m]]           (0 where the target is ignore_index)
+ *     dX[m] = E(dloss[m] (softmax(z[m]) - 1 at the target) W)   (zeros there)
+ * dX NULL: no gradient.  dloss NULL: ones.  There is no dW: the head is frozen.
+ * A target that is neither an entry nor ignore_index gives a NaN loss and
+ * gradient.  The target's term is kept apart in fp32, so that small losses and
+ * their gradients keep their digits; the others' weights are rounded to 16 bits
+ * for the product with W (fp16: those 2^-29 below the largest are zero).
+ *   X        any stride ldx >= K and 2-byte alignment
+ *   W        16-byte aligned, ldw a multiple of 8 up to 2^22; K a multiple of 8, at least 8, up to 2^20
+ *   V        at least 1, up to 2^24
+ *   targets  device int64 [M]; loss, lse, dloss fp32 [M]; dX contiguous, 16-byte
+ *            aligned; it may be X itself (ldx == K)
+ * Workspace: qlora_cross_entropy_workspace_bytes(M, K, V, with dX), all of it
+ * needed (QLORA_ERR_WORKSPACE); it stops growing with M at 8192 tokens.  Same
+ * inputs, same bits.
+ */
+size_t qlora_cross_entropy_workspace_bytes(int64_t M, int64_t K, int64_t V, int with_gradient);
+int qlora_cross_entropy(const void *X, int64_t ldx, const void *W, int64_t ldw, const int64_t *targets,
+                        int64_t M, int64_t K, int64_t V, int64_t ignore_index, const float *dloss,
+                        float *loss, float *lse, uint16_t *dX, int dtype, void *ws, size_t ws_bytes,
+                        hipStream_t stream);
+
+/* Y[m][k] = E(g[m] X[m][k]): rows of a contiguous 16-bit matrix times fp32
+ * numbers, K a multiple of 8 (the loss's gradient times what comes from above). */
+int qlora_scale_rows(const uint16_t *X, const float *g, int64_t M, int64_t K, uint16_t *Y, int dtype,
+                     hipStream_t stream);
+
 /* Host function: static description of a status code. */
 const char *qlora_status_string(int status);
 
