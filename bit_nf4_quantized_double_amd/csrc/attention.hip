@@ -82,7 +82,6 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
   const int32_t wfirst = first + (KW == 1 ? wave * 32 : 0);
   const int32_t end = a.causal ? max(0, min(ks.n, (min(first + BM, rows) - 1) / a.group + off + 1)) : ks.n;
   const int32_t whole = a.causal ? min(ks.n, first / a.group + off + 1) : ks.n;
-  const int32_t wwhole = a.causal ? min(ks.n, wfirst / a.group + off + 1) : ks.n;
   const int32_t wend = a.causal ? min(ks.n, (min(wfirst + 32, rows) - 1) / a.group + off + 1) : ks.n;
   const int32_t ntiles = (end + BN - 1) / BN, per = (ntiles + a.splits - 1) / a.splits;
   const int32_t k0 = z * per + (KW == 1 ? 0 : wave), k1 = min(ntiles, (z + 1) * per);
@@ -135,7 +134,9 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
   for (int b = 0; b < DB; ++b) o[b] = (f32x16)(0.f);
   const float c2 = a.scale * kLog2e;
 
-  auto tile = [&](int32_t kt, const uint8_t* kb, bool bad) {
+  // MASKED: a tile that some of the rows do not see in full
+  auto tile = [&](int32_t kt, const uint8_t* kb, bool bad, auto MASKED) {
+    constexpr bool kMasked = decltype(MASKED)::value;
     const uint8_t* vb = kb + BYTES;
     f32x16 s[NU];
 #pragma unroll
@@ -144,8 +145,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
 #pragma unroll
       for (int i = 0; i < 2 * DB; ++i) s[u] = E::mfma32(frag_rows<E, DB>(kb, 32 * u, i, lane), qf[i], s[u]);
     }
-    const bool masked = (kt + 1) * BN > wwhole;
-    if (masked) {
+    if constexpr (kMasked) {
 #pragma unroll
       for (int u = 0; u < NU; ++u)
 #pragma unroll
@@ -181,24 +181,25 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
     typename E::v8 p[2 * NU];
 #pragma unroll
     for (int i = 0; i < 2 * NU; ++i) p[i] = pack8<E>(s[i / 2], 8 * (i % 2));
-    if (!bad) {
 #pragma unroll
-      for (int b = 0; b < DB; ++b)
+    for (int b = 0; b < DB; ++b) {
+      if (!kMasked || !bad) {
 #pragma unroll
         for (int i = 0; i < 2 * NU; ++i) o[b] = E::mfma32(E::vec(frag_cols<DB>(vb, 16 * i, b, lane)), p[i], o[b]);
-    } else {
+      } else {
+        f32x16 c = (f32x16)(0.f);
 #pragma unroll
-      for (int b = 0; b < DB; ++b) {
+        for (int i = 0; i < 2 * NU; ++i) {
+          const uint4 v = frag_cols<DB>(vb, 16 * i, b, lane);
+          f32x16 sees;
 #pragma unroll
-        for (int i = 0; i < 2 * NU; ++i)
-          o[b] = E::mfma32(E::vec(finite_part<E>(frag_cols<DB>(vb, 16 * i, b, lane))), p[i], o[b]);
+          for (int r = 8 * (i % 2); r < 8 * (i % 2) + 8; ++r)
+            sees[r] = kt * BN + 32 * (i / 2) + 8 * (r / 4) + 4 * half + r % 4 > last ? 0.f : 1.f;
+          o[b] = E::mfma32(E::vec(finite_part<E>(v)), p[i], o[b]);
+          c = E::mfma32(E::vec(nonfinite_counts<E>(v)), pack8<E>(sees, 8 * (i % 2)), c);
+        }
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
-#pragma unroll 1
-          for (int j = 0; j < BN; ++j) {
-            const float x = tile_value<E, DB>(vb, j, 32 * b + 8 * (r / 4) + 4 * half + r % 4);
-            if (kt * BN + j <= last && !(fabsf(x) < INFINITY)) o[b][r] += x;
-          }
+        for (int r = 0; r < 16; ++r) o[b][r] += counted(c[r]);
       }
     }
   };
@@ -210,22 +211,28 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
     store(k0, 0);
     load(k0 + 1);
     __syncthreads();
-    for (int32_t kt = k0; kt < k1; ++kt) {
-      const int buf = (kt - k0) & 1;
-      if (kt + 1 < k1) {
-        store(kt + 1, buf ^ 1);
-        load(kt + 2);
+    auto go = [&](int32_t from, int32_t to, auto MASKED) {
+      for (int32_t kt = from; kt < to; ++kt) {
+        const int buf = (kt - k0) & 1;
+        if (kt + 1 < k1) {
+          store(kt + 1, buf ^ 1);
+          load(kt + 2);
+        }
+        if (!decltype(MASKED)::value || kt * BN < wend) tile(kt, mine + buf * 2 * BYTES, s_bad[buf] == kt + 1, MASKED);
+        __syncthreads();
       }
-      if (kt * BN < wend) tile(kt, mine + buf * 2 * BYTES, s_bad[buf] == kt + 1);
-      __syncthreads();
-    }
+    };
+    const int32_t kf = max(k0, min(k1, whole / BN));  // the first tile that not all rows see in full
+    go(k0, kf, std::false_type{});
+    go(kf, k1, std::true_type{});
   } else {
     load(k0);
     for (int32_t kt = k0; kt < k1; kt += KW) {
       const bool bad = store(kt, 0);
       load(kt + KW);
       own_lds_order();
-      tile(kt, mine, bad);
+      if ((kt + 1) * BN <= whole) tile(kt, mine, false, std::false_type{});
+      else tile(kt, mine, bad, std::true_type{});
       own_lds_order();
     }
   }
@@ -262,7 +269,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
   } else {
     // the waves' keys together: block b of the rows' values by wave b
     float* so = reinterpret_cast<float*>(lds);
-    static_assert(sizeof(lds) >= KW * DB * 16 * 64 * 4 || KW == 1, "sums of all waves");
+    static_assert(sizeof(lds) >= (size_t)KW * DB * 16 * 64 * 4 || KW == 1, "sums of all waves");
     if (half == 0) {
       s_m[wave][lane] = run.m;
       s_l[wave][lane] = run.l;

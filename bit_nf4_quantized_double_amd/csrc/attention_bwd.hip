@@ -143,7 +143,6 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
   const int32_t last = !live ? -1 : a.causal ? min(ks.n - 1, tok + off) : ks.n - 1;
   const int32_t end = a.causal ? max(0, min(ks.n, (min(first + BM, rows) - 1) / a.group + off + 1)) : ks.n;
   const int32_t whole = a.causal ? min(ks.n, first / a.group + off + 1) : ks.n;
-  const int32_t wwhole = a.causal ? min(ks.n, wfirst / a.group + off + 1) : ks.n;
   const int32_t wend = a.causal ? min(ks.n, (min(wfirst + 32, rows) - 1) / a.group + off + 1) : ks.n;
   const int32_t k1 = (end + BN - 1) / BN;
 
@@ -201,9 +200,10 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
   f32x16 dq[DB];
 #pragma unroll
   for (int b = 0; b < DB; ++b) dq[b] = (f32x16)(0.f);
-  auto tile = [&](int32_t kt, const uint8_t* kb, bool bad) {
+  // MASKED: a tile that some of the rows do not see in full
+  auto tile = [&](int32_t kt, const uint8_t* kb, bool bad, auto MASKED) {
+    constexpr bool kMasked = decltype(MASKED)::value;
     const uint8_t* vb = kb + BYTES;
-    const bool masked = (kt + 1) * BN > wwhole;
 #pragma unroll
     for (int u = 0; u < BN / 32; ++u) {
       f32x16 s = (f32x16)(0.f), dp = (f32x16)(0.f);
@@ -214,7 +214,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
 #pragma unroll
       for (int r = 0; r < 16; ++r)
         s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], c2, -lse)) * ((dp[r] - delta) * up);
-      if (masked) {
+      if constexpr (kMasked) {
 #pragma unroll
         for (int r = 0; r < 16; ++r)
           if (kt * BN + 32 * u + 8 * (r / 4) + 4 * half + r % 4 > last) s[r] = 0.f;
@@ -222,24 +222,24 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
       typename E::v8 p[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) p[i] = pack8<E>(s, 8 * i);
-      if (!bad) {
 #pragma unroll
-        for (int b = 0; b < DB; ++b)
+      for (int b = 0; b < DB; ++b) {
+        if (!kMasked || !bad) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) dq[b] = E::mfma32(E::vec(frag_cols<DB>(kb, 32 * u + 16 * i, b, lane)), p[i], dq[b]);
-      } else {
+        } else {
+          f32x16 c = (f32x16)(0.f), sees;
 #pragma unroll
-        for (int b = 0; b < DB; ++b) {
+          for (int r = 0; r < 16; ++r) sees[r] = kt * BN + 32 * u + 8 * (r / 4) + 4 * half + r % 4 > last ? 0.f : 1.f;
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            dq[b] = E::mfma32(E::vec(finite_part<E>(frag_cols<DB>(kb, 32 * u + 16 * i, b, lane))), p[i], dq[b]);
+          for (int i = 0; i < 2; ++i) {
+            const uint4 k = frag_cols<DB>(kb, 32 * u + 16 * i, b, lane);
+            dq[b] = E::mfma32(E::vec(finite_part<E>(k)), p[i], dq[b]);
+            c = E::mfma32(E::vec(nonfinite_counts<E>(k)), pack8<E>(sees, 8 * i), c);
+          }
+          // a key that is not finite makes scores of 0 or NaN weight: NaN
 #pragma unroll
-          for (int r = 0; r < 16; ++r)
-#pragma unroll 1
-            for (int j = 0; j < 32; ++j) {
-              const float x = tile_value<E, DB>(kb, 32 * u + j, 32 * b + 8 * (r / 4) + 4 * half + r % 4);
-              if (kt * BN + 32 * u + j <= last && !(fabsf(x) < INFINITY)) dq[b][r] += x * 0.f;
-            }
+          for (int r = 0; r < 16; ++r) dq[b][r] += c[r] > 0.f ? NAN : 0.f;
         }
       }
     }
@@ -251,15 +251,20 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
   store(0, 0);
   load(1);
   __syncthreads();
-  for (int32_t kt = 0; kt < k1; ++kt) {
-    const int buf = kt & 1;
-    if (kt + 1 < k1) {
-      store(kt + 1, buf ^ 1);
-      load(kt + 2);
+  auto go = [&](int32_t from, int32_t to, auto MASKED) {
+    for (int32_t kt = from; kt < to; ++kt) {
+      const int buf = kt & 1;
+      if (kt + 1 < k1) {
+        store(kt + 1, buf ^ 1);
+        load(kt + 2);
+      }
+      if (!decltype(MASKED)::value || kt * BN < wend) tile(kt, lds + buf * 2 * BYTES, s_bad[buf] == kt + 1, MASKED);
+      __syncthreads();
     }
-    if (kt * BN < wend) tile(kt, lds + buf * 2 * BYTES, s_bad[buf] == kt + 1);
-    __syncthreads();
-  }
+  };
+  const int32_t kf = max(0, min(k1, whole / BN));  // the first tile that not all rows see in full
+  go(0, kf, std::false_type{});
+  go(kf, k1, std::true_type{});
   const float f = a.scale / up;
 #pragma unroll
   for (int b = 0; b < DB; ++b) store_block<E>(a.dq, at, live, b, a.d, dq[b], f, lane);
@@ -270,7 +275,7 @@ template <typename E, int DB>
 __global__ __launch_bounds__(256, 2) void k_attn_bwd_kv(AttnArgs a) {
   constexpr int BQ = 32, BK = 128;
   constexpr int CH = TileLayout<DB>::kChunks, PER = BQ * CH / 256, BYTES = BQ * TileLayout<DB>::kPitch;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[4 * BYTES];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[4 * BYTES], s_v[BK * TileLayout<DB>::kPitch];
   __shared__ __attribute__((aligned(16))) float s_lse[2][BQ], s_delta[2][BQ];
   __shared__ __attribute__((aligned(16))) int s_last[2][BQ];
   __shared__ int s_bad[2];
@@ -298,14 +303,26 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_kv(AttnArgs a) {
   const int64_t qsize = clampl(region_start(a.cu_q, a.batch, a.tq, rg.seq + 2), q0, a.tq) - q0;
   const int32_t nq = seq_length(a.len_q, rg.seq, a.batch, qsize), rows = nq * a.group, off = nk - nq;
   const int32_t t0 = a.causal ? max(0, key0 - off) : 0;  // the first query that sees the first key
+  // tiles of rows: from r0 on; from rf on every row sees all keys here.  (Rows past
+  // the last have P = 0, keys past the last are not stored: neither needs a mask.)
+  const int64_t tf = a.causal ? max(0, min(key0 + BK, nk) - 1 - off) : 0;
   const int32_t r0 = (int32_t)min((int64_t)t0 * a.group, (int64_t)rows) / BQ, r1 = (rows + BQ - 1) / BQ;
+  const int32_t rf = max(r0, (int32_t)min((tf * a.group + BQ - 1) / BQ, (int64_t)r1));
 
-  typename E::v8 kf[2 * DB], vf[2 * DB];
+  // K's operands stay in registers; V's are read from LDS each time (with both in
+  // registers beside dK and dV the kernel spills)
+  typename E::v8 kf[2 * DB];
 #pragma unroll
   for (int s = 0; s < 2 * DB; ++s) {
     const int c = 16 * s + 8 * half;
     kf[s] = E::vec(load16(a.k, (rg.start + key) * a.k.token + kv_head * a.k.head + c, live && c < a.d));
-    vf[s] = E::vec(load16(a.v, (rg.start + key) * a.v.token + kv_head * a.v.head + c, live && c < a.d));
+  }
+#pragma unroll
+  for (int u = 0; u < BK * CH / 256; ++u) {
+    const int c = u * 256 + tid, ch = c % CH;
+    const int32_t k = key0 + c / CH;
+    *reinterpret_cast<uint4*>(s_v + TileLayout<DB>::at(c / CH, ch)) =
+        load16(a.v, (rg.start + k) * a.v.token + kv_head * a.v.head + ch * 8, k < nk && ch * 8 < a.d);
   }
   float up = 1.f;
   if constexpr (IsF16<E>::value) {
@@ -351,7 +368,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_kv(AttnArgs a) {
       const int c = u * 256 + tid;
       *reinterpret_cast<uint4*>(to + TileLayout<DB>::at(c / CH, c % CH)) = st[0][u];
       *reinterpret_cast<uint4*>(to + BYTES + TileLayout<DB>::at(c / CH, c % CH)) = st[1][u];
-      nf |= not_finite<E>(st[0][u]) | not_finite<E>(st[1][u]);
+      if (rt < rf) nf |= not_finite<E>(st[0][u]) | not_finite<E>(st[1][u]);
     }
     if (nf) s_bad[buf] = rt + 1;
     if (tid < BQ) {
@@ -364,13 +381,14 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_kv(AttnArgs a) {
   f32x16 dk[DB], dv[DB];
 #pragma unroll
   for (int b = 0; b < DB; ++b) dk[b] = dv[b] = (f32x16)(0.f);
-  auto tile = [&](int32_t rt, int buf) {
+  auto tile = [&](int32_t rt, int buf, auto MASKED) {
+    constexpr bool kMasked = decltype(MASKED)::value;
     const uint8_t *qb = lds + buf * 2 * BYTES, *db = qb + BYTES;
     f32x16 s = (f32x16)(0.f), dp = (f32x16)(0.f);
 #pragma unroll
     for (int i = 0; i < 2 * DB; ++i) s = E::mfma32(frag_rows<E, DB>(qb, 0, i, lane), kf[i], s);
 #pragma unroll
-    for (int i = 0; i < 2 * DB; ++i) dp = E::mfma32(frag_rows<E, DB>(db, 0, i, lane), vf[i], dp);
+    for (int i = 0; i < 2 * DB; ++i) dp = E::mfma32(frag_rows<E, DB>(db, 0, i, lane), frag_rows<E, DB>(s_v, 32 * wave, i, lane), dp);
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       const float4 l = *reinterpret_cast<const float4*>(&s_lse[buf][8 * g + 4 * half]);
@@ -383,9 +401,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_kv(AttnArgs a) {
         dp[r] = s[r] * ((dp[r] - es[j]) * ups);
       }
     }
-    // the first row sees the fewest keys
-    const bool masked = (rt + 1) * BQ > rows || wkey0 + 31 > s_last[buf][0];
-    if (masked) {
+    if constexpr (kMasked) {
 #pragma unroll
       for (int r = 0; r < 16; ++r)
         if (key > s_last[buf][8 * (r / 4) + 4 * half + r % 4]) s[r] = dp[r] = 0.f;
@@ -396,32 +412,32 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_kv(AttnArgs a) {
       p[i] = pack8<E>(s, 8 * i);
       ds[i] = pack8<E>(dp, 8 * i);
     }
-    if (!(masked && s_bad[buf] == rt + 1)) {
+    const bool bad = kMasked && s_bad[buf] == rt + 1;
 #pragma unroll
-      for (int b = 0; b < DB; ++b)
+    for (int b = 0; b < DB; ++b) {
+      if (!kMasked || !bad) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           dv[b] = E::mfma32(E::vec(frag_cols<DB>(db, 16 * i, b, lane)), p[i], dv[b]);
           dk[b] = E::mfma32(E::vec(frag_cols<DB>(qb, 16 * i, b, lane)), ds[i], dk[b]);
         }
-    } else {
+      } else {
+        f32x16 c = (f32x16)(0.f), e = (f32x16)(0.f), sees;
 #pragma unroll
-      for (int b = 0; b < DB; ++b) {
+        for (int r = 0; r < 16; ++r) sees[r] = key > s_last[buf][8 * (r / 4) + 4 * half + r % 4] ? 0.f : 1.f;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          dv[b] = E::mfma32(E::vec(finite_part<E>(frag_cols<DB>(db, 16 * i, b, lane))), p[i], dv[b]);
-          dk[b] = E::mfma32(E::vec(finite_part<E>(frag_cols<DB>(qb, 16 * i, b, lane))), ds[i], dk[b]);
+          const uint4 x = frag_cols<DB>(db, 16 * i, b, lane), y = frag_cols<DB>(qb, 16 * i, b, lane);
+          dv[b] = E::mfma32(E::vec(finite_part<E>(x)), p[i], dv[b]);
+          dk[b] = E::mfma32(E::vec(finite_part<E>(y)), ds[i], dk[b]);
+          c = E::mfma32(E::vec(nonfinite_counts<E>(x)), pack8<E>(sees, 8 * i), c);
+          e = E::mfma32(E::vec(nonfinite_counts<E>(y)), pack8<E>(sees, 8 * i), e);
         }
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
-#pragma unroll 1
-          for (int j = 0; j < BQ; ++j) {
-            if (key > s_last[buf][j]) continue;
-            const int c = 32 * b + 8 * (r / 4) + 4 * half + r % 4;
-            const float x = tile_value<E, DB>(db, j, c), y = tile_value<E, DB>(qb, j, c);
-            if (!(fabsf(x) < INFINITY)) dv[b][r] += x;
-            if (!(fabsf(y) < INFINITY)) dk[b][r] += y * 0.f;
-          }
+        for (int r = 0; r < 16; ++r) {
+          dv[b][r] += counted(c[r]);
+          dk[b][r] += e[r] > 0.f ? NAN : 0.f;
+        }
       }
     }
   };
@@ -432,15 +448,19 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_kv(AttnArgs a) {
   store(r0, 0);
   load(r0 + 1);
   __syncthreads();
-  for (int32_t rt = r0; rt < r1; ++rt) {
-    const int buf = (rt - r0) & 1;
-    if (rt + 1 < r1) {
-      store(rt + 1, buf ^ 1);
-      load(rt + 2);
+  auto go = [&](int32_t from, int32_t to, auto MASKED) {
+    for (int32_t rt = from; rt < to; ++rt) {
+      const int buf = (rt - r0) & 1;
+      if (rt + 1 < r1) {
+        store(rt + 1, buf ^ 1);
+        load(rt + 2);
+      }
+      tile(rt, buf, MASKED);
+      __syncthreads();
     }
-    tile(rt, buf);
-    __syncthreads();
-  }
+  };
+  go(r0, rf, std::true_type{});
+  go(rf, r1, std::false_type{});
   const float fk = a.scale / up, fv = __builtin_amdgcn_exp2f(-kShift);
 #pragma unroll
   for (int b = 0; b < DB; ++b) {

@@ -78,23 +78,17 @@ __device__ __forceinline__ Keys keys_of(const AttnArgs& a, int32_t seq) {
   return Keys{s, seq_length(a.len_k, seq, a.batch, e - s)};
 }
 
-// 16-byte chunks of a tile's row in LDS are permuted by chunk ^ spread(row): the
-// 8 (16) rows that a wave's b128 reads of one column touch at a time, and the 4
-// rows by 32 (64) bytes of its transposing reads, fall into different banks.
-template <int DB>
-__device__ __forceinline__ uint32_t spread(uint32_t r) {
-  const uint32_t f = (((r ^ (r >> 3)) & 1) << 3) | ((r & 3) << 1 & 4) | ((r & 1) << 1) | ((r >> 2) & 1);
-  return DB >= 4 ? f : f & 7;
-}
-
-// A tile: rows of DB * 32 16-bit values (chunks past d are zeros).
+// A tile in LDS: rows of DB * 32 16-bit values (chunks of 16 bytes past d are
+// zeros), 32 bytes further apart than they are long.  The 8 rows that a wave's
+// b128 reads of one column touch at a time, and the 4 rows by 32 bytes of its
+// transposing reads, then fall into different banks, and every address is a
+// lane's base plus a constant (with chunks permuted by row instead, each needed
+// a register of its own).
 template <int DB>
 struct TileLayout {
-  static constexpr int kPitch = DB * 64;   // bytes of a row
-  static constexpr int kChunks = DB * 4;   // 16-byte chunks of a row
-  static __device__ __forceinline__ uint32_t at(uint32_t row, uint32_t chunk) {
-    return row * kPitch + ((chunk ^ spread<DB>(row)) << 4);
-  }
+  static constexpr int kPitch = DB * 64 + 32;  // bytes of a row
+  static constexpr int kChunks = DB * 4;       // 16-byte chunks of a row
+  static __device__ __forceinline__ uint32_t at(uint32_t row, uint32_t chunk) { return row * kPitch + chunk * 16; }
 };
 
 // MFMA operand (32 x 16): row r0 + lane % 32, columns 16 step + 8 (lane / 32) .. + 7.
@@ -148,10 +142,27 @@ template <typename E>
 __device__ __forceinline__ uint4 finite_part(const uint4& u) {
   return make_uint4(finite_part<E>(u.x), finite_part<E>(u.y), finite_part<E>(u.z), finite_part<E>(u.w));
 }
-// value (row, column) of a tile
-template <typename E, int DB>
-__device__ __forceinline__ float tile_value(const uint8_t* tile, int row, int col) {
-  return E::widen(*reinterpret_cast<const uint16_t*>(tile + TileLayout<DB>::at(row, col >> 3) + 2 * (col & 7)));
+// What infinities and NaNs of a sum's terms make of it, counted by the matrix
+// cores: +inf counts 1, -inf 128, NaN 16384 (at most 64 terms: exact in fp32).
+template <typename E>
+__device__ __forceinline__ uint4 nonfinite_counts(const uint4& u) {
+  const uint32_t d[4] = {u.x, u.y, u.z, u.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float f[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float x = E::widen((uint16_t)(d[i] >> (16 * j)));
+      f[j] = x != x ? 16384.f : x == INFINITY ? 1.f : x == -INFINITY ? 128.f : 0.f;
+    }
+    o[i] = E::pack2(f[0], f[1]);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+__device__ __forceinline__ float counted(float c) {
+  const bool minus = c >= 128.f, plus = c - 128.f * floorf(c * (1.f / 128)) > 0.f;
+  return c >= 16384.f || (minus && plus) ? NAN : minus ? -INFINITY : plus ? INFINITY : 0.f;
 }
 
 // Between a wave's own writes to LDS and other lanes' reads of them, or the
