@@ -86,7 +86,7 @@ int check_attention(const qlora_attention* a) {
     if (a->tokens_q > most / group) return fail(QLORA_ERR_SHAPE, "tokens_q * heads / kv_heads exceeds 2^31 - 256");
     // workgroups of a launch: fewer than 2^24
     if (((a->tokens_q * group + 31) / 32 + a->batch + 2) * a->kv_heads >= (1 << 24) ||
-        ((a->tokens_k + 127) / 128 + a->batch + 2) * a->kv_heads >= (1 << 24))
+        ((a->tokens_k + 127) / 128 + a->batch + 2) * a->heads >= (1 << 24))
       return fail(QLORA_ERR_SHAPE, "too many rows for one launch");
   }
   return QLORA_OK;
@@ -108,7 +108,19 @@ qlora::AttnPlan plan_of(const qlora_attention* a, int cus) {
   return qlora::attn_plan(a->tokens_q, a->tokens_k, a->batch, a->heads, a->kv_heads, cus);
 }
 
-size_t delta_bytes(const qlora_attention* a) { return round_up((size_t)a->tokens_q * (size_t)a->heads * 4u); }
+// Workspace of a backward: [delta][maxima][split sums].
+struct BwdWs {
+  size_t top, part, total;
+  int splits;
+};
+BwdWs bwd_ws(const qlora_attention* a) {
+  BwdWs L{};
+  L.splits = qlora::attn_bwd_splits(a->tokens_k, a->batch, a->heads, a->kv_heads, qlora::device_compute_units());
+  L.top = round_up((size_t)a->tokens_q * (size_t)a->heads * 4u);
+  L.part = L.top + 2 * qlora::kAttnTops * 4u;
+  L.total = L.part + qlora::attn_bwd_part_bytes(L.splits, a->tokens_k, a->kv_heads, a->head_dim);
+  return L;
+}
 
 int check_ce_sizes(int64_t M, int64_t K, int64_t V) {
   int st;
@@ -170,7 +182,7 @@ size_t qlora_attention_workspace_bytes(int op, const qlora_attention* a) {
     if (op == QLORA_OP_FWD)
       n = qlora::attn_part_bytes(plan_of(a, qlora::device_compute_units()), a->tokens_q, a->heads, a->head_dim);
     else if (op == QLORA_OP_BWD)
-      n = delta_bytes(a) + 2 * qlora::kAttnTops * 4u;
+      n = bwd_ws(a).total;
     return (int)QLORA_OK;
   });
   return n;
@@ -236,9 +248,11 @@ int qlora_attention_bwd(const qlora_attention* a, const qlora_heads* dO, const q
     g.dout = heads_arg(dO, tq, h, d); g.q = heads_arg(Q, tq, h, d); g.k = heads_arg(K, tk, hk, d);
     g.v = heads_arg(V, tk, hk, d); g.o = heads_arg(O, tq, h, d); g.lse = const_cast<float*>(lse);
     g.dq = heads_arg(dQ, tq, h, d); g.dk = heads_arg(dK, tk, hk, d); g.dv = heads_arg(dV, tk, hk, d);
-    float* delta = static_cast<float*>(ws);
-    float* top = reinterpret_cast<float*>(static_cast<char*>(ws) + delta_bytes(a));
-    return done(qlora::launch_attn_bwd(g, delta, top, stream), "attention backward launch");
+    const BwdWs L = bwd_ws(a);
+    char* base = static_cast<char*>(ws);
+    return done(qlora::launch_attn_bwd(g, reinterpret_cast<float*>(base), reinterpret_cast<float*>(base + L.top),
+                                       reinterpret_cast<float*>(base + L.part), L.splits, stream),
+                "attention backward launch");
   });
 }
 

@@ -13,12 +13,8 @@
 // one query only, so maxima and sums need a single exchange between the
 // wave's halves, and the accumulators' order is the operand order of the second
 // product (O transposed = V^T P^T) with V read through the transposing LDS load.
-//
-// A masked key has weight zero, but 0 times an infinity or a NaN is a NaN: in
-// tiles where some rows do not see some keys, V is searched for such values; if
-// there are any they are left out of the product and added to the rows that see
-// them (a weight is positive, so an infinity keeps its sign).
 #include <algorithm>
+#include <climits>
 #include <type_traits>
 
 #include "attention_common.h"
@@ -42,7 +38,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
   constexpr int CH = TileLayout<DB>::kChunks, PER = BN * CH / TH, BYTES = BN * TileLayout<DB>::kPitch;
   constexpr int NBUF = KW == 1 ? 2 : 1;
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * BYTES * NBUF * KW];
-  __shared__ int s_bad[2];
+  __shared__ NonFinite<32 * DB> s_bad;
   __shared__ float s_m[4][32], s_l[4][32];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int half = lane >> 5, part_tid = KW == 1 ? tid : lane;
@@ -104,28 +100,16 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
       st[1][u] = load16(a.v, (ks.start + key) * a.v.token + kv_head * a.v.head + ch * 8, ok);
     }
   };
-  // true where the tile has keys that not all rows see, and infinities or NaNs in V
   auto store = [&](int32_t kt, int buf) {
     uint8_t* const to = mine + buf * 2 * BYTES;
+    const bool part = (kt + 1) * BN > whole;
 #pragma unroll
     for (int u = 0; u < PER; ++u) {
       const int c = u * TH + part_tid;
+      if (part && not_finite<E>(st[1][u])) s_bad.template take<E, true>(st[1][u], c % CH * 8, kt * BN + c / CH);
       *reinterpret_cast<uint4*>(to + TileLayout<DB>::at(c / CH, c % CH)) = st[0][u];
       *reinterpret_cast<uint4*>(to + BYTES + TileLayout<DB>::at(c / CH, c % CH)) = st[1][u];
     }
-    bool bad = false;
-    if ((kt + 1) * BN > whole) {
-      uint32_t nf = 0;
-#pragma unroll
-      for (int u = 0; u < PER; ++u) nf |= not_finite<E>(st[1][u]);
-      bad = nf != 0;
-      if constexpr (KW == 1) {
-        if (bad) s_bad[buf] = kt + 1;  // any writer writes the same
-      } else {
-        bad = __ballot(bad) != 0;
-      }
-    }
-    return bad;
   };
 
   Running run{-INFINITY, 0.f};
@@ -135,7 +119,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
   const float c2 = a.scale * kLog2e;
 
   // MASKED: a tile that some of the rows do not see in full
-  auto tile = [&](int32_t kt, const uint8_t* kb, bool bad, auto MASKED) {
+  auto tile = [&](int32_t kt, const uint8_t* kb, auto MASKED) {
     constexpr bool kMasked = decltype(MASKED)::value;
     const uint8_t* vb = kb + BYTES;
     f32x16 s[NU];
@@ -183,30 +167,14 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
     for (int i = 0; i < 2 * NU; ++i) p[i] = pack8<E>(s[i / 2], 8 * (i % 2));
 #pragma unroll
     for (int b = 0; b < DB; ++b) {
-      if (!kMasked || !bad) {
 #pragma unroll
-        for (int i = 0; i < 2 * NU; ++i) o[b] = E::mfma32(E::vec(frag_cols<DB>(vb, 16 * i, b, lane)), p[i], o[b]);
-      } else {
-        f32x16 c = (f32x16)(0.f);
-#pragma unroll
-        for (int i = 0; i < 2 * NU; ++i) {
-          const uint4 v = frag_cols<DB>(vb, 16 * i, b, lane);
-          f32x16 sees;
-#pragma unroll
-          for (int r = 8 * (i % 2); r < 8 * (i % 2) + 8; ++r)
-            sees[r] = kt * BN + 32 * (i / 2) + 8 * (r / 4) + 4 * half + r % 4 > last ? 0.f : 1.f;
-          o[b] = E::mfma32(E::vec(finite_part<E>(v)), p[i], o[b]);
-          c = E::mfma32(E::vec(nonfinite_counts<E>(v)), pack8<E>(sees, 8 * (i % 2)), c);
-        }
-#pragma unroll
-        for (int r = 0; r < 16; ++r) o[b][r] += counted(c[r]);
-      }
+      for (int i = 0; i < 2 * NU; ++i) o[b] = E::mfma32(E::vec(frag_cols<DB>(vb, 16 * i, b, lane)), p[i], o[b]);
     }
   };
 
+  s_bad.clear(INT_MAX);
+  __syncthreads();
   if constexpr (KW == 1) {
-    if (tid < 2) s_bad[tid] = 0;
-    __syncthreads();
     load(k0);
     store(k0, 0);
     load(k0 + 1);
@@ -218,7 +186,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
           store(kt + 1, buf ^ 1);
           load(kt + 2);
         }
-        if (!decltype(MASKED)::value || kt * BN < wend) tile(kt, mine + buf * 2 * BYTES, s_bad[buf] == kt + 1, MASKED);
+        if (!decltype(MASKED)::value || kt * BN < wend) tile(kt, mine + buf * 2 * BYTES, MASKED);
         __syncthreads();
       }
     };
@@ -228,19 +196,23 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
   } else {
     load(k0);
     for (int32_t kt = k0; kt < k1; kt += KW) {
-      const bool bad = store(kt, 0);
+      store(kt, 0);
       load(kt + KW);
       own_lds_order();
-      if ((kt + 1) * BN <= whole) tile(kt, mine, false, std::false_type{});
-      else tile(kt, mine, bad, std::true_type{});
+      if ((kt + 1) * BN <= whole) tile(kt, mine, std::false_type{});
+      else tile(kt, mine, std::true_type{});
       own_lds_order();
     }
   }
 
   run.l = half_sum(run.l);
   float* part = a.part;
-  auto finish = [&](int b, const f32x16& acc, float m, float l) {
+  auto finish = [&](int b, f32x16& acc, float m, float l) {
     const float f = l == 0.f ? 0.f : 1.f / l;
+    if (s_bad.any) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[r] += s_bad.template seen<true>(32 * b + 8 * (r / 4) + 4 * half + r % 4, last);
+    }
     if (a.splits == 1) {
       store_block<E>(a.o, o_at, live, b, a.d, acc, f, lane);
     } else if (l != 0.f) {

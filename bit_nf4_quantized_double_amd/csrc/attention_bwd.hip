@@ -14,10 +14,13 @@
 // from a bound on it: |dS| <= 2 d max|dO| max|V|, taken to 2^14 at most.  The
 // maxima are of the finite values (over the row for dQ, over all for dK).
 //
-// Masked places: P and dS are set to zero there, whatever the values are; in
-// tiles that some rows see only in part, infinities and NaNs of the second
-// products' other operand are left out and added where they are seen.
+// Masked places: P and dS are set to zero there, whatever the values are, and
+// infinities and NaNs of the second products' other operand are kept out of tiles
+// that are seen only in part.  dO's are added to dV at the end where they are
+// seen; Q's show in dK (and dV) through their rows' lse, which is a NaN; a K that
+// is not finite makes the dQ of the rows that see it NaN.
 #include <algorithm>
+#include <climits>
 #include <type_traits>
 
 #include "attention_common.h"
@@ -120,7 +123,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
   constexpr int BN = 64, BM = 128;
   constexpr int CH = TileLayout<DB>::kChunks, PER = BN * CH / 256, BYTES = BN * TileLayout<DB>::kPitch;
   __shared__ __attribute__((aligned(16))) uint8_t lds[4 * BYTES];
-  __shared__ int s_bad[2];
+  __shared__ int s_bad;  // the first key that is not finite
   __shared__ float s_top[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = lane >> 5;
   const int32_t kv_head = blockIdx.x % a.kv_heads;
@@ -183,17 +186,16 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
   };
   auto store = [&](int32_t kt, int buf) {
     uint8_t* const to = lds + buf * 2 * BYTES;
+    const bool part = (kt + 1) * BN > whole;
 #pragma unroll
     for (int u = 0; u < PER; ++u) {
       const int c = u * 256 + tid;
+      if (part && not_finite<E>(st[0][u])) {
+        atomicMin(&s_bad, kt * BN + c / CH);
+        st[0][u] = finite_part<E>(st[0][u]);
+      }
       *reinterpret_cast<uint4*>(to + TileLayout<DB>::at(c / CH, c % CH)) = st[0][u];
       *reinterpret_cast<uint4*>(to + BYTES + TileLayout<DB>::at(c / CH, c % CH)) = st[1][u];
-    }
-    if ((kt + 1) * BN > whole) {
-      uint32_t nf = 0;
-#pragma unroll
-      for (int u = 0; u < PER; ++u) nf |= not_finite<E>(st[0][u]);
-      if (nf) s_bad[buf] = kt + 1;
     }
   };
 
@@ -201,7 +203,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
 #pragma unroll
   for (int b = 0; b < DB; ++b) dq[b] = (f32x16)(0.f);
   // MASKED: a tile that some of the rows do not see in full
-  auto tile = [&](int32_t kt, const uint8_t* kb, bool bad, auto MASKED) {
+  auto tile = [&](int32_t kt, const uint8_t* kb, auto MASKED) {
     constexpr bool kMasked = decltype(MASKED)::value;
     const uint8_t* vb = kb + BYTES;
 #pragma unroll
@@ -224,28 +226,13 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
       for (int i = 0; i < 2; ++i) p[i] = pack8<E>(s, 8 * i);
 #pragma unroll
       for (int b = 0; b < DB; ++b) {
-        if (!kMasked || !bad) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) dq[b] = E::mfma32(E::vec(frag_cols<DB>(kb, 32 * u + 16 * i, b, lane)), p[i], dq[b]);
-        } else {
-          f32x16 c = (f32x16)(0.f), sees;
-#pragma unroll
-          for (int r = 0; r < 16; ++r) sees[r] = kt * BN + 32 * u + 8 * (r / 4) + 4 * half + r % 4 > last ? 0.f : 1.f;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint4 k = frag_cols<DB>(kb, 32 * u + 16 * i, b, lane);
-            dq[b] = E::mfma32(E::vec(finite_part<E>(k)), p[i], dq[b]);
-            c = E::mfma32(E::vec(nonfinite_counts<E>(k)), pack8<E>(sees, 8 * i), c);
-          }
-          // a key that is not finite makes scores of 0 or NaN weight: NaN
-#pragma unroll
-          for (int r = 0; r < 16; ++r) dq[b][r] += c[r] > 0.f ? NAN : 0.f;
-        }
+        for (int i = 0; i < 2; ++i) dq[b] = E::mfma32(E::vec(frag_cols<DB>(kb, 32 * u + 16 * i, b, lane)), p[i], dq[b]);
       }
     }
   };
 
-  if (tid < 2) s_bad[tid] = 0;
+  if (tid == 0) s_bad = INT_MAX;
   __syncthreads();
   load(0);
   store(0, 0);
@@ -258,19 +245,26 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
         store(kt + 1, buf ^ 1);
         load(kt + 2);
       }
-      if (!decltype(MASKED)::value || kt * BN < wend) tile(kt, lds + buf * 2 * BYTES, s_bad[buf] == kt + 1, MASKED);
+      if (!decltype(MASKED)::value || kt * BN < wend) tile(kt, lds + buf * 2 * BYTES, MASKED);
       __syncthreads();
     }
   };
   const int32_t kf = max(0, min(k1, whole / BN));  // the first tile that not all rows see in full
   go(0, kf, std::false_type{});
   go(kf, k1, std::true_type{});
-  const float f = a.scale / up;
+  const float f = s_bad <= last ? NAN : a.scale / up;
 #pragma unroll
   for (int b = 0; b < DB; ++b) store_block<E>(a.dq, at, live, b, a.d, dq[b], f, lane);
 }
 
 // dK and dV: 128 keys a workgroup, 32 a wave, tiles of 32 rows of queries.
+// Workgroups of split z take every query head z of a key head's sets of
+// group / splits heads; with more than one split their sums go to `part`.
+//
+// dK and dV take 128 registers, K's operands 32; V's are read from LDS each time
+// (in registers they would leave none for operands on their way).  The products
+// run in groups of two to four, whose operands are read from LDS during the group
+// before; exponentials and dS are made between the MFMAs of dO V^T and of dV.
 template <typename E, int DB>
 __global__ __launch_bounds__(256, 2) void k_attn_bwd_kv(AttnArgs a) {
   constexpr int BQ = 32, BK = 128;
@@ -278,18 +272,18 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_kv(AttnArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[4 * BYTES], s_v[BK * TileLayout<DB>::kPitch];
   __shared__ __attribute__((aligned(16))) float s_lse[2][BQ], s_delta[2][BQ];
   __shared__ __attribute__((aligned(16))) int s_last[2][BQ];
-  __shared__ int s_bad[2];
+  __shared__ NonFinite<32 * DB> s_bad;
   __shared__ float s_top[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = lane >> 5;
-  const int32_t kv_head = blockIdx.x % a.kv_heads;
-  const Region rg = find_region(a.cu_k, a.batch, a.tk, 1, BK, blockIdx.x / a.kv_heads);
+  const int32_t kv_head = blockIdx.x % a.kv_heads, z = blockIdx.x / a.kv_heads % a.splits;
+  const Region rg = find_region(a.cu_k, a.batch, a.tk, 1, BK, blockIdx.x / a.kv_heads / a.splits);
   if (rg.tile < 0 || (int64_t)rg.tile * BK >= rg.size) return;
   const int32_t nk = seq_length(a.len_k, rg.seq, a.batch, rg.size);
-  const int32_t key0 = rg.tile * BK, wkey0 = key0 + wave * 32, key = wkey0 + (lane & 31);
+  const int32_t key0 = rg.tile * BK, key = key0 + wave * 32 + (lane & 31);
   const bool live = key < nk;
-  const int64_t k_at = (rg.start + key) * a.dk.token + kv_head * a.dk.head;
-  const int64_t v_at = (rg.start + key) * a.dv.token + kv_head * a.dv.head;
-  if (a.zero_rest && !live && key < rg.size)
+  const int64_t tok = rg.start + key;
+  const int64_t k_at = tok * a.dk.token + kv_head * a.dk.head, v_at = tok * a.dv.token + kv_head * a.dv.head;
+  if (a.zero_rest && z == 0 && !live && key < rg.size)
     for (int c = 8 * half; c < a.d; c += 16) {
       if (in_bounds(k_at + c, 8, a.dk.n))
         *reinterpret_cast<uint4*>(const_cast<uint16_t*>(a.dk.p) + k_at + c) = make_uint4(0, 0, 0, 0);
@@ -301,21 +295,20 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_kv(AttnArgs a) {
   // the sequence's queries
   const int64_t q0 = region_start(a.cu_q, a.batch, a.tq, rg.seq + 1);
   const int64_t qsize = clampl(region_start(a.cu_q, a.batch, a.tq, rg.seq + 2), q0, a.tq) - q0;
-  const int32_t nq = seq_length(a.len_q, rg.seq, a.batch, qsize), rows = nq * a.group, off = nk - nq;
+  const int32_t nq = seq_length(a.len_q, rg.seq, a.batch, qsize), off = nk - nq;
+  const int32_t group = a.group / a.splits, rows = nq * group, head0 = kv_head * a.group + z * group;
   const int32_t t0 = a.causal ? max(0, key0 - off) : 0;  // the first query that sees the first key
   // tiles of rows: from r0 on; from rf on every row sees all keys here.  (Rows past
   // the last have P = 0, keys past the last are not stored: neither needs a mask.)
   const int64_t tf = a.causal ? max(0, min(key0 + BK, nk) - 1 - off) : 0;
-  const int32_t r0 = (int32_t)min((int64_t)t0 * a.group, (int64_t)rows) / BQ, r1 = (rows + BQ - 1) / BQ;
-  const int32_t rf = max(r0, (int32_t)min((tf * a.group + BQ - 1) / BQ, (int64_t)r1));
+  const int32_t r0 = (int32_t)min((int64_t)t0 * group, (int64_t)rows) / BQ, r1 = (rows + BQ - 1) / BQ;
+  const int32_t rf = max(r0, (int32_t)min((tf * group + BQ - 1) / BQ, (int64_t)r1));
 
-  // K's operands stay in registers; V's are read from LDS each time (with both in
-  // registers beside dK and dV the kernel spills)
-  typename E::v8 kf[2 * DB];
+  uint4 kf[2 * DB];
 #pragma unroll
   for (int s = 0; s < 2 * DB; ++s) {
     const int c = 16 * s + 8 * half;
-    kf[s] = E::vec(load16(a.k, (rg.start + key) * a.k.token + kv_head * a.k.head + c, live && c < a.d));
+    kf[s] = load16(a.k, tok * a.k.token + kv_head * a.k.head + c, live && c < a.d);
   }
 #pragma unroll
   for (int u = 0; u < BK * CH / 256; ++u) {
@@ -333,44 +326,56 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_kv(AttnArgs a) {
   const float ups = up * __builtin_amdgcn_exp2f(-kShift);
   const float c2 = a.scale * kLog2e;
 
+  // This thread's rows of a tile, tid / CH + u 256 / CH: as token and head, moved
+  // on from tile to tile without a division.
+  RowAt at[PER], lat;
+#pragma unroll
+  for (int u = 0; u < PER; ++u) at[u] = RowAt(r0 * BQ + (u * 256 + tid) / CH, group);
+  lat = RowAt(r0 * BQ + (tid & 31), group);
+  const int ch8 = tid % CH * 8;
+  const int64_t q_at = q0 * a.q.token + head0 * a.q.head, d_at = q0 * a.dout.token + head0 * a.dout.head;
   uint4 st[2][PER];
-  float st_lse, st_delta;
-  int st_last;
-  auto load = [&](int32_t rt) {
+  float st_lse = 0.f, st_delta = 0.f;
+  int st_last = 0;
+  // the tile that `at` stands on (nothing past the last row), and on to the next
+  auto load = [&]() {
 #pragma unroll
     for (int u = 0; u < PER; ++u) {
-      const int c = u * 256 + tid, ch = c % CH;
-      const int32_t r = rt * BQ + c / CH, tok = r / a.group, head = kv_head * a.group + r % a.group;
-      const bool ok = rt < r1 && r < rows && ch * 8 < a.d;
-      st[0][u] = load16(a.q, (q0 + tok) * a.q.token + head * a.q.head + ch * 8, ok);
-      st[1][u] = load16(a.dout, (q0 + tok) * a.dout.token + head * a.dout.head + ch * 8, ok);
+      const bool ok = at[u].tok < nq && ch8 < a.d;
+      st[0][u] = load16(a.q, q_at + at[u].tok * a.q.token + at[u].head * a.q.head + ch8, ok);
+      st[1][u] = load16(a.dout, d_at + at[u].tok * a.dout.token + at[u].head * a.dout.head + ch8, ok);
+      at[u].move(BQ, group);
     }
     if (tid < BQ) {
-      const int32_t r = rt * BQ + tid, tok = r / a.group, head = kv_head * a.group + r % a.group;
-      const int64_t at = (q0 + tok) * a.heads + head;
+      const int64_t i = (q0 + lat.tok) * a.heads + head0 + lat.head;
       st_lse = INFINITY;
       st_delta = 0.f;
       st_last = -1;
-      if (rt < r1 && r < rows && in_bounds(at, 1, a.tq * a.heads)) {
-        st_lse = a.lse[at] * kLog2e;
+      if (lat.tok < nq && in_bounds(i, 1, a.tq * a.heads)) {
+        st_lse = a.lse[i] * kLog2e;
         if (st_lse == -INFINITY) st_lse = INFINITY;  // a row that sees nothing: P = 0
         st_lse -= kShift;
-        st_delta = a.delta[at];
-        st_last = a.causal ? min(nk - 1, tok + off) : nk - 1;
+        st_delta = a.delta[i];
+        st_last = a.causal ? min(nk - 1, lat.tok + off) : nk - 1;
       }
+      lat.move(BQ, group);
     }
   };
   auto store = [&](int32_t rt, int buf) {
     uint8_t* const to = lds + buf * 2 * BYTES;
-    uint32_t nf = 0;
 #pragma unroll
     for (int u = 0; u < PER; ++u) {
       const int c = u * 256 + tid;
+      if (rt < rf) {
+        if (not_finite<E>(st[1][u])) {
+          const int32_t t = (rt * BQ + c / CH) / group;
+          s_bad.template take<E, false>(st[1][u], ch8, a.causal ? min(nk - 1, t + off) : nk - 1);
+        }
+        if (not_finite<E>(st[0][u])) st[0][u] = finite_part<E>(st[0][u]);
+      }
       *reinterpret_cast<uint4*>(to + TileLayout<DB>::at(c / CH, c % CH)) = st[0][u];
       *reinterpret_cast<uint4*>(to + BYTES + TileLayout<DB>::at(c / CH, c % CH)) = st[1][u];
-      if (rt < rf) nf |= not_finite<E>(st[0][u]) | not_finite<E>(st[1][u]);
     }
-    if (nf) s_bad[buf] = rt + 1;
     if (tid < BQ) {
       s_lse[buf][tid] = st_lse;
       s_delta[buf][tid] = st_delta;
@@ -383,98 +388,206 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_kv(AttnArgs a) {
   for (int b = 0; b < DB; ++b) dk[b] = dv[b] = (f32x16)(0.f);
   auto tile = [&](int32_t rt, int buf, auto MASKED) {
     constexpr bool kMasked = decltype(MASKED)::value;
-    const uint8_t *qb = lds + buf * 2 * BYTES, *db = qb + BYTES;
+    const uint8_t *qb = lds + buf * 2 * BYTES, *db = qb + BYTES, *vb = s_v + 32 * wave * TileLayout<DB>::kPitch;
     f32x16 s = (f32x16)(0.f), dp = (f32x16)(0.f);
+    uint4 x[2][4];
+    auto rows_q = [&](int g, uint4 (&f)[4]) {
 #pragma unroll
-    for (int i = 0; i < 2 * DB; ++i) s = E::mfma32(frag_rows<E, DB>(qb, 0, i, lane), kf[i], s);
+      for (int i = 0; i < 4; ++i) f[i] = raw_rows<DB>(qb, 0, 4 * g + i, lane);
+    };
+    auto rows_d = [&](int g, uint4 (&f)[4]) {
 #pragma unroll
-    for (int i = 0; i < 2 * DB; ++i) dp = E::mfma32(frag_rows<E, DB>(db, 0, i, lane), frag_rows<E, DB>(s_v, 32 * wave, i, lane), dp);
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const float4 l = *reinterpret_cast<const float4*>(&s_lse[buf][8 * g + 4 * half]);
-      const float4 e = *reinterpret_cast<const float4*>(&s_delta[buf][8 * g + 4 * half]);
-      const float ls[4] = {l.x, l.y, l.z, l.w}, es[4] = {e.x, e.y, e.z, e.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = 4 * g + j;
-        s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], c2, -ls[j]));
-        dp[r] = s[r] * ((dp[r] - es[j]) * ups);
+      for (int i = 0; i < 2; ++i) {
+        f[i] = raw_rows<DB>(db, 0, 2 * g + i, lane);
+        f[2 + i] = raw_rows<DB>(vb, 0, 2 * g + i, lane);
       }
+    };
+    auto cols = [&](const uint8_t* t, int b, uint4 (&f)[4]) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) f[i] = frag_cols<DB>(t, 16 * i, b, lane);
+    };
+    constexpr int NS = DB / 2;  // groups of S
+    rows_q(0, x[0]);
+#pragma unroll
+    for (int g = 0; g < NS; ++g) {
+      if (g + 1 < NS) rows_q(g + 1, x[(g + 1) & 1]);
+      else rows_d(0, x[(g + 1) & 1]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s = E::mfma32(E::vec(x[g & 1][i]), E::vec(kf[4 * g + i]), s);
+      __builtin_amdgcn_sched_barrier(0);
     }
+    // dO V^T in DB groups of two; between them P, 16 / DB rows a group
+    constexpr int RG = 16 / DB;
+#pragma unroll
+    for (int g = 0; g < DB; ++g) {
+      uint4(&f)[4] = x[(NS + g) & 1];
+      if (g + 1 < DB) rows_d(g + 1, x[(NS + g + 1) & 1]);
+      else cols(db, 0, x[(NS + g + 1) & 1]);
+      float4 l[RG / 4];
+#pragma unroll
+      for (int j = 0; j < RG / 4; ++j) l[j] = *reinterpret_cast<const float4*>(&s_lse[buf][8 * (g * RG / 4 + j) + 4 * half]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) dp = E::mfma32(E::vec(f[i]), E::vec(f[2 + i]), dp);
+#pragma unroll
+      for (int j = 0; j < RG / 4; ++j) {
+        const float ls[4] = {l[j].x, l[j].y, l[j].z, l[j].w};
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int at = g * RG + 4 * j + r;
+          s[at] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[at], c2, -ls[r]));
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    bool seen[16];
     if constexpr (kMasked) {
 #pragma unroll
-      for (int r = 0; r < 16; ++r)
-        if (key > s_last[buf][8 * (r / 4) + 4 * half + r % 4]) s[r] = dp[r] = 0.f;
+      for (int r = 0; r < 16; ++r) {
+        seen[r] = key <= s_last[buf][8 * (r / 4) + 4 * half + r % 4];
+        s[r] = seen[r] ? s[r] : 0.f;
+      }
     }
     typename E::v8 p[2], ds[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      p[i] = pack8<E>(s, 8 * i);
-      ds[i] = pack8<E>(dp, 8 * i);
-    }
-    const bool bad = kMasked && s_bad[buf] == rt + 1;
+    for (int i = 0; i < 2; ++i) p[i] = pack8<E>(s, 8 * i);
+    // dV in DB groups of two; between them dS
+    auto row_delta = [&](int g) { return *reinterpret_cast<const float4*>(&s_delta[buf][8 * g + 4 * half]); };
+    auto make_ds = [&](int g, const float4& e) {
+      const float d[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+      for (int r = 4 * g; r < 4 * g + 4; ++r) {
+        dp[r] = s[r] * ((dp[r] - d[r % 4]) * ups);
+        if constexpr (kMasked) dp[r] = seen[r] ? dp[r] : 0.f;
+      }
+    };
+    constexpr int X0 = (NS + DB) & 1;
 #pragma unroll
     for (int b = 0; b < DB; ++b) {
-      if (!kMasked || !bad) {
+      uint4(&f)[4] = x[(X0 + b) & 1];
+      if (b + 1 < DB) cols(db, b + 1, x[(X0 + b + 1) & 1]);
+      else cols(qb, 0, x[(X0 + b + 1) & 1]);
+      float4 e[RG / 4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          dv[b] = E::mfma32(E::vec(frag_cols<DB>(db, 16 * i, b, lane)), p[i], dv[b]);
-          dk[b] = E::mfma32(E::vec(frag_cols<DB>(qb, 16 * i, b, lane)), ds[i], dk[b]);
-        }
-      } else {
-        f32x16 c = (f32x16)(0.f), e = (f32x16)(0.f), sees;
+      for (int j = 0; j < RG / 4; ++j) e[j] = row_delta(b * RG / 4 + j);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int r = 0; r < 16; ++r) sees[r] = key > s_last[buf][8 * (r / 4) + 4 * half + r % 4] ? 0.f : 1.f;
+      for (int i = 0; i < 2; ++i) dv[b] = E::mfma32(E::vec(f[i]), p[i], dv[b]);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint4 x = frag_cols<DB>(db, 16 * i, b, lane), y = frag_cols<DB>(qb, 16 * i, b, lane);
-          dv[b] = E::mfma32(E::vec(finite_part<E>(x)), p[i], dv[b]);
-          dk[b] = E::mfma32(E::vec(finite_part<E>(y)), ds[i], dk[b]);
-          c = E::mfma32(E::vec(nonfinite_counts<E>(x)), pack8<E>(sees, 8 * i), c);
-          e = E::mfma32(E::vec(nonfinite_counts<E>(y)), pack8<E>(sees, 8 * i), e);
-        }
+      for (int j = 0; j < RG / 4; ++j) make_ds(b * RG / 4 + j, e[j]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          dv[b][r] += counted(c[r]);
-          dk[b][r] += e[r] > 0.f ? NAN : 0.f;
-        }
-      }
+    for (int i = 0; i < 2; ++i) ds[i] = pack8<E>(dp, 8 * i);
+    constexpr int X1 = (X0 + DB) & 1;
+#pragma unroll
+    for (int b = 0; b < DB; ++b) {
+      uint4(&f)[4] = x[(X1 + b) & 1];
+      if (b + 1 < DB) cols(qb, b + 1, x[(X1 + b + 1) & 1]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) dk[b] = E::mfma32(E::vec(f[i]), ds[i], dk[b]);
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
 
-  if (tid < 2) s_bad[tid] = 0;
+  s_bad.clear(-1);
   __syncthreads();
-  load(r0);
+  load();
   store(r0, 0);
-  load(r0 + 1);
+  load();
   __syncthreads();
   auto go = [&](int32_t from, int32_t to, auto MASKED) {
     for (int32_t rt = from; rt < to; ++rt) {
       const int buf = (rt - r0) & 1;
-      if (rt + 1 < r1) {
-        store(rt + 1, buf ^ 1);
-        load(rt + 2);
-      }
+      store(rt + 1, buf ^ 1);
+      load();
       tile(rt, buf, MASKED);
       __syncthreads();
     }
   };
   go(r0, rf, std::true_type{});
   go(rf, r1, std::false_type{});
-  const float fk = a.scale / up, fv = __builtin_amdgcn_exp2f(-kShift);
+  if (s_bad.any) {
 #pragma unroll
-  for (int b = 0; b < DB; ++b) {
-    store_block<E>(a.dk, k_at, live, b, a.d, dk[b], fk, lane);
-    store_block<E>(a.dv, v_at, live, b, a.d, dv[b], fv, lane);
+    for (int b = 0; b < DB; ++b)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) dv[b][r] += s_bad.template seen<false>(32 * b + 8 * (r / 4) + 4 * half + r % 4, key);
+  }
+  const float fk = a.scale / up, fv = __builtin_amdgcn_exp2f(-kShift);
+  if (a.splits == 1) {
+#pragma unroll
+    for (int b = 0; b < DB; ++b) {
+      store_block<E>(a.dk, k_at, live, b, a.d, dk[b], fk, lane);
+      store_block<E>(a.dv, v_at, live, b, a.d, dv[b], fv, lane);
+    }
+    return;
+  }
+  const int64_t pat = ((z * a.tk + tok) * a.kv_heads + kv_head) * 2 * a.d, n = a.splits * a.tk * a.kv_heads * 2 * a.d;
+#pragma unroll
+  for (int b = 0; b < DB; ++b)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = 32 * b + 8 * i + 4 * half;
+      if (!live || c >= a.d || !in_bounds(pat + c, 4, n) || !in_bounds(pat + a.d + c, 4, n)) continue;
+      *reinterpret_cast<float4*>(a.part + pat + c) =
+          make_float4(dk[b][4 * i] * fk, dk[b][4 * i + 1] * fk, dk[b][4 * i + 2] * fk, dk[b][4 * i + 3] * fk);
+      *reinterpret_cast<float4*>(a.part + pat + a.d + c) =
+          make_float4(dv[b][4 * i] * fv, dv[b][4 * i + 1] * fv, dv[b][4 * i + 2] * fv, dv[b][4 * i + 3] * fv);
+    }
+}
+
+// The splits' sums together: 16 keys' values of all key heads a workgroup.
+template <typename E>
+__global__ __launch_bounds__(256) void k_attn_bwd_join(AttnArgs a) {
+  const Region rg = find_region(a.cu_k, a.batch, a.tk, 1, kDeltaTokens, blockIdx.x);
+  if (rg.tile < 0) return;
+  const int32_t n = seq_length(a.len_k, rg.seq, a.batch, rg.size), first = rg.tile * kDeltaTokens;
+  const int32_t keys = max(0, min(n - first, kDeltaTokens)), pieces = a.d / 8, width = a.kv_heads * 2 * pieces;
+  const int64_t size = a.tk * a.kv_heads * 2 * a.d;
+  for (int32_t i = threadIdx.x; i < keys * width; i += 256) {
+    const int32_t c = i % pieces * 8, rest = i / pieces, which = rest & 1, head = rest / 2 % a.kv_heads;
+    const int64_t tok = rg.start + first + rest / 2 / a.kv_heads;
+    const int64_t at = ((tok * a.kv_heads + head) * 2 + which) * a.d + c;
+    float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int z = 0; z < a.splits; ++z) {
+      if (!in_bounds(z * size + at, 8, a.splits * size)) continue;
+      const float4 x = *reinterpret_cast<const float4*>(a.part + z * size + at);
+      const float4 y = *reinterpret_cast<const float4*>(a.part + z * size + at + 4);
+      s[0] += x.x; s[1] += x.y; s[2] += x.z; s[3] += x.w;
+      s[4] += y.x; s[5] += y.y; s[6] += y.z; s[7] += y.w;
+    }
+    const Heads& o = which ? a.dv : a.dk;
+    const int64_t to = tok * o.token + head * o.head + c;
+    if (in_bounds(to, 8, o.n))
+      *reinterpret_cast<uint4*>(const_cast<uint16_t*>(o.p) + to) =
+          make_uint4(E::pack2(s[0], s[1]), E::pack2(s[2], s[3]), E::pack2(s[4], s[5]), E::pack2(s[6], s[7]));
   }
 }
 
 }  // namespace
 
-hipError_t launch_attn_bwd(const AttnArgs& args, float* delta, float* top, hipStream_t stream) {
+// Over how many workgroups the query heads of a key head are split: as few as
+// make four workgroups a compute unit (under a causal mask they differ in length).
+int attn_bwd_splits(int64_t tk, int64_t batch, int64_t heads, int64_t kv_heads, int compute_units) {
+  if (heads <= 0 || kv_heads <= 0) return 1;
+  const int64_t group = heads / kv_heads, units = kv_heads * std::max<int64_t>((tk + 127) / 128, batch);
+  int64_t s = 1;
+  while (s < group && (group % s != 0 || units * s < 4 * compute_units)) ++s;
+  return (int)s;
+}
+
+size_t attn_bwd_part_bytes(int splits, int64_t tk, int64_t kv_heads, int64_t d) {
+  return splits > 1 ? (size_t)splits * tk * kv_heads * 2 * d * 4 : 0;
+}
+
+hipError_t launch_attn_bwd(const AttnArgs& args, float* delta, float* top, float* part, int splits, hipStream_t stream) {
   AttnArgs a = args;
   a.delta = delta;
   a.top = top;
+  a.part = part;
+  a.splits = splits;
   const auto run = [&](auto e, auto db) {
     using E = decltype(e);
     constexpr int DB = decltype(db)::value;
@@ -485,8 +598,11 @@ hipError_t launch_attn_bwd(const AttnArgs& args, float* delta, float* top, hipSt
     } else if (a.tq > 0) {
       k_attn_delta<E><<<(uint32_t)std::min<int64_t>(dt, 1 << 20), 256, 0, stream>>>(a, delta, top);
     }
-    if (a.tk > 0)
-      k_attn_bwd_kv<E, DB><<<(uint32_t)(attn_tiles(a.tk, 1, a.batch, 128) * a.kv_heads), 256, 0, stream>>>(a);
+    if (a.tk > 0) {
+      k_attn_bwd_kv<E, DB><<<(uint32_t)(attn_tiles(a.tk, 1, a.batch, 128) * a.kv_heads * a.splits), 256, 0, stream>>>(a);
+      if (a.splits > 1)
+        k_attn_bwd_join<E><<<(uint32_t)attn_tiles(a.tk, 1, a.batch, kDeltaTokens), 256, 0, stream>>>(a);
+    }
     if (a.tq > 0)
       k_attn_bwd_q<E, DB><<<(uint32_t)(attn_tiles(a.tq, a.group, a.batch, 128) * a.kv_heads), 256, 0, stream>>>(a);
   };

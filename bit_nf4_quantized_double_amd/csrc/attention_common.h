@@ -66,6 +66,22 @@ __device__ __forceinline__ int32_t seq_length(const int32_t* len, int32_t seq, i
   return in_bounds(seq, 1, batch) ? (int32_t)clampl(len[seq], 0, size) : 0;
 }
 
+// A packed row of a sequence as token and head of the group, moved on by whole rows.
+struct RowAt {
+  int32_t tok, head;
+  RowAt() = default;
+  __device__ __forceinline__ RowAt(int32_t row, int32_t group) : tok(row / group), head(row % group) {}
+  // by n rows; n % group and n / group are the same for all lanes
+  __device__ __forceinline__ void move(int32_t n, int32_t group) {
+    tok += n / group;
+    head += n % group;
+    if (head >= group) {
+      head -= group;
+      ++tok;
+    }
+  }
+};
+
 // Keys of a sequence: [start, start + n).
 struct Keys {
   int64_t start;
@@ -92,9 +108,13 @@ struct TileLayout {
 };
 
 // MFMA operand (32 x 16): row r0 + lane % 32, columns 16 step + 8 (lane / 32) .. + 7.
+template <int DB>
+__device__ __forceinline__ uint4 raw_rows(const uint8_t* tile, int r0, int step, int lane) {
+  return *reinterpret_cast<const uint4*>(tile + TileLayout<DB>::at(r0 + (lane & 31), 2 * step + (lane >> 5)));
+}
 template <typename E, int DB>
 __device__ __forceinline__ typename E::v8 frag_rows(const uint8_t* tile, int r0, int step, int lane) {
-  return E::vec(*reinterpret_cast<const uint4*>(tile + TileLayout<DB>::at(r0 + (lane & 31), 2 * step + (lane >> 5))));
+  return E::vec(raw_rows<DB>(tile, r0, step, lane));
 }
 
 typedef __attribute__((ext_vector_type(4))) short s16x4;
@@ -142,28 +162,47 @@ template <typename E>
 __device__ __forceinline__ uint4 finite_part(const uint4& u) {
   return make_uint4(finite_part<E>(u.x), finite_part<E>(u.y), finite_part<E>(u.z), finite_part<E>(u.w));
 }
-// What infinities and NaNs of a sum's terms make of it, counted by the matrix
-// cores: +inf counts 1, -inf 128, NaN 16384 (at most 64 terms: exact in fp32).
-template <typename E>
-__device__ __forceinline__ uint4 nonfinite_counts(const uint4& u) {
-  const uint32_t d[4] = {u.x, u.y, u.z, u.w};
-  uint32_t o[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float f[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const float x = E::widen((uint16_t)(d[i] >> (16 * j)));
-      f[j] = x != x ? 16384.f : x == INFINITY ? 1.f : x == -INFINITY ? 128.f : 0.f;
-    }
-    o[i] = E::pack2(f[0], f[1]);
+// Infinities and NaNs in masked places.  A masked weight is zero, but zero times
+// one of them is a NaN, so where rows see only a part of a tile its values that
+// are not finite are kept out of LDS (zeros instead) and remembered by column:
+// which key is the first (the last query's reach is the furthest) with a +inf, a
+// -inf or a NaN.  Since masks are monotone, that is all it takes to add them, at
+// the end, to the sums that see them (weights are positive: infinities keep their
+// sign).
+template <int COLS>
+struct NonFinite {
+  int at[3][COLS];
+  int any;
+  // all threads; a barrier has to follow
+  __device__ __forceinline__ void clear(int none) {
+    for (int i = threadIdx.x; i < 3 * COLS; i += 256) at[i / COLS][i % COLS] = none;
+    if (threadIdx.x == 0) any = 0;
   }
-  return make_uint4(o[0], o[1], o[2], o[3]);
-}
-__device__ __forceinline__ float counted(float c) {
-  const bool minus = c >= 128.f, plus = c - 128.f * floorf(c * (1.f / 128)) > 0.f;
-  return c >= 16384.f || (minus && plus) ? NAN : minus ? -INFINITY : plus ? INFINITY : 0.f;
-}
+  // takes them out of columns c .. c + 7 in u, of the key (or with the reach) `value`
+  template <typename E, bool MIN>
+  __device__ __forceinline__ void take(uint4& u, int c, int value) {
+    const uint32_t d[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t w = i < 2 ? d[0] : i < 4 ? d[1] : i < 6 ? d[2] : d[3];
+      const float x = E::widen((uint16_t)(w >> (16 * (i & 1))));
+      if (fabsf(x) < INFINITY) continue;
+      int* const to = &at[x != x ? 2 : x > 0.f ? 0 : 1][c + i];
+      if (MIN) atomicMin(to, value);
+      else atomicMax(to, value);
+    }
+    any = 1;
+    u = finite_part<E>(u);
+  }
+  // what column c's make of a sum: those with a key up to (a reach from) `value` on are seen
+  template <bool MIN>
+  __device__ __forceinline__ float seen(int c, int value) const {
+    bool y[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) y[i] = MIN ? at[i][c] <= value : at[i][c] >= value;
+    return y[2] || (y[0] && y[1]) ? NAN : y[0] ? INFINITY : y[1] ? -INFINITY : 0.f;
+  }
+};
 
 // Between a wave's own writes to LDS and other lanes' reads of them, or the
 // reverse: the hardware keeps a wave's LDS operations in order, the compiler has to.

@@ -37,7 +37,8 @@ struct AttnArgs {
   const float* delta;      // [tq, heads]
   const float* top;        // fp16 backward: [2 kAttnTops] partial maxima of |dO|, then of |V|
   const int32_t *cu_q, *cu_k, *len_q, *len_k;
-  float* part;             // split keys: [splits][tq][heads][d] and then [splits][tq][heads] log-sums
+  float* part;             // forward, split keys: [splits][tq][heads][d] and then [splits][tq][heads] log-sums;
+                           // backward, split query heads: [splits][tk][kv_heads][dK, dV][d]
   int64_t tq, tk;
   int32_t batch, heads, kv_heads, group, d;
   int32_t splits;
@@ -56,7 +57,9 @@ AttnPlan attn_plan(int64_t tq, int64_t tk, int64_t batch, int64_t heads, int64_t
 size_t attn_part_bytes(const AttnPlan& p, int64_t tq, int64_t heads, int64_t d);
 
 hipError_t launch_attn_fwd(const AttnArgs& a, const AttnPlan& p, hipStream_t stream);
-hipError_t launch_attn_bwd(const AttnArgs& a, float* delta, float* top, hipStream_t stream);
+int attn_bwd_splits(int64_t tk, int64_t batch, int64_t heads, int64_t kv_heads, int compute_units);
+size_t attn_bwd_part_bytes(int splits, int64_t tk, int64_t kv_heads, int64_t d);
+hipError_t launch_attn_bwd(const AttnArgs& a, float* delta, float* top, float* part, int splits, hipStream_t stream);
 
 // ---- the head's cross entropy (cross_entropy.hip) ----
 struct CeArgs {
