@@ -40,7 +40,7 @@ int check_type16(int dtype) {
   return fail(QLORA_ERR_INVALID_ARG, "unsupported element type");
 }
 
-constexpr int64_t kMostStride = (int64_t)1 << 40;
+constexpr int64_t kMostStride = (int64_t)1 << 40, kMostTokenStride = 1 << 23;
 
 // [tokens, heads, d]: there, aligned to `align` bytes, its strides multiples of
 // that, and for an output without two elements in one place.
@@ -58,6 +58,14 @@ int check_heads(const qlora_heads* x, int64_t tokens, int64_t heads, int64_t d, 
     if (!by_token && !by_head) return fail(QLORA_ERR_INVALID_ARG, std::string(name) + ": an output's elements overlap");
   }
   return QLORA_OK;
+}
+
+// the same for attention: 16 bytes at a time, tokens near enough for 32-bit offsets inside a tile
+int check_attn_heads(const qlora_heads* x, int64_t tokens, int64_t heads, int64_t d, bool out, const char* name) {
+  const int st = check_heads(x, tokens, heads, d, 16, out, name);
+  if (st == QLORA_OK && x && tokens > 1 && heads > 0 && x->token_stride > kMostTokenStride)
+    return fail(QLORA_ERR_SHAPE, std::string(name) + ": the token stride exceeds 2^23 elements");
+  return st;
 }
 
 qlora::Heads heads_arg(const qlora_heads* x, int64_t tokens, int64_t heads, int64_t d) {
@@ -206,10 +214,10 @@ int qlora_attention_fwd(const qlora_attention* a, const qlora_heads* Q, const ql
     int st;
     if ((st = check_attention(a))) return st;
     const int64_t d = a->head_dim;
-    if ((st = check_heads(Q, a->tokens_q, a->heads, d, 16, false, "Q")) ||
-        (st = check_heads(K, a->tokens_k, a->kv_heads, d, 16, false, "K")) ||
-        (st = check_heads(V, a->tokens_k, a->kv_heads, d, 16, false, "V")) ||
-        (st = check_heads(O, a->tokens_q, a->heads, d, 16, true, "O")))
+    if ((st = check_attn_heads(Q, a->tokens_q, a->heads, d, false, "Q")) ||
+        (st = check_attn_heads(K, a->tokens_k, a->kv_heads, d, false, "K")) ||
+        (st = check_attn_heads(V, a->tokens_k, a->kv_heads, d, false, "V")) ||
+        (st = check_attn_heads(O, a->tokens_q, a->heads, d, true, "O")))
       return st;
     if (nothing(a) || a->tokens_q == 0) return (int)QLORA_OK;
     if (!lse) return fail(QLORA_ERR_INVALID_ARG, "lse is NULL");
@@ -233,10 +241,10 @@ int qlora_attention_bwd(const qlora_attention* a, const qlora_heads* dO, const q
     int st;
     if ((st = check_attention(a))) return st;
     const int64_t d = a->head_dim, tq = a->tokens_q, tk = a->tokens_k, h = a->heads, hk = a->kv_heads;
-    if ((st = check_heads(dO, tq, h, d, 16, false, "dO")) || (st = check_heads(Q, tq, h, d, 16, false, "Q")) ||
-        (st = check_heads(K, tk, hk, d, 16, false, "K")) || (st = check_heads(V, tk, hk, d, 16, false, "V")) ||
-        (st = check_heads(O, tq, h, d, 16, false, "O")) || (st = check_heads(dQ, tq, h, d, 16, true, "dQ")) ||
-        (st = check_heads(dK, tk, hk, d, 16, true, "dK")) || (st = check_heads(dV, tk, hk, d, 16, true, "dV")))
+    if ((st = check_attn_heads(dO, tq, h, d, false, "dO")) || (st = check_attn_heads(Q, tq, h, d, false, "Q")) ||
+        (st = check_attn_heads(K, tk, hk, d, false, "K")) || (st = check_attn_heads(V, tk, hk, d, false, "V")) ||
+        (st = check_attn_heads(O, tq, h, d, false, "O")) || (st = check_attn_heads(dQ, tq, h, d, true, "dQ")) ||
+        (st = check_attn_heads(dK, tk, hk, d, true, "dK")) || (st = check_attn_heads(dV, tk, hk, d, true, "dV")))
       return st;
     if (nothing(a)) return (int)QLORA_OK;
     if (tq > 0 && !lse) return fail(QLORA_ERR_INVALID_ARG, "lse is NULL");

@@ -89,15 +89,19 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
     qf[s] = E::vec(load16(a.q, (rg.start + tok) * a.q.token + head * a.q.head + c, live && c < a.d));
   }
 
+  // a thread's pieces of a tile: rows part_tid / CH + u TH / CH, the same chunk
   uint4 st[2][PER];
+  const uint32_t ch8 = part_tid % CH * 8;
+  const uint32_t k_off = ch8 < (uint32_t)a.d ? (part_tid / CH * (uint32_t)a.k.token + ch8) * 2 : kOOB;
+  const uint32_t v_off = ch8 < (uint32_t)a.d ? (part_tid / CH * (uint32_t)a.v.token + ch8) * 2 : kOOB;
   auto load = [&](int32_t kt) {
+    const int64_t key = ks.start + (int64_t)kt * BN, left = kt < k1 ? ks.n - (int64_t)kt * BN : 0;
+    const __amdgpu_buffer_rsrc_t rk = rows_rsrc(a.k, key * a.k.token + kv_head * a.k.head, left, a.d);
+    const __amdgpu_buffer_rsrc_t rv = rows_rsrc(a.v, key * a.v.token + kv_head * a.v.head, left, a.d);
 #pragma unroll
     for (int u = 0; u < PER; ++u) {
-      const int c = u * TH + part_tid, ch = c % CH;
-      const int32_t key = kt * BN + c / CH;
-      const bool ok = kt < k1 && key < ks.n && ch * 8 < a.d;
-      st[0][u] = load16(a.k, (ks.start + key) * a.k.token + kv_head * a.k.head + ch * 8, ok);
-      st[1][u] = load16(a.v, (ks.start + key) * a.v.token + kv_head * a.v.head + ch * 8, ok);
+      st[0][u] = buf_load16(rk, k_off + u * (TH / CH) * 2 * (uint32_t)a.k.token);
+      st[1][u] = buf_load16(rv, v_off + u * (TH / CH) * 2 * (uint32_t)a.v.token);
     }
   };
   auto store = [&](int32_t kt, int buf) {

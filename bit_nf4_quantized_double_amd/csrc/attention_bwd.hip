@@ -173,15 +173,19 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
   }
   const float c2 = a.scale * kLog2e;
 
+  // a thread's pieces of a tile: rows tid / CH + u 256 / CH, the same chunk
   uint4 st[2][PER];
+  const uint32_t ch8 = tid % CH * 8;
+  const uint32_t k_off = ch8 < (uint32_t)a.d ? (tid / CH * (uint32_t)a.k.token + ch8) * 2 : kOOB;
+  const uint32_t v_off = ch8 < (uint32_t)a.d ? (tid / CH * (uint32_t)a.v.token + ch8) * 2 : kOOB;
   auto load = [&](int32_t kt) {
+    const int64_t key = ks.start + (int64_t)kt * BN, left = kt < k1 ? ks.n - (int64_t)kt * BN : 0;
+    const __amdgpu_buffer_rsrc_t rk = rows_rsrc(a.k, key * a.k.token + kv_head * a.k.head, left, a.d);
+    const __amdgpu_buffer_rsrc_t rv = rows_rsrc(a.v, key * a.v.token + kv_head * a.v.head, left, a.d);
 #pragma unroll
     for (int u = 0; u < PER; ++u) {
-      const int c = u * 256 + tid, ch = c % CH;
-      const int32_t key = kt * BN + c / CH;
-      const bool ok = kt < k1 && key < ks.n && ch * 8 < a.d;
-      st[0][u] = load16(a.k, (ks.start + key) * a.k.token + kv_head * a.k.head + ch * 8, ok);
-      st[1][u] = load16(a.v, (ks.start + key) * a.v.token + kv_head * a.v.head + ch * 8, ok);
+      st[0][u] = buf_load16(rk, k_off + u * (256 / CH) * 2 * (uint32_t)a.k.token);
+      st[1][u] = buf_load16(rv, v_off + u * (256 / CH) * 2 * (uint32_t)a.v.token);
     }
   };
   auto store = [&](int32_t kt, int buf) {
@@ -265,6 +269,9 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
 // (in registers they would leave none for operands on their way).  The products
 // run in groups of two to four, whose operands are read from LDS during the group
 // before; exponentials and dS are made between the MFMAs of dO V^T and of dV.
+#ifndef RINGV
+#define RINGV 4
+#endif
 template <typename E, int DB>
 __global__ __launch_bounds__(256, 2) void k_attn_bwd_kv(AttnArgs a) {
   constexpr int BQ = 32, BK = 128;
@@ -326,47 +333,60 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_kv(AttnArgs a) {
   const float ups = up * __builtin_amdgcn_exp2f(-kShift);
   const float c2 = a.scale * kLog2e;
 
-  // This thread's rows of a tile, tid / CH + u 256 / CH: as token and head, moved
-  // on from tile to tile without a division.
-  RowAt at[PER], lat;
-#pragma unroll
-  for (int u = 0; u < PER; ++u) at[u] = RowAt(r0 * BQ + (u * 256 + tid) / CH, group);
-  lat = RowAt(r0 * BQ + (tid & 31), group);
-  const int ch8 = tid % CH * 8;
+  // This thread's rows of a tile: tid / CH + u 256 / CH.  Where the group's size
+  // divides them, their places in the tile are the same in every tile; otherwise
+  // each tile costs divisions.
+  const uint32_t ch8 = tid % CH * 8;
   const int64_t q_at = q0 * a.q.token + head0 * a.q.head, d_at = q0 * a.dout.token + head0 * a.dout.head;
+  const int32_t mytok = tid / CH / group, myhead = tid / CH % group;
+  const bool quick = 256 / CH % group == 0 && (group - 1) * max(a.q.head, a.dout.head) < (1 << 28);
+  const uint32_t q_off = (uint32_t)(mytok * a.q.token + myhead * a.q.head + ch8) * 2;
+  const uint32_t d_off = (uint32_t)(mytok * a.dout.token + myhead * a.dout.head + ch8) * 2;
   uint4 st[2][PER];
   float st_lse = 0.f, st_delta = 0.f;
   int st_last = 0;
-  // the tile that `at` stands on (nothing past the last row), and on to the next
-  auto load = [&]() {
+  // nothing past the last row
+  auto load = [&](int32_t rt) {
+    if (quick) {
+      const int32_t tok0 = rt * BQ / group, left = (ch8 < (uint32_t)a.d ? nq : 0) - tok0 - mytok;
+      const __amdgpu_buffer_rsrc_t rq = make_rsrc(a.q.p + (tok0 < nq ? q_at + tok0 * a.q.token : 0), 0x7fffffff);
+      const __amdgpu_buffer_rsrc_t rd = make_rsrc(a.dout.p + (tok0 < nq ? d_at + tok0 * a.dout.token : 0), 0x7fffffff);
 #pragma unroll
-    for (int u = 0; u < PER; ++u) {
-      const bool ok = at[u].tok < nq && ch8 < a.d;
-      st[0][u] = load16(a.q, q_at + at[u].tok * a.q.token + at[u].head * a.q.head + ch8, ok);
-      st[1][u] = load16(a.dout, d_at + at[u].tok * a.dout.token + at[u].head * a.dout.head + ch8, ok);
-      at[u].move(BQ, group);
+      for (int u = 0; u < PER; ++u) {
+        const int32_t on = u * (256 / CH) / group;
+        st[0][u] = buf_load16(rq, on < left ? q_off + on * 2 * (uint32_t)a.q.token : kOOB);
+        st[1][u] = buf_load16(rd, on < left ? d_off + on * 2 * (uint32_t)a.dout.token : kOOB);
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < PER; ++u) {
+        const int32_t r = rt * BQ + (u * 256 + tid) / CH, tok = r / group, head = r % group;
+        const bool ok = tok < nq && ch8 < (uint32_t)a.d;
+        st[0][u] = load16(a.q, q_at + tok * a.q.token + head * a.q.head + ch8, ok);
+        st[1][u] = load16(a.dout, d_at + tok * a.dout.token + head * a.dout.head + ch8, ok);
+      }
     }
     if (tid < BQ) {
-      const int64_t i = (q0 + lat.tok) * a.heads + head0 + lat.head;
+      const int32_t r = rt * BQ + tid, tok = r / group;
+      const int64_t i = (q0 + tok) * a.heads + head0 + r % group;
       st_lse = INFINITY;
       st_delta = 0.f;
       st_last = -1;
-      if (lat.tok < nq && in_bounds(i, 1, a.tq * a.heads)) {
+      if (tok < nq && in_bounds(i, 1, a.tq * a.heads)) {
         st_lse = a.lse[i] * kLog2e;
         if (st_lse == -INFINITY) st_lse = INFINITY;  // a row that sees nothing: P = 0
         st_lse -= kShift;
         st_delta = a.delta[i];
-        st_last = a.causal ? min(nk - 1, lat.tok + off) : nk - 1;
+        st_last = a.causal ? min(nk - 1, tok + off) : nk - 1;
       }
-      lat.move(BQ, group);
     }
   };
-  auto store = [&](int32_t rt, int buf) {
+  auto store = [&](int32_t rt, int buf, auto MASKED) {
     uint8_t* const to = lds + buf * 2 * BYTES;
 #pragma unroll
     for (int u = 0; u < PER; ++u) {
       const int c = u * 256 + tid;
-      if (rt < rf) {
+      if (decltype(MASKED)::value && rt < rf) {
         if (not_finite<E>(st[1][u])) {
           const int32_t t = (rt * BQ + c / CH) / group;
           s_bad.template take<E, false>(st[1][u], ch8, a.causal ? min(nk - 1, t + off) : nk - 1);
@@ -389,56 +409,44 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_kv(AttnArgs a) {
   auto tile = [&](int32_t rt, int buf, auto MASKED) {
     constexpr bool kMasked = decltype(MASKED)::value;
     const uint8_t *qb = lds + buf * 2 * BYTES, *db = qb + BYTES, *vb = s_v + 32 * wave * TileLayout<DB>::kPitch;
-    f32x16 s = (f32x16)(0.f), dp = (f32x16)(0.f);
-    uint4 x[2][4];
-    auto rows_q = [&](int g, uint4 (&f)[4]) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] = raw_rows<DB>(qb, 0, 4 * g + i, lane);
+    // Operands in the order of their use, each read from LDS into a ring of
+    // registers while the products before it run.
+    constexpr int N = 2 * DB, RING = RINGV, EP = 16 / N;
+    uint4 ring[RING];
+    auto fetch = [&](int f) {
+      if (f < N) ring[f % RING] = raw_rows<DB>(qb, 0, f, lane);
+      else if (f < 3 * N) ring[f % RING] = raw_rows<DB>((f - N) % 2 ? vb : db, 0, (f - N) / 2, lane);
+      else if (f < 5 * N) ring[f % RING] = frag_cols<DB>(f < 4 * N ? db : qb, 16 * (f % 2), (f - (f < 4 * N ? 3 : 4) * N) / 2, lane);
     };
-    auto rows_d = [&](int g, uint4 (&f)[4]) {
+    // row values (lse, delta) of accumulators EP i .. EP i + EP - 1
+    float aux[2][EP];
+    auto fetch_rows = [&](const float* v, int i) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        f[i] = raw_rows<DB>(db, 0, 2 * g + i, lane);
-        f[2 + i] = raw_rows<DB>(vb, 0, 2 * g + i, lane);
+      for (int j = 0; j < EP; ++j) {
+        const int r = EP * i + j;
+        aux[i % 2][j] = v[8 * (r / 4) + 4 * half + r % 4];
       }
     };
-    auto cols = [&](const uint8_t* t, int b, uint4 (&f)[4]) {
+    f32x16 s = (f32x16)(0.f), dp = (f32x16)(0.f);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) f[i] = frag_cols<DB>(t, 16 * i, b, lane);
-    };
-    constexpr int NS = DB / 2;  // groups of S
-    rows_q(0, x[0]);
+    for (int f = 0; f < RING; ++f) fetch(f);
 #pragma unroll
-    for (int g = 0; g < NS; ++g) {
-      if (g + 1 < NS) rows_q(g + 1, x[(g + 1) & 1]);
-      else rows_d(0, x[(g + 1) & 1]);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s = E::mfma32(E::vec(x[g & 1][i]), E::vec(kf[4 * g + i]), s);
+    for (int i = 0; i < N; ++i) {
+      s = E::mfma32(E::vec(ring[i % RING]), E::vec(kf[i]), s);
+      fetch(i + RING);
+      if (i == N - 1) fetch_rows(s_lse[buf], 0);
       __builtin_amdgcn_sched_barrier(0);
     }
-    // dO V^T in DB groups of two; between them P, 16 / DB rows a group
-    constexpr int RG = 16 / DB;
+    // dO V^T, and P beside it
 #pragma unroll
-    for (int g = 0; g < DB; ++g) {
-      uint4(&f)[4] = x[(NS + g) & 1];
-      if (g + 1 < DB) rows_d(g + 1, x[(NS + g + 1) & 1]);
-      else cols(db, 0, x[(NS + g + 1) & 1]);
-      float4 l[RG / 4];
+    for (int i = 0; i < N; ++i) {
+      const int f = N + 2 * i;
+      dp = E::mfma32(E::vec(ring[f % RING]), E::vec(ring[(f + 1) % RING]), dp);
+      fetch(f + RING);
+      fetch(f + 1 + RING);
+      fetch_rows(i + 1 < N ? s_lse[buf] : s_delta[buf], (i + 1) % N);
 #pragma unroll
-      for (int j = 0; j < RG / 4; ++j) l[j] = *reinterpret_cast<const float4*>(&s_lse[buf][8 * (g * RG / 4 + j) + 4 * half]);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) dp = E::mfma32(E::vec(f[i]), E::vec(f[2 + i]), dp);
-#pragma unroll
-      for (int j = 0; j < RG / 4; ++j) {
-        const float ls[4] = {l[j].x, l[j].y, l[j].z, l[j].w};
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int at = g * RG + 4 * j + r;
-          s[at] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[at], c2, -ls[r]));
-        }
-      }
+      for (int j = 0; j < EP; ++j) s[EP * i + j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[EP * i + j], c2, -aux[i % 2][j]));
       __builtin_amdgcn_sched_barrier(0);
     }
     bool seen[16];
@@ -452,57 +460,41 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_kv(AttnArgs a) {
     typename E::v8 p[2], ds[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) p[i] = pack8<E>(s, 8 * i);
-    // dV in DB groups of two; between them dS
-    auto row_delta = [&](int g) { return *reinterpret_cast<const float4*>(&s_delta[buf][8 * g + 4 * half]); };
-    auto make_ds = [&](int g, const float4& e) {
-      const float d[4] = {e.x, e.y, e.z, e.w};
+    // dV, and dS beside it
 #pragma unroll
-      for (int r = 4 * g; r < 4 * g + 4; ++r) {
-        dp[r] = s[r] * ((dp[r] - d[r % 4]) * ups);
+    for (int i = 0; i < N; ++i) {
+      dv[i / 2] = E::mfma32(E::vec(ring[(3 * N + i) % RING]), p[i % 2], dv[i / 2]);
+      fetch(3 * N + i + RING);
+      if (i + 1 < N) fetch_rows(s_delta[buf], i + 1);
+#pragma unroll
+      for (int j = 0; j < EP; ++j) {
+        const int r = EP * i + j;
+        dp[r] = s[r] * ((dp[r] - aux[i % 2][j]) * ups);
         if constexpr (kMasked) dp[r] = seen[r] ? dp[r] : 0.f;
       }
-    };
-    constexpr int X0 = (NS + DB) & 1;
-#pragma unroll
-    for (int b = 0; b < DB; ++b) {
-      uint4(&f)[4] = x[(X0 + b) & 1];
-      if (b + 1 < DB) cols(db, b + 1, x[(X0 + b + 1) & 1]);
-      else cols(qb, 0, x[(X0 + b + 1) & 1]);
-      float4 e[RG / 4];
-#pragma unroll
-      for (int j = 0; j < RG / 4; ++j) e[j] = row_delta(b * RG / 4 + j);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) dv[b] = E::mfma32(E::vec(f[i]), p[i], dv[b]);
-#pragma unroll
-      for (int j = 0; j < RG / 4; ++j) make_ds(b * RG / 4 + j, e[j]);
       __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) ds[i] = pack8<E>(dp, 8 * i);
-    constexpr int X1 = (X0 + DB) & 1;
 #pragma unroll
-    for (int b = 0; b < DB; ++b) {
-      uint4(&f)[4] = x[(X1 + b) & 1];
-      if (b + 1 < DB) cols(qb, b + 1, x[(X1 + b + 1) & 1]);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) dk[b] = E::mfma32(E::vec(f[i]), ds[i], dk[b]);
+    for (int i = 0; i < N; ++i) {
+      dk[i / 2] = E::mfma32(E::vec(ring[(4 * N + i) % RING]), ds[i % 2], dk[i / 2]);
+      fetch(4 * N + i + RING);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
 
   s_bad.clear(-1);
   __syncthreads();
-  load();
-  store(r0, 0);
-  load();
+  load(r0);
+  store(r0, 0, std::true_type{});
+  load(r0 + 1);
   __syncthreads();
   auto go = [&](int32_t from, int32_t to, auto MASKED) {
     for (int32_t rt = from; rt < to; ++rt) {
       const int buf = (rt - r0) & 1;
-      store(rt + 1, buf ^ 1);
-      load();
+      store(rt + 1, buf ^ 1, MASKED);
+      load(rt + 2);
       tile(rt, buf, MASKED);
       __syncthreads();
     }

@@ -66,22 +66,6 @@ __device__ __forceinline__ int32_t seq_length(const int32_t* len, int32_t seq, i
   return in_bounds(seq, 1, batch) ? (int32_t)clampl(len[seq], 0, size) : 0;
 }
 
-// A packed row of a sequence as token and head of the group, moved on by whole rows.
-struct RowAt {
-  int32_t tok, head;
-  RowAt() = default;
-  __device__ __forceinline__ RowAt(int32_t row, int32_t group) : tok(row / group), head(row % group) {}
-  // by n rows; n % group and n / group are the same for all lanes
-  __device__ __forceinline__ void move(int32_t n, int32_t group) {
-    tok += n / group;
-    head += n % group;
-    if (head >= group) {
-      head -= group;
-      ++tok;
-    }
-  }
-};
-
 // Keys of a sequence: [start, start + n).
 struct Keys {
   int64_t start;
@@ -244,6 +228,13 @@ __device__ __forceinline__ void store_block(const Heads& o, int64_t at, bool ok,
     if (ok && c < d && in_bounds(at + c, 8, o.n))
       *reinterpret_cast<uint4*>(const_cast<uint16_t*>(o.p) + at + c) = make_uint4(w[0], w[1], w[2], w[3]);
   }
+}
+
+// `rows` tokens of one head from element `at` on as a buffer: past its end
+// (token strides are at most 2^23 elements, tiles at most 128 tokens) reads zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const Heads& x, int64_t at, int64_t rows, int32_t d) {
+  const int64_t n = min(rows, (int64_t)128);
+  return make_rsrc(x.p + (n > 0 ? at : 0), n > 0 ? (uint32_t)(((n - 1) * x.token + d) * 2) : 0u);
 }
 
 __device__ __forceinline__ uint4 load16(const Heads& x, int64_t at, bool ok) {

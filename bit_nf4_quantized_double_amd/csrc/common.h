@@ -140,6 +140,44 @@ __device__ __forceinline__ uint32_t buf_load1(__amdgpu_buffer_rsrc_t r, uint32_t
   return __builtin_amdgcn_raw_buffer_load_b8(r, off, 0, 0);
 }
 
+// ---- loads straight into LDS ----
+// 16 bytes a lane from a buffer (an offset past its end reads zeros) to LDS at
+// byte `to` + 16 lane: no registers, and nothing waits for it.  It counts as one
+// of the wave's vector memory loads, in order: before other waves read the data,
+// the wave waits (wait_loads) and meets them at a barrier.  Written as an
+// instruction because the compiler, which sees LDS written by the builtin, would
+// have every later read of LDS wait for it.
+struct LdsSource {
+  u32x4 r;
+};
+__device__ __forceinline__ LdsSource lds_source(const void* p, uint32_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(p);
+  LdsSource s;
+  s.r[0] = __builtin_amdgcn_readfirstlane((uint32_t)a);
+  s.r[1] = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32) & 0xffffu);
+  s.r[2] = __builtin_amdgcn_readfirstlane(bytes);
+  s.r[3] = 0x00020000u;
+  return s;
+}
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+__device__ __forceinline__ void load_to_lds16(const LdsSource& s, uint32_t off, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :: "s"(__builtin_amdgcn_readfirstlane(to)), "v"(off), "s"(s.r) : "memory");
+}
+__device__ __forceinline__ void load_to_lds4(const LdsSource& s, uint32_t off, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+               :: "s"(__builtin_amdgcn_readfirstlane(to)), "v"(off), "s"(s.r) : "memory");
+}
+// All of the wave's vector memory loads are there.  (The builtin, so that the
+// compiler knows of it: it counts its own loads only, and would later wait for
+// too many.)
+__device__ __forceinline__ void wait_loads() {
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt 0, the other counters as they are
+  asm volatile("" ::: "memory");
+}
+
 // ---- bounds-checked build ---------------------------------------------------
 // Every raw global store, and every raw global load of caller-sized data
 // (buffer loads are range checked by the hardware), is guarded by

@@ -103,7 +103,7 @@ __device__ __forceinline__ uint32_t lower(uint32_t d, uint32_t b) {
 // Both products: 256 tokens x 128 outputs a workgroup, 4 waves of 64 tokens, in
 // 16 x 16 x 32 MFMAs (A: outputs, B: tokens).  The tokens' operand is in tiles of
 // 1 KB in lane order and goes straight into registers, one step of 64 ahead; W's
-// goes through LDS, two steps ahead, double buffered, one barrier a step.
+// goes straight into LDS, four buffers, three steps ahead, one barrier a step.
 //   TRANS = false: outputs are rows of W, the reduction its columns
 //   TRANS = true:  outputs are columns of W, the reduction its rows, read from
 //                  LDS through the transposing load; a lane's 8 rows are 4 g .. + 3
@@ -111,52 +111,46 @@ __device__ __forceinline__ uint32_t lower(uint32_t d, uint32_t b) {
 template <typename E, bool TRANS>
 struct CeProduct {
   static constexpr int kTile = 128 * 64 * 2;  // bytes of a step's W tile
-  static constexpr int NS = 8, KC = 2, kStage = 4;
+  static constexpr int kBuffers = 4;
+  static constexpr int NS = 8, KC = 2;
+  static constexpr int kRow = TRANS ? 16 : 8;  // 16-byte chunks of a tile's row
 
   f32x4 acc[NS][4];
+
+  // A tile's chunks are in LDS in the order of rows, permuted inside a row by
+  // chunk ^ spread(row): the rows that a read touches at a time (16 of one column;
+  // for a transposing one 4 of 32 bytes) fall into different banks.
+  static __device__ __forceinline__ uint32_t spread(uint32_t r) {
+    return TRANS ? (r & 3) << 2 | (r >> 2 & 1) : r >> 1 & 7;
+  }
 
   // w: W's tile origin; wrows, wcols: what there is of it from there on.
   // x: the wave's first tile of tokens, whose rows of tiles are `xpitch` bytes
   // apart, xbytes long.  steps: [s0, s1).  below: TRANS, [vtile][16][4] of this wave's tokens,
-  // `bpitch` elements apart.
+  // `bpitch` elements apart (n_below 0: a wave without tokens).
   __device__ __forceinline__ void run(uint8_t* lds, const uint16_t* w, int64_t ldw, int64_t wrows, int64_t wcols,
                                       const uint16_t* x, uint32_t xpitch, int64_t xbytes, uint32_t s0, uint32_t s1,
                                       const uint16_t* below, int64_t bpitch, int64_t n_below) {
-    const int tid = threadIdx.x, lane = tid & 63;
-    constexpr int ROWS = TRANS ? 64 : 128;
-    // TRANS: the resource moves with the steps, so that offsets stay in 32 bits
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const auto wbytes = [&](int64_t rows) { return rows > 0 ? (uint32_t)(((rows - 1) * ldw + wcols) * 2) : 0u; };
-    const __amdgpu_buffer_rsrc_t rw = make_rsrc(w, wbytes(min(wrows, (int64_t)ROWS)));
     const __amdgpu_buffer_rsrc_t rx = make_rsrc(x, (uint32_t)min(xbytes, (int64_t)0x7fffffff));
-    uint4 st[2][kStage], xf[KC][4], wf[2][4];
+    uint4 xf[KC][4], wf[2][4];
     uint2 low[KC];
-    auto load_stage = [&](uint32_t s, int d) {
+    const uint32_t lds0 = lds_offset(lds);
+    // this thread's chunks of a tile: tid + 256 u, rows 256 / kRow apart
+    const uint32_t row0 = tid / kRow, col0 = (tid % kRow ^ spread(row0)) * 8;  // (rows 16 or 32 apart have the same spread)
+    const uint32_t woff = (row0 * (uint32_t)ldw + col0) * 2;
+    auto load_w = [&](uint32_t s) {
+      // the buffer moves with the step, so that offsets stay in 32 bits
+      const int64_t left = TRANS ? wrows - (int64_t)s * 64 : min(wrows, (int64_t)128);
+      const bool some = s < s1;
+      const LdsSource src = TRANS ? lds_source(w + (some ? (int64_t)s * 64 * ldw : 0), some ? wbytes(min(left, (int64_t)64)) : 0u)
+                                  : lds_source(w, some ? wbytes(left) : 0u);
+      const uint32_t col = TRANS ? col0 : s * 64 + col0;
 #pragma unroll
-      for (int u = 0; u < kStage; ++u) {
-        const uint32_t i = u * 256 + tid;
-        if constexpr (!TRANS) {
-          const uint32_t row = i / 8, col = s * 64 + i % 8 * 8;
-          st[d][u] = buf_load16(rw, s < s1 && row < wrows && col < wcols ? (row * (uint32_t)ldw + col) * 2 : kOOB);
-        } else {
-          const uint32_t row = i / 16, col = i % 16 * 8;
-          const __amdgpu_buffer_rsrc_t rs = make_rsrc(w + (int64_t)s * 64 * ldw, s < s1 ? wbytes(min(wrows - (int64_t)s * 64, (int64_t)64)) : 0u);
-          st[d][u] = buf_load16(rs, s < s1 && (int64_t)s * 64 + row < wrows && col < wcols ? (row * (uint32_t)ldw + col) * 2 : kOOB);
-        }
-      }
-    };
-    auto write_stage = [&](int buf, int d) {
-#pragma unroll
-      for (int u = 0; u < kStage; ++u) {
-        const uint32_t i = u * 256 + tid;
-        uint32_t at;
-        if constexpr (!TRANS) {
-          const uint32_t row = i / 8, ch = i % 8;
-          at = ((row / 16) * KC + ch / 4) * 1024 + ((ch % 4) * 16 + ((row ^ ch) & 15)) * 16;
-        } else {
-          const uint32_t row = i / 16, ch = i % 16;
-          at = row * 256 + ((ch ^ spread(row)) << 4);
-        }
-        *reinterpret_cast<uint4*>(lds + buf * kTile + at) = st[d][u];
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t off = woff + u * (256 / kRow) * 2 * (uint32_t)ldw + (TRANS ? 0u : s * 128);
+        load_to_lds16(src, col < wcols ? off : kOOB, lds0 + (s - s0) % kBuffers * kTile + (u * 256 + wave * 64) * 16);
       }
     };
     auto load_x = [&](uint32_t s, int j) {
@@ -169,21 +163,31 @@ struct CeProduct {
       }
     };
     constexpr int P = NS / 4, Q = KC * P;  // sub-steps of a chunk of 32, and of a step
-    auto read_w = [&](int buf, int q, uint4 (&f)[4]) {
-      const int g = lane >> 4;
+    // a lane's places in a tile: of its row's chunk (TRANS: of unit k = strip / 2)
+    const int g = lane >> 4;
+    uint32_t at[TRANS ? 4 : 2];
+    if constexpr (TRANS) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t row = 4 * g + (lane >> 2 & 3);
+        at[k] = row * 256 + ((4 * k + (lane >> 1 & 1)) ^ spread(row)) * 16 + 8 * (lane & 1);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) at[k] = (lane & 15) * 128 + ((4 * k + g) ^ spread(lane & 15)) * 16;
+    }
+    auto read_w = [&](const uint8_t* tile, int q, uint4 (&f)[4]) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int strip = 4 * (q % P) + i, chunk = q / P;
         if constexpr (!TRANS) {
-          const uint32_t ch = chunk * 4 + g;
-          f[i] = *reinterpret_cast<const uint4*>(lds + buf * kTile + (strip * KC + chunk) * 1024 + (g * 16 + ((lane ^ ch) & 15)) * 16);
+          f[i] = *reinterpret_cast<const uint4*>(tile + strip * 2048 + at[chunk]);
         } else {
           uint2 h[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const uint32_t row = 32 * chunk + 16 * e + 4 * g + ((lane & 15) >> 2), ch = 2 * strip + ((lane & 3) >> 1);
             typedef __attribute__((ext_vector_type(4))) short s16x4;
-            const uint8_t* p = lds + buf * kTile + row * 256 + ((ch ^ spread(row)) << 4) + 8 * (lane & 1);
+            const uint8_t* p = tile + at[strip / 2] + (32 * chunk + 16 * e) * 256 + strip % 2 * 32;
             h[e] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p));
           }
           f[i] = make_uint4(h[0].x, h[0].y, h[1].x, h[1].y);
@@ -194,26 +198,27 @@ struct CeProduct {
     for (int i = 0; i < NS; ++i)
 #pragma unroll
       for (int t = 0; t < 4; ++t) acc[i][t] = (f32x4)(0.f);
-    load_stage(s0, 0);
+#pragma unroll
+    for (int j = 0; j < 3; ++j) load_w(s0 + j);
 #pragma unroll
     for (int j = 0; j < KC; ++j) load_x(s0, j);
-    write_stage(0, 0);
-    load_stage(s0 + 1, 1);
-    load_stage(s0 + 2, 0);
+    wait_loads();
     lds_barrier();
-    read_w(0, 0, wf[0]);
-    // step s, B = parity: W tile s is in LDS buffer B, s + 1 in st[B ^ 1], s + 2 on its way to st[B]
-    auto step = [&](uint32_t s, auto parity) {
-      constexpr int B = decltype(parity)::value;
+    read_w(lds, 0, wf[0]);
+    // step s: W tile s is in buffer (s - s0) % 4.  The barrier in its last sub-step
+    // ends the reads of that buffer and begins those of the next one.
+    auto step = [&](uint32_t s, auto buffer) {
+      constexpr int B = decltype(buffer)::value;
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
-        if (q == 0) {
-          write_stage(B ^ 1, B ^ 1);
-          load_stage(s + 3, B ^ 1);
+        if (q == 1) {
+          // the second half of this step's tokens, issued two sub-steps ago, and every W tile up to s + 2
+          wait_loads();
+          load_w(s + 3);
         }
         if (q == Q - 1) lds_barrier();
-        if (q < Q - 1) read_w(B, q + 1, wf[(q + 1) & 1]);
-        else read_w(B ^ 1, 0, wf[0]);
+        if (q < Q - 1) read_w(lds + B * kTile, q + 1, wf[(q + 1) & 1]);
+        else read_w(lds + (B + 1) % kBuffers * kTile, 0, wf[0]);
         if constexpr (TRANS) {
           if (q % P == 0) {
 #pragma unroll
@@ -234,16 +239,13 @@ struct CeProduct {
         __builtin_amdgcn_sched_barrier(0);
       }
     };
-    for (uint32_t s = s0; s < s1; s += 2) {
+    for (uint32_t s = s0; s < s1; s += 4) {
       step(s, std::integral_constant<int, 0>{});
       if (s + 1 < s1) step(s + 1, std::integral_constant<int, 1>{});
+      if (s + 2 < s1) step(s + 2, std::integral_constant<int, 2>{});
+      if (s + 3 < s1) step(s + 3, std::integral_constant<int, 3>{});
     }
-  }
-
-  // rows of 256 bytes: 16-byte chunks permuted, so that the 4 rows by 32 bytes
-  // of a transposing read fall into different banks
-  static __device__ __forceinline__ uint32_t spread(uint32_t r) {
-    return (((r ^ (r >> 3)) & 1) << 3) | ((r & 3) << 1 & 4) | ((r & 1) << 1) | ((r >> 2) & 1);
+    wait_loads();
   }
 };
 
@@ -260,7 +262,7 @@ __device__ __forceinline__ float token_sum(float x) {
 template <typename E, bool GRAD>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_ce_logits(CeArgs a, CeRound r) {
   typedef CeProduct<E, false> G;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * G::kTile];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[G::kBuffers * G::kTile];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, c = lane & 15;
   uint32_t tm, tn;
   tile_of(blockIdx.x, (uint32_t)((r.m + kTileM - 1) / kTileM), (uint32_t)((r.vn + kTileN - 1) / kTileN), tm, tn);
@@ -403,7 +405,7 @@ __global__ __launch_bounds__(256) void k_ce_stats(CeArgs a, CeRound r, bool firs
 template <typename E>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_ce_grad(CeArgs a, CeRound r, bool first) {
   typedef CeProduct<E, true> G;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * G::kTile];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[G::kBuffers * G::kTile];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t mt = (uint32_t)((r.m + kTileM - 1) / kTileM), nt = (uint32_t)((a.k + kTileN - 1) / kTileN), tiles = mt * nt;
   const uint32_t z = blockIdx.x / tiles;

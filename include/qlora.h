@@ -593,7 +593,8 @@ int qlora_rope(const qlora_heads *Q, int64_t heads, const qlora_heads *K, int64_
  *   zero_rest   nonzero: tokens of O (backward: dQ, dK, dV) that belong to no
  *               sequence become zeros (lse: -inf); zero: they are left as they are
  *   head_dim    a multiple of 8, at most 128.  Pointers are 16-byte aligned and
- *               strides multiples of 8 (QLORA_ERR_ALIGN); scale is positive.
+ *               strides multiples of 8 (QLORA_ERR_ALIGN), token strides at most
+ *               2^23 elements (QLORA_ERR_SHAPE); scale is positive.
  *               tokens_q * heads / kv_heads and tokens_k at most 2^31 - 256.
  * Backward, from dO, O, lse (as the forward wrote them):
  *     dV = sum P dO, dS = P (dO V - sum dO O), dQ = scale dS K, dK = scale sum dS Q,
