@@ -116,15 +116,16 @@ qlora::AttnPlan plan_of(const qlora_attention* a, int cus) {
   return qlora::attn_plan(a->tokens_q, a->tokens_k, a->batch, a->heads, a->kv_heads, cus);
 }
 
-// Workspace of a backward: [delta][maxima][split sums].
+// Workspace of a backward: [delta][lse in base 2][maxima][split sums].
 struct BwdWs {
-  size_t top, part, total;
+  size_t lse2, top, part, total;
   int splits;
 };
 BwdWs bwd_ws(const qlora_attention* a) {
   BwdWs L{};
   L.splits = qlora::attn_bwd_splits(a->tokens_k, a->batch, a->heads, a->kv_heads, qlora::device_compute_units());
-  L.top = round_up((size_t)a->tokens_q * (size_t)a->heads * 4u);
+  L.lse2 = round_up((size_t)a->tokens_q * (size_t)a->heads * 4u);
+  L.top = 2 * L.lse2;
   L.part = L.top + 2 * qlora::kAttnTops * 4u;
   L.total = L.part + qlora::attn_bwd_part_bytes(L.splits, a->tokens_k, a->kv_heads, a->head_dim);
   return L;
@@ -258,8 +259,9 @@ int qlora_attention_bwd(const qlora_attention* a, const qlora_heads* dO, const q
     g.dq = heads_arg(dQ, tq, h, d); g.dk = heads_arg(dK, tk, hk, d); g.dv = heads_arg(dV, tk, hk, d);
     const BwdWs L = bwd_ws(a);
     char* base = static_cast<char*>(ws);
-    return done(qlora::launch_attn_bwd(g, reinterpret_cast<float*>(base), reinterpret_cast<float*>(base + L.top),
-                                       reinterpret_cast<float*>(base + L.part), L.splits, stream),
+    return done(qlora::launch_attn_bwd(g, reinterpret_cast<float*>(base), reinterpret_cast<float*>(base + L.lse2),
+                                       reinterpret_cast<float*>(base + L.top), reinterpret_cast<float*>(base + L.part), L.splits,
+                                       stream),
                 "attention backward launch");
   });
 }

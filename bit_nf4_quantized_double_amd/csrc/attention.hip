@@ -28,6 +28,9 @@ struct Running {
   float m, l;
 };
 
+#ifndef RINGF
+#define RINGF 4
+#endif
 // KW = 1: 128 rows a workgroup, 32 a wave; tiles of 64 keys, double buffered,
 // shared by the waves.  KW = 4 (few rows, many keys): 32 rows a workgroup, whose
 // waves take tiles of 32 keys in turn, each through its own LDS.
@@ -35,7 +38,7 @@ template <typename E, int DB, int KW>
 __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
   constexpr int NU = KW == 1 ? 2 : 1, BN = 32 * NU, BM = KW == 1 ? 128 : 32;
   constexpr int TH = 256 / KW;                       // threads that share a tile
-  constexpr int CH = TileLayout<DB>::kChunks, PER = BN * CH / TH, BYTES = BN * TileLayout<DB>::kPitch;
+  constexpr int CH = Tile<DB>::kChunks, PER = BN * CH / TH, BYTES = BN * Tile<DB>::kPitch;
   constexpr int NBUF = KW == 1 ? 2 : 1;
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * BYTES * NBUF * KW];
   __shared__ NonFinite<32 * DB> s_bad;
@@ -73,12 +76,12 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
   if (first >= rows) return;
 
   // keys: row sees 0 .. last; the tile up to `end`, all its rows up to `whole`
-  const int32_t off = ks.n - nq;
-  const int32_t last = !live ? -1 : a.causal ? min(ks.n - 1, tok + off) : ks.n - 1;
+  const int32_t shift = ks.n - nq;
+  const int32_t last = !live ? -1 : a.causal ? min(ks.n - 1, tok + shift) : ks.n - 1;
   const int32_t wfirst = first + (KW == 1 ? wave * 32 : 0);
-  const int32_t end = a.causal ? max(0, min(ks.n, (min(first + BM, rows) - 1) / a.group + off + 1)) : ks.n;
-  const int32_t whole = a.causal ? min(ks.n, first / a.group + off + 1) : ks.n;
-  const int32_t wend = a.causal ? min(ks.n, (min(wfirst + 32, rows) - 1) / a.group + off + 1) : ks.n;
+  const int32_t end = a.causal ? max(0, min(ks.n, (min(first + BM, rows) - 1) / a.group + shift + 1)) : ks.n;
+  const int32_t whole = a.causal ? min(ks.n, first / a.group + shift + 1) : ks.n;
+  const int32_t wend = a.causal ? min(ks.n, (min(wfirst + 32, rows) - 1) / a.group + shift + 1) : ks.n;
   const int32_t ntiles = (end + BN - 1) / BN, per = (ntiles + a.splits - 1) / a.splits;
   const int32_t k0 = z * per + (KW == 1 ? 0 : wave), k1 = min(ntiles, (z + 1) * per);
 
@@ -89,19 +92,21 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
     qf[s] = E::vec(load16(a.q, (rg.start + tok) * a.q.token + head * a.q.head + c, live && c < a.d));
   }
 
-  // a thread's pieces of a tile: rows part_tid / CH + u TH / CH, the same chunk
+  // a thread's pieces of a tile, through registers (columns past d: none)
+  const Tile<DB> at(lane);
   uint4 st[2][PER];
-  const uint32_t ch8 = part_tid % CH * 8;
-  const uint32_t k_off = ch8 < (uint32_t)a.d ? (part_tid / CH * (uint32_t)a.k.token + ch8) * 2 : kOOB;
-  const uint32_t v_off = ch8 < (uint32_t)a.d ? (part_tid / CH * (uint32_t)a.v.token + ch8) * 2 : kOOB;
+  const auto off = [&](const Heads& x, int u) {
+    const uint32_t c = Fill<DB>::column(part_tid, TH, u);
+    return c < (uint32_t)a.d ? ((Fill<DB>::row(part_tid) + u * (TH / CH)) * (uint32_t)x.token + c) * 2 : kOOB;
+  };
+  const auto first_key = [&](const Heads& x, int32_t kt) { return (ks.start + (int64_t)kt * BN) * x.token + kv_head * x.head; };
   auto load = [&](int32_t kt) {
-    const int64_t key = ks.start + (int64_t)kt * BN, left = kt < k1 ? ks.n - (int64_t)kt * BN : 0;
-    const __amdgpu_buffer_rsrc_t rk = rows_rsrc(a.k, key * a.k.token + kv_head * a.k.head, left, a.d);
-    const __amdgpu_buffer_rsrc_t rv = rows_rsrc(a.v, key * a.v.token + kv_head * a.v.head, left, a.d);
+    const int64_t left = kt < k1 ? ks.n - (int64_t)kt * BN : 0;
+    const __amdgpu_buffer_rsrc_t rk = rows_rsrc(a.k, first_key(a.k, kt), left, a.d), rv = rows_rsrc(a.v, first_key(a.v, kt), left, a.d);
 #pragma unroll
     for (int u = 0; u < PER; ++u) {
-      st[0][u] = buf_load16(rk, k_off + u * (TH / CH) * 2 * (uint32_t)a.k.token);
-      st[1][u] = buf_load16(rv, v_off + u * (TH / CH) * 2 * (uint32_t)a.v.token);
+      st[0][u] = buf_load16(rk, off(a.k, u));
+      st[1][u] = buf_load16(rv, off(a.v, u));
     }
   };
   auto store = [&](int32_t kt, int buf) {
@@ -110,9 +115,10 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
 #pragma unroll
     for (int u = 0; u < PER; ++u) {
       const int c = u * TH + part_tid;
-      if (part && not_finite<E>(st[1][u])) s_bad.template take<E, true>(st[1][u], c % CH * 8, kt * BN + c / CH);
-      *reinterpret_cast<uint4*>(to + TileLayout<DB>::at(c / CH, c % CH)) = st[0][u];
-      *reinterpret_cast<uint4*>(to + BYTES + TileLayout<DB>::at(c / CH, c % CH)) = st[1][u];
+      if (part && not_finite<E>(st[1][u]))
+        s_bad.template take<E, true>(st[1][u], Fill<DB>::column(part_tid, TH, u), kt * BN + c / CH);
+      *reinterpret_cast<uint4*>(to + c * 16) = st[0][u];
+      *reinterpret_cast<uint4*>(to + BYTES + c * 16) = st[1][u];
     }
   };
 
@@ -122,29 +128,9 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
   for (int b = 0; b < DB; ++b) o[b] = (f32x16)(0.f);
   const float c2 = a.scale * kLog2e;
 
-  // MASKED: a tile that some of the rows do not see in full
-  auto tile = [&](int32_t kt, const uint8_t* kb, auto MASKED) {
-    constexpr bool kMasked = decltype(MASKED)::value;
-    const uint8_t* vb = kb + BYTES;
-    f32x16 s[NU];
-#pragma unroll
-    for (int u = 0; u < NU; ++u) {
-      s[u] = (f32x16)(0.f);
-#pragma unroll
-      for (int i = 0; i < 2 * DB; ++i) s[u] = E::mfma32(frag_rows<E, DB>(kb, 32 * u, i, lane), qf[i], s[u]);
-    }
-    if constexpr (kMasked) {
-#pragma unroll
-      for (int u = 0; u < NU; ++u)
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if (kt * BN + 32 * u + 8 * (r / 4) + 4 * half + r % 4 > last) s[u][r] = -INFINITY;
-    }
-    float top = s[0][0];
-#pragma unroll
-    for (int u = 0; u < NU; ++u)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) top = fmaxf(top, s[u][r]);
+  // the largest score of a lane's row so far in a tile -> the reference, and what
+  // there is of the sums moved to it
+  auto refer = [&](float top) {
     top = half_max(top) * c2;
     if (__ballot(top > run.m + 8.f)) {
       const float m = fmaxf(run.m, top);
@@ -156,7 +142,32 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[b][r] *= f;
     }
-    const float ref = run.m == -INFINITY ? 0.f : run.m;
+    return run.m == -INFINITY ? 0.f : run.m;
+  };
+
+  // a tile by itself.  MASKED: some of the rows do not see it in full
+  auto tile = [&](int32_t kt, const uint8_t* kb, auto MASKED) {
+    const uint8_t* vb = kb + BYTES;
+    f32x16 s[NU];
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+      s[u] = (f32x16)(0.f);
+#pragma unroll
+      for (int i = 0; i < 2 * DB; ++i) s[u] = E::mfma32(E::vec(at.rows(kb, 32 * u, i)), qf[i], s[u]);
+    }
+    if constexpr (decltype(MASKED)::value) {
+#pragma unroll
+      for (int u = 0; u < NU; ++u)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (kt * BN + 32 * u + 8 * (r / 4) + 4 * half + r % 4 > last) s[u][r] = -INFINITY;
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) top = fmaxf(top, s[u][r]);
+    const float ref = refer(top);
     float sum = 0.f;
 #pragma unroll
     for (int u = 0; u < NU; ++u)
@@ -166,37 +177,116 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
         sum += s[u][r];
       }
     run.l += sum;
-    typename E::v8 p[2 * NU];
 #pragma unroll
-    for (int i = 0; i < 2 * NU; ++i) p[i] = pack8<E>(s[i / 2], 8 * (i % 2));
+    for (int i = 0; i < 2 * NU; ++i) {
+      const typename E::v8 p = pack8<E>(s[i / 2], 8 * (i % 2));
 #pragma unroll
-    for (int b = 0; b < DB; ++b) {
+      for (int b = 0; b < DB; ++b) o[b] = E::mfma32(E::vec(at.cols(vb, 16 * i, b)), p, o[b]);
+    }
+  };
+
+  // Whole tiles, one in advance: the scores of the next tile are computed between
+  // the exponentials of this one, and their maximum between the products with V.
+  // Operands are read from LDS into a ring of registers, RING products ahead.
+  // K's next tile is there in full when this one's turn comes, V's own.
+  auto scores = [&](const uint8_t* kb, f32x16 (&s)[2]) {
 #pragma unroll
-      for (int i = 0; i < 2 * NU; ++i) o[b] = E::mfma32(E::vec(frag_cols<DB>(vb, 16 * i, b, lane)), p[i], o[b]);
+    for (int u = 0; u < NU; ++u) {
+      s[u] = (f32x16)(0.f);
+#pragma unroll
+      for (int i = 0; i < 2 * DB; ++i) s[u] = E::mfma32(E::vec(at.rows(kb, 32 * u, i)), qf[i], s[u]);
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) top = fmaxf(top, s[u][r]);
+    return top;
+  };
+  auto step = [&](const uint8_t* kb, const uint8_t* vb, f32x16 (&s)[2], f32x16 (&next)[2], float& top) {
+    constexpr int N = 4 * DB, RING = RINGF, EP = 32 / N;  // products of each kind, elements beside each
+    uint4 ring[RING];
+    auto fetch = [&](int f) {
+      if (f < N) ring[f % RING] = at.rows(kb, 32 * (f / (2 * DB)), f % (2 * DB));
+      else if (f < 2 * N) ring[f % RING] = at.cols(vb, 16 * (f % 4), (f - N) / 4);
+    };
+#pragma unroll
+    for (int f = 0; f < RING; ++f) fetch(f);
+    const float ref = refer(top);
+    float sum = 0.f;
+    typename E::v8 p[4];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) next[u] = (f32x16)(0.f);
+#pragma unroll
+    for (int f = 0; f < N; ++f) {
+      next[f / (2 * DB)] = E::mfma32(E::vec(ring[f % RING]), qf[f % (2 * DB)], next[f / (2 * DB)]);
+      fetch(f + RING);
+#pragma unroll
+      for (int e = EP * f; e < EP * f + EP; ++e) {
+        s[e / 16][e % 16] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e / 16][e % 16], c2, -ref));
+        sum += s[e / 16][e % 16];
+      }
+      if (EP * (f + 1) % 8 == 0) p[(EP * (f + 1) - 1) / 8] = pack8<E>(s[(EP * f) / 16], (EP * f) / 8 % 2 * 8);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    run.l += sum;
+    top = next[0][0];
+#pragma unroll
+    for (int f = 0; f < N; ++f) {
+      o[f / 4] = E::mfma32(E::vec(ring[(N + f) % RING]), p[f % 4], o[f / 4]);
+      fetch(N + f + RING);
+#pragma unroll
+      for (int e = EP * f; e < EP * f + EP; ++e) top = fmaxf(top, next[e / 16][e % 16]);
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
 
   s_bad.clear(INT_MAX);
   __syncthreads();
   if constexpr (KW == 1) {
-    load(k0);
-    store(k0, 0);
-    load(k0 + 1);
-    __syncthreads();
-    auto go = [&](int32_t from, int32_t to, auto MASKED) {
-      for (int32_t kt = from; kt < to; ++kt) {
-        const int buf = (kt - k0) & 1;
+    const int32_t kf = max(k0, min(k1, whole / BN));  // the first tile that not all rows see in full
+    if (k0 < kf) {
+      // whole tiles: K's buffers first, then V's
+      const uint32_t lds0 = lds_offset(lds) + wave * 1024;
+      auto direct = [&](const Heads& x, int32_t kt, uint32_t to) {
+        const LdsSource src = rows_source(x, first_key(x, kt), kt < kf ? BN : 0, a.d);
+#pragma unroll
+        for (int u = 0; u < PER; ++u) load_to_lds16(src, off(x, u), to + u * 4096);
+      };
+      direct(a.k, k0, lds0);
+      direct(a.v, k0, lds0 + 2 * BYTES);
+      direct(a.k, k0 + 1, lds0 + BYTES);
+      tile_barrier();
+      f32x16 s[2], next[2];
+      float top = scores(lds, s);
+      tile_barrier();
+      for (int32_t kt = k0; kt < kf; kt += 2) {
+        direct(a.k, kt + 2, lds0);
+        direct(a.v, kt + 1, lds0 + 3 * BYTES);
+        step(lds + BYTES, lds + 2 * BYTES, s, next, top);
+        tile_barrier();
+        if (kt + 1 >= kf) break;
+        direct(a.k, kt + 3, lds0 + BYTES);
+        direct(a.v, kt + 2, lds0 + 2 * BYTES);
+        step(lds, lds + 3 * BYTES, next, s, top);
+        tile_barrier();
+      }
+    }
+    if (kf < k1) {
+      load(kf);
+      store(kf, 0);
+      load(kf + 1);
+      __syncthreads();
+      for (int32_t kt = kf; kt < k1; ++kt) {
+        const int buf = (kt - kf) & 1;
         if (kt + 1 < k1) {
           store(kt + 1, buf ^ 1);
           load(kt + 2);
         }
-        if (!decltype(MASKED)::value || kt * BN < wend) tile(kt, mine + buf * 2 * BYTES, MASKED);
+        if (kt * BN < wend) tile(kt, mine + buf * 2 * BYTES, std::true_type{});
         __syncthreads();
       }
-    };
-    const int32_t kf = max(k0, min(k1, whole / BN));  // the first tile that not all rows see in full
-    go(k0, kf, std::false_type{});
-    go(kf, k1, std::true_type{});
+    }
   } else {
     load(k0);
     for (int32_t kt = k0; kt < k1; kt += KW) {

@@ -51,10 +51,13 @@ __device__ __forceinline__ int tops_of(int64_t tokens, int64_t batch) {
   return (int)(n < kAttnTops ? n : kAttnTops);
 }
 
-// delta = sum_d dO O, 16 lanes a row; in fp16 (blockIdx.y: dO, V) also the
+template <typename E>
+constexpr float kShift = IsF16<E>::value ? kPShift : 0.f;
+
+// delta = sum_d dO O, 16 lanes a row, and lse in base 2, less P's power of two; in fp16 (blockIdx.y: dO, V) also the
 // largest finite magnitude of each workgroup's rows.
 template <typename E>
-__global__ __launch_bounds__(256) void k_attn_delta(AttnArgs a, float* delta, float* top) {
+__global__ __launch_bounds__(256) void k_attn_delta(AttnArgs a, float* delta, float* lse2, float* top) {
   const bool isv = blockIdx.y == 1;
   const Heads& x = isv ? a.v : a.dout;
   const int32_t heads = isv ? a.kv_heads : a.heads;
@@ -84,7 +87,11 @@ __global__ __launch_bounds__(256) void k_attn_delta(AttnArgs a, float* delta, fl
       }
 #pragma unroll
       for (int s = 8; s > 0; s >>= 1) sum += __shfl_xor(sum, s, 16);
-      if (!isv && l16 == 0 && in_bounds(tok * heads + head, 1, a.tq * heads)) delta[tok * heads + head] = sum;
+      if (!isv && l16 == 0 && in_bounds(tok * heads + head, 1, a.tq * heads)) {
+        const float l = a.lse[tok * heads + head] * kLog2e;
+        delta[tok * heads + head] = sum;
+        lse2[tok * heads + head] = l == -INFINITY ? INFINITY : l - kShift<E>;  // a row that sees nothing: P = 0
+      }
     }
   }
   if constexpr (IsF16<E>::value) {
@@ -117,11 +124,14 @@ __device__ __forceinline__ float to_range(float bound) {
   return __builtin_bit_cast(float, (uint32_t)(max(-100, min(100, 14 - e)) + 127) << 23);
 }
 
+#ifndef RINGQ
+#define RINGQ 4
+#endif
 // dQ: 128 rows a workgroup, 32 a wave, tiles of 64 keys.
 template <typename E, int DB>
 __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
   constexpr int BN = 64, BM = 128;
-  constexpr int CH = TileLayout<DB>::kChunks, PER = BN * CH / 256, BYTES = BN * TileLayout<DB>::kPitch;
+  constexpr int CH = Tile<DB>::kChunks, PER = BN * CH / 256, BYTES = BN * Tile<DB>::kPitch;
   __shared__ __attribute__((aligned(16))) uint8_t lds[4 * BYTES];
   __shared__ int s_bad;  // the first key that is not finite
   __shared__ float s_top[4];
@@ -135,36 +145,34 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
   const int32_t rows = nq * a.group, first = rg.tile * BM, wfirst = first + wave * 32, row = wfirst + (lane & 31);
   const bool live = row < rows;
   const int32_t tok = row / a.group, head = kv_head * a.group + row % a.group;
-  const int64_t at = (rg.start + tok) * a.dq.token + head * a.dq.head;
+  const int64_t o_at = (rg.start + tok) * a.dq.token + head * a.dq.head;
   if (a.zero_rest && !live && row < rg.size * a.group)
     for (int c = 8 * half; c < a.d; c += 16)
-      if (in_bounds(at + c, 8, a.dq.n))
-        *reinterpret_cast<uint4*>(const_cast<uint16_t*>(a.dq.p) + at + c) = make_uint4(0, 0, 0, 0);
+      if (in_bounds(o_at + c, 8, a.dq.n))
+        *reinterpret_cast<uint4*>(const_cast<uint16_t*>(a.dq.p) + o_at + c) = make_uint4(0, 0, 0, 0);
   if (first >= rows) return;
 
-  const int32_t off = ks.n - nq;
-  const int32_t last = !live ? -1 : a.causal ? min(ks.n - 1, tok + off) : ks.n - 1;
-  const int32_t end = a.causal ? max(0, min(ks.n, (min(first + BM, rows) - 1) / a.group + off + 1)) : ks.n;
-  const int32_t whole = a.causal ? min(ks.n, first / a.group + off + 1) : ks.n;
-  const int32_t wend = a.causal ? min(ks.n, (min(wfirst + 32, rows) - 1) / a.group + off + 1) : ks.n;
+  const int32_t shift = ks.n - nq;
+  const int32_t last = !live ? -1 : a.causal ? min(ks.n - 1, tok + shift) : ks.n - 1;
+  const int32_t end = a.causal ? max(0, min(ks.n, (min(first + BM, rows) - 1) / a.group + shift + 1)) : ks.n;
+  const int32_t whole = a.causal ? min(ks.n, first / a.group + shift + 1) : ks.n;
+  const int32_t wend = a.causal ? min(ks.n, (min(wfirst + 32, rows) - 1) / a.group + shift + 1) : ks.n;
   const int32_t k1 = (end + BN - 1) / BN;
 
-  typename E::v8 qf[2 * DB], df[2 * DB];
+  uint4 qf[2 * DB], df[2 * DB];
   float most = 0.f;
 #pragma unroll
   for (int s = 0; s < 2 * DB; ++s) {
     const int c = 16 * s + 8 * half;
-    qf[s] = E::vec(load16(a.q, (rg.start + tok) * a.q.token + head * a.q.head + c, live && c < a.d));
-    const uint4 u = load16(a.dout, (rg.start + tok) * a.dout.token + head * a.dout.head + c, live && c < a.d);
-    df[s] = E::vec(u);
-    if (IsF16<E>::value) most = fmaxf(most, finite_max<E>(u));
+    qf[s] = load16(a.q, (rg.start + tok) * a.q.token + head * a.q.head + c, live && c < a.d);
+    df[s] = load16(a.dout, (rg.start + tok) * a.dout.token + head * a.dout.head + c, live && c < a.d);
+    if (IsF16<E>::value) most = fmaxf(most, finite_max<E>(df[s]));
   }
   const int64_t r_at = (rg.start + tok) * a.heads + head;
   float lse = INFINITY, delta = 0.f;  // a row that sees nothing: P = 0
   if (live && in_bounds(r_at, 1, a.tq * a.heads)) {
-    lse = a.lse[r_at] * kLog2e;
+    lse = a.lse2[r_at] + kShift<E>;
     delta = a.delta[r_at];
-    if (lse == -INFINITY) lse = INFINITY;
   }
   float up = 1.f;
   if constexpr (IsF16<E>::value) {
@@ -173,19 +181,21 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
   }
   const float c2 = a.scale * kLog2e;
 
-  // a thread's pieces of a tile: rows tid / CH + u 256 / CH, the same chunk
+  // a thread's pieces of a tile (columns past d: none)
+  const Tile<DB> at(lane);
   uint4 st[2][PER];
-  const uint32_t ch8 = tid % CH * 8;
-  const uint32_t k_off = ch8 < (uint32_t)a.d ? (tid / CH * (uint32_t)a.k.token + ch8) * 2 : kOOB;
-  const uint32_t v_off = ch8 < (uint32_t)a.d ? (tid / CH * (uint32_t)a.v.token + ch8) * 2 : kOOB;
+  const auto off = [&](const Heads& x, int u) {
+    const uint32_t c = Fill<DB>::column(tid, 256, u);
+    return c < (uint32_t)a.d ? ((Fill<DB>::row(tid) + u * (256 / CH)) * (uint32_t)x.token + c) * 2 : kOOB;
+  };
+  const auto first_key = [&](const Heads& x, int32_t kt) { return (ks.start + (int64_t)kt * BN) * x.token + kv_head * x.head; };
   auto load = [&](int32_t kt) {
-    const int64_t key = ks.start + (int64_t)kt * BN, left = kt < k1 ? ks.n - (int64_t)kt * BN : 0;
-    const __amdgpu_buffer_rsrc_t rk = rows_rsrc(a.k, key * a.k.token + kv_head * a.k.head, left, a.d);
-    const __amdgpu_buffer_rsrc_t rv = rows_rsrc(a.v, key * a.v.token + kv_head * a.v.head, left, a.d);
+    const int64_t left = kt < k1 ? ks.n - (int64_t)kt * BN : 0;
+    const __amdgpu_buffer_rsrc_t rk = rows_rsrc(a.k, first_key(a.k, kt), left, a.d), rv = rows_rsrc(a.v, first_key(a.v, kt), left, a.d);
 #pragma unroll
     for (int u = 0; u < PER; ++u) {
-      st[0][u] = buf_load16(rk, k_off + u * (256 / CH) * 2 * (uint32_t)a.k.token);
-      st[1][u] = buf_load16(rv, v_off + u * (256 / CH) * 2 * (uint32_t)a.v.token);
+      st[0][u] = buf_load16(rk, off(a.k, u));
+      st[1][u] = buf_load16(rv, off(a.v, u));
     }
   };
   auto store = [&](int32_t kt, int buf) {
@@ -198,67 +208,103 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
         atomicMin(&s_bad, kt * BN + c / CH);
         st[0][u] = finite_part<E>(st[0][u]);
       }
-      *reinterpret_cast<uint4*>(to + TileLayout<DB>::at(c / CH, c % CH)) = st[0][u];
-      *reinterpret_cast<uint4*>(to + BYTES + TileLayout<DB>::at(c / CH, c % CH)) = st[1][u];
+      *reinterpret_cast<uint4*>(to + c * 16) = st[0][u];
+      *reinterpret_cast<uint4*>(to + BYTES + c * 16) = st[1][u];
     }
   };
 
   f32x16 dq[DB];
 #pragma unroll
   for (int b = 0; b < DB; ++b) dq[b] = (f32x16)(0.f);
-  // MASKED: a tile that some of the rows do not see in full
+  // The scores of a tile's second half are computed beside dS of the first, dQ of
+  // the first beside dS of the second; operands come from LDS through a ring of
+  // registers, RING products ahead.  MASKED: some of the rows do not see it in full
   auto tile = [&](int32_t kt, const uint8_t* kb, auto MASKED) {
-    constexpr bool kMasked = decltype(MASKED)::value;
     const uint8_t* vb = kb + BYTES;
+    constexpr int N = 2 * DB, RING = RINGQ, EP = 8 / DB;  // products of each kind, dS beside each of them
+    uint4 ring[RING];
+    auto fetch = [&](int f) {
+      if (f < 4 * N) ring[f % RING] = at.rows(f / N % 2 ? vb : kb, 32 * (f / (2 * N)), f % N);
+      else if (f < 6 * N) ring[f % RING] = at.cols(kb, 16 * ((f - 4 * N) / N * 2 + f % 2), f % N / 2);
+    };
+    f32x16 s[2], dp[2];
+    typename E::v8 ds[2][2];
+    auto make_ds = [&](int u, int e) {
+      s[u][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][e], c2, -lse)) * ((dp[u][e] - delta) * up);
+      if constexpr (decltype(MASKED)::value)
+        if (kt * BN + 32 * u + 8 * (e / 4) + 4 * half + e % 4 > last) s[u][e] = 0.f;
+      if (e % 8 == 7) ds[u][e / 8] = pack8<E>(s[u], e / 8 * 8);
+    };
 #pragma unroll
-    for (int u = 0; u < BN / 32; ++u) {
-      f32x16 s = (f32x16)(0.f), dp = (f32x16)(0.f);
+    for (int f = 0; f < RING; ++f) fetch(f);
 #pragma unroll
-      for (int i = 0; i < 2 * DB; ++i) s = E::mfma32(frag_rows<E, DB>(kb, 32 * u, i, lane), qf[i], s);
+    for (int u = 0; u < 2; ++u) s[u] = dp[u] = (f32x16)(0.f);
 #pragma unroll
-      for (int i = 0; i < 2 * DB; ++i) dp = E::mfma32(frag_rows<E, DB>(vb, 32 * u, i, lane), df[i], dp);
+    for (int f = 0; f < 4 * N; ++f) {
+      const int u = f / (2 * N);
+      if (f / N % 2 == 0) s[u] = E::mfma32(E::vec(ring[f % RING]), E::vec(qf[f % N]), s[u]);
+      else dp[u] = E::mfma32(E::vec(ring[f % RING]), E::vec(df[f % N]), dp[u]);
+      fetch(f + RING);
+      if (u == 1) {
 #pragma unroll
-      for (int r = 0; r < 16; ++r)
-        s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], c2, -lse)) * ((dp[r] - delta) * up);
-      if constexpr (kMasked) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if (kt * BN + 32 * u + 8 * (r / 4) + 4 * half + r % 4 > last) s[r] = 0.f;
+        for (int e = EP / 2 * (f - 2 * N); e < EP / 2 * (f - 2 * N + 1); ++e) make_ds(0, e);
       }
-      typename E::v8 p[2];
+      __builtin_amdgcn_sched_barrier(0);
+    }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) p[i] = pack8<E>(s, 8 * i);
+    for (int f = 4 * N; f < 6 * N; ++f) {
+      const int u = (f - 4 * N) / N, b = f % N / 2;
+      dq[b] = E::mfma32(E::vec(ring[f % RING]), ds[u][f % 2], dq[b]);
+      fetch(f + RING);
+      if (u == 0) {
 #pragma unroll
-      for (int b = 0; b < DB; ++b) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) dq[b] = E::mfma32(E::vec(frag_cols<DB>(kb, 32 * u + 16 * i, b, lane)), p[i], dq[b]);
+        for (int e = EP * (f - 4 * N); e < EP * (f - 4 * N + 1); ++e) make_ds(1, e);
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
 
   if (tid == 0) s_bad = INT_MAX;
-  __syncthreads();
-  load(0);
-  store(0, 0);
-  load(1);
-  __syncthreads();
-  auto go = [&](int32_t from, int32_t to, auto MASKED) {
-    for (int32_t kt = from; kt < to; ++kt) {
+  const int32_t kf = max(0, min(k1, whole / BN));  // the first tile that not all rows see in full
+  if (kf > 0) {
+    const uint32_t lds0 = lds_offset(lds) + wave * 1024;
+    auto direct = [&](int32_t kt, uint32_t to) {
+      const LdsSource rk = rows_source(a.k, first_key(a.k, kt), kt < kf ? BN : 0, a.d);
+      const LdsSource rv = rows_source(a.v, first_key(a.v, kt), kt < kf ? BN : 0, a.d);
+#pragma unroll
+      for (int u = 0; u < PER; ++u) {
+        load_to_lds16(rk, off(a.k, u), to + u * 4096);
+        load_to_lds16(rv, off(a.v, u), to + BYTES + u * 4096);
+      }
+    };
+    direct(0, lds0);
+    tile_barrier();
+    for (int32_t kt = 0; kt < kf; ++kt) {
       const int buf = kt & 1;
+      direct(kt + 1, lds0 + (buf ^ 1) * 2 * BYTES);
+      tile(kt, lds + buf * 2 * BYTES, std::false_type{});
+      tile_barrier();
+    }
+  }
+  if (kf < k1) {
+    __syncthreads();
+    load(kf);
+    store(kf, 0);
+    load(kf + 1);
+    __syncthreads();
+    for (int32_t kt = kf; kt < k1; ++kt) {
+      const int buf = (kt - kf) & 1;
       if (kt + 1 < k1) {
         store(kt + 1, buf ^ 1);
         load(kt + 2);
       }
-      if (!decltype(MASKED)::value || kt * BN < wend) tile(kt, lds + buf * 2 * BYTES, MASKED);
+      if (kt * BN < wend) tile(kt, lds + buf * 2 * BYTES, std::true_type{});
       __syncthreads();
     }
-  };
-  const int32_t kf = max(0, min(k1, whole / BN));  // the first tile that not all rows see in full
-  go(0, kf, std::false_type{});
-  go(kf, k1, std::true_type{});
+  }
   const float f = s_bad <= last ? NAN : a.scale / up;
 #pragma unroll
-  for (int b = 0; b < DB; ++b) store_block<E>(a.dq, at, live, b, a.d, dq[b], f, lane);
+  for (int b = 0; b < DB; ++b) store_block<E>(a.dq, o_at, live, b, a.d, dq[b], f, lane);
 }
 
 // dK and dV: 128 keys a workgroup, 32 a wave, tiles of 32 rows of queries.
@@ -275,9 +321,9 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
 template <typename E, int DB>
 __global__ __launch_bounds__(256, 2) void k_attn_bwd_kv(AttnArgs a) {
   constexpr int BQ = 32, BK = 128;
-  constexpr int CH = TileLayout<DB>::kChunks, PER = BQ * CH / 256, BYTES = BQ * TileLayout<DB>::kPitch;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[4 * BYTES], s_v[BK * TileLayout<DB>::kPitch];
-  __shared__ __attribute__((aligned(16))) float s_lse[2][BQ], s_delta[2][BQ];
+  constexpr int CH = Tile<DB>::kChunks, PER = BQ * CH / 256, BYTES = BQ * Tile<DB>::kPitch;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[4 * BYTES], s_v[BK * Tile<DB>::kPitch];
+  __shared__ __attribute__((aligned(16))) float s_lse[2][64], s_delta[2][64];
   __shared__ __attribute__((aligned(16))) int s_last[2][BQ];
   __shared__ NonFinite<32 * DB> s_bad;
   __shared__ float s_top[4];
@@ -319,52 +365,35 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_kv(AttnArgs a) {
   }
 #pragma unroll
   for (int u = 0; u < BK * CH / 256; ++u) {
-    const int c = u * 256 + tid, ch = c % CH;
+    const int c = u * 256 + tid, col = Fill<DB>::column(tid, 256, u);
     const int32_t k = key0 + c / CH;
-    *reinterpret_cast<uint4*>(s_v + TileLayout<DB>::at(c / CH, ch)) =
-        load16(a.v, (rg.start + k) * a.v.token + kv_head * a.v.head + ch * 8, k < nk && ch * 8 < a.d);
+    *reinterpret_cast<uint4*>(s_v + c * 16) =
+        load16(a.v, (rg.start + k) * a.v.token + kv_head * a.v.head + col, k < nk && col < a.d);
   }
   float up = 1.f;
   if constexpr (IsF16<E>::value) {
     const float dtop = all_tops(a.top, tops_of(a.tq, a.batch), s_top);
     up = to_range(2.f * a.d * dtop * all_tops(a.top + kAttnTops, tops_of(a.tk, a.batch), s_top));
   }
-  constexpr float kShift = IsF16<E>::value ? kPShift : 0.f;
-  const float ups = up * __builtin_amdgcn_exp2f(-kShift);
+  const float ups = up * __builtin_amdgcn_exp2f(-kShift<E>);
   const float c2 = a.scale * kLog2e;
 
-  // This thread's rows of a tile: tid / CH + u 256 / CH.  Where the group's size
-  // divides them, their places in the tile are the same in every tile; otherwise
-  // each tile costs divisions.
-  const uint32_t ch8 = tid % CH * 8;
+  // a thread's pieces of a tile, of Q and dO: rows tid / CH + u 256 / CH, the same
+  // columns ch8 .. + 7 (256 / CH is a multiple of 16: so is the permutation)
+  const Tile<DB> at(lane);
+  const uint32_t ch8 = Fill<DB>::column(tid, 256, 0);
   const int64_t q_at = q0 * a.q.token + head0 * a.q.head, d_at = q0 * a.dout.token + head0 * a.dout.head;
-  const int32_t mytok = tid / CH / group, myhead = tid / CH % group;
-  const bool quick = 256 / CH % group == 0 && (group - 1) * max(a.q.head, a.dout.head) < (1 << 28);
-  const uint32_t q_off = (uint32_t)(mytok * a.q.token + myhead * a.q.head + ch8) * 2;
-  const uint32_t d_off = (uint32_t)(mytok * a.dout.token + myhead * a.dout.head + ch8) * 2;
   uint4 st[2][PER];
   float st_lse = 0.f, st_delta = 0.f;
   int st_last = 0;
-  // nothing past the last row
+  // through registers; nothing past the last row
   auto load = [&](int32_t rt) {
-    if (quick) {
-      const int32_t tok0 = rt * BQ / group, left = (ch8 < (uint32_t)a.d ? nq : 0) - tok0 - mytok;
-      const __amdgpu_buffer_rsrc_t rq = make_rsrc(a.q.p + (tok0 < nq ? q_at + tok0 * a.q.token : 0), 0x7fffffff);
-      const __amdgpu_buffer_rsrc_t rd = make_rsrc(a.dout.p + (tok0 < nq ? d_at + tok0 * a.dout.token : 0), 0x7fffffff);
 #pragma unroll
-      for (int u = 0; u < PER; ++u) {
-        const int32_t on = u * (256 / CH) / group;
-        st[0][u] = buf_load16(rq, on < left ? q_off + on * 2 * (uint32_t)a.q.token : kOOB);
-        st[1][u] = buf_load16(rd, on < left ? d_off + on * 2 * (uint32_t)a.dout.token : kOOB);
-      }
-    } else {
-#pragma unroll
-      for (int u = 0; u < PER; ++u) {
-        const int32_t r = rt * BQ + (u * 256 + tid) / CH, tok = r / group, head = r % group;
-        const bool ok = tok < nq && ch8 < (uint32_t)a.d;
-        st[0][u] = load16(a.q, q_at + tok * a.q.token + head * a.q.head + ch8, ok);
-        st[1][u] = load16(a.dout, d_at + tok * a.dout.token + head * a.dout.head + ch8, ok);
-      }
+    for (int u = 0; u < PER; ++u) {
+      const int32_t r = rt * BQ + (u * 256 + tid) / CH, tok = r / group, head = r % group;
+      const bool ok = tok < nq && ch8 < (uint32_t)a.d;
+      st[0][u] = load16(a.q, q_at + tok * a.q.token + head * a.q.head + ch8, ok);
+      st[1][u] = load16(a.dout, d_at + tok * a.dout.token + head * a.dout.head + ch8, ok);
     }
     if (tid < BQ) {
       const int32_t r = rt * BQ + tid, tok = r / group;
@@ -373,28 +402,26 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_kv(AttnArgs a) {
       st_delta = 0.f;
       st_last = -1;
       if (tok < nq && in_bounds(i, 1, a.tq * a.heads)) {
-        st_lse = a.lse[i] * kLog2e;
-        if (st_lse == -INFINITY) st_lse = INFINITY;  // a row that sees nothing: P = 0
-        st_lse -= kShift;
+        st_lse = a.lse2[i];
         st_delta = a.delta[i];
         st_last = a.causal ? min(nk - 1, tok + off) : nk - 1;
       }
     }
   };
-  auto store = [&](int32_t rt, int buf, auto MASKED) {
+  auto store = [&](int32_t rt, int buf) {
     uint8_t* const to = lds + buf * 2 * BYTES;
 #pragma unroll
     for (int u = 0; u < PER; ++u) {
       const int c = u * 256 + tid;
-      if (decltype(MASKED)::value && rt < rf) {
+      if (rt < rf) {
         if (not_finite<E>(st[1][u])) {
           const int32_t t = (rt * BQ + c / CH) / group;
           s_bad.template take<E, false>(st[1][u], ch8, a.causal ? min(nk - 1, t + off) : nk - 1);
         }
         if (not_finite<E>(st[0][u])) st[0][u] = finite_part<E>(st[0][u]);
       }
-      *reinterpret_cast<uint4*>(to + TileLayout<DB>::at(c / CH, c % CH)) = st[0][u];
-      *reinterpret_cast<uint4*>(to + BYTES + TileLayout<DB>::at(c / CH, c % CH)) = st[1][u];
+      *reinterpret_cast<uint4*>(to + c * 16) = st[0][u];
+      *reinterpret_cast<uint4*>(to + BYTES + c * 16) = st[1][u];
     }
     if (tid < BQ) {
       s_lse[buf][tid] = st_lse;
@@ -408,15 +435,15 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_kv(AttnArgs a) {
   for (int b = 0; b < DB; ++b) dk[b] = dv[b] = (f32x16)(0.f);
   auto tile = [&](int32_t rt, int buf, auto MASKED) {
     constexpr bool kMasked = decltype(MASKED)::value;
-    const uint8_t *qb = lds + buf * 2 * BYTES, *db = qb + BYTES, *vb = s_v + 32 * wave * TileLayout<DB>::kPitch;
+    const uint8_t *qb = lds + buf * 2 * BYTES, *db = qb + BYTES, *vb = s_v + 32 * wave * Tile<DB>::kPitch;
     // Operands in the order of their use, each read from LDS into a ring of
     // registers while the products before it run.
     constexpr int N = 2 * DB, RING = RINGV, EP = 16 / N;
     uint4 ring[RING];
     auto fetch = [&](int f) {
-      if (f < N) ring[f % RING] = raw_rows<DB>(qb, 0, f, lane);
-      else if (f < 3 * N) ring[f % RING] = raw_rows<DB>((f - N) % 2 ? vb : db, 0, (f - N) / 2, lane);
-      else if (f < 5 * N) ring[f % RING] = frag_cols<DB>(f < 4 * N ? db : qb, 16 * (f % 2), (f - (f < 4 * N ? 3 : 4) * N) / 2, lane);
+      if (f < N) ring[f % RING] = at.rows(qb, 0, f);
+      else if (f < 3 * N) ring[f % RING] = at.rows((f - N) % 2 ? vb : db, 0, (f - N) / 2);
+      else if (f < 5 * N) ring[f % RING] = at.cols(f < 4 * N ? db : qb, 16 * (f % 2), f % N / 2);
     };
     // row values (lse, delta) of accumulators EP i .. EP i + EP - 1
     float aux[2][EP];
@@ -486,28 +513,65 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_kv(AttnArgs a) {
 
   s_bad.clear(-1);
   __syncthreads();
-  load(r0);
-  store(r0, 0, std::true_type{});
-  load(r0 + 1);
-  __syncthreads();
-  auto go = [&](int32_t from, int32_t to, auto MASKED) {
-    for (int32_t rt = from; rt < to; ++rt) {
+  // Rows that do not see all keys go through registers, the others straight into
+  // LDS, where a workgroup's rows are at the same places in every tile (that is,
+  // where the group divides the rows of a piece).
+  const bool quick = 256 / CH % group == 0 && (group - 1) * max(a.q.head, a.dout.head) < (1 << 28);
+  const int32_t rd = quick ? rf : r1;
+  if (r0 < rd) {
+    load(r0);
+    store(r0, 0);
+    load(r0 + 1);
+    __syncthreads();
+    for (int32_t rt = r0; rt < rd; ++rt) {
       const int buf = (rt - r0) & 1;
-      store(rt + 1, buf ^ 1, MASKED);
-      load(rt + 2);
-      tile(rt, buf, MASKED);
+      if (rt + 1 < rd) {
+        store(rt + 1, buf ^ 1);
+        load(rt + 2);
+      }
+      tile(rt, buf, std::true_type{});
       __syncthreads();
     }
-  };
-  go(r0, rf, std::true_type{});
-  go(rf, r1, std::false_type{});
+  }
+  if (rd < r1) {
+    const int32_t mytok = tid / CH / group, myhead = tid / CH % group, ltok = (lane & 31) / group, lhead = (lane & 31) % group;
+    const uint32_t q_off = (uint32_t)(mytok * a.q.token + myhead * a.q.head + ch8) * 2;
+    const uint32_t d_off = (uint32_t)(mytok * a.dout.token + myhead * a.dout.head + ch8) * 2;
+    const uint32_t l_off = (uint32_t)(ltok * a.heads + lhead) * 4;
+    const uint32_t lds0 = lds_offset(lds) + wave * 1024, rows0 = lds_offset(wave == 0 ? &s_lse[0][0] : &s_delta[0][0]);
+    auto direct = [&](int32_t rt, int buf) {
+      const int32_t tok0 = rt * BQ / group, left = rt < r1 ? nq - tok0 : 0;  // whole tokens: group divides BQ
+      const LdsSource rq = lds_source(a.q.p + (left > 0 ? q_at + tok0 * a.q.token : 0), 0x7fffffff);
+      const LdsSource ro = lds_source(a.dout.p + (left > 0 ? d_at + tok0 * a.dout.token : 0), 0x7fffffff);
+#pragma unroll
+      for (int u = 0; u < PER; ++u) {
+        const int32_t on = u * (256 / CH) / group;
+        const bool ok = mytok + on < left && ch8 < (uint32_t)a.d;
+        load_to_lds16(rq, ok ? q_off + on * 2 * (uint32_t)a.q.token : kOOB, lds0 + buf * 2 * BYTES + u * 4096);
+        load_to_lds16(ro, ok ? d_off + on * 2 * (uint32_t)a.dout.token : kOOB, lds0 + buf * 2 * BYTES + BYTES + u * 4096);
+      }
+      // rows past the last: zeros, and so P dO and dS Q are zero whatever P is
+      if (wave < 2) {
+        const LdsSource rl = lds_source((wave == 0 ? a.lse2 : a.delta) + (left > 0 ? (q0 + tok0) * a.heads + head0 : 0), 0x7fffffff);
+        load_to_lds4(rl, lane < BQ && ltok < left ? l_off : kOOB, rows0 + buf * 256);
+      }
+    };
+    direct(rd, 0);
+    tile_barrier();
+    for (int32_t rt = rd; rt < r1; ++rt) {
+      const int buf = (rt - rd) & 1;
+      direct(rt + 1, buf ^ 1);
+      tile(rt, buf, std::false_type{});
+      tile_barrier();
+    }
+  }
   if (s_bad.any) {
 #pragma unroll
     for (int b = 0; b < DB; ++b)
 #pragma unroll
       for (int r = 0; r < 16; ++r) dv[b][r] += s_bad.template seen<false>(32 * b + 8 * (r / 4) + 4 * half + r % 4, key);
   }
-  const float fk = a.scale / up, fv = __builtin_amdgcn_exp2f(-kShift);
+  const float fk = a.scale / up, fv = __builtin_amdgcn_exp2f(-kShift<E>);
   if (a.splits == 1) {
 #pragma unroll
     for (int b = 0; b < DB; ++b) {
@@ -574,9 +638,11 @@ size_t attn_bwd_part_bytes(int splits, int64_t tk, int64_t kv_heads, int64_t d) 
   return splits > 1 ? (size_t)splits * tk * kv_heads * 2 * d * 4 : 0;
 }
 
-hipError_t launch_attn_bwd(const AttnArgs& args, float* delta, float* top, float* part, int splits, hipStream_t stream) {
+hipError_t launch_attn_bwd(const AttnArgs& args, float* delta, float* lse2, float* top, float* part, int splits,
+                           hipStream_t stream) {
   AttnArgs a = args;
   a.delta = delta;
+  a.lse2 = lse2;
   a.top = top;
   a.part = part;
   a.splits = splits;
@@ -586,9 +652,9 @@ hipError_t launch_attn_bwd(const AttnArgs& args, float* delta, float* top, float
     const int64_t dt = attn_tiles(a.tq, 1, a.batch, kDeltaTokens), vt = attn_tiles(a.tk, 1, a.batch, kDeltaTokens);
     if (a.f16) {
       // as many workgroups as partial maxima, the same for dO and V
-      k_attn_delta<E><<<dim3((uint32_t)std::min<int64_t>(std::max(dt, vt), kAttnTops), 2), 256, 0, stream>>>(a, delta, top);
+      k_attn_delta<E><<<dim3((uint32_t)std::min<int64_t>(std::max(dt, vt), kAttnTops), 2), 256, 0, stream>>>(a, delta, lse2, top);
     } else if (a.tq > 0) {
-      k_attn_delta<E><<<(uint32_t)std::min<int64_t>(dt, 1 << 20), 256, 0, stream>>>(a, delta, top);
+      k_attn_delta<E><<<(uint32_t)std::min<int64_t>(dt, 1 << 20), 256, 0, stream>>>(a, delta, lse2, top);
     }
     if (a.tk > 0) {
       k_attn_bwd_kv<E, DB><<<(uint32_t)(attn_tiles(a.tk, 1, a.batch, 128) * a.kv_heads * a.splits), 256, 0, stream>>>(a);

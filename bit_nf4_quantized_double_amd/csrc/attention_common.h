@@ -79,48 +79,57 @@ __device__ __forceinline__ Keys keys_of(const AttnArgs& a, int32_t seq) {
 }
 
 // A tile in LDS: rows of DB * 32 16-bit values (chunks of 16 bytes past d are
-// zeros), 32 bytes further apart than they are long.  The 8 rows that a wave's
-// b128 reads of one column touch at a time, and the 4 rows by 32 bytes of its
-// transposing reads, then fall into different banks, and every address is a
-// lane's base plus a constant (with chunks permuted by row instead, each needed
-// a register of its own).
+// zeros) one after another, as loads straight into LDS leave them; the chunks of a
+// row are permuted by chunk ^ spread(row), so that the 8 rows that a wave's b128
+// reads of one column touch at a time, and the 4 rows by 32 bytes of its
+// transposing reads, fall into different banks.
 template <int DB>
-struct TileLayout {
-  static constexpr int kPitch = DB * 64 + 32;  // bytes of a row
-  static constexpr int kChunks = DB * 4;       // 16-byte chunks of a row
-  static __device__ __forceinline__ uint32_t at(uint32_t row, uint32_t chunk) { return row * kPitch + chunk * 16; }
+struct Tile {
+  static constexpr int kPitch = DB * 64;  // bytes of a row
+  static constexpr int kChunks = DB * 4;  // 16-byte chunks of a row
+  static __device__ __forceinline__ uint32_t spread(uint32_t r) {
+    return (DB == 4 ? (r & 3) << 2 : (r >> 1 & 1) << 2) | (r >> 2 & 1);
+  }
+
+  // A lane's places in a tile; with these every address is one plus a constant.
+  uint32_t row[DB], col[DB];
+  __device__ __forceinline__ explicit Tile(int lane) {
+    const uint32_t r = lane & 31, t = 4 * (lane >> 5) + ((lane & 15) >> 2);
+#pragma unroll
+    for (int k = 0; k < DB; ++k) {
+      row[k] = r * kPitch + ((4 * k + (lane >> 5)) ^ spread(r)) * 16;
+      col[k] = t * kPitch + ((4 * k + 2 * (lane >> 4 & 1) + ((lane & 3) >> 1)) ^ spread(t)) * 16 + 8 * (lane & 1);
+    }
+  }
+  // MFMA operand (32 x 16): row r0 + lane % 32, columns 16 step + 8 (lane / 32) .. + 7.  r0 a multiple of 32.
+  __device__ __forceinline__ uint4 rows(const uint8_t* tile, int r0, int step) const {
+    return *reinterpret_cast<const uint4*>(tile + row[step >> 1] + r0 * kPitch + (step & 1) * 32);
+  }
+  // The transposed operand (32 x 16): column 32 block + lane % 32 of rows r0 ..
+  // r0 + 15, in the order in which the accumulators of a 32 x 32 product hold
+  // their rows: element e of lane half h is row r0 + 8 (e / 4) + 4 h + e % 4.
+  // (ds_read_b64_tr_b16: 16 lanes give the addresses of 4 rows of 16 values, 4 a
+  // lane, and each gets one column of them.)  r0 a multiple of 16.
+  __device__ __forceinline__ uint4 cols(const uint8_t* tile, int r0, int block) const {
+    typedef __attribute__((ext_vector_type(4))) short s16x4;
+    uint2 u[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      u[i] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (__attribute__((address_space(3))) s16x4*)(tile + col[block] + (r0 + 8 * i) * kPitch)));
+    return make_uint4(u[0].x, u[0].y, u[1].x, u[1].y);
+  }
 };
 
-// MFMA operand (32 x 16): row r0 + lane % 32, columns 16 step + 8 (lane / 32) .. + 7.
+// How `threads` threads fill a tile: piece u of thread t is the 16 bytes t + u
+// threads of it, of row t / chunks + u step, whose source is this column.
 template <int DB>
-__device__ __forceinline__ uint4 raw_rows(const uint8_t* tile, int r0, int step, int lane) {
-  return *reinterpret_cast<const uint4*>(tile + TileLayout<DB>::at(r0 + (lane & 31), 2 * step + (lane >> 5)));
-}
-template <typename E, int DB>
-__device__ __forceinline__ typename E::v8 frag_rows(const uint8_t* tile, int r0, int step, int lane) {
-  return E::vec(raw_rows<DB>(tile, r0, step, lane));
-}
-
-typedef __attribute__((ext_vector_type(4))) short s16x4;
-
-// The transposed operand (32 x 16): column 32 block + lane % 32 of rows r0 ..
-// r0 + 15, in the order in which the accumulators of a 32 x 32 product hold
-// their rows: element e of lane half h is row r0 + 8 (e / 4) + 4 h + e % 4.
-// (ds_read_b64_tr_b16: 16 lanes give the addresses of 4 rows of 16 values, 4 a
-// lane, and each gets one column of them.)
-template <int DB>
-__device__ __forceinline__ uint4 frag_cols(const uint8_t* tile, int r0, int block, int lane) {
-  uint2 u[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t row = r0 + 8 * i + 4 * (lane >> 5) + ((lane & 15) >> 2);
-    const uint32_t chunk = 4 * block + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-    const uint8_t* p = tile + TileLayout<DB>::at(row, chunk) + 8 * (lane & 1);
-    const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
-    u[i] = __builtin_bit_cast(uint2, v);
+struct Fill {
+  static __device__ __forceinline__ uint32_t row(uint32_t t) { return t / Tile<DB>::kChunks; }
+  static __device__ __forceinline__ uint32_t column(uint32_t t, uint32_t threads, uint32_t u) {
+    return (t % Tile<DB>::kChunks ^ Tile<DB>::spread(row(t) + u * (threads / Tile<DB>::kChunks))) * 8;
   }
-  return make_uint4(u[0].x, u[0].y, u[1].x, u[1].y);
-}
+};
 
 // Halves of d that are infinite or NaN: their top bits.
 template <typename E>
@@ -232,9 +241,22 @@ __device__ __forceinline__ void store_block(const Heads& o, int64_t at, bool ok,
 
 // `rows` tokens of one head from element `at` on as a buffer: past its end
 // (token strides are at most 2^23 elements, tiles at most 128 tokens) reads zeros.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const Heads& x, int64_t at, int64_t rows, int32_t d) {
+__device__ __forceinline__ uint32_t rows_bytes(const Heads& x, int64_t rows, int32_t d) {
   const int64_t n = min(rows, (int64_t)128);
-  return make_rsrc(x.p + (n > 0 ? at : 0), n > 0 ? (uint32_t)(((n - 1) * x.token + d) * 2) : 0u);
+  return n > 0 ? (uint32_t)(((n - 1) * x.token + d) * 2) : 0u;
+}
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const Heads& x, int64_t at, int64_t rows, int32_t d) {
+  return make_rsrc(x.p + (rows > 0 ? at : 0), rows_bytes(x, rows, d));
+}
+__device__ __forceinline__ LdsSource rows_source(const Heads& x, int64_t at, int64_t rows, int32_t d) {
+  return lds_source(x.p + (rows > 0 ? at : 0), rows_bytes(x, rows, d));
+}
+
+// Hand-off of LDS between waves: all of this wave's loads and LDS operations are
+// done, then the barrier.
+__device__ __forceinline__ void tile_barrier() {
+  wait_loads();
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
 __device__ __forceinline__ uint4 load16(const Heads& x, int64_t at, bool ok) {

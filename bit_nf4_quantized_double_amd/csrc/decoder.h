@@ -34,7 +34,7 @@ hipError_t launch_rope(const RopeArgs& a, hipStream_t stream);
 struct AttnArgs {
   Heads q, k, v, o, dout, dq, dk, dv;
   float* lse;              // [tq, heads]
-  const float* delta;      // [tq, heads]
+  const float *delta, *lse2;  // backward: [tq, heads]
   const float* top;        // fp16 backward: [2 kAttnTops] partial maxima of |dO|, then of |V|
   const int32_t *cu_q, *cu_k, *len_q, *len_k;
   float* part;             // forward, split keys: [splits][tq][heads][d] and then [splits][tq][heads] log-sums;
@@ -59,7 +59,8 @@ size_t attn_part_bytes(const AttnPlan& p, int64_t tq, int64_t heads, int64_t d);
 hipError_t launch_attn_fwd(const AttnArgs& a, const AttnPlan& p, hipStream_t stream);
 int attn_bwd_splits(int64_t tk, int64_t batch, int64_t heads, int64_t kv_heads, int compute_units);
 size_t attn_bwd_part_bytes(int splits, int64_t tk, int64_t kv_heads, int64_t d);
-hipError_t launch_attn_bwd(const AttnArgs& a, float* delta, float* top, float* part, int splits, hipStream_t stream);
+hipError_t launch_attn_bwd(const AttnArgs& a, float* delta, float* lse2, float* top, float* part, int splits,
+                           hipStream_t stream);
 
 // ---- the head's cross entropy (cross_entropy.hip) ----
 struct CeArgs {
