@@ -155,6 +155,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
 #pragma unroll
       for (int i = 0; i < 2 * DB; ++i) s[u] = E::mfma32(E::vec(at.rows(kb, 32 * u, i)), qf[i], s[u]);
     }
+    if (KW > 1) __builtin_amdgcn_sched_barrier(0);  // fewer operands on their way: nothing spills
     if constexpr (decltype(MASKED)::value) {
 #pragma unroll
       for (int u = 0; u < NU; ++u)
@@ -182,6 +183,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
       const typename E::v8 p = pack8<E>(s[i / 2], 8 * (i % 2));
 #pragma unroll
       for (int b = 0; b < DB; ++b) o[b] = E::mfma32(E::vec(at.cols(vb, 16 * i, b)), p, o[b]);
+      if (KW > 1) __builtin_amdgcn_sched_barrier(0);
     }
   };
 
@@ -362,7 +364,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
   }
 }
 
-// The splits of a token's rows together: weights exp(lse_z - lse).
+// The splits of a row together: weights exp(lse_z - lse).  8 values a thread.
 template <typename E>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   const int64_t token = blockIdx.x;
@@ -377,34 +379,35 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   if (token - start >= seq_length(a.len_q, n - 1, a.batch, size)) return;
   const int64_t r_n = a.tq * a.heads;
   const float* sums = a.part + a.splits * r_n * a.d;
-  const int pieces = a.d / 8;
-  for (int i = threadIdx.x; i < a.heads * pieces; i += 256) {
-    const int head = i / pieces, c = i % pieces * 8;
-    const int64_t r = token * a.heads + head;
-    float top = -INFINITY;
-    for (int z = 0; z < a.splits; ++z)
-      if (in_bounds(z * r_n + r, 1, a.splits * r_n)) top = fmaxf(top, sums[z * r_n + r]);
-    const float ref = top == -INFINITY ? 0.f : top;
-    float l = 0.f, acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (int z = 0; z < a.splits; ++z) {
-      const float s = in_bounds(z * r_n + r, 1, a.splits * r_n) ? sums[z * r_n + r] : -INFINITY;
-      if (s == -INFINITY) continue;  // no key of the split is seen: its part is not written
-      const float w = __builtin_amdgcn_exp2f((s - ref) * kLog2e);
-      l += w;
-      const int64_t at = (z * r_n + r) * a.d + c;
-      if (!in_bounds(at, 8, a.splits * r_n * a.d)) continue;
-      const float4 x = *reinterpret_cast<const float4*>(a.part + at), y = *reinterpret_cast<const float4*>(a.part + at + 4);
-      acc[0] += w * x.x; acc[1] += w * x.y; acc[2] += w * x.z; acc[3] += w * x.w;
-      acc[4] += w * y.x; acc[5] += w * y.y; acc[6] += w * y.z; acc[7] += w * y.w;
-    }
-    const float f = l == 0.f ? 0.f : 1.f / l;
-    const int64_t at = token * a.o.token + head * a.o.head + c;
-    if (in_bounds(at, 8, a.o.n))
-      *reinterpret_cast<uint4*>(const_cast<uint16_t*>(a.o.p) + at) =
-          make_uint4(E::pack2(acc[0] * f, acc[1] * f), E::pack2(acc[2] * f, acc[3] * f), E::pack2(acc[4] * f, acc[5] * f),
-                     E::pack2(acc[6] * f, acc[7] * f));
-    if (c == 0 && in_bounds(r, 1, r_n)) a.lse[r] = l == 0.f ? -INFINITY : ref + __log2f(l) * kLn2;
+  const int pieces = a.d / 8, i = blockIdx.y * 256 + threadIdx.x;
+  if (i >= a.heads * pieces) return;
+  const int head = i / pieces, c = i % pieces * 8;
+  const int64_t r = token * a.heads + head;
+  float top = -INFINITY;
+#pragma unroll 8
+  for (int z = 0; z < a.splits; ++z)
+    if (in_bounds(z * r_n + r, 1, a.splits * r_n)) top = fmaxf(top, sums[z * r_n + r]);
+  const float ref = top == -INFINITY ? 0.f : top;
+  float l = 0.f, acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 4
+  for (int z = 0; z < a.splits; ++z) {
+    const float s = in_bounds(z * r_n + r, 1, a.splits * r_n) ? sums[z * r_n + r] : -INFINITY;
+    const int64_t at = (z * r_n + r) * a.d + c;
+    // a split that sees no key has not written its part
+    if (s == -INFINITY || !in_bounds(at, 8, a.splits * r_n * a.d)) continue;
+    const float w = __builtin_amdgcn_exp2f((s - ref) * kLog2e);
+    l += w;
+    const float4 x = *reinterpret_cast<const float4*>(a.part + at), y = *reinterpret_cast<const float4*>(a.part + at + 4);
+    acc[0] += w * x.x; acc[1] += w * x.y; acc[2] += w * x.z; acc[3] += w * x.w;
+    acc[4] += w * y.x; acc[5] += w * y.y; acc[6] += w * y.z; acc[7] += w * y.w;
   }
+  const float f = l == 0.f ? 0.f : 1.f / l;
+  const int64_t at = token * a.o.token + head * a.o.head + c;
+  if (in_bounds(at, 8, a.o.n))
+    *reinterpret_cast<uint4*>(const_cast<uint16_t*>(a.o.p) + at) =
+        make_uint4(E::pack2(acc[0] * f, acc[1] * f), E::pack2(acc[2] * f, acc[3] * f), E::pack2(acc[4] * f, acc[5] * f),
+                   E::pack2(acc[6] * f, acc[7] * f));
+  if (c == 0 && in_bounds(r, 1, r_n)) a.lse[r] = l == 0.f ? -INFINITY : ref + __log2f(l) * kLn2;
 }
 
 }  // namespace
@@ -434,7 +437,7 @@ hipError_t launch_attn_fwd(const AttnArgs& args, const AttnPlan& p, hipStream_t 
     constexpr int DB = decltype(db)::value;
     if (p.rows == 32) k_attn_fwd<E, DB, 4><<<(uint32_t)blocks, 256, 0, stream>>>(a);
     else k_attn_fwd<E, DB, 1><<<(uint32_t)blocks, 256, 0, stream>>>(a);
-    if (a.splits > 1) k_attn_join<E><<<(uint32_t)a.tq, 256, 0, stream>>>(a);
+    if (a.splits > 1) k_attn_join<E><<<dim3((uint32_t)a.tq, (uint32_t)((a.heads * a.d / 8 + 255) / 256)), 256, 0, stream>>>(a);
   };
   const auto typed = [&](auto e) {
     if (a.d <= 64) run(e, std::integral_constant<int, 2>{});

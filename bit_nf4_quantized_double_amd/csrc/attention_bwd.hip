@@ -28,7 +28,7 @@
 namespace qlora {
 namespace {
 
-constexpr int kDeltaTokens = 16;  // tokens of a delta tile
+constexpr int kDeltaTokens = 4;  // tokens of a delta tile
 constexpr float kPShift = 12.f;   // fp16: P times 2^12
 
 template <typename E>
@@ -594,7 +594,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_kv(AttnArgs a) {
     }
 }
 
-// The splits' sums together: 16 keys' values of all key heads a workgroup.
+// The splits' sums together: a few keys' values of all key heads a workgroup.
 template <typename E>
 __global__ __launch_bounds__(256) void k_attn_bwd_join(AttnArgs a) {
   const Region rg = find_region(a.cu_k, a.batch, a.tk, 1, kDeltaTokens, blockIdx.x);
