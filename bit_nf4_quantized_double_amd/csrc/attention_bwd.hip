@@ -124,9 +124,6 @@ __device__ __forceinline__ float to_range(float bound) {
   return __builtin_bit_cast(float, (uint32_t)(max(-100, min(100, 14 - e)) + 127) << 23);
 }
 
-#ifndef RINGQ
-#define RINGQ 4
-#endif
 // dQ: 128 rows a workgroup, 32 a wave, tiles of 64 keys.
 template <typename E, int DB>
 __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
@@ -221,7 +218,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
   // registers, RING products ahead.  MASKED: some of the rows do not see it in full
   auto tile = [&](int32_t kt, const uint8_t* kb, auto MASKED) {
     const uint8_t* vb = kb + BYTES;
-    constexpr int N = 2 * DB, RING = RINGQ, EP = 8 / DB;  // products of each kind, dS beside each of them
+    constexpr int N = 2 * DB, RING = 4, EP = 8 / DB;  // products of each kind, dS beside each of them
     uint4 ring[RING];
     auto fetch = [&](int f) {
       if (f < 4 * N) ring[f % RING] = at.rows(f / N % 2 ? vb : kb, 32 * (f / (2 * N)), f % N);
@@ -315,9 +312,6 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
 // (in registers they would leave none for operands on their way).  The products
 // run in groups of two to four, whose operands are read from LDS during the group
 // before; exponentials and dS are made between the MFMAs of dO V^T and of dV.
-#ifndef RINGV
-#define RINGV 4
-#endif
 template <typename E, int DB>
 __global__ __launch_bounds__(256, 2) void k_attn_bwd_kv(AttnArgs a) {
   constexpr int BQ = 32, BK = 128;
@@ -438,7 +432,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_kv(AttnArgs a) {
     const uint8_t *qb = lds + buf * 2 * BYTES, *db = qb + BYTES, *vb = s_v + 32 * wave * Tile<DB>::kPitch;
     // Operands in the order of their use, each read from LDS into a ring of
     // registers while the products before it run.
-    constexpr int N = 2 * DB, RING = RINGV, EP = 16 / N;
+    constexpr int N = 2 * DB, RING = 4, EP = 16 / N;
     uint4 ring[RING];
     auto fetch = [&](int f) {
       if (f < N) ring[f % RING] = at.rows(qb, 0, f);

@@ -31,6 +31,7 @@ SHAPES = [
     ([3, 1, 17], [190, 65, 400], 8, 2, 128, True),   # new tokens behind prefixes
     ([130], [500], 2, 2, 56, True),
     ([260, 5], [131, 260], 6, 3, 40, True),
+    ([200], [2100], 2, 2, 128, True),           # keys split over workgroups of 128 rows
 ]
 
 
@@ -83,7 +84,8 @@ def test_plans_cover_split_keys():
     q = lambda t, h: torch.empty(t, h, 128, dtype=BF16, device="cuda")
     assert attention.plan(q(6, 16), q(4200, 2), ends(6, 1))["rows"] == 32
     assert attention.plan(q(6, 16), q(4200, 2), ends(6, 1))["splits"] > 1
-    assert attention.plan(q(300, 2), q(300, 1), ends(1, 300)) == {"rows": 128, "splits": 2}
+    assert attention.plan(q(200, 2), q(2100, 2), ends(1, 200)) == {"rows": 128, "splits": 5}
+    assert attention.plan(q(300, 2), q(300, 1), ends(1, 300)) == {"rows": 128, "splits": 1}
     assert attention.plan(q(8192, 32), q(8192, 8), ends(1, 8192)) == {"rows": 128, "splits": 1}
 
 
