@@ -29,6 +29,7 @@ namespace qlora {
 namespace {
 
 constexpr int kDeltaTokens = 4;  // tokens of a delta tile
+constexpr int kExactKeys = 32;
 constexpr float kPShift = 12.f;   // fp16: P times 2^12
 
 template <typename E>
@@ -51,6 +52,19 @@ __device__ __forceinline__ int tops_of(int64_t tokens, int64_t batch) {
   return (int)(n < kAttnTops ? n : kAttnTops);
 }
 
+// sum of 8 products
+template <typename E>
+__device__ __forceinline__ float dot8(const uint4& u, const uint4& v) {
+  const uint32_t p[4] = {u.x, u.y, u.z, u.w}, q[4] = {v.x, v.y, v.z, v.w};
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s += E::widen((uint16_t)p[i]) * E::widen((uint16_t)q[i]);
+    s += E::widen((uint16_t)(p[i] >> 16)) * E::widen((uint16_t)(q[i] >> 16));
+  }
+  return s;
+}
+
 template <typename E>
 constexpr float kShift = IsF16<E>::value ? kPShift : 0.f;
 
@@ -69,6 +83,7 @@ __global__ __launch_bounds__(256) void k_attn_delta(AttnArgs a, float* delta, fl
     if (rg.tile < 0) continue;
     const int32_t n = seq_length(isv ? a.len_k : a.len_q, rg.seq, a.batch, rg.size), first = rg.tile * kDeltaTokens;
     const int32_t rows = max(0, min(n - first, kDeltaTokens)) * heads;
+    const Keys ks = keys_of(a, rg.seq);
     for (int32_t r = sub; r < rows; r += 16) {
       const int64_t tok = rg.start + first + r / heads, head = r % heads;
       float sum = 0.f;
@@ -76,19 +91,35 @@ __global__ __launch_bounds__(256) void k_attn_delta(AttnArgs a, float* delta, fl
         const uint4 u = load16(x, tok * x.token + head * x.head + c, true);
         if (IsF16<E>::value) most = fmaxf(most, finite_max<E>(u));
         if (!isv) {
-          const uint4 v = load16(a.o, tok * a.o.token + head * a.o.head + c, true);
-          const uint32_t p[4] = {u.x, u.y, u.z, u.w}, q[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            sum += E::widen((uint16_t)p[i]) * E::widen((uint16_t)q[i]);
-            sum += E::widen((uint16_t)(p[i] >> 16)) * E::widen((uint16_t)(q[i] >> 16));
-          }
+          sum += dot8<E>(u, load16(a.o, tok * a.o.token + head * a.o.head + c, true));
         }
       }
 #pragma unroll
       for (int s = 8; s > 0; s >>= 1) sum += __shfl_xor(sum, s, 16);
-      if (!isv && l16 == 0 && in_bounds(tok * heads + head, 1, a.tq * heads)) {
-        const float l = a.lse[tok * heads + head] * kLog2e;
+      if (isv || !in_bounds(tok * heads + head, 1, a.tq * heads)) continue;
+      const float l = a.lse[tok * heads + head] * kLog2e;
+      // Few keys: from P and dO V instead, since O is rounded, by up to half a step
+      // of itself, and a row's dS is as far off as delta.  (Where a row spreads over
+      // many keys, O is small beside the V it is made of.)
+      const int32_t sees = a.causal ? min(ks.n, first + r / heads + ks.n - n + 1) : ks.n;
+      if (sees <= kExactKeys) {
+        sum = 0.f;
+        const bool in = 8 * l16 < a.d;
+        const uint4 d = load16(a.dout, tok * a.dout.token + head * a.dout.head + 8 * l16, in);
+        const uint4 q = load16(a.q, tok * a.q.token + head * a.q.head + 8 * l16, in);
+        for (int32_t j = 0; j < sees; ++j) {
+          const uint4 k = load16(a.k, (ks.start + j) * a.k.token + head / a.group * a.k.head + 8 * l16, in);
+          const uint4 v = load16(a.v, (ks.start + j) * a.v.token + head / a.group * a.v.head + 8 * l16, in);
+          float z = dot8<E>(q, k), dp = dot8<E>(d, v);
+#pragma unroll
+          for (int s = 8; s > 0; s >>= 1) {
+            z += __shfl_xor(z, s, 16);
+            dp += __shfl_xor(dp, s, 16);
+          }
+          sum += __builtin_amdgcn_exp2f(z * (a.scale * kLog2e) - l) * dp;
+        }
+      }
+      if (l16 == 0) {
         delta[tok * heads + head] = sum;
         lse2[tok * heads + head] = l == -INFINITY ? INFINITY : l - kShift<E>;  // a row that sees nothing: P = 0
       }

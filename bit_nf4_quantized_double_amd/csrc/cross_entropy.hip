@@ -77,6 +77,35 @@ __global__ __launch_bounds__(256) void k_ce_pack(CeArgs a, CeRound r) {
   if (in_bounds(i * 8, 8, r.n_xt)) *reinterpret_cast<uint4*>(r.xt + i * 8) = make_uint4(u.x, u.y, u.z, u.w);
 }
 
+// The target's logit of each token, a wave each: sums of k / 64 terms a lane.
+// (Where a token is known well its loss is as far off, relative to itself, as
+// this logit, and the matrix cores add up k / 32 times in a row.)
+template <typename E>
+__global__ __launch_bounds__(256) void k_ce_target(CeArgs a, CeRound r) {
+  const int64_t m = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  if (m >= r.m || !in_bounds(m, 1, r.m)) return;
+  const int64_t y = a.targets[m];
+  if (y == a.ignore || y < 0 || y >= a.v) return;
+  float s[2] = {0.f, 0.f};
+  for (int64_t c = 8 * lane; c < a.k; c += 512) {
+    Bytes16 u = {0, 0, 0, 0};
+    uint4 w = make_uint4(0, 0, 0, 0);
+    if (in_bounds(m * a.ldx + c, 8, (a.m - 1) * a.ldx + a.k)) __builtin_memcpy(&u, a.x + m * a.ldx + c, 16);
+    if (in_bounds(y * a.ldw + c, 8, (a.v - 1) * a.ldw + a.k)) w = *reinterpret_cast<const uint4*>(a.w + y * a.ldw + c);
+    const uint32_t p[4] = {u.x, u.y, u.z, u.w}, q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s[0] += E::widen((uint16_t)p[i]) * E::widen((uint16_t)q[i]);
+      s[1] += E::widen((uint16_t)(p[i] >> 16)) * E::widen((uint16_t)(q[i] >> 16));
+    }
+  }
+  float sum = s[0] + s[1];
+#pragma unroll
+  for (int i = 32; i > 0; i >>= 1) sum += __shfl_xor(sum, i);
+  if (lane == 0) r.target[m] = sum;
+}
+
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 // Workgroups are dealt round-robin to the 8 XCDs: each gets a contiguous run of
@@ -285,7 +314,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
           for (int t = 0; t < 4; ++t) p.acc[i][t][e] = -INFINITY;
   }
-  // the target's own entry apart
+  // the target's own entry apart (k_ce_target has it)
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
     const int64_t m = m0 + 16 * t + c;
@@ -297,10 +326,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       for (int i = 0; i < G::NS; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (at == 16 * i + e) {
-            if (in_bounds(m, 1, r.mp)) r.target[m] = p.acc[i][t][e];
-            p.acc[i][t][e] = -INFINITY;
-          }
+          if (at == 16 * i + e) p.acc[i][t][e] = -INFINITY;
     }
   }
 #pragma unroll
@@ -544,6 +570,7 @@ CeRound ce_round(int64_t m, int64_t k, int64_t v, bool grad, int cus, char* ws, 
 template <typename E, bool GRAD>
 void run_round(const CeArgs& a, CeRound r, hipStream_t stream) {
   k_ce_pack<E><<<grid_of((r.n_xt / 8 + 255) / 256), 256, 0, stream>>>(a, r);
+  k_ce_target<E><<<(uint32_t)((r.m + 3) / 4), 256, 0, stream>>>(a, r);
   for (int64_t v0 = 0; v0 < a.v; v0 += r.piece) {
     r.v0 = v0;
     r.vn = std::min(r.piece, a.v - v0);

@@ -22,7 +22,20 @@ import torch
 from . import qlora
 from .rows import DTYPES, _stream
 
-_TWO_PI = 2 * Fraction("3.14159265358979323846264338327950288419716939937510582097494459")
+# 2^320 / (2 pi), to 256 bits and more
+_PER_RADIAN = round(Fraction(2**320) / (2 * Fraction(
+    "3.1415926535897932384626433832795028841971693993751058209749445923078164062862089986280348253421170679821480865")))
+
+
+def _turns(f: float) -> int:
+    """f radians as a signed 64-bit fraction of a turn, to the nearest."""
+    m, e = math.frexp(f)
+    up = 320 - 64 + 53 - e  # f = m 2^e, m a multiple of 2^-53
+    n = int(m * 2.0**53) * _PER_RADIAN
+    t = (n + (1 << (up - 1))) >> up if up > 0 else n << -up
+    t &= 2**64 - 1
+    return t - 2**64 if t >= 2**63 else t
+
 
 
 class Frequencies:
@@ -31,14 +44,13 @@ class Frequencies:
     position times frequency is exact modulo a turn."""
 
     def __init__(self, f, factor: float = 1.0, device="cuda"):
-        f = torch.as_tensor(f, dtype=torch.float64).cpu()
+        f = torch.as_tensor(f, dtype=torch.float64, device="cpu")
         if f.dim() != 1 or not bool(torch.isfinite(f).all()):
             raise ValueError("f must be a vector of finite frequencies")
         if not math.isfinite(factor):
             raise ValueError("factor must be finite")
-        turns = [round(Fraction(x) * 2**64 / _TWO_PI) % 2**64 for x in f.tolist()]
-        self.turns = torch.tensor([t - 2**64 if t >= 2**63 else t for t in turns], dtype=torch.int64, device=device)
-        self.rot, self.factor = 2 * len(turns), float(factor)
+        self.turns = torch.tensor([_turns(x) for x in f.tolist()], dtype=torch.int64, device=device)
+        self.rot, self.factor = 2 * f.shape[0], float(factor)
 
 
 def frequencies(rot: int, base: float = 10000.0, *, scaling: str | None = None, by: float = 1.0, trained: int = 4096,
