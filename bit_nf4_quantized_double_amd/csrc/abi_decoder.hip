@@ -94,7 +94,8 @@ int check_attention(const qlora_attention* a) {
     if (a->tokens_q > most / group) return fail(QLORA_ERR_SHAPE, "tokens_q * heads / kv_heads exceeds 2^31 - 256");
     // workgroups of a launch: fewer than 2^24
     if (((a->tokens_q * group + 31) / 32 + a->batch + 2) * a->kv_heads >= (1 << 24) ||
-        ((a->tokens_k + 127) / 128 + a->batch + 2) * a->heads >= (1 << 24))
+        ((a->tokens_k + 127) / 128 + a->batch + 2) * a->heads >= (1 << 24) ||
+        (a->tokens_q + a->tokens_k) / 4 + a->batch >= (1 << 24) - 2)
       return fail(QLORA_ERR_SHAPE, "too many rows for one launch");
   }
   return QLORA_OK;

@@ -29,7 +29,7 @@ namespace qlora {
 namespace {
 
 constexpr int kDeltaTokens = 4;  // tokens of a delta tile
-constexpr int kExactKeys = 32;
+constexpr int kFewKeys = 32;      // rows that see no more get delta from P and dO V
 constexpr float kPShift = 12.f;   // fp16: P times 2^12
 
 template <typename E>
@@ -96,31 +96,10 @@ __global__ __launch_bounds__(256) void k_attn_delta(AttnArgs a, float* delta, fl
       }
 #pragma unroll
       for (int s = 8; s > 0; s >>= 1) sum += __shfl_xor(sum, s, 16);
-      if (isv || !in_bounds(tok * heads + head, 1, a.tq * heads)) continue;
-      const float l = a.lse[tok * heads + head] * kLog2e;
-      // Few keys: from P and dO V instead, since O is rounded, by up to half a step
-      // of itself, and a row's dS is as far off as delta.  (Where a row spreads over
-      // many keys, O is small beside the V it is made of.)
       const int32_t sees = a.causal ? min(ks.n, first + r / heads + ks.n - n + 1) : ks.n;
-      if (sees <= kExactKeys) {
-        sum = 0.f;
-        const bool in = 8 * l16 < a.d;
-        const uint4 d = load16(a.dout, tok * a.dout.token + head * a.dout.head + 8 * l16, in);
-        const uint4 q = load16(a.q, tok * a.q.token + head * a.q.head + 8 * l16, in);
-        for (int32_t j = 0; j < sees; ++j) {
-          const uint4 k = load16(a.k, (ks.start + j) * a.k.token + head / a.group * a.k.head + 8 * l16, in);
-          const uint4 v = load16(a.v, (ks.start + j) * a.v.token + head / a.group * a.v.head + 8 * l16, in);
-          float z = dot8<E>(q, k), dp = dot8<E>(d, v);
-#pragma unroll
-          for (int s = 8; s > 0; s >>= 1) {
-            z += __shfl_xor(z, s, 16);
-            dp += __shfl_xor(dp, s, 16);
-          }
-          sum += __builtin_amdgcn_exp2f(z * (a.scale * kLog2e) - l) * dp;
-        }
-      }
-      if (l16 == 0) {
-        delta[tok * heads + head] = sum;
+      if (!isv && l16 == 0 && in_bounds(tok * heads + head, 1, a.tq * heads)) {
+        const float l = a.lse[tok * heads + head] * kLog2e;
+        if (sees <= 0 || sees > kFewKeys) delta[tok * heads + head] = sum;  // the others: k_attn_delta_few
         lse2[tok * heads + head] = l == -INFINITY ? INFINITY : l - kShift<E>;  // a row that sees nothing: P = 0
       }
     }
@@ -134,6 +113,57 @@ __global__ __launch_bounds__(256) void k_attn_delta(AttnArgs a, float* delta, fl
     const int at = (isv ? kAttnTops : 0) + blockIdx.x;
     if (threadIdx.x == 0 && in_bounds(at, 1, 2 * kAttnTops))
       top[at] = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
+  }
+}
+
+// delta of the rows that see few keys, as sum P (dO V) by the matrix cores: O is
+// rounded, by up to half a step of itself, and a row's dS is as far off as its
+// delta.  (Where a row spreads over many keys, O is small beside the V that it is
+// made of.)  A wave for each sequence and head.
+template <typename E, int DB>
+__global__ __launch_bounds__(256) void k_attn_delta_few(AttnArgs a, float* delta) {
+  const int lane = threadIdx.x & 63, half = lane >> 5;
+  const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (w >= (int64_t)a.batch * a.heads) return;
+  const int32_t seq = (int32_t)(w / a.heads), head = (int32_t)(w % a.heads);
+  const int64_t start = region_start(a.cu_q, a.batch, a.tq, seq + 1);
+  const int64_t size = clampl(region_start(a.cu_q, a.batch, a.tq, seq + 2), start, a.tq) - start;
+  const int32_t n = seq_length(a.len_q, seq, a.batch, size);
+  const Keys ks = keys_of(a, seq);
+  // the rows that see 1 .. kFewKeys keys
+  const int32_t shift = ks.n - n;
+  const int32_t from = a.causal ? max(0, -shift) : 0;
+  const int32_t to = a.causal ? min(n, kFewKeys - shift) : ks.n <= kFewKeys ? n : 0;
+  if (ks.n == 0) return;
+  const int32_t key = lane & 31, kv_head = head / a.group;
+  const bool live = key < ks.n;
+  for (int32_t t0 = from; t0 < to; t0 += 32) {
+    const int32_t t = t0 + (lane & 31);
+    const bool row = t < to;
+    const int64_t tok = start + t;
+    f32x16 s = (f32x16)(0.f), dp = (f32x16)(0.f);
+#pragma unroll
+    for (int i = 0; i < 2 * DB; ++i) {
+      const int c = 16 * i + 8 * half;
+      const bool in = c < a.d;
+      const uint4 k = load16(a.k, (ks.start + key) * a.k.token + kv_head * a.k.head + c, live && in);
+      const uint4 v = load16(a.v, (ks.start + key) * a.v.token + kv_head * a.v.head + c, live && in);
+      const uint4 q = load16(a.q, tok * a.q.token + head * a.q.head + c, row && in);
+      const uint4 d = load16(a.dout, tok * a.dout.token + head * a.dout.head + c, row && in);
+      s = E::mfma32(E::vec(k), E::vec(q), s);
+      dp = E::mfma32(E::vec(v), E::vec(d), dp);
+    }
+    const int64_t at = tok * a.heads + head;
+    const bool ok = row && in_bounds(at, 1, a.tq * a.heads);
+    const float l = ok ? a.lse[at] * kLog2e : 0.f;
+    const int32_t sees = a.causal ? min(ks.n, t + shift + 1) : ks.n;
+    float sum = 0.f;
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      if (8 * (r / 4) + 4 * half + r % 4 < sees)
+        sum += __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], a.scale * kLog2e, -l)) * dp[r];
+    sum = half_sum(sum);
+    if (ok && half == 0) delta[at] = sum;
   }
 }
 
@@ -681,6 +711,8 @@ hipError_t launch_attn_bwd(const AttnArgs& args, float* delta, float* lse2, floa
     } else if (a.tq > 0) {
       k_attn_delta<E><<<(uint32_t)std::min<int64_t>(dt, 1 << 20), 256, 0, stream>>>(a, delta, lse2, top);
     }
+    if (a.tq > 0 && a.tk > 0)
+      k_attn_delta_few<E, DB><<<(uint32_t)(((int64_t)a.batch * a.heads + 3) / 4), 256, 0, stream>>>(a, delta);
     if (a.tk > 0) {
       k_attn_bwd_kv<E, DB><<<(uint32_t)(attn_tiles(a.tk, 1, a.batch, 128) * a.kv_heads * a.splits), 256, 0, stream>>>(a);
       if (a.splits > 1)
