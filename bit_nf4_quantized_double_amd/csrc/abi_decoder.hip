@@ -95,7 +95,7 @@ int check_attention(const qlora_attention* a) {
     // workgroups of a launch: fewer than 2^24
     if (((a->tokens_q * group + 31) / 32 + a->batch + 2) * a->kv_heads >= (1 << 24) ||
         ((a->tokens_k + 127) / 128 + a->batch + 2) * a->heads >= (1 << 24) ||
-        (a->tokens_q + a->tokens_k) / 4 + a->batch >= (1 << 24) - 2)
+        (a->tokens_k / 4 + a->batch >= (1 << 24) - 2) || a->batch * a->heads / 4 >= (1 << 24) - (1 << 20) - 1)
       return fail(QLORA_ERR_SHAPE, "too many rows for one launch");
   }
   return QLORA_OK;

@@ -68,62 +68,13 @@ __device__ __forceinline__ float dot8(const uint4& u, const uint4& v) {
 template <typename E>
 constexpr float kShift = IsF16<E>::value ? kPShift : 0.f;
 
-// delta = sum_d dO O, 16 lanes a row, and lse in base 2, less P's power of two; in fp16 (blockIdx.y: dO, V) also the
-// largest finite magnitude of each workgroup's rows.
-template <typename E>
-__global__ __launch_bounds__(256) void k_attn_delta(AttnArgs a, float* delta, float* lse2, float* top) {
-  const bool isv = blockIdx.y == 1;
-  const Heads& x = isv ? a.v : a.dout;
-  const int32_t heads = isv ? a.kv_heads : a.heads;
-  const int64_t tokens = isv ? a.tk : a.tq, tiles = attn_tiles(tokens, 1, a.batch, kDeltaTokens);
-  const int sub = threadIdx.x >> 4, l16 = threadIdx.x & 15;
-  float most = 0.f;
-  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const Region rg = find_region(isv ? a.cu_k : a.cu_q, a.batch, tokens, 1, kDeltaTokens, t);
-    if (rg.tile < 0) continue;
-    const int32_t n = seq_length(isv ? a.len_k : a.len_q, rg.seq, a.batch, rg.size), first = rg.tile * kDeltaTokens;
-    const int32_t rows = max(0, min(n - first, kDeltaTokens)) * heads;
-    const Keys ks = keys_of(a, rg.seq);
-    for (int32_t r = sub; r < rows; r += 16) {
-      const int64_t tok = rg.start + first + r / heads, head = r % heads;
-      float sum = 0.f;
-      for (int c = 8 * l16; c < a.d; c += 128) {
-        const uint4 u = load16(x, tok * x.token + head * x.head + c, true);
-        if (IsF16<E>::value) most = fmaxf(most, finite_max<E>(u));
-        if (!isv) {
-          sum += dot8<E>(u, load16(a.o, tok * a.o.token + head * a.o.head + c, true));
-        }
-      }
-#pragma unroll
-      for (int s = 8; s > 0; s >>= 1) sum += __shfl_xor(sum, s, 16);
-      const int32_t sees = a.causal ? min(ks.n, first + r / heads + ks.n - n + 1) : ks.n;
-      if (!isv && l16 == 0 && in_bounds(tok * heads + head, 1, a.tq * heads)) {
-        const float l = a.lse[tok * heads + head] * kLog2e;
-        if (sees <= 0 || sees > kFewKeys) delta[tok * heads + head] = sum;  // the others: k_attn_delta_few
-        lse2[tok * heads + head] = l == -INFINITY ? INFINITY : l - kShift<E>;  // a row that sees nothing: P = 0
-      }
-    }
-  }
-  if constexpr (IsF16<E>::value) {
-    __shared__ float s_top[4];
-#pragma unroll
-    for (int s = 32; s > 0; s >>= 1) most = fmaxf(most, __shfl_xor(most, s));
-    if ((threadIdx.x & 63) == 0) s_top[threadIdx.x >> 6] = most;
-    __syncthreads();
-    const int at = (isv ? kAttnTops : 0) + blockIdx.x;
-    if (threadIdx.x == 0 && in_bounds(at, 1, 2 * kAttnTops))
-      top[at] = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
-  }
-}
-
 // delta of the rows that see few keys, as sum P (dO V) by the matrix cores: O is
 // rounded, by up to half a step of itself, and a row's dS is as far off as its
 // delta.  (Where a row spreads over many keys, O is small beside the V that it is
-// made of.)  A wave for each sequence and head.
+// made of.)  Wave w: sequence w / heads, head w % heads.
 template <typename E, int DB>
-__global__ __launch_bounds__(256) void k_attn_delta_few(AttnArgs a, float* delta) {
+__device__ __forceinline__ void delta_few(const AttnArgs& a, int64_t w, float* delta) {
   const int lane = threadIdx.x & 63, half = lane >> 5;
-  const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (w >= (int64_t)a.batch * a.heads) return;
   const int32_t seq = (int32_t)(w / a.heads), head = (int32_t)(w % a.heads);
   const int64_t start = region_start(a.cu_q, a.batch, a.tq, seq + 1);
@@ -164,6 +115,59 @@ __global__ __launch_bounds__(256) void k_attn_delta_few(AttnArgs a, float* delta
         sum += __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], a.scale * kLog2e, -l)) * dp[r];
     sum = half_sum(sum);
     if (ok && half == 0) delta[at] = sum;
+  }
+}
+
+// delta = sum_d dO O, 16 lanes a row, and lse in base 2, less P's power of two; in fp16 (blockIdx.y: dO, V) also the
+// largest finite magnitude of each workgroup's rows.
+// The first `few` workgroups (of blockIdx.y 0) see to the rows with few keys.
+template <typename E, int DB>
+__global__ __launch_bounds__(256) void k_attn_delta(AttnArgs a, uint32_t few, float* delta, float* lse2, float* top) {
+  const bool isv = blockIdx.y == 1;
+  if (blockIdx.x < few) {
+    if (!isv) delta_few<E, DB>(a, (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), delta);
+    return;
+  }
+  const Heads& x = isv ? a.v : a.dout;
+  const int32_t heads = isv ? a.kv_heads : a.heads;
+  const int64_t tokens = isv ? a.tk : a.tq, tiles = attn_tiles(tokens, 1, a.batch, kDeltaTokens);
+  const int sub = threadIdx.x >> 4, l16 = threadIdx.x & 15;
+  float most = 0.f;
+  for (int64_t t = blockIdx.x - few; t < tiles; t += gridDim.x - few) {
+    const Region rg = find_region(isv ? a.cu_k : a.cu_q, a.batch, tokens, 1, kDeltaTokens, t);
+    if (rg.tile < 0) continue;
+    const int32_t n = seq_length(isv ? a.len_k : a.len_q, rg.seq, a.batch, rg.size), first = rg.tile * kDeltaTokens;
+    const int32_t rows = max(0, min(n - first, kDeltaTokens)) * heads;
+    const Keys ks = keys_of(a, rg.seq);
+    for (int32_t r = sub; r < rows; r += 16) {
+      const int64_t tok = rg.start + first + r / heads, head = r % heads;
+      float sum = 0.f;
+      for (int c = 8 * l16; c < a.d; c += 128) {
+        const uint4 u = load16(x, tok * x.token + head * x.head + c, true);
+        if (IsF16<E>::value) most = fmaxf(most, finite_max<E>(u));
+        if (!isv) {
+          sum += dot8<E>(u, load16(a.o, tok * a.o.token + head * a.o.head + c, true));
+        }
+      }
+#pragma unroll
+      for (int s = 8; s > 0; s >>= 1) sum += __shfl_xor(sum, s, 16);
+      const int32_t sees = a.causal ? min(ks.n, first + r / heads + ks.n - n + 1) : ks.n;
+      if (!isv && l16 == 0 && in_bounds(tok * heads + head, 1, a.tq * heads)) {
+        const float l = a.lse[tok * heads + head] * kLog2e;
+        if (sees <= 0 || sees > kFewKeys) delta[tok * heads + head] = sum;  // the others: delta_few
+        lse2[tok * heads + head] = l == -INFINITY ? INFINITY : l - kShift<E>;  // a row that sees nothing: P = 0
+      }
+    }
+  }
+  if constexpr (IsF16<E>::value) {
+    __shared__ float s_top[4];
+#pragma unroll
+    for (int s = 32; s > 0; s >>= 1) most = fmaxf(most, __shfl_xor(most, s));
+    if ((threadIdx.x & 63) == 0) s_top[threadIdx.x >> 6] = most;
+    __syncthreads();
+    const int at = (isv ? kAttnTops : 0) + blockIdx.x - few;
+    if (threadIdx.x == 0 && in_bounds(at, 1, 2 * kAttnTops))
+      top[at] = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
   }
 }
 
@@ -705,14 +709,10 @@ hipError_t launch_attn_bwd(const AttnArgs& args, float* delta, float* lse2, floa
     using E = decltype(e);
     constexpr int DB = decltype(db)::value;
     const int64_t dt = attn_tiles(a.tq, 1, a.batch, kDeltaTokens), vt = attn_tiles(a.tk, 1, a.batch, kDeltaTokens);
-    if (a.f16) {
-      // as many workgroups as partial maxima, the same for dO and V
-      k_attn_delta<E><<<dim3((uint32_t)std::min<int64_t>(std::max(dt, vt), kAttnTops), 2), 256, 0, stream>>>(a, delta, lse2, top);
-    } else if (a.tq > 0) {
-      k_attn_delta<E><<<(uint32_t)std::min<int64_t>(dt, 1 << 20), 256, 0, stream>>>(a, delta, lse2, top);
-    }
-    if (a.tq > 0 && a.tk > 0)
-      k_attn_delta_few<E, DB><<<(uint32_t)(((int64_t)a.batch * a.heads + 3) / 4), 256, 0, stream>>>(a, delta);
+    const uint32_t few = a.tq > 0 && a.tk > 0 ? (uint32_t)(((int64_t)a.batch * a.heads + 3) / 4) : 0;
+    // fp16: as many workgroups as partial maxima, the same for dO and V
+    const int64_t n = a.f16 ? std::min<int64_t>(std::max(dt, vt), kAttnTops) : std::min<int64_t>(dt, 1 << 20);
+    k_attn_delta<E, DB><<<dim3(few + (uint32_t)n, a.f16 ? 2 : 1), 256, 0, stream>>>(a, few, delta, lse2, top);
     if (a.tk > 0) {
       k_attn_bwd_kv<E, DB><<<(uint32_t)(attn_tiles(a.tk, 1, a.batch, 128) * a.kv_heads * a.splits), 256, 0, stream>>>(a);
       if (a.splits > 1)
