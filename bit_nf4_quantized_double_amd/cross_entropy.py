@@ -94,23 +94,46 @@ def scale_rows(X: torch.Tensor, g: torch.Tensor, Y: torch.Tensor | None = None) 
     return Y
 
 
+def reduce_losses(loss: torch.Tensor, targets: torch.Tensor, mean: bool, *, ignore_index: int = -100) -> torch.Tensor:
+    """fp32 [2]: the sum or mean of the losses whose target is not ignore_index, and
+    what one of them counts in it.  In one launch, for captured graphs too."""
+    if not isinstance(loss, torch.Tensor) or loss.dim() != 1 or not loss.is_cuda:
+        raise ValueError("loss must be a vector on the GPU")
+    m, dev = loss.shape[0], loss.device
+    p, t = check_vector(loss, _F32, m, "loss", dev), check_vector(targets, (torch.int64,), m, "targets", dev)
+    out = torch.empty(2, dtype=torch.float32, device=dev)
+    st = qlora.lib().qlora_loss_sum(p, t, m, ignore_index, bool(mean), out.data_ptr(), _stream(dev))
+    if st:
+        qlora._check(st, "qlora_loss_sum")
+    return out
+
+
 class LinearCrossEntropyFunction(torch.autograd.Function):
-    """(X [tokens, width], W, targets) -> losses.  The gradient is made in the
-    forward, for losses that count once, and the backward multiplies its rows."""
+    """(X [tokens, width], W, targets) -> losses, or their sum or mean.  The gradient
+    is made in the forward, for losses that count once, and the backward multiplies
+    its rows."""
 
     @staticmethod
-    def forward(ctx, X, W, targets, ignore_index: int):
-        if not ctx.needs_input_grad[0]:
-            return linear_cross_entropy_fwd(X, W, targets, ignore_index=ignore_index)[0]
-        loss, _, dX = linear_cross_entropy_grad(X, W, targets, ignore_index=ignore_index)
-        ctx.save_for_backward(dX)
-        return loss
+    def forward(ctx, X, W, targets, ignore_index: int, reduction: str, gradient: bool):
+        if gradient:
+            loss, _, dX = linear_cross_entropy_grad(X, W, targets, ignore_index=ignore_index)
+        else:
+            loss, _ = linear_cross_entropy_fwd(X, W, targets, ignore_index=ignore_index)
+        both = None if reduction == "none" else reduce_losses(loss, targets, reduction == "mean", ignore_index=ignore_index)
+        if gradient:
+            ctx.save_for_backward(dX, targets if both is None else both[1])
+            ctx.ignore_index, ctx.reduction = ignore_index, reduction
+        return loss if both is None else both[0]
 
     @staticmethod
     @qlora._once
     def backward(ctx, dloss):
-        dX, = ctx.saved_tensors
-        return scale_rows(dX, dloss.contiguous()), None, None, None
+        dX, with_ = ctx.saved_tensors
+        if ctx.reduction == "none":  # whatever comes for ignored tokens
+            g = dloss.masked_fill(with_ == ctx.ignore_index, 0.0)
+        else:
+            g = (dloss * with_).expand(dX.shape[0])
+        return scale_rows(dX, g.contiguous()), None, None, None, None, None
 
 
 def linear_cross_entropy(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, *, ignore_index: int = -100,
@@ -129,11 +152,9 @@ def linear_cross_entropy(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor
         raise ValueError(f"targets must have shape {tuple(X.shape[:-1])}, got {tuple(targets.shape)}")
     n = math.prod(targets.shape)
     flat = targets.reshape(n).contiguous()
-    loss = LinearCrossEntropyFunction.apply(rows._rows_of(X, X.shape[-1]), W, flat, ignore_index)
-    if reduction == "none":
-        return loss.reshape(targets.shape)
-    total = loss.sum()
-    return total if reduction == "sum" else total / (flat != ignore_index).sum()
+    gradient = X.requires_grad and torch.is_grad_enabled()
+    loss = LinearCrossEntropyFunction.apply(rows._rows_of(X, X.shape[-1]), W, flat, ignore_index, reduction, gradient)
+    return loss.reshape(targets.shape) if reduction == "none" else loss
 
 
 def _bind(L: ctypes.CDLL) -> None:
@@ -141,6 +162,7 @@ def _bind(L: ctypes.CDLL) -> None:
     sig = {
         "qlora_cross_entropy_workspace_bytes": (sz, [i64, i64, i64, i32]),
         "qlora_cross_entropy": (i32, [vp, i64, vp, i64, vp, i64, i64, i64, i64, vp, vp, vp, vp, i32, vp, sz, vp]),
+        "qlora_loss_sum": (i32, [vp, vp, i64, i64, i32, vp, vp]),
         "qlora_scale_rows": (i32, [vp, vp, i64, i64, vp, i32, vp]),
     }
     for name, (res, args) in sig.items():

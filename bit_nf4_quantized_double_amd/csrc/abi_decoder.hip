@@ -4,6 +4,7 @@
 #include <climits>
 #include <cmath>
 #include <exception>
+#include <initializer_list>
 
 #include "../../include/qlora.h"
 #include "abi.h"
@@ -97,6 +98,18 @@ int check_attention(const qlora_attention* a) {
         ((a->tokens_k + 127) / 128 + a->batch + 2) * a->heads >= (1 << 24) ||
         (a->tokens_k / 4 + a->batch >= (1 << 24) - 2) || a->batch * a->heads / 4 >= (1 << 24) - (1 << 20) - 1)
       return fail(QLORA_ERR_SHAPE, "too many rows for one launch");
+  }
+  return QLORA_OK;
+}
+
+// Kernels read inputs after they have written outputs of other rows.
+int check_apart(std::initializer_list<const qlora_heads*> out, std::initializer_list<const qlora_heads*> in) {
+  for (auto o = out.begin(); o != out.end(); ++o) {
+    if (!*o || !(*o)->p) continue;
+    for (auto x = out.begin(); x != o; ++x)
+      if (*x && (*x)->p == (*o)->p) return fail(QLORA_ERR_INVALID_ARG, "two outputs are the same tensor");
+    for (const qlora_heads* x : in)
+      if (x && x->p == (*o)->p) return fail(QLORA_ERR_INVALID_ARG, "an output is an input");
   }
   return QLORA_OK;
 }
@@ -225,6 +238,7 @@ int qlora_attention_fwd(const qlora_attention* a, const qlora_heads* Q, const ql
     if (!lse) return fail(QLORA_ERR_INVALID_ARG, "lse is NULL");
     if (!aligned16(lse)) return fail(QLORA_ERR_ALIGN, "lse must be 16-byte aligned");
     if (ws && !aligned16(ws)) return fail(QLORA_ERR_ALIGN, "workspace must be 16-byte aligned");
+    if ((st = check_apart({O}, {Q, K, V}))) return st;
     qlora::AttnArgs g = attention_args(a);
     g.q = heads_arg(Q, a->tokens_q, a->heads, d); g.k = heads_arg(K, a->tokens_k, a->kv_heads, d);
     g.v = heads_arg(V, a->tokens_k, a->kv_heads, d); g.o = heads_arg(O, a->tokens_q, a->heads, d);
@@ -254,6 +268,7 @@ int qlora_attention_bwd(const qlora_attention* a, const qlora_heads* dO, const q
     if (!ws || ws_bytes < qlora_attention_workspace_bytes(QLORA_OP_BWD, a))
       return fail(QLORA_ERR_WORKSPACE, "attention backward workspace too small");
     if (!aligned16(ws)) return fail(QLORA_ERR_ALIGN, "workspace must be 16-byte aligned");
+    if ((st = check_apart({dQ, dK, dV}, {dO, Q, K, V, O}))) return st;
     qlora::AttnArgs g = attention_args(a);
     g.dout = heads_arg(dO, tq, h, d); g.q = heads_arg(Q, tq, h, d); g.k = heads_arg(K, tk, hk, d);
     g.v = heads_arg(V, tk, hk, d); g.o = heads_arg(O, tq, h, d); g.lse = const_cast<float*>(lse);
@@ -316,6 +331,17 @@ int qlora_scale_rows(const uint16_t* X, const float* g, int64_t M, int64_t K, ui
     if (M == 0 || K == 0) return (int)QLORA_OK;
     if ((st = check_aligned(X, 16, "X")) || (st = check_aligned(g, 4, "g")) || (st = check_aligned(Y, 16, "Y"))) return st;
     return done(qlora::launch_scale_rows(X, g, M, K, Y, dtype == QLORA_F16, stream), "row scale launch");
+  });
+}
+
+int qlora_loss_sum(const float* loss, const int64_t* targets, int64_t M, int64_t ignore_index, int mean, float* out,
+                   hipStream_t stream) {
+  return guarded([&] {
+    int st;
+    if ((st = check_range(M, INT_MAX, "M"))) return st;
+    if (M > 0 && ((st = check_aligned(loss, 4, "loss")) || (st = check_aligned(targets, 8, "targets")))) return st;
+    if ((st = check_aligned(out, 4, "out"))) return st;
+    return done(qlora::launch_loss_sum(loss, targets, M, ignore_index, mean != 0, out, stream), "loss sum launch");
   });
 }
 

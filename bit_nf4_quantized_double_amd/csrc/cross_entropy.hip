@@ -518,6 +518,39 @@ __global__ __launch_bounds__(256) void k_scale_rows(const uint16_t* x, const flo
   *reinterpret_cast<uint4*>(out + at) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// The losses' sum or mean over the tokens that count, in 64 bits and a fixed
+// order: one workgroup (8192 tokens are 96 KB, read in 3 us).  out[0] the result,
+// out[1] what each loss counts in it.
+__global__ __launch_bounds__(1024) void k_loss_sum(const float* loss, const int64_t* targets, int64_t m, int64_t ignore, bool mean,
+                                                   float* out) {
+  __shared__ double s_sum[16];
+  __shared__ int64_t s_n[16];
+  double sum = 0.0;
+  int64_t n = 0;
+  for (int64_t i = threadIdx.x; i < m; i += 1024)
+    if (targets[i] != ignore) {
+      sum += (double)loss[i];
+      ++n;
+    }
+#pragma unroll
+  for (int s = 32; s > 0; s >>= 1) {
+    sum += __shfl_xor(sum, s);
+    n += __shfl_xor(n, s);
+  }
+  if ((threadIdx.x & 63) == 0) {
+    s_sum[threadIdx.x >> 6] = sum;
+    s_n[threadIdx.x >> 6] = n;
+  }
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int w = 1; w < 16; ++w) {
+    sum += s_sum[w];
+    n += s_n[w];
+  }
+  out[0] = (float)(mean ? sum / (double)n : sum);
+  out[1] = (float)(mean ? 1.0 / (double)n : 1.0);
+}
+
 struct Layout {
   size_t bytes = 0;
   size_t take(size_t n) {
@@ -622,6 +655,12 @@ hipError_t launch_scale_rows(const uint16_t* x, const float* g, int64_t m, int64
   const dim3 grid = grid_of((m * k / 8 + 255) / 256);
   if (f16) k_scale_rows<F16><<<grid, 256, 0, stream>>>(x, g, m, k, out);
   else k_scale_rows<Bf16><<<grid, 256, 0, stream>>>(x, g, m, k, out);
+  return hipGetLastError();
+}
+
+hipError_t launch_loss_sum(const float* loss, const int64_t* targets, int64_t m, int64_t ignore, bool mean, float* out,
+                           hipStream_t stream) {
+  k_loss_sum<<<1, 1024, 0, stream>>>(loss, targets, m, ignore, mean, out);
   return hipGetLastError();
 }
 

@@ -77,5 +77,7 @@ size_t ce_workspace_bytes(int64_t m, int64_t k, int64_t v, bool grad, int comput
 hipError_t launch_ce(const CeArgs& a, void* ws, int compute_units, hipStream_t stream);
 hipError_t launch_scale_rows(const uint16_t* x, const float* g, int64_t m, int64_t k, uint16_t* out, bool f16,
                              hipStream_t stream);
+hipError_t launch_loss_sum(const float* loss, const int64_t* targets, int64_t m, int64_t ignore, bool mean, float* out,
+                           hipStream_t stream);
 
 }  // namespace qlora

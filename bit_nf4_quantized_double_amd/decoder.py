@@ -66,7 +66,10 @@ class Cache:
         return cu, positions
 
     def put(self, layer: int, k: torch.Tensor, v: torch.Tensor):
-        """A layer's new keys and values; returns all of them."""
+        """A layer's new keys and values; returns all of them.  Not for training:
+        the cache would hold one call's graph into the next."""
+        if torch.is_grad_enabled() and (k.requires_grad or v.requires_grad):
+            raise RuntimeError("a cache keeps no gradients: call under torch.no_grad()")
         self.k[layer].index_copy_(0, self.rows, k)
         self.v[layer].index_copy_(0, self.rows, v)
         return self.k[layer], self.v[layer]

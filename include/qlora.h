@@ -604,7 +604,8 @@ int qlora_rope(const qlora_heads *Q, int64_t heads, const qlora_heads *K, int64_
  * dQ and of the whole batch for dK; what is 2^-30 below these bounds is lost.
  * Workspace: qlora_attention_workspace_bytes(op, ...).  The forward's is for keys
  * split over workgroups and optional (without room it runs unsplit, as right);
- * the backward's is needed (QLORA_ERR_WORKSPACE).
+ * the backward's is needed (QLORA_ERR_WORKSPACE).  Outputs lie apart from inputs
+ * and from each other (the same pointer twice: QLORA_ERR_INVALID_ARG).
  */
 #define QLORA_MAX_HEAD_DIM 128
 typedef struct {
@@ -659,6 +660,12 @@ int qlora_cross_entropy(const void *X, int64_t ldx, const void *W, int64_t ldw, 
  * numbers, K a multiple of 8 (the loss's gradient times what comes from above). */
 int qlora_scale_rows(const uint16_t *X, const float *g, int64_t M, int64_t K, uint16_t *Y, int dtype,
                      hipStream_t stream);
+
+/* The losses (fp32 [M], finite or not) of the tokens whose target is not
+ * ignore_index: out[0] = their sum, or `mean` (no token: NaN), out[1] = what one
+ * of them counts in it (1, or 1 / their number).  Summed in 64 bits. */
+int qlora_loss_sum(const float *loss, const int64_t *targets, int64_t M, int64_t ignore_index, int mean,
+                   float *out, hipStream_t stream);
 
 /* Host function: static description of a status code. */
 const char *qlora_status_string(int status);

@@ -112,6 +112,24 @@ def test_attention_refuses_outputs(L):
     assert L.qlora_attention_workspace_bytes(7, ctypes.byref(c)) == 0
 
 
+def test_attention_refuses_outputs_that_are_inputs(L):
+    """With all else right (these have the same pointer throughout)."""
+    at = lambda p: heads(p, **WIDE)
+    apart = [at(P + 0x1000 * i) for i in range(9)]
+    c = describe()
+    assert L.qlora_attention_fwd(ctypes.byref(c), *apart[:3], apart[1], P, None, 0, None) == INVALID
+    assert b"output is an input" in L.qlora_last_error()
+    n = L.qlora_attention_workspace_bytes(BWD, ctypes.byref(c))
+    for i in (5, 6, 7):  # dQ, dK, dV
+        for other in (0, 1, 2, 3, 4):
+            t = list(apart[:8])
+            t[i] = t[other]
+            assert L.qlora_attention_bwd(ctypes.byref(c), *t[:5], P, *t[5:], P, n, None) == INVALID
+            assert b"output is an input" in L.qlora_last_error()
+    assert L.qlora_attention_bwd(ctypes.byref(c), *apart[:5], P, apart[5], apart[6], apart[6], P, n, None) == INVALID
+    assert b"same tensor" in L.qlora_last_error()
+
+
 def test_attention_has_nothing_to_do(L):
     none = heads(0)
     c = describe(tokens_q=0)
@@ -165,6 +183,15 @@ def test_cross_entropy_workspace(L):
     assert ws(10 ** 6, 4096, 128256, 1) <= 2 * most and ws(8192 * 100, 4096, 128256, 1) == most
     # a smaller last round may need more for its splits: the whole is never less than either
     assert ws(8192 + 70, 64, 70001, 1) >= max(ws(8192, 64, 70001, 1), ws(70, 64, 70001, 1))
+
+
+def test_loss_sum_refuses(L):
+    call = lambda loss=P, targets=P, m=4, out=P: L.qlora_loss_sum(loss, targets, m, -100, 1, out, None)
+    assert call(m=-1) == call(loss=None) == call(targets=None) == call(out=None) == INVALID
+    assert call(loss=P2) == call(targets=P + 4) == call(out=P2) == ALIGN
+    assert call(m=1 << 31) == SHAPE
+    with pytest.raises(ValueError, match="on the GPU"):
+        cross_entropy.reduce_losses(torch.zeros(3), torch.zeros(3, dtype=torch.int64), True)
 
 
 def test_scale_rows_refuses(L):

@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from bit_nf4_quantized_double_amd import attention
+from bit_nf4_quantized_double_amd import attention, rotary
 from decoder_util import attention_reference, close, cu, starts
 from rows_util import f64, need_gpu, rand
 
@@ -302,6 +302,90 @@ def test_in_a_graph():
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(out, want))
+
+
+def test_autograd_in_a_graph():
+    """Rotary positions and attention, forward and backward, captured and replayed."""
+    need_gpu()
+    t, h, hk, d = 200, 6, 2, 64
+    q, k, v, do = _inputs([t], [t], h, hk, d, BF16)
+    leaves = [x.requires_grad_() for x in (q, k, v)]
+    ends, positions, f = cu([150, 50]), torch.arange(t, device="cuda"), rotary.frequencies(d)
+
+    def run():
+        a, b = rotary.rotary(q, k, positions, f)
+        o = attention.attention(a, b, v, ends)
+        return (o.detach(), *torch.autograd.grad(o, leaves, do))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = run()
+    for seed, lens in ((10, [150, 50]), (20, [1, 199]), (30, [0, 200])):
+        with torch.no_grad():
+            for x, y in zip((q, k, v, do), _inputs([t], [t], h, hk, d, BF16, seed)):
+                x.copy_(y)
+            ends.copy_(cu(lens))
+        want = run()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(out, want))
+
+
+def test_graphs_that_share_a_workspace():
+    """Single tokens over a cache (split keys) and a backward, replayed in turn while
+    the cache's lengths grow."""
+    need_gpu()
+    h, hk, d, room = 8, 2, 64, 4096
+    q, k, v, _ = _inputs([1, 1], [room, room], h, hk, d, BF16)
+    lens = torch.tensor([3, 4000], dtype=torch.int32, device="cuda")
+    one = dict(lengths_k=lens)
+    tq, tk, tv, do = _inputs([70], [70], h, hk, d, BF16, 5)
+    o, lse = attention.attention_fwd(tq, tk, tv, cu([70]))
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    runs = [lambda ws=None: attention.attention_fwd(q, k, v, cu_q, cu_k, ws=ws, **one),
+            lambda ws=None: attention.attention_bwd(do, tq, tk, tv, o, lse, cu_t, ws=ws)]
+    cu_q, cu_k, cu_t = cu([1, 1]), cu([room, room]), cu([70])
+    assert attention.plan(q, k, cu_q)["splits"] > 1
+    graphs, outs = [], []
+    for run in runs:
+        run(ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(run(ws))
+        graphs.append(g)
+    for i in (0, 1, 0, 0, 1, 0):
+        lens += 17
+        for t in outs[i]:
+            t.zero_()
+        graphs[i].replay()
+        want = runs[i]()
+        assert all(torch.equal(a, b) for a, b in zip(outs[i], want))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_many_sequences(dtype):
+    """More sequences than a wave's lanes, none of whose ends is a tile's."""
+    need_gpu()
+    lq = [(i * 5) % 12 for i in range(330)]
+    lk = [n + i % 4 for i, n in enumerate(lq)]
+    for h, hk in ((7, 1), (4, 4)):
+        test_forward_and_backward(lq, lk, h, hk, 64, True, dtype)
+
+
+def test_no_sequences():
+    need_gpu()
+    q, k, v, do = _inputs([5], [5], 2, 2, 64, BF16)
+    ends = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o, lse = attention.attention_fwd(q, k, v, ends)
+    assert bool((o == 0).all()) and bool((lse == -float("inf")).all())
+    for g in attention.attention_bwd(do, q, k, v, o, lse, ends):
+        assert bool((g == 0).all())
 
 
 def test_another_stream():

@@ -78,7 +78,7 @@ def test_loss_and_gradient(m, k, v, dtype):
         check(loss, lse, dx, x, w, y, g)
 
 
-def test_pieces_of_the_vocabulary(monkeypatch):
+def test_pieces_of_the_vocabulary():
     """More tokens than a round of launches, and a vocabulary in several pieces."""
     need_gpu()
     m, k, v = 8192 + 70, 64, 70001  # 2 rounds; 3 pieces in the first
@@ -209,6 +209,92 @@ def test_same_bits_and_graph():
             g.replay()
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_sums_of_losses():
+    """Against 64 bits (one rounding), whatever ignored tokens hold; none that counts."""
+    need_gpu()
+    for m in (0, 1, 63, 1025, 70001):
+        loss = rand((m,), m + 1, torch.float32).square() if m else torch.empty(0, device="cuda")
+        y = torch.arange(m, device="cuda") % 7
+        loss[y == 3] = float("nan")
+        live = (y != 3).cpu()
+        for mean in (False, True):
+            got = cross_entropy.reduce_losses(loss, y, mean, ignore_index=3)
+            n = int(live.sum())
+            want = loss.cpu().double()[live].sum() / (n if mean else 1)
+            assert torch.allclose(got[0].cpu().double(), want, rtol=2.0 ** -23, atol=0, equal_nan=True)
+            assert float(got[1]) == (float(np.float32(1) / np.float32(n)) if mean and n else float("inf") if mean else 1.0)
+    y.fill_(3)
+    assert bool(torch.isnan(cross_entropy.reduce_losses(loss, y, True, ignore_index=3)[0]))
+    assert float(cross_entropy.reduce_losses(loss, y, False, ignore_index=3)[0]) == 0.0
+
+
+def test_training_step_in_a_graph():
+    """Loss and gradient of more tokens than a block of any reduction, captured and
+    replayed on new inputs with eager work between."""
+    need_gpu()
+    m, k, v = 70001, 8, 16
+    x, w, y = _inputs(m, k, v, BF16)
+    x.requires_grad_()
+
+    def run(reduction):
+        loss = cross_entropy.linear_cross_entropy(x, w, y, reduction=reduction)
+        return loss.detach(), torch.autograd.grad(loss, x)[0]
+
+    for reduction in ("sum", "mean"):
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            run(reduction)
+        torch.cuda.current_stream().wait_stream(side)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = run(reduction)
+        for seed in range(5, 9):
+            with torch.no_grad():
+                for a, b in zip((x, w, y), _inputs(m, k, v, BF16, seed)):
+                    a.copy_(b)
+                y[::seed] = IGNORE
+            want = run(reduction)
+            g.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_graphs_that_share_a_workspace():
+    need_gpu()
+    ins = [_inputs(m, 136, v, BF16, m) for m, v in ((300, 1000), (20, 4000))]
+    ws = torch.empty(max(cross_entropy.workspace_bytes(len(y), 136, len(w), True) for _, w, y in ins), dtype=torch.uint8,
+                     device="cuda")
+    graphs, outs = [], []
+    for x, w, y in ins:
+        run = lambda: cross_entropy.linear_cross_entropy_grad(x, w, y, ws=ws)
+        run()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(run())
+        graphs.append(g)
+    for i in (0, 1, 1, 0, 1, 0):
+        for t in outs[i]:
+            t.zero_()
+        graphs[i].replay()
+        want = cross_entropy.linear_cross_entropy_grad(*ins[i])
+        assert all(torch.equal(a, b) for a, b in zip(outs[i], want))
+
+
+def test_ignored_tokens_take_no_gradient():
+    """Whatever comes from above for them; and no gradient is made without grad mode."""
+    need_gpu()
+    x, w, y = _inputs(20, 64, 50, BF16)
+    y[::2] = IGNORE
+    x.requires_grad_()
+    up = torch.where(y == IGNORE, float("nan"), 1.0)
+    g, = torch.autograd.grad(cross_entropy.linear_cross_entropy(x, w, y, reduction="none"), x, up)
+    assert bool((g[::2] == 0).all()) and bool(torch.isfinite(g).all())
+    with torch.no_grad():
+        assert not cross_entropy.linear_cross_entropy(x, w, y).requires_grad
 
 
 def test_refusals():

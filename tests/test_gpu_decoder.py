@@ -148,6 +148,18 @@ def test_cache_token_by_token():
         cache.extend([1])
 
 
+def test_cache_without_new_tokens_and_with_gradients():
+    need_gpu()
+    m = _model()
+    tokens, targets, _, _ = _inputs([5, 0], 3)
+    cache, other = m.cache(2, 8), m.cache(2, 8)
+    m.score(tokens, targets, *cache.extend([5, 0]), cache)
+    none = m.score(tokens[:0], targets[:0], *cache.extend([0, 0]), cache)
+    assert none.shape == (0,) and cache.used == [5, 0]
+    with pytest.raises(RuntimeError, match="no gradients"):
+        m(tokens, *other.extend([5, 0]), other)
+
+
 def test_command():
     need_gpu()
     out = decoder.main(["--width", "128", "--hidden", "256", "--heads", "4", "--vocabulary", "500", "--tokens", "200",
