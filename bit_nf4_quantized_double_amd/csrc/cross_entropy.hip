@@ -106,6 +106,12 @@ __global__ __launch_bounds__(256) void k_ce_target(CeArgs a, CeRound r) {
   if (lane == 0) r.target[m] = sum;
 }
 
+// All but the 24 latest of the wave's vector memory loads are there.
+__device__ __forceinline__ void wait_loads_but_24() {
+  __builtin_amdgcn_s_waitcnt(0x4f78);
+  asm volatile("" ::: "memory");
+}
+
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 // Workgroups are dealt round-robin to the 8 XCDs: each gets a contiguous run of
@@ -131,8 +137,8 @@ __device__ __forceinline__ uint32_t lower(uint32_t d, uint32_t b) {
 
 // Both products: 256 tokens x 128 outputs a workgroup, 4 waves of 64 tokens, in
 // 16 x 16 x 32 MFMAs (A: outputs, B: tokens).  The tokens' operand is in tiles of
-// 1 KB in lane order and goes straight into registers, one step of 64 ahead; W's
-// goes straight into LDS, four buffers, three steps ahead, one barrier a step.
+// 1 KB in lane order and goes straight into registers, three chunks of 32 ahead;
+// W's goes straight into LDS, four buffers, three steps of 64 ahead, one barrier a step.
 //   TRANS = false: outputs are rows of W, the reduction its columns
 //   TRANS = true:  outputs are columns of W, the reduction its rows, read from
 //                  LDS through the transposing load; a lane's 8 rows are 4 g .. + 3
@@ -142,6 +148,7 @@ struct CeProduct {
   static constexpr int kTile = 128 * 64 * 2;  // bytes of a step's W tile
   static constexpr int kBuffers = 4;
   static constexpr int NS = 8, KC = 2;
+  static constexpr int RING = 3;               // chunks of 32 of the tokens' operand
   static constexpr int kRow = TRANS ? 16 : 8;  // 16-byte chunks of a tile's row
 
   f32x4 acc[NS][4];
@@ -150,7 +157,7 @@ struct CeProduct {
   // chunk ^ spread(row): the rows that a read touches at a time (16 of one column;
   // for a transposing one 4 of 32 bytes) fall into different banks.
   static __device__ __forceinline__ uint32_t spread(uint32_t r) {
-    return TRANS ? (r & 3) << 2 | (r >> 2 & 1) : r >> 1 & 7;
+    return TRANS ? (r & 3) << 2 | (r >> 2 & 1) << 1 : r >> 1 & 7;
   }
 
   // w: W's tile origin; wrows, wcols: what there is of it from there on.
@@ -159,47 +166,52 @@ struct CeProduct {
   // `bpitch` elements apart (n_below 0: a wave without tokens).
   __device__ __forceinline__ void run(uint8_t* lds, const uint16_t* w, int64_t ldw, int64_t wrows, int64_t wcols,
                                       const uint16_t* x, uint32_t xpitch, int64_t xbytes, uint32_t s0, uint32_t s1,
-                                      const uint16_t* below, int64_t bpitch, int64_t n_below) {
+                                      const uint16_t* below, uint32_t bpitch, int64_t n_below) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const auto wbytes = [&](int64_t rows) { return rows > 0 ? (uint32_t)(((rows - 1) * ldw + wcols) * 2) : 0u; };
-    const __amdgpu_buffer_rsrc_t rx = make_rsrc(x, (uint32_t)min(xbytes, (int64_t)0x7fffffff));
-    uint4 xf[KC][4], wf[2][4];
-    uint2 low[KC];
-    const uint32_t lds0 = lds_offset(lds);
+    uint4 xf[RING][4], wf[2][4];
+    uint2 low[RING];
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_offset(lds)) + wave * 1024;
     // this thread's chunks of a tile: tid + 256 u, rows 256 / kRow apart
     const uint32_t row0 = tid / kRow, col0 = (tid % kRow ^ spread(row0)) * 8;  // (rows 16 or 32 apart have the same spread)
     const uint32_t woff = (row0 * (uint32_t)ldw + col0) * 2;
-    auto load_w = [&](uint32_t s) {
+    const uint32_t most = (uint32_t)min(wrows, (int64_t)128);
+    // (from step s1 on nothing: a buffer without bytes)
+    auto load_w = [&](uint32_t s, int buffer) {
       // the buffer moves with the step, so that offsets stay in 32 bits
-      const int64_t left = TRANS ? wrows - (int64_t)s * 64 : min(wrows, (int64_t)128);
-      const bool some = s < s1;
-      const LdsSource src = TRANS ? lds_source(w + (some ? (int64_t)s * 64 * ldw : 0), some ? wbytes(min(left, (int64_t)64)) : 0u)
-                                  : lds_source(w, some ? wbytes(left) : 0u);
+      const int64_t left = TRANS ? wrows - (int64_t)s * 64 : most;
+      const uint32_t rows = s < s1 ? (uint32_t)max(min(left, (int64_t)(TRANS ? 64 : 128)), (int64_t)0) : 0u;
+      const LdsSource src = lds_source(TRANS ? w + (int64_t)s * 64 * ldw : w,
+                                       (rows * (uint32_t)ldw - ((uint32_t)ldw - (uint32_t)wcols)) * (rows > 0 ? 2u : 0u));
       const uint32_t col = TRANS ? col0 : s * 64 + col0;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const uint32_t off = woff + u * (256 / kRow) * 2 * (uint32_t)ldw + (TRANS ? 0u : s * 128);
-        load_to_lds16(src, col < wcols ? off : kOOB, lds0 + (s - s0) % kBuffers * kTile + (u * 256 + wave * 64) * 16);
+        load_to_lds16(src, col < wcols ? off : kOOB, lds0 + buffer * kTile + u * 4096);
       }
     };
-    auto load_x = [&](uint32_t s, int j) {
+    // chunk c (of 32, from this part's first on), into the ring's place j.  (Chunks
+    // past the part's last are another's or zeros, and not used.)  Here, too, the
+    // buffer moves, and a lane's offsets stay.
+    const int32_t xb = (int32_t)min(xbytes, (int64_t)0x7fffffff), lb = (int32_t)max(n_below, (int64_t)0) * 2;
+    auto load_x = [&](uint32_t c, int j) {
+      c += s0 * KC;
+      const __amdgpu_buffer_rsrc_t rx = make_rsrc(x + (int64_t)c * 512, (uint32_t)max(xb - (int32_t)(c * 1024), 0));
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
-        xf[j][t] = buf_load16(rx, s < s1 ? t * xpitch + (s * KC + j) * 1024u + lane * 16u : kOOB);
+      for (int t = 0; t < 4; ++t) xf[j][t] = buf_load16(rx, t * xpitch + lane * 16u);
       if constexpr (TRANS) {
-        const int64_t at = (int64_t)(s / 2) * bpitch + (lane & 15) * 4;
-        low[j] = s < s1 && n_below > 0 && in_bounds(at, 4, n_below) ? *reinterpret_cast<const uint2*>(below + at) : make_uint2(0, 0);
+        const int32_t past = (int32_t)(c / 4 * bpitch);
+        low[j] = buf_load8(make_rsrc(below + past, (uint32_t)max(lb - past * 2, 0)), (lane & 15) * 8);
       }
     };
     constexpr int P = NS / 4, Q = KC * P;  // sub-steps of a chunk of 32, and of a step
-    // a lane's places in a tile: of its row's chunk (TRANS: of unit k = strip / 2)
+    // a lane's places in a tile: of its row's chunk (TRANS: of strip k)
     const int g = lane >> 4;
-    uint32_t at[TRANS ? 4 : 2];
+    uint32_t at[TRANS ? 8 : 2];
     if constexpr (TRANS) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < 8; ++k) {
         const uint32_t row = 4 * g + (lane >> 2 & 3);
-        at[k] = row * 256 + ((4 * k + (lane >> 1 & 1)) ^ spread(row)) * 16 + 8 * (lane & 1);
+        at[k] = row * 256 + ((2 * k + (lane >> 1 & 1)) ^ spread(row)) * 16 + 8 * (lane & 1);
       }
     } else {
 #pragma unroll
@@ -216,7 +228,7 @@ struct CeProduct {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             typedef __attribute__((ext_vector_type(4))) short s16x4;
-            const uint8_t* p = tile + at[strip / 2] + (32 * chunk + 16 * e) * 256 + strip % 2 * 32;
+            const uint8_t* p = tile + at[strip] + (32 * chunk + 16 * e) * 256;
             h[e] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p));
           }
           f[i] = make_uint4(h[0].x, h[0].y, h[1].x, h[1].y);
@@ -228,32 +240,32 @@ struct CeProduct {
 #pragma unroll
       for (int t = 0; t < 4; ++t) acc[i][t] = (f32x4)(0.f);
 #pragma unroll
-    for (int j = 0; j < 3; ++j) load_w(s0 + j);
+    for (int j = 0; j < 3; ++j) load_w(s0 + j, j);
 #pragma unroll
-    for (int j = 0; j < KC; ++j) load_x(s0, j);
+    for (int j = 0; j < RING; ++j) load_x(j, j);
     wait_loads();
     lds_barrier();
     read_w(lds, 0, wf[0]);
-    // step s: W tile s is in buffer (s - s0) % 4.  The barrier in its last sub-step
-    // ends the reads of that buffer and begins those of the next one.
-    auto step = [&](uint32_t s, auto buffer) {
-      constexpr int B = decltype(buffer)::value;
+    // step s = s0 + 12 n + I: W tile s is in buffer I % 4.  The barrier in its last
+    // sub-step ends the reads of that buffer and begins those of the next one.
+    auto step = [&](uint32_t s, auto which) {
+      constexpr int I = decltype(which)::value, B = I % kBuffers;
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
-        if (q == 1) {
-          // the second half of this step's tokens, issued two sub-steps ago, and every W tile up to s + 2
-          wait_loads();
-          load_w(s + 3);
+        const int j = (I * KC + q / P) % RING;
+        if (q == Q - 1) {
+          // W tile s + 1 is there: since then at least 4 chunks and 2 tiles were loaded, 4 loads each
+          wait_loads_but_24();
+          lds_barrier();
         }
-        if (q == Q - 1) lds_barrier();
         if (q < Q - 1) read_w(lds + B * kTile, q + 1, wf[(q + 1) & 1]);
         else read_w(lds + (B + 1) % kBuffers * kTile, 0, wf[0]);
         if constexpr (TRANS) {
           if (q % P == 0) {
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-              const uint32_t l = t < 2 ? low[q / P].x : low[q / P].y, b = (t & 1 ? l >> 16 : l & 0xffffu) * 0x10001u;
-              uint4& f = xf[q / P][t];
+              const uint32_t l = t < 2 ? low[j].x : low[j].y, b = (t & 1 ? l >> 16 : l & 0xffffu) * 0x10001u;
+              uint4& f = xf[j][t];
               f = make_uint4(lower<E>(f.x, b), lower<E>(f.y, b), lower<E>(f.z, b), lower<E>(f.w, b));
             }
           }
@@ -262,18 +274,23 @@ struct CeProduct {
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int t = 0; t < 4; ++t)
-            acc[4 * (q % P) + i][t] = E::mfma16(E::vec(wf[q & 1][i]), E::vec(xf[q / P][t]), acc[4 * (q % P) + i][t]);
-        if (q % P == P - 1) load_x(s + 1, q / P);
+            acc[4 * (q % P) + i][t] = E::mfma16(E::vec(wf[q & 1][i]), E::vec(xf[j][t]), acc[4 * (q % P) + i][t]);
+        if (q % P == P - 1) load_x((s - s0) * KC + q / P + RING, j);
+        if (q == P - 1) load_w(s + 3, (B + 3) % kBuffers);
         // each sub-step's loads stay ahead of its MFMAs
         __builtin_amdgcn_sched_barrier(0);
       }
     };
-    for (uint32_t s = s0; s < s1; s += 4) {
-      step(s, std::integral_constant<int, 0>{});
-      if (s + 1 < s1) step(s + 1, std::integral_constant<int, 1>{});
-      if (s + 2 < s1) step(s + 2, std::integral_constant<int, 2>{});
-      if (s + 3 < s1) step(s + 3, std::integral_constant<int, 3>{});
-    }
+    // (Each step follows one other only, or the compiler has to take the loads that
+    // are out for those of any order, and waits for all of them.)
+    uint32_t s = s0;
+    const auto steps = [&](auto... i) { return (... && (step(s, i), ++s < s1)); };
+    if (s < s1)
+      while (steps(std::integral_constant<int, 0>{}, std::integral_constant<int, 1>{}, std::integral_constant<int, 2>{},
+                   std::integral_constant<int, 3>{}, std::integral_constant<int, 4>{}, std::integral_constant<int, 5>{},
+                   std::integral_constant<int, 6>{}, std::integral_constant<int, 7>{}, std::integral_constant<int, 8>{},
+                   std::integral_constant<int, 9>{}, std::integral_constant<int, 10>{}, std::integral_constant<int, 11>{})) {
+      }
     wait_loads();
   }
 };
