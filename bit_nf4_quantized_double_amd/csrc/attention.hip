@@ -95,7 +95,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
   }
 
   // a thread's pieces of a tile, through registers (columns past d: none)
-  const Tile<DB> at(lane);
+  Tile<DB> at(lane);
   uint4 st[2][PER];
   const auto off = [&](const Heads& x, int u) {
     const uint32_t c = Fill<DB>::column(part_tid, TH, u);
@@ -149,6 +149,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
 
   // a tile by itself.  MASKED: some of the rows do not see it in full
   auto tile = [&](int32_t kt, const uint8_t* kb, auto MASKED) {
+    at.renew();
     const uint8_t* vb = kb + BYTES;
     f32x16 s[NU];
 #pragma unroll
@@ -208,6 +209,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
     return top;
   };
   auto step = [&](const uint8_t* kb, const uint8_t* vb, f32x16 (&s)[2], f32x16 (&next)[2], float& top) {
+    at.renew();
     constexpr int N = 4 * DB, RING = 4, EP = 32 / N;  // products of each kind, elements beside each
     uint4 ring[RING];
     auto fetch = [&](int f) {

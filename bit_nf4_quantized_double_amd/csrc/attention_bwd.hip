@@ -244,7 +244,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
   const float c2 = a.scale * kLog2e;
 
   // a thread's pieces of a tile (columns past d: none)
-  const Tile<DB> at(lane);
+  Tile<DB> at(lane);
   uint4 st[2][PER];
   const auto off = [&](const Heads& x, int u) {
     const uint32_t c = Fill<DB>::column(tid, 256, u);
@@ -282,6 +282,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
   // the first beside dS of the second; operands come from LDS through a ring of
   // registers, RING products ahead.  MASKED: some of the rows do not see it in full
   auto tile = [&](int32_t kt, const uint8_t* kb, auto MASKED) {
+    at.renew();
     const uint8_t* vb = kb + BYTES;
     constexpr int N = 2 * DB, RING = 4, EP = 8 / DB;  // products of each kind, dS beside each of them
     uint4 ring[RING];
@@ -439,7 +440,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_kv(AttnArgs a) {
 
   // a thread's pieces of a tile, of Q and dO: rows tid / CH + u 256 / CH, the same
   // columns ch8 .. + 7 (256 / CH is a multiple of 16: so is the permutation)
-  const Tile<DB> at(lane);
+  Tile<DB> at(lane);
   const uint32_t ch8 = Fill<DB>::column(tid, 256, 0);
   const int64_t q_at = q0 * a.q.token + head0 * a.q.head, d_at = q0 * a.dout.token + head0 * a.dout.head;
   uint4 st[2][PER];
@@ -493,6 +494,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_kv(AttnArgs a) {
 #pragma unroll
   for (int b = 0; b < DB; ++b) dk[b] = dv[b] = (f32x16)(0.f);
   auto tile = [&](int32_t rt, int buf, auto MASKED) {
+    at.renew();
     constexpr bool kMasked = decltype(MASKED)::value;
     const uint8_t *qb = lds + buf * 2 * BYTES, *db = qb + BYTES, *vb = s_v + 32 * wave * Tile<DB>::kPitch;
     // Operands in the order of their use, each read from LDS into a ring of

@@ -80,30 +80,33 @@ __device__ __forceinline__ Keys keys_of(const AttnArgs& a, int32_t seq) {
 
 // A tile in LDS: rows of DB * 32 16-bit values (chunks of 16 bytes past d are
 // zeros) one after another, as loads straight into LDS leave them; the chunks of a
-// row are permuted by chunk ^ spread(row), so that the 8 rows that a wave's b128
-// reads of one column touch at a time, and the 4 rows by 32 bytes of its
-// transposing reads, fall into different banks.
+// row are permuted by chunk ^ spread(row), so that the 16 rows that a wave's b128
+// reads of one column touch at a time, and the 4 rows by 64 bytes of its
+// transposing reads, fall into different banks (64 of 4 bytes).
 template <int DB>
 struct Tile {
   static constexpr int kPitch = DB * 64;  // bytes of a row
   static constexpr int kChunks = DB * 4;  // 16-byte chunks of a row
   static __device__ __forceinline__ uint32_t spread(uint32_t r) {
-    return (DB == 4 ? (r & 3) << 2 : (r >> 1 & 1) << 2) | (r >> 2 & 1);
+    return (DB == 4 ? (r & 3) << 2 : (r >> 1 & 1) << 2) | (r >> 2 & 3);
   }
 
-  // A lane's places in a tile; with these every address is one plus a constant.
-  uint32_t row[DB], col[DB];
+  // A lane's places in a tile.  The permutation is an exclusive or, and so is the
+  // way from a column to the next: an address is (place ^ constant) + base, one
+  // instruction.
+  uint32_t row, col;
   __device__ __forceinline__ explicit Tile(int lane) {
     const uint32_t r = lane & 31, t = 4 * (lane >> 5) + ((lane & 15) >> 2);
-#pragma unroll
-    for (int k = 0; k < DB; ++k) {
-      row[k] = r * kPitch + ((4 * k + (lane >> 5)) ^ spread(r)) * 16;
-      col[k] = t * kPitch + ((4 * k + 2 * (lane >> 4 & 1) + ((lane & 3) >> 1)) ^ spread(t)) * 16 + 8 * (lane & 1);
-    }
+    row = r * kPitch + ((lane >> 5) ^ spread(r)) * 16;
+    col = t * kPitch + ((2 * (lane >> 4 & 1) + ((lane & 3) >> 1)) ^ spread(t)) * 16 + 8 * (lane & 1);
   }
+  // To the compiler these change here: it would make all addresses ahead of a
+  // loop and keep them in registers that there are not.
+  __device__ __forceinline__ void renew() { asm volatile("" : "+v"(row), "+v"(col)); }
+
   // MFMA operand (32 x 16): row r0 + lane % 32, columns 16 step + 8 (lane / 32) .. + 7.  r0 a multiple of 32.
   __device__ __forceinline__ uint4 rows(const uint8_t* tile, int r0, int step) const {
-    return *reinterpret_cast<const uint4*>(tile + row[step >> 1] + r0 * kPitch + (step & 1) * 32);
+    return *reinterpret_cast<const uint4*>(tile + (row ^ (uint32_t)step << 5) + r0 * kPitch);
   }
   // The transposed operand (32 x 16): column 32 block + lane % 32 of rows r0 ..
   // r0 + 15, in the order in which the accumulators of a 32 x 32 product hold
@@ -116,7 +119,7 @@ struct Tile {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       u[i] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (__attribute__((address_space(3))) s16x4*)(tile + col[block] + (r0 + 8 * i) * kPitch)));
+          (__attribute__((address_space(3))) s16x4*)(tile + (col ^ (uint32_t)(block << 6 | i << 5)) + (r0 + 8 * i) * kPitch)));
     return make_uint4(u[0].x, u[0].y, u[1].x, u[1].y);
   }
 };
