@@ -183,6 +183,11 @@ int qlora_rope(const qlora_heads* Q, int64_t heads, const qlora_heads* K, int64_
         (st = check_heads(Ko, tokens, kv_heads, head_dim, 2, true, "Ko")))
       return st;
     if (tokens == 0 || heads + kv_heads == 0 || head_dim == 0) return (int)QLORA_OK;
+    const auto in_place = [&](const qlora_heads* x, const qlora_heads* y, int64_t h) {
+      return h == 0 || x->p != y->p || ((tokens == 1 || x->token_stride == y->token_stride) && (h == 1 || x->head_stride == y->head_stride));
+    };
+    if (!in_place(Q, Qo, heads) || !in_place(K, Ko, kv_heads))
+      return fail(QLORA_ERR_INVALID_ARG, "in place, strides must be the same");
     if (rot > 0) {
       if (!positions || !turns) return fail(QLORA_ERR_INVALID_ARG, "positions or turns is NULL");
       if (reinterpret_cast<uintptr_t>(positions) % (positions64 ? 8 : 4) || reinterpret_cast<uintptr_t>(turns) % 8)

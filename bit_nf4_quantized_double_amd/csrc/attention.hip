@@ -30,12 +30,20 @@ struct Running {
 
 // Keys of a split at least: a workgroup with fewer spends its time on finding its
 // rows and keys (16 sequences of 1 to 16384 keys, 64 heads on 8: 90 us with 16
-// splits whatever the length, 82 with these).
+// splits whatever the length, 82 with these at the time).
 constexpr int kLeastKeys = 512;
 
 // KW = 1: 128 rows a workgroup, 32 a wave; tiles of 64 keys, double buffered,
-// shared by the waves.  KW = 4 (few rows, many keys): 32 rows a workgroup, whose
-// waves take tiles of 32 keys in turn, each through its own LDS.
+// shared by the waves.  Bound by the matrix cores, 56 % busy near 1.8 GHz, and the
+// waits between their products (8192 causal tokens, 32 heads of 128 on 8: 530 to 580
+// us, 0.95 to 1.04 PFLOP/s).  Each operand read from LDS serves one product; 64 rows a
+// wave would halve the reads (28 % of the cycles), but with 512 registers a lane the half
+// that only the matrix instructions can use costs 5 moves a product (440 -> 585 us for
+// four turns of a prompt, 64 heads on 8).
+// KW = 4 (few rows, many keys): 32 rows a workgroup, whose waves take tiles of 32
+// keys in turn, each through its own LDS.  Bound by reading the keys (16 sequences
+// of 1 to 16384 keys, 64 heads on 8, 310 MB: 67 to 76 us, 4.1 to 4.6 TB/s; 6 us in
+// k_attn_join) and by the longest sequence's workgroups.
 template <typename E, int DB, int KW>
 __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
   constexpr int NU = KW == 1 ? 2 : 1, BN = 32 * NU, BM = KW == 1 ? 128 : 32;

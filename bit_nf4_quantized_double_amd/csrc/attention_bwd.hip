@@ -118,9 +118,11 @@ __device__ __forceinline__ void delta_few(const AttnArgs& a, int64_t w, float* d
   }
 }
 
-// delta = sum_d dO O, 16 lanes a row, and lse in base 2, less P's power of two; in fp16 (blockIdx.y: dO, V) also the
-// largest finite magnitude of each workgroup's rows.
-// The first `few` workgroups (of blockIdx.y 0) see to the rows with few keys.
+// delta = sum_d dO O, 16 lanes a row, and lse in base 2, less P's power of two; in
+// fp16 (blockIdx.y: dO, V) also the largest finite magnitude of each workgroup's
+// rows.  The first `few` workgroups (of blockIdx.y 0) see to the rows with few keys.
+// Bound by memory where there are many tokens (8192, 32 heads of 128: 30 to 34 us,
+// 4.0 to 4.5 TB/s; tiles of 4 tokens, since tiles of 32 left compute units idle at 2048).
 template <typename E, int DB>
 __global__ __launch_bounds__(256) void k_attn_delta(AttnArgs a, uint32_t few, float* delta, float* lse2, float* top) {
   const bool isv = blockIdx.y == 1;
@@ -189,7 +191,10 @@ __device__ __forceinline__ float to_range(float bound) {
   return __builtin_bit_cast(float, (uint32_t)(max(-100, min(100, 14 - e)) + 127) << 23);
 }
 
-// dQ: 128 rows a workgroup, 32 a wave, tiles of 64 keys.
+// dQ: 128 rows a workgroup, 32 a wave, tiles of 64 keys.  Q, dO and dQ stay in
+// registers.  Bound by the matrix cores, 66 % busy near 1.8 GHz (8192 causal tokens, 32
+// heads of 128 on 8: 690 to 770 us, 1.07 to 1.19 PFLOP/s); they wait for operands from
+// LDS, one read a product, and for the exponentials.
 template <typename E, int DB>
 __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
   constexpr int BN = 64, BM = 128;
@@ -375,9 +380,14 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
 // group / splits heads; with more than one split their sums go to `part`.
 //
 // dK and dV take 128 registers, K's operands 32; V's are read from LDS each time
-// (in registers they would leave none for operands on their way).  The products
-// run in groups of two to four, whose operands are read from LDS during the group
-// before; exponentials and dS are made between the MFMAs of dO V^T and of dV.
+// (in registers they would leave none for operands on their way: slower, as were 64
+// keys a wave with 512 registers a lane).  Operands come from LDS through a ring of
+// four, ahead of their products (six and eight were slower); exponentials are made
+// beside dO V^T and dS beside dV.  Bound by waits for operands, one or two of which
+// each product reads from LDS (36 % busy): matrix cores 48 % busy (8192 causal tokens,
+// 32 heads of 128 on 8: 1.1 to 1.3 ms, 0.85 to 1.0 PFLOP/s), and 14 % of the time the last
+// workgroups leave places empty.  Waves that skip row tiles none of whose rows see
+// their keys: no faster.
 template <typename E, int DB>
 __global__ __launch_bounds__(256, 2) void k_attn_bwd_kv(AttnArgs a) {
   constexpr int BQ = 32, BK = 128;
@@ -656,6 +666,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_kv(AttnArgs a) {
 }
 
 // The splits' sums together: a few keys' values of all key heads a workgroup.
+// Bound by memory (8192 keys, 8 heads of 128, two splits: 28 us, 6 TB/s).
 template <typename E>
 __global__ __launch_bounds__(256) void k_attn_bwd_join(AttnArgs a) {
   const Region rg = find_region(a.cu_k, a.batch, a.tk, 1, kDeltaTokens, blockIdx.x);
@@ -686,12 +697,15 @@ __global__ __launch_bounds__(256) void k_attn_bwd_join(AttnArgs a) {
 }  // namespace
 
 // Over how many workgroups the query heads of a key head are split: as few as
-// make four workgroups a compute unit (under a causal mask they differ in length).
+// make eight workgroups a compute unit, two of which it runs at a time (under a
+// causal mask they differ in length, and the last ones leave units idle).  Forward
+// and backward of 8192 tokens, 32 heads on 8: 2.52 ms with two, 2.36 with four, 2.32
+// with eight, which takes 268 MB of workspace.
 int attn_bwd_splits(int64_t tk, int64_t batch, int64_t heads, int64_t kv_heads, int compute_units) {
   if (heads <= 0 || kv_heads <= 0) return 1;
   const int64_t group = heads / kv_heads, units = kv_heads * std::max<int64_t>((tk + 127) / 128, batch);
   int64_t s = 1;
-  while (s < group && (group % s != 0 || units * s < 4 * compute_units)) ++s;
+  while (s < group && (group % s != 0 || units * s < 8 * compute_units)) ++s;
   return (int)s;
 }
 

@@ -11,8 +11,10 @@
 // Its top bits give the eighth of a turn and a remainder of at most an eighth,
 // where sine and cosine are their power series.
 //
-// Bound by memory: each value is read and written once.  A thread keeps the
-// sines of its 8 pairs for all the heads it turns.
+// Bound by memory: each value is read and written once (8192 tokens, 32 query and
+// 8 key heads of 128: 33 to 35 us, 4.9 to 5.1 TB/s, a copy's rate).  A thread
+// keeps the sines of its 8 pairs for all the heads it turns, 8 of them; few tokens
+// are bound by the launch (16 tokens: 4.5 us), and spread over more threads.
 #include <algorithm>
 
 #include "common.h"

@@ -44,6 +44,11 @@ def test_rope_refuses(L, args, want):
     assert rope(L, **args) == want and L.qlora_last_error()
 
 
+def test_rope_refuses_other_strides_in_place(L):
+    assert rope(L, qo=heads(token=512)) == INVALID and b"strides" in L.qlora_last_error()
+    assert rope(L, k=heads(), hk=4, ko=heads(head=72, token=288)) == INVALID and b"strides" in L.qlora_last_error()
+
+
 def test_rope_has_nothing_to_do(L):
     assert rope(L, t=0, q=heads(0), qo=heads(0), pos=None, turns=None) == 0
     assert rope(L, h=0, q=heads(0), qo=heads(0)) == 0
