@@ -65,8 +65,7 @@ struct Half<F16> {
 
 // x in operand order, padded with zeros: 16 bytes a thread.
 template <typename E>
-__global__ __launch_bounds__(256) void k_ce_pack(CeArgs a, CeRound r) {
-  const int64_t i = block_of(blockIdx.x, blockIdx.y) * 256 + threadIdx.x;
+__device__ __forceinline__ void pack(const CeArgs& a, const CeRound& r, int64_t i) {
   const int64_t chunks = r.kp / 32, tile = i >> 6;
   if (tile >= r.mp / 16 * chunks) return;
   const int lane = (int)(i & 63);
@@ -81,8 +80,7 @@ __global__ __launch_bounds__(256) void k_ce_pack(CeArgs a, CeRound r) {
 // (Where a token is known well its loss is as far off, relative to itself, as
 // this logit, and the matrix cores add up k / 32 times in a row.)
 template <typename E>
-__global__ __launch_bounds__(256) void k_ce_target(CeArgs a, CeRound r) {
-  const int64_t m = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+__device__ __forceinline__ void target_logit(const CeArgs& a, const CeRound& r, int64_t m) {
   const int lane = threadIdx.x & 63;
   if (m >= r.m || !in_bounds(m, 1, r.m)) return;
   const int64_t y = a.targets[m];
@@ -110,6 +108,14 @@ __global__ __launch_bounds__(256) void k_ce_target(CeArgs a, CeRound r) {
 __device__ __forceinline__ void wait_loads_but_24() {
   __builtin_amdgcn_s_waitcnt(0x4f78);
   asm volatile("" ::: "memory");
+}
+
+// Both in one launch, the targets' workgroups first.
+template <typename E>
+__global__ __launch_bounds__(256) void k_ce_prepare(CeArgs a, CeRound r, int64_t targets) {
+  const int64_t b = block_of(blockIdx.x, blockIdx.y);
+  if (b < targets) target_logit<E>(a, r, b * 4 + (threadIdx.x >> 6));
+  else pack<E>(a, r, (b - targets) * 256 + threadIdx.x);
 }
 
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
@@ -334,7 +340,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
           for (int t = 0; t < 4; ++t) p.acc[i][t][e] = -INFINITY;
   }
-  // the target's own entry apart (k_ce_target has it)
+  // the target's own entry apart (k_ce_prepare has it)
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
     const int64_t m = m0 + 16 * t + c;
@@ -387,26 +393,31 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   }
 }
 
-// 16 tokens a workgroup, 16 threads each: a piece's tiles into the running m
-// and l; after the last piece the loss, the log-sum and the gradient's factors.
+// 16 tokens a workgroup, 64 threads each: a piece's tiles into the running m and
+// l; after the last piece the loss, the log-sum and the gradient's factors.  Bound by
+// the latency of its loads, so that many are out at a time (16 tokens, 1002 tiles: 12 us
+// for 49 with 16 threads a token; 8192 tokens, 251 tiles: 17 for 21).
+constexpr int kStatParts = 64;
 template <typename E, bool GRAD>
-__global__ __launch_bounds__(256) void k_ce_stats(CeArgs a, CeRound r, bool first, bool final) {
+__global__ __launch_bounds__(16 * kStatParts) void k_ce_stats(CeArgs a, CeRound r, bool first, bool final) {
   const int part = threadIdx.x >> 4, lane16 = threadIdx.x & 15;
   const int64_t m = (int64_t)blockIdx.x * 16 + lane16;
   const int64_t tiles = (r.vn + kTileN - 1) / kTileN;
-  __shared__ float s[16][17];
+  __shared__ float s[kStatParts][17];
   const float old_m = first ? -kMost : r.run_m[m], old_l = first ? 0.f : r.run_l[m];
   float top = -kMost;
-  for (int64_t t = part; t < tiles; t += 16)
+#pragma unroll 4
+  for (int64_t t = part; t < tiles; t += kStatParts)
     if (in_bounds(t * r.mp + m, 1, r.n_stat)) top = fmaxf(top, r.tile_m[t * r.mp + m]);
   s[part][lane16] = top;
   __syncthreads();
   top = old_m;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) top = fmaxf(top, s[i][lane16]);
+#pragma unroll 16
+  for (int i = 0; i < kStatParts; ++i) top = fmaxf(top, s[i][lane16]);
   __syncthreads();
   float l = 0.f;
-  for (int64_t t = part; t < tiles; t += 16) {
+#pragma unroll 4
+  for (int64_t t = part; t < tiles; t += kStatParts) {
     if (!in_bounds(t * r.mp + m, 1, r.n_stat)) continue;
     const float d = top - r.tile_m[t * r.mp + m];  // a whole number
     l += r.tile_l[t * r.mp + m] * __builtin_amdgcn_exp2f(-d);
@@ -421,8 +432,8 @@ __global__ __launch_bounds__(256) void k_ce_stats(CeArgs a, CeRound r, bool firs
   if (part != 0) return;
   const float shift = __builtin_amdgcn_exp2f(old_m - top);
   l = old_l * shift;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) l += s[i][lane16];
+#pragma unroll 16
+  for (int i = 0; i < kStatParts; ++i) l += s[i][lane16];
   r.run_m[m] = top;
   r.run_l[m] = l;
   if constexpr (GRAD) r.shift[m] = shift;
@@ -622,14 +633,14 @@ CeRound ce_round(int64_t m, int64_t k, int64_t v, bool grad, int cus, char* ws, 
 
 template <typename E, bool GRAD>
 void run_round(const CeArgs& a, CeRound r, hipStream_t stream) {
-  k_ce_pack<E><<<grid_of((r.n_xt / 8 + 255) / 256), 256, 0, stream>>>(a, r);
-  k_ce_target<E><<<(uint32_t)((r.m + 3) / 4), 256, 0, stream>>>(a, r);
+  const int64_t targets = (r.m + 3) / 4;
+  k_ce_prepare<E><<<grid_of(targets + (r.n_xt / 8 + 255) / 256), 256, 0, stream>>>(a, r, targets);
   for (int64_t v0 = 0; v0 < a.v; v0 += r.piece) {
     r.v0 = v0;
     r.vn = std::min(r.piece, a.v - v0);
     const int64_t mt = (r.m + kTileM - 1) / kTileM, vt = (r.vn + kTileN - 1) / kTileN;
     k_ce_logits<E, GRAD><<<(uint32_t)(mt * vt), 256, 0, stream>>>(a, r);
-    k_ce_stats<E, GRAD><<<(uint32_t)(r.mp / 16), 256, 0, stream>>>(a, r, v0 == 0, v0 + r.piece >= a.v);
+    k_ce_stats<E, GRAD><<<(uint32_t)(r.mp / 16), 16 * kStatParts, 0, stream>>>(a, r, v0 == 0, v0 + r.piece >= a.v);
     if constexpr (GRAD)
       k_ce_grad<E><<<(uint32_t)(mt * ((a.k + kTileN - 1) / kTileN) * r.splits), 256, 0, stream>>>(a, r, v0 == 0);
   }
