@@ -30,7 +30,7 @@ struct Running {
 
 // Keys of a split at least: a workgroup with fewer spends its time on finding its
 // rows and keys (16 sequences of 1 to 16384 keys, 64 heads on 8: 90 us with 16
-// splits whatever the length, 82 with these at the time).
+// splits whatever the length, 82 with these; 77 since).
 constexpr int kLeastKeys = 512;
 
 // KW = 1: 128 rows a workgroup, 32 a wave; tiles of 64 keys, double buffered,

@@ -267,9 +267,9 @@ __device__ __forceinline__ uint4 load16(const Heads& x, int64_t at, bool ok) {
 }
 
 template <typename E, typename A>
-__device__ __forceinline__ typename E::v8 pack8(const A& p, int i, float f = 1.f) {
-  return E::vec(make_uint4(E::pack2(p[i] * f, p[i + 1] * f), E::pack2(p[i + 2] * f, p[i + 3] * f),
-                           E::pack2(p[i + 4] * f, p[i + 5] * f), E::pack2(p[i + 6] * f, p[i + 7] * f)));
+__device__ __forceinline__ typename E::v8 pack8(const A& p, int i) {
+  return E::vec(make_uint4(E::pack2(p[i], p[i + 1]), E::pack2(p[i + 2], p[i + 3]), E::pack2(p[i + 4], p[i + 5]),
+                           E::pack2(p[i + 6], p[i + 7])));
 }
 
 }  // namespace
