@@ -378,6 +378,33 @@ def test_many_sequences(dtype):
         test_forward_and_backward(lq, lk, h, hk, 64, True, dtype)
 
 
+def test_offsets_past_32_bits():
+    """Tokens so far apart that their offsets need more than 32 bits, forward and
+    backward, few queries and many: the same bits as close together."""
+    need_gpu()
+    far, t, hk, d = 1 << 20, 4200, 2, 64
+    room = [torch.empty((t - 1) * far + hk * d, dtype=BF16, device="cuda") for _ in range(2)]
+
+    def apart(x, into):
+        y = into.as_strided(x.shape, (far, d, 1))
+        y.copy_(x)
+        return y
+
+    for lq in ([2, 1], [4200]):
+        lk = [4000, 200] if len(lq) > 1 else [4200]
+        q, k, v, do = _inputs(lq, lk, 4, hk, d, BF16)
+        o, lse = attention.attention_fwd(q, k, v, cu(lq), cu(lk))
+        want = (o, lse, *attention.attention_bwd(do, q, k, v, o, lse, cu(lq), cu(lk)))
+        k, v = apart(k, room[0]), apart(v, room[1])
+        got = attention.attention_fwd(q, k, v, cu(lq), cu(lk))
+        got += attention.attention_bwd(do, q, k, v, o, lse, cu(lq), cu(lk))
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        dk, dv = torch.empty_like(want[3]), room[1].as_strided(k.shape, (far, d, 1))
+        v = want[4].new_empty(want[4].shape).copy_(v)
+        attention.attention_bwd(do, q, k, v, o, lse, cu(lq), cu(lk), dQ=torch.empty_like(q), dK=dk, dV=dv)
+        assert torch.equal(dv, want[4]) and torch.equal(dk, want[3])
+
+
 def test_no_sequences():
     need_gpu()
     q, k, v, do = _inputs([5], [5], 2, 2, 64, BF16)

@@ -127,6 +127,20 @@ def test_strides_alignment_and_in_place():
     assert got[2] is x2 and all(torch.equal(a, b) for a, b in zip(want, got))
 
 
+def test_offsets_past_32_bits():
+    """Rows so far apart that their offsets need more than 32 bits: the same bits."""
+    need_gpu()
+    m, k, v, far = 2200, 72, 3000, 1 << 20
+    x, w, y = _inputs(m, k, v, BF16)
+    want = cross_entropy.linear_cross_entropy_grad(x, w, y)
+    room = torch.empty((v - 1) * far + k, dtype=BF16, device="cuda")
+    for wide in (0, 1):
+        t = room.as_strided((v, k) if wide else (m, k), (far, 1))
+        t.copy_(w if wide else x)
+        got = cross_entropy.linear_cross_entropy_grad(x if wide else t, t if wide else w, y)
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
 def test_ignored_and_invalid_targets():
     """An ignored token's row has no effect and no gradient, whatever it holds; a
     target outside the vocabulary shows as NaN; neither reaches other tokens."""

@@ -114,6 +114,19 @@ def test_slices_and_in_place(offset, interleaved):
     assert torch.equal(wide[:, offset + (h + hk) * d:], before[:, offset + (h + hk) * d:])
 
 
+def test_offsets_past_32_bits():
+    """Tokens so far apart that their offsets need more than 32 bits, in place."""
+    need_gpu()
+    t, h, d, far = 2200, 2, 64, 1 << 20
+    x, f = rand((t, h, d), 1), rotary.frequencies(d)
+    p = torch.arange(t, device="cuda")
+    want, _ = rotary.rotate(x, None, p, f)
+    y = torch.empty((t - 1) * far + h * d, dtype=x.dtype, device="cuda").as_strided((t, h, d), (far, d, 1))
+    y.copy_(x)
+    rotary.rotate(y, None, p, f, Q_out=y)
+    assert torch.equal(y, want)
+
+
 def test_autograd():
     """The gradient is the inverse rotation, also where one output is not used."""
     need_gpu()
