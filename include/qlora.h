@@ -601,8 +601,9 @@ int qlora_rope(const qlora_heads *Q, int64_t heads, const qlora_heads *K, int64_
  * dK and dV summed over the heads that share them (sum dO O as sum P (dO V) for a
  * query that sees up to 32 keys: O is rounded).  P and dS are rounded to 16 bits for
  * the products.  A K that is not finite makes dQ of the queries that see it NaN.
- * Same inputs, same bits: no atomics.  fp16: dS is kept in range by a power of two from the largest finite |dO| and |V|, of the row for
- * dQ and of the whole batch for dK; what is 2^-30 below these bounds is lost.
+ * Same inputs, same bits: no atomics.  fp16: dS is kept in range by a power of two
+ * from the largest finite |dO| and |V|, of the row for dQ and of the whole batch
+ * for dK; what is 2^-30 below these bounds is lost.
  * Workspace: qlora_attention_workspace_bytes(op, ...).  The forward's is for keys
  * split over workgroups and optional (without room it runs unsplit, as right);
  * the backward's is needed (QLORA_ERR_WORKSPACE).  Outputs lie apart from inputs
