@@ -333,6 +333,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
   };
 
   if (tid == 0) s_bad = INT_MAX;
+  __syncthreads();  // here: where no row sees a key there is no other before s_bad is read
   const int32_t kf = max(0, min(k1, whole / BN));  // the first tile that not all rows see in full
   if (kf > 0) {
     const uint32_t lds0 = lds_offset(lds) + wave * 1024;

@@ -57,6 +57,29 @@ def test_forward_and_backward(lq, lk, h, hk, d, causal, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lq,lk,causal", [([300], [0], True), ([300], [0], False), ([1000], [10], True),
+                                          ([260, 400, 70], [0, 20, 70], True)])
+def test_whole_tiles_that_see_nothing(lq, lk, causal, d, dtype):
+    """Row tiles none of whose rows see a key: their dQ is zero, whatever a workgroup
+    that ran before has left in LDS."""
+    need_gpu()
+    h, hk = 4, 2
+    q, k, v, do = _inputs(lq, lk, h, hk, d, dtype)
+    want = attention_reference(q, k, v, lq, lk, causal, do=do)
+    fill = [-abs(x) for x in _inputs([4096], [4096], h, hk, d, dtype, 9)]  # negative numbers all over LDS
+    o, lse = attention.attention_fwd(q, k, v, cu(lq), cu(lk), causal=causal)
+    fo, fl = attention.attention_fwd(*fill[:3], cu([4096]))
+    attention.attention_bwd(fill[3], *fill[:3], fo, fl, cu([4096]))
+    dq, dk, dv = attention.attention_bwd(do, q, k, v, o, lse, cu(lq), cu(lk), causal=causal)
+    for at, n, m in zip(starts(lq), lq, lk):
+        blind = n if m == 0 else max(n - m, 0) if causal else 0
+        assert bool((dq[at:at + blind] == 0).all())
+    for got, name in ((dq, "dq"), (dk, "dk"), (dv, "dv")):
+        close(got, want[name], name)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("new,room,lk,h,hk,d", [
     (1, 40, [40, 1, 17], 4, 4, 128), (1, 700, [700, 513, 512, 33, 1, 0], 16, 2, 128), (4, 300, [300, 4, 257], 8, 1, 64),
     (1, 5000, [5000, 4097], 8, 8, 128), (2, 3000, [2999], 7, 1, 72)])
