@@ -121,18 +121,18 @@ class LinearCrossEntropyFunction(torch.autograd.Function):
             loss, _ = linear_cross_entropy_fwd(X, W, targets, ignore_index=ignore_index)
         both = None if reduction == "none" else reduce_losses(loss, targets, reduction == "mean", ignore_index=ignore_index)
         if gradient:
-            ctx.save_for_backward(dX, targets if both is None else both[1])
-            ctx.ignore_index, ctx.reduction = ignore_index, reduction
+            ctx.save_for_backward(dX, targets, None if both is None else both[1])
+            ctx.ignore_index = ignore_index
         return loss if both is None else both[0]
 
     @staticmethod
     @qlora._once
     def backward(ctx, dloss):
-        dX, with_ = ctx.saved_tensors
-        if ctx.reduction == "none":  # whatever comes for ignored tokens
-            g = dloss.masked_fill(with_ == ctx.ignore_index, 0.0)
-        else:
-            g = (dloss * with_).expand(dX.shape[0])
+        dX, targets, weight = ctx.saved_tensors
+        if weight is not None:
+            dloss = (dloss * weight).expand(dX.shape[0])
+        # ignored tokens get none whatever comes: an infinite loss scale, or the mean of no losses
+        g = dloss.masked_fill(targets == ctx.ignore_index, 0.0)
         return scale_rows(dX, g.contiguous()), None, None, None, None, None
 
 

@@ -311,6 +311,24 @@ def test_ignored_tokens_take_no_gradient():
         assert not cross_entropy.linear_cross_entropy(x, w, y).requires_grad
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("reduction", ["sum", "mean"])
+def test_reduced_losses_give_ignored_tokens_no_gradient(reduction, dtype):
+    """All tokens ignored (the mean is a NaN then), and an infinite gradient from
+    above with some of them."""
+    need_gpu()
+    x, w, y = _inputs(20, 64, 50, dtype)
+    x.requires_grad_()
+    some = y.clone()
+    some[::2] = IGNORE
+    for targets, up in ((torch.full_like(y, IGNORE), 1.0), (torch.full_like(y, IGNORE), float("inf")), (some, float("inf"))):
+        loss = cross_entropy.linear_cross_entropy(x, w, targets, reduction=reduction)
+        g, = torch.autograd.grad(loss, x, torch.tensor(up, device="cuda"))
+        live = targets != IGNORE
+        assert bool((g[~live] == 0).all())
+        assert not bool(torch.isfinite(g[live]).all(1).any())
+
+
 def test_refusals():
     need_gpu()
     x, w, y = _inputs(4, 64, 50, BF16)
