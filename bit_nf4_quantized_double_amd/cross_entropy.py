@@ -3,7 +3,8 @@ libqlora.so: loss and gradient in one pass over the vocabulary, without the
 logits.
 
 :func:`linear_cross_entropy_fwd` gives each token's loss (evaluation),
-:func:`linear_cross_entropy_grad` the gradient of the hidden states as well, and
+:func:`linear_cross_entropy_grad` the gradient of the hidden states as well
+(:func:`linear_cross_entropy_units` for one that is multiplied later), and
 :func:`linear_cross_entropy` is the differentiable form.  The head is frozen, as
 every weight here: there is no dW.  Formulas, rounding and limits:
 include/qlora.h.
@@ -40,7 +41,7 @@ def workspace_bytes(m: int, k: int, v: int, gradient: bool) -> int:
     return int(qlora.lib().qlora_cross_entropy_workspace_bytes(m, k, v, gradient))
 
 
-def _call(X, W, targets, ignore_index, dloss, gradient, dX, ws):
+def _call(X, W, targets, ignore_index, dloss, gradient, dX, ws, units=False):
     x, ldx, m, k = _matrix(X, "X")
     dt, dev = X.dtype, X.device
     w, ldw, v, _ = _matrix(W, "W", k)
@@ -57,9 +58,16 @@ def _call(X, W, targets, ignore_index, dloss, gradient, dX, ws):
         dX = _out(dX, X.shape, dt, "dX", dev)
     L = qlora.lib()
     wst, wsn = qlora._ws(L.qlora_cross_entropy_workspace_bytes(m, k, v, gradient), dev, ws)
+    rest = DTYPES[dt], None if wst is None else wst.data_ptr(), wsn, _stream(dev)
+    if units:
+        unit = torch.empty(m, dtype=torch.float32, device=dev)
+        st = L.qlora_cross_entropy_units(x, ldx, w, ldw, t, m, k, v, ignore_index, loss.data_ptr(), lse.data_ptr(),
+                                         dX.data_ptr(), unit.data_ptr(), *rest)
+        if st:
+            qlora._check(st, "qlora_cross_entropy_units")
+        return loss, lse, dX, unit
     st = L.qlora_cross_entropy(x, ldx, w, ldw, t, m, k, v, ignore_index, g, loss.data_ptr(), lse.data_ptr(),
-                               dX.data_ptr() if gradient else None, DTYPES[dt], None if wst is None else wst.data_ptr(),
-                               wsn, _stream(dev))
+                               dX.data_ptr() if gradient else None, *rest)
     if st:
         qlora._check(st, "qlora_cross_entropy")
     return loss, lse, dX
@@ -79,6 +87,14 @@ def linear_cross_entropy_grad(X: torch.Tensor, W: torch.Tensor, targets: torch.T
     """Returns (loss, lse, dX) with dX the gradient of sum(dloss loss); dloss
     (fp32 [tokens]) None: ones.  ``dX`` may be X (overwritten)."""
     return _call(X, W, targets, ignore_index, dloss, True, dX, ws)
+
+
+def linear_cross_entropy_units(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, *, ignore_index: int = -100,
+                               dX: torch.Tensor | None = None, ws: torch.Tensor | None = None):
+    """Returns (loss, lse, dX, unit): dX as for losses that count once, its rows
+    times unit (fp32 [tokens], powers of two) so that small ones keep their digits
+    until ``scale_rows(dX, g / unit)``."""
+    return _call(X, W, targets, ignore_index, None, True, dX, ws, True)
 
 
 def scale_rows(X: torch.Tensor, g: torch.Tensor, Y: torch.Tensor | None = None) -> torch.Tensor:
@@ -111,28 +127,34 @@ def reduce_losses(loss: torch.Tensor, targets: torch.Tensor, mean: bool, *, igno
 class LinearCrossEntropyFunction(torch.autograd.Function):
     """(X [tokens, width], W, targets) -> losses, or their sum or mean.  The gradient
     is made in the forward, for losses that count once, and the backward multiplies
-    its rows."""
+    its rows.  In fp16 it is kept in units of each row: a loss scale that comes
+    only from above would find small gradients rounded to nothing."""
 
     @staticmethod
     def forward(ctx, X, W, targets, ignore_index: int, reduction: str, gradient: bool):
-        if gradient:
+        unit = None
+        if gradient and X.dtype == torch.float16:
+            loss, _, dX, unit = linear_cross_entropy_units(X, W, targets, ignore_index=ignore_index)
+        elif gradient:
             loss, _, dX = linear_cross_entropy_grad(X, W, targets, ignore_index=ignore_index)
         else:
             loss, _ = linear_cross_entropy_fwd(X, W, targets, ignore_index=ignore_index)
         both = None if reduction == "none" else reduce_losses(loss, targets, reduction == "mean", ignore_index=ignore_index)
         if gradient:
-            ctx.save_for_backward(dX, targets, None if both is None else both[1])
+            ctx.save_for_backward(dX, unit, targets, None if both is None else both[1])
             ctx.ignore_index = ignore_index
         return loss if both is None else both[0]
 
     @staticmethod
     @qlora._once
     def backward(ctx, dloss):
-        dX, targets, weight = ctx.saved_tensors
+        dX, unit, targets, weight = ctx.saved_tensors
         if weight is not None:
             dloss = (dloss * weight).expand(dX.shape[0])
         # ignored tokens get none whatever comes: an infinite loss scale, or the mean of no losses
         g = dloss.masked_fill(targets == ctx.ignore_index, 0.0)
+        if unit is not None:
+            g = g / unit
         return scale_rows(dX, g.contiguous()), None, None, None, None, None
 
 
@@ -162,6 +184,7 @@ def _bind(L: ctypes.CDLL) -> None:
     sig = {
         "qlora_cross_entropy_workspace_bytes": (sz, [i64, i64, i64, i32]),
         "qlora_cross_entropy": (i32, [vp, i64, vp, i64, vp, i64, i64, i64, i64, vp, vp, vp, vp, i32, vp, sz, vp]),
+        "qlora_cross_entropy_units": (i32, [vp, i64, vp, i64, vp, i64, i64, i64, i64, vp, vp, vp, vp, i32, vp, sz, vp]),
         "qlora_loss_sum": (i32, [vp, vp, i64, i64, i32, vp, vp]),
         "qlora_scale_rows": (i32, [vp, vp, i64, i64, vp, i32, vp]),
     }

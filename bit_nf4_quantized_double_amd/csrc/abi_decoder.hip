@@ -161,6 +161,36 @@ int check_aligned(const void* p, int align, const char* name) {
   return QLORA_OK;
 }
 
+int run_cross_entropy(const void* X, int64_t ldx, const void* W, int64_t ldw, const int64_t* targets, int64_t M, int64_t K,
+                      int64_t V, int64_t ignore_index, const float* dloss, float* loss, float* lse, uint16_t* dX, float* unit,
+                      bool units, int dtype, void* ws, size_t ws_bytes, hipStream_t stream) {
+  int st;
+  if ((st = check_ce_sizes(M, K, V)) || (st = check_type16(dtype))) return st;
+  if (M == 0) return (int)QLORA_OK;
+  if ((st = check_aligned(X, 2, "X")) || (st = check_aligned(W, 16, "W")) || (st = check_aligned(targets, 8, "targets")) ||
+      (st = check_aligned(loss, 4, "loss")) || (st = check_aligned(lse, 4, "lse")))
+    return st;
+  if (dloss && (st = check_aligned(dloss, 4, "dloss"))) return st;
+  if (units && (st = check_aligned(unit, 4, "unit"))) return st;
+  if ((dX || units) && (st = check_aligned(dX, 16, "dX"))) return st;
+  if (M == 1) ldx = K;
+  if (V == 1) ldw = K;
+  if (ldx < K || ldw < K) return fail(QLORA_ERR_INVALID_ARG, "a row stride is below the row length");
+  if (ldx > kMostStride || ldw > (1 << 22)) return fail(QLORA_ERR_SHAPE, "a row stride is too large");
+  if (ldw % 8) return fail(QLORA_ERR_ALIGN, "ldw must be a multiple of 8");
+  if ((const void*)dX == X && ldx != K) return fail(QLORA_ERR_INVALID_ARG, "dX may be X only where its rows are contiguous");
+  const int cus = qlora::device_compute_units();
+  if (!ws || ws_bytes < qlora::ce_workspace_bytes(M, K, V, dX != nullptr, cus))
+    return fail(QLORA_ERR_WORKSPACE, "cross entropy workspace too small");
+  if (!aligned16(ws)) return fail(QLORA_ERR_ALIGN, "workspace must be 16-byte aligned");
+  qlora::CeArgs a{};
+  a.x = static_cast<const uint16_t*>(X); a.w = static_cast<const uint16_t*>(W);
+  a.ldx = ldx; a.ldw = ldw; a.m = M; a.k = K; a.v = V;
+  a.targets = targets; a.ignore = ignore_index; a.dloss = dloss;
+  a.loss = loss; a.lse = lse; a.dx = dX; a.unit = unit; a.f16 = dtype == QLORA_F16;
+  return done(qlora::launch_ce(a, ws, cus, stream), "cross entropy launch");
+}
+
 }  // namespace
 
 extern "C" {
@@ -301,30 +331,17 @@ int qlora_cross_entropy(const void* X, int64_t ldx, const void* W, int64_t ldw, 
                         int64_t K, int64_t V, int64_t ignore_index, const float* dloss, float* loss, float* lse,
                         uint16_t* dX, int dtype, void* ws, size_t ws_bytes, hipStream_t stream) {
   return guarded([&] {
-    int st;
-    if ((st = check_ce_sizes(M, K, V)) || (st = check_type16(dtype))) return st;
-    if (M == 0) return (int)QLORA_OK;
-    if ((st = check_aligned(X, 2, "X")) || (st = check_aligned(W, 16, "W")) || (st = check_aligned(targets, 8, "targets")) ||
-        (st = check_aligned(loss, 4, "loss")) || (st = check_aligned(lse, 4, "lse")))
-      return st;
-    if (dloss && (st = check_aligned(dloss, 4, "dloss"))) return st;
-    if (dX && (st = check_aligned(dX, 16, "dX"))) return st;
-    if (M == 1) ldx = K;
-    if (V == 1) ldw = K;
-    if (ldx < K || ldw < K) return fail(QLORA_ERR_INVALID_ARG, "a row stride is below the row length");
-    if (ldx > kMostStride || ldw > (1 << 22)) return fail(QLORA_ERR_SHAPE, "a row stride is too large");
-    if (ldw % 8) return fail(QLORA_ERR_ALIGN, "ldw must be a multiple of 8");
-    if ((const void*)dX == X && ldx != K) return fail(QLORA_ERR_INVALID_ARG, "dX may be X only where its rows are contiguous");
-    const int cus = qlora::device_compute_units();
-    if (!ws || ws_bytes < qlora::ce_workspace_bytes(M, K, V, dX != nullptr, cus))
-      return fail(QLORA_ERR_WORKSPACE, "cross entropy workspace too small");
-    if (!aligned16(ws)) return fail(QLORA_ERR_ALIGN, "workspace must be 16-byte aligned");
-    qlora::CeArgs a{};
-    a.x = static_cast<const uint16_t*>(X); a.w = static_cast<const uint16_t*>(W);
-    a.ldx = ldx; a.ldw = ldw; a.m = M; a.k = K; a.v = V;
-    a.targets = targets; a.ignore = ignore_index; a.dloss = dloss;
-    a.loss = loss; a.lse = lse; a.dx = dX; a.f16 = dtype == QLORA_F16;
-    return done(qlora::launch_ce(a, ws, cus, stream), "cross entropy launch");
+    return run_cross_entropy(X, ldx, W, ldw, targets, M, K, V, ignore_index, dloss, loss, lse, dX, nullptr, false, dtype, ws,
+                             ws_bytes, stream);
+  });
+}
+
+int qlora_cross_entropy_units(const void* X, int64_t ldx, const void* W, int64_t ldw, const int64_t* targets, int64_t M,
+                              int64_t K, int64_t V, int64_t ignore_index, float* loss, float* lse, uint16_t* dX, float* unit,
+                              int dtype, void* ws, size_t ws_bytes, hipStream_t stream) {
+  return guarded([&] {
+    return run_cross_entropy(X, ldx, W, ldw, targets, M, K, V, ignore_index, nullptr, loss, lse, dX, unit, true, dtype, ws,
+                             ws_bytes, stream);
   });
 }
 

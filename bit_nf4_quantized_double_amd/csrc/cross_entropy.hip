@@ -495,6 +495,16 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     }
 }
 
+// What a row of dx with dloss 1 is multiplied by to be stored, where it is only
+// multiplied again later: a power of two that takes 1 - p of the target, in [2^-e, 2^-e+1),
+// to [1/8, 1/4).  dx is 1 - p times the difference of an average of W's rows and one
+// of them, so that it then has the size of W's entries: as far in range as they are.
+// At most 2^64 (a row below 2^-67 is as good as zero).
+__device__ __forceinline__ float unit_of(float rest) {
+  const int e = 127 - (int)(__builtin_bit_cast(uint32_t, rest) >> 23);
+  return rest >= 0x1p-67f && rest <= 1.f ? __builtin_bit_cast(float, (uint32_t)(127 - 3 + e) << 23) : rest < 0x1p-67f ? 0x1p64f : 1.f;
+}
+
 // dx from the sums: 16 tokens x 16 pieces of 8 columns a workgroup.
 template <typename E>
 __global__ __launch_bounds__(256) void k_ce_finish(CeArgs a, CeRound r) {
@@ -518,9 +528,12 @@ __global__ __launch_bounds__(256) void k_ce_finish(CeArgs a, CeRound r) {
   }
   const int64_t y = in_bounds(m, 1, r.m) ? a.targets[m] : a.ignore;
   uint4 out = make_uint4(0, 0, 0, 0);
+  float unit = 1.f;
   if (y != a.ignore) {
     const bool bad = y < 0 || y >= a.v;
-    const float g1 = bad ? NAN : a.dloss ? a.dloss[m] : 1.f, c1 = r.c1[m], c2 = r.c2[m];
+    const float c1 = r.c1[m], c2 = r.c2[m];
+    if (a.unit && !bad) unit = unit_of(c2);
+    const float g1 = bad ? NAN : a.dloss ? a.dloss[m] : unit;
     const int64_t at = (bad ? 0 : y) * a.ldw + col;
     uint4 w = make_uint4(0, 0, 0, 0);
     if (in_bounds(at, 8, (a.v - 1) * a.ldw + a.k)) w = *reinterpret_cast<const uint4*>(a.w + at);
@@ -533,6 +546,7 @@ __global__ __launch_bounds__(256) void k_ce_finish(CeArgs a, CeRound r) {
     out = make_uint4(o[0], o[1], o[2], o[3]);
   }
   if (in_bounds(m * a.k + col, 8, a.m * a.k)) *reinterpret_cast<uint4*>(a.dx + m * a.k + col) = out;
+  if (a.unit && col == 0 && in_bounds(m, 1, a.m)) a.unit[m] = unit;
 }
 
 // out = g x, row by row, 8 values a thread.
@@ -671,6 +685,7 @@ hipError_t launch_ce(const CeArgs& args, void* ws, int compute_units, hipStream_
     a.lse += m0;
     if (a.dloss) a.dloss += m0;
     if (a.dx) a.dx += m0 * a.k;
+    if (a.unit) a.unit += m0;
     size_t bytes;
     const CeRound r = ce_round(a.m, a.k, a.v, a.dx != nullptr, compute_units, static_cast<char*>(ws), &bytes);
     if (a.dx) a.f16 ? run_round<F16, true>(a, r, stream) : run_round<Bf16, true>(a, r, stream);

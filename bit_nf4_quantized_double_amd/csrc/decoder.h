@@ -71,6 +71,7 @@ struct CeArgs {
   const float* dloss;      // [m] or NULL (ones)
   float *loss, *lse;       // [m]
   uint16_t* dx;            // [m, k] contiguous, or NULL: no gradient
+  float* unit;             // [m] or NULL: dx times a power of two for each row, written here
   bool f16;
 };
 size_t ce_workspace_bytes(int64_t m, int64_t k, int64_t v, bool grad, int compute_units);

@@ -658,6 +658,16 @@ int qlora_cross_entropy(const void *X, int64_t ldx, const void *W, int64_t ldw, 
                         float *loss, float *lse, uint16_t *dX, int dtype, void *ws, size_t ws_bytes,
                         hipStream_t stream);
 
+/* The same for a gradient that is multiplied only later (a differentiable loss):
+ *     dX[m] = E(unit[m] (softmax(z[m]) - 1 at the target) W)
+ * with unit[m] (fp32 [M], written) the power of two that takes 1 - p of the target to
+ * [1/8, 1/4), 2^64 at most, and 1 where the target is no entry: small gradients
+ * keep their digits in fp16 too, and qlora_scale_rows with g / unit ends it. */
+int qlora_cross_entropy_units(const void *X, int64_t ldx, const void *W, int64_t ldw, const int64_t *targets,
+                              int64_t M, int64_t K, int64_t V, int64_t ignore_index, float *loss, float *lse,
+                              uint16_t *dX, float *unit, int dtype, void *ws, size_t ws_bytes,
+                              hipStream_t stream);
+
 /* Y[m][k] = E(g[m] X[m][k]): rows of a contiguous 16-bit matrix times fp32
  * numbers, K a multiple of 8 (the loss's gradient times what comes from above). */
 int qlora_scale_rows(const uint16_t *X, const float *g, int64_t M, int64_t K, uint16_t *Y, int dtype,

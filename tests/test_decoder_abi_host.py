@@ -178,6 +178,18 @@ def test_cross_entropy_refuses(L, args, want):
     assert loss(L, **{**dict(dx=0x90000), **args}) == want and L.qlora_last_error()
 
 
+def test_cross_entropy_units_refuses(L):
+    def call(x=P, ldx=64, w=P, m=4, k=64, v=100, loss=P, dx=0x90000, unit=P, dtype=BF16, ws=P, n=1 << 30):
+        return L.qlora_cross_entropy_units(x, ldx, w, 64, P, m, k, v, -100, loss, P, dx, unit, dtype, ws, n, None)
+
+    for args, want in ((dict(dx=None), INVALID), (dict(unit=None), INVALID), (dict(unit=P2), ALIGN), (dict(dx=P2), ALIGN),
+                       (dict(x=None), INVALID), (dict(loss=None), INVALID), (dict(w=P2), ALIGN), (dict(m=-1), INVALID),
+                       (dict(k=60), SHAPE), (dict(v=0), SHAPE), (dict(dtype=2), INVALID), (dict(ldx=72, dx=P), INVALID),
+                       (dict(n=1000), WORKSPACE), (dict(ws=P2), ALIGN)):
+        assert call(**args) == want and L.qlora_last_error(), args
+    assert call(m=0, x=None, loss=None, dx=None, unit=None, ws=None, n=0) == 0
+
+
 def test_cross_entropy_workspace(L):
     ws = L.qlora_cross_entropy_workspace_bytes
     assert loss(L, m=0, x=None, t=None, loss=None, lse=None, dx=None, ws=None, n=0) == 0

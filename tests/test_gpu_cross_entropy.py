@@ -329,6 +329,99 @@ def test_reduced_losses_give_ignored_tokens_no_gradient(reduction, dtype):
         assert not bool(torch.isfinite(g[live]).all(1).any())
 
 
+@pytest.mark.parametrize("reduction", ["none", "sum", "mean"])
+def test_f16_keeps_small_gradients(reduction):
+    """Tokens known to 1 - p of 1e-3 to 1e-9 under a loss scale, in fp16: as far from
+    64 bits as three roundings leave them.
+
+    The row is stored times unit with (1 - p) unit at least 1/8, off by U of itself and
+    half of fp16's smallest step, 2^-25 / unit <= 2^-22 (1 - p); then multiplied and
+    rounded once more.  What comes before is check()'s bound, where the weights that
+    are lost are 2^-28 of the largest of the target's rivals (the target's own is not
+    among them)."""
+    need_gpu()
+    m, k, v, scale = 100, 256, 1000, 65536.0
+    _, w, y = _inputs(m, k, v, F16)
+    y[::9] = IGNORE
+    gain = torch.linspace(14, 28, m, device="cuda")[:, None]
+    own = w[y.clamp(min=0)].float()
+    x = (gain * own / own.square().sum(1, keepdim=True)).to(F16).requires_grad_()
+    out = cross_entropy.linear_cross_entropy(x, w, y, reduction=reduction)
+    n = int((y != IGNORE).sum())
+    # as large as no product leaves fp16's range: (1 - p) |w| is below 2^-9
+    up = torch.full(out.shape, scale * (n if reduction == "mean" else 1), device="cuda")
+    out.backward(up)
+    got, X, W, Y = f64(x.grad), f64(x), f64(w), y.cpu().numpy()
+    want = ref.cross_entropy(X, W, Y, IGNORE, np.full(m, scale))[2]
+    live = Y != IGNORE
+    assert (got[~live] == 0).all()
+    z = X @ W.T
+    rel = 2 * (k + 8) * 2.0 ** -24 * (np.abs(X) @ np.abs(W).T).max(1) + 2.0 ** -20
+    lse = z.max(1) + np.log(np.exp(z - z.max(1)[:, None]).sum(1))
+    p = np.exp(z - lse[:, None])
+    p[np.arange(m), np.where(live, Y, 0)] = 0
+    u, rest = U[F16], p.sum(1)
+    assert rest[live].max() > 1e-4 and rest[live].min() < 1e-8
+    mag = (u + rel)[:, None] * (p @ np.abs(W)) + (rest * rel)[:, None] * np.abs(W[np.where(live, Y, 0)])
+    mag += 2.0 ** -28 * p.max(1)[:, None] * np.abs(W).sum(0) + 2.0 ** -22 * rest[:, None]
+    bound = scale * mag + 2 * u * np.abs(want) * (1 + 2.0 ** -6) + TINY[F16]
+    bad = ~(np.abs(got - want) <= bound) & live[:, None]
+    assert not bad.any(), (bad.sum(), np.argwhere(bad)[0], got[bad][0], want[bad][0], bound[bad][0])
+
+
+def test_units():
+    """dX in units: the same values as without where nothing is lost, powers of two;
+    1 for targets that are no entry, whose rows are as ever."""
+    need_gpu()
+    for dtype in (BF16, F16):
+        x, w, y = _inputs(300, 72, 500, dtype)
+        y[::7], y[3] = IGNORE, 500
+        loss, lse, dx = cross_entropy.linear_cross_entropy_grad(x, w, y)
+        l2, s2, du, unit = cross_entropy.linear_cross_entropy_units(x, w, y)
+        assert torch.equal(lse, s2) and torch.equal(loss[y < 500], l2[y < 500]) and bool(l2[3].isnan())
+        assert bool((torch.frexp(unit)[0] == 0.5).all()) and bool((unit[::7] == 1).all()) and float(unit[3]) == 1
+        assert bool((du[::7] == 0).all()) and bool(du[3].isnan().all())
+        rest = -torch.expm1(-loss.double())
+        at = ((y >= 0) & (y < 500) & (rest > 2.0 ** -60)).nonzero()[:, 0]
+        # [1/8, 1/4), up to the rounding of the loss where it is next to a power of two
+        assert bool(((rest * unit)[at] > 0.12499).all()) and bool(((rest * unit)[at] < 0.25001).all())
+        back = cross_entropy.scale_rows(du, 1 / unit)
+        # bf16: the exponent only; fp16: what the direct form rounds below its normal range
+        if dtype == BF16:
+            assert torch.equal(back[at], dx[at])
+        else:
+            far = (dx.float().abs() >= 2.0 ** -14) & ((du.float().abs() >= 2.0 ** -14)) & (y >= 0)[:, None] & (y < 500)[:, None]
+            assert torch.equal(back[far], dx[far]) and int(far.sum()) > 1000
+
+
+def test_f16_training_step_in_a_graph():
+    need_gpu()
+    x, w, y = _inputs(300, 72, 500, F16)
+    x.requires_grad_()
+
+    def run():
+        loss = cross_entropy.linear_cross_entropy(x, w, y)
+        return loss.detach(), torch.autograd.grad(loss * 4096.0, x)[0]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = run()
+    for seed in range(5, 9):
+        with torch.no_grad():
+            for a, b in zip((x, w, y), _inputs(300, 72, 500, F16, seed)):
+                a.copy_(b)
+            y[::seed] = IGNORE
+        want = run()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
 def test_refusals():
     need_gpu()
     x, w, y = _inputs(4, 64, 50, BF16)

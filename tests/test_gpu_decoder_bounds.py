@@ -91,3 +91,14 @@ def test_cross_entropy(m, k, v, apart, dtype):
                   *cross_entropy.linear_cross_entropy_grad(x, w, y, torch.ones(m, device="cuda"))))
     g = rand((m, k), 3, dtype)
     both(lambda: (cross_entropy.scale_rows(g, torch.arange(m, dtype=torch.float32, device="cuda")),))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("m,k,v", [(1, 8, 1), (17, 72, 129), (8200, 64, 300)])
+def test_cross_entropy_in_units(m, k, v, dtype):
+    need_gpu()
+    x, w = rand((m, k), 1, dtype), rand((v, k), 2, dtype, 0.1)
+    y = torch.randint(0, v, (m,), device="cuda")
+    y[1::3] = -100
+    y[2::5] = 2 ** 50
+    both(lambda: cross_entropy.linear_cross_entropy_units(x, w, y))
