@@ -3,11 +3,14 @@
 //
 // One pass over the keys with a running reference m and sum l in base 2:
 //   p = 2^(c s - m),  c = scale log2 e,  l = sum p,  O = (sum p V) / l.
-// m moves (and O, l are rescaled) only once a row's maximum is more than 2^8
-// above it: p stays below 2^8, which every type here holds, and most tiles need
-// no rescaling.  l is summed in fp32 from the unrounded p; p is rounded to 16
-// bits because it is a matrix operand (a relative 2^-9 or 2^-12 of each term,
-// independent of one another).
+// bf16: m starts at a row's maximum and moves (and O, l are rescaled) only once the
+// maximum is more than 2^8 above: most tiles need no rescaling.  l is summed in fp32
+// from the unrounded p; p is rounded to 16 bits because it is a matrix operand (a
+// relative 2^-9 or 2^-12 of each term, independent of one another).
+// fp16: small p would fall below the type's range and be missing from O but not
+// from l.  m is set 2^12 below the maximum, where p is 2^12, and moves once that is
+// 2^3 more: p stays at most 2^15, is a normal number from 2^-26 of the row's largest on,
+// and nothing above 2^-37 of it is lost.
 //
 // Scores are computed transposed (keys x queries): a lane then holds scores of
 // one query only, so maxima and sums need a single exchange between the
@@ -21,6 +24,15 @@
 
 namespace qlora {
 namespace {
+
+template <typename E>
+struct Reference {
+  static constexpr float below = 0.f, room = 8.f;  // of the maximum; how far that may rise
+};
+template <>
+struct Reference<F16> {
+  static constexpr float below = 12.f, room = 3.f;
+};
 
 // One online-softmax step's state of a lane: reference, and the sum over the
 // keys of its half of the wave.
@@ -141,8 +153,8 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
   // the largest score of a lane's row so far in a tile -> the reference, and what
   // there is of the sums moved to it
   auto refer = [&](float top) {
-    top = half_max(top) * c2;
-    if (__ballot(top > run.m + 8.f)) {
+    top = half_max(top) * c2 - Reference<E>::below;
+    if (__ballot(top > run.m + Reference<E>::room)) {
       const float m = fmaxf(run.m, top);
       const float f = m == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(run.m - m);
       run.m = m;
@@ -334,7 +346,8 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnArgs a) {
       }
     }
     if (b == 0 && half == 0 && live) {
-      const float lse = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+      constexpr float below = Reference<E>::below, f = 1.f / (1 << (int)below);
+      const float lse = l == 0.f ? -INFINITY : ((m + below) + __log2f(l * f)) * kLn2;
       if (a.splits == 1) {
         if (in_bounds(r_at, 1, r_n)) a.lse[r_at] = lse;
       } else {

@@ -586,7 +586,8 @@ int qlora_rope(const qlora_heads *Q, int64_t heads, const qlora_heads *K, int64_
  *     lse = log sum_j exp(scale Q K_j)     (fp32 [tokens_q, heads])
  * A query that sees no key gets O = 0 and lse = -inf, and no gradient.  Masked
  * keys have no effect, whatever they hold: infinities and NaNs as well.
- * Scores, sums and lse are fp32; p is rounded to 16 bits for the product with V.
+ * Scores, sums and lse are fp32; p is rounded to 16 bits for the product with V
+ * (fp16: those 2^-37 below a row's largest are lost to it).
  *   cu_q, cu_k  device int32 [batch + 1], ascending; values outside the tensors
  *               are taken to their ends (no access goes outside)
  *   len_q, len_k  device int32 [batch] or NULL

@@ -7,7 +7,7 @@ import torch
 
 from bit_nf4_quantized_double_amd import attention, rotary
 from decoder_util import attention_reference, close, cu, starts
-from rows_util import f64, need_gpu, rand
+from rows_util import U, f64, need_gpu, rand
 
 pytestmark = pytest.mark.gpu
 
@@ -234,6 +234,31 @@ def test_large_scores():
     close(lse, want["lse"], "lse")
     for got, name in zip(attention.attention_bwd(do, q, k, v, o, lse, cu(lq), cu(lk)), ("dq", "dk", "dv")):
         close(got, want[name], name)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("tq,h,hk", [(1, 2, 2), (2, 64, 64), (200, 2, 1), (300, 128, 2)])
+@pytest.mark.parametrize("sink", [0, 1777, 4096])
+@pytest.mark.parametrize("gap", [8.0, 17.5, 22.0])
+def test_many_small_weights(gap, sink, tq, h, hk, dtype):
+    """One key far above 4096 others, its value zero: what the others add up to is
+    all there is of O.  Scores are exact.  A weight is off by U of itself, and in fp16
+    by at most half the smallest step times 2^-12: 2^-37 of the largest."""
+    need_gpu()
+    tk, d = 4097, 64
+    q, k, v = rand((tq, h, d), 1, dtype), torch.zeros((tk, hk, d), dtype=dtype, device="cuda"), rand((tk, hk, d), 3, dtype)
+    q[..., 0], k[sink, :, 0] = 4.0, gap / 4
+    v = v.abs() + 0.5
+    v[sink] = 0
+    o, lse = attention.attention_fwd(q, k, v, cu([tq]), cu([tk]), causal=False, scale=1.0)
+    p, V = np.exp(-gap), f64(v)
+    total = 1 + 4096 * p
+    want = np.broadcast_to(np.repeat(p * V.sum(0) / total, h // hk, 0), (tq, h, d))
+    assert np.abs(f64(lse) - (gap + np.log(total))).max() <= 2.0 ** -20 * (1 + gap)
+    bound = (U[dtype] * 2 + 2.0 ** -19) * want
+    if dtype == F16:
+        bound = bound + 2.0 ** -37 * np.repeat(V.sum(0), h // hk, 0) / total
+    close(o, (want, bound), "o")
 
 
 @pytest.mark.parametrize("loss_scale", [1.0, 2.0 ** 14, 2.0 ** -14])
