@@ -74,11 +74,11 @@ qlora::Heads heads_arg(const qlora_heads* x, int64_t tokens, int64_t heads, int6
   return qlora::heads_of(x->p, tokens > 1 ? x->token_stride : 0, heads > 1 ? x->head_stride : 0, tokens, heads, d);
 }
 
-int check_attention(const qlora_attention* a) {
+int check_attention(const qlora_attention* a, bool backward) {
   if (!a) return fail(QLORA_ERR_INVALID_ARG, "attention descriptor is NULL");
   const int64_t most = INT_MAX - 255;
   int st;
-  if ((st = check_range(a->tokens_q, most, "tokens_q")) || (st = check_range(a->tokens_k, most, "tokens_k")) ||
+  if ((st = check_range(a->tokens_q, most, "tokens_q")) || (st = check_range(a->tokens_k, (1 << 30) - 1, "tokens_k")) ||
       (st = check_range(a->batch, 1 << 24, "batch")) || (st = check_range(a->heads, 65536, "heads")) ||
       (st = check_range(a->kv_heads, 65536, "kv_heads")) ||
       (st = check_range(a->head_dim, QLORA_MAX_HEAD_DIM, "head_dim")) || (st = check_type16(a->dtype)))
@@ -93,11 +93,14 @@ int check_attention(const qlora_attention* a) {
   if (a->heads) {
     const int64_t group = a->heads / a->kv_heads;
     if (a->tokens_q > most / group) return fail(QLORA_ERR_SHAPE, "tokens_q * heads / kv_heads exceeds 2^31 - 256");
-    // workgroups of a launch: fewer than 2^24
-    if (((a->tokens_q * group + 31) / 32 + a->batch + 2) * a->kv_heads >= (1 << 24) ||
-        ((a->tokens_k + 127) / 128 + a->batch + 2) * a->heads >= (1 << 24) ||
-        (a->tokens_k / 4 + a->batch >= (1 << 24) - 2) || a->batch * a->heads / 4 >= (1 << 24) - (1 << 20) - 1)
+    // workgroups of a launch: fewer than 2^24 (the forward's are of rows of queries only;
+    // the backward's of dK and dV and of their join; delta's, at most batch heads / 4 +
+    // 2^20, are then fewer too)
+    if (((a->tokens_q * group + 31) / 32 + a->batch + 2) * a->kv_heads >= (1 << 24))
       return fail(QLORA_ERR_SHAPE, "too many rows for one launch");
+    if (backward && (((a->tokens_k + 127) / 128 + a->batch + 2) * a->heads >= (1 << 24) ||
+                     a->tokens_k / 4 + a->batch >= (1 << 24) - 2))
+      return fail(QLORA_ERR_SHAPE, "too many keys or sequences for one launch of the backward");
   }
   return QLORA_OK;
 }
@@ -236,7 +239,7 @@ int qlora_rope(const qlora_heads* Q, int64_t heads, const qlora_heads* K, int64_
 size_t qlora_attention_workspace_bytes(int op, const qlora_attention* a) {
   size_t n = 0;
   guarded([&] {
-    if (check_attention(a) != QLORA_OK || nothing(a)) return (int)QLORA_OK;
+    if (check_attention(a, op == QLORA_OP_BWD) != QLORA_OK || nothing(a)) return (int)QLORA_OK;
     if (op == QLORA_OP_FWD)
       n = qlora::attn_part_bytes(plan_of(a, qlora::device_compute_units()), a->tokens_q, a->heads, a->head_dim);
     else if (op == QLORA_OP_BWD)
@@ -250,7 +253,7 @@ int qlora_attention_plan(const qlora_attention* a, int compute_units, int64_t ou
   return guarded([&] {
     if (!out) return fail(QLORA_ERR_INVALID_ARG, "out is NULL");
     int st;
-    if ((st = check_attention(a))) return st;
+    if ((st = check_attention(a, false))) return st;
     const qlora::AttnPlan p = plan_of(a, compute_units > 0 ? compute_units : qlora::device_compute_units());
     out[0] = p.rows;
     out[1] = p.splits;
@@ -262,7 +265,7 @@ int qlora_attention_fwd(const qlora_attention* a, const qlora_heads* Q, const ql
                         const qlora_heads* O, float* lse, void* ws, size_t ws_bytes, hipStream_t stream) {
   return guarded([&] {
     int st;
-    if ((st = check_attention(a))) return st;
+    if ((st = check_attention(a, false))) return st;
     const int64_t d = a->head_dim;
     if ((st = check_attn_heads(Q, a->tokens_q, a->heads, d, false, "Q")) ||
         (st = check_attn_heads(K, a->tokens_k, a->kv_heads, d, false, "K")) ||
@@ -290,7 +293,7 @@ int qlora_attention_bwd(const qlora_attention* a, const qlora_heads* dO, const q
                         const qlora_heads* dK, const qlora_heads* dV, void* ws, size_t ws_bytes, hipStream_t stream) {
   return guarded([&] {
     int st;
-    if ((st = check_attention(a))) return st;
+    if ((st = check_attention(a, true))) return st;
     const int64_t d = a->head_dim, tq = a->tokens_q, tk = a->tokens_k, h = a->heads, hk = a->kv_heads;
     if ((st = check_attn_heads(dO, tq, h, d, false, "dO")) || (st = check_attn_heads(Q, tq, h, d, false, "Q")) ||
         (st = check_attn_heads(K, tk, hk, d, false, "K")) || (st = check_attn_heads(V, tk, hk, d, false, "V")) ||

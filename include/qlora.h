@@ -596,7 +596,11 @@ int qlora_rope(const qlora_heads *Q, int64_t heads, const qlora_heads *K, int64_
  *   head_dim    a multiple of 8, at most 128.  Pointers are 16-byte aligned and
  *               strides multiples of 8 (QLORA_ERR_ALIGN), token strides at most
  *               2^23 elements (QLORA_ERR_SHAPE); scale is positive.
- *               tokens_q * heads / kv_heads and tokens_k at most 2^31 - 256.
+ *               tokens_q * heads / kv_heads is at most 2^31 - 256, tokens_k below 2^30, batch
+ *               at most 2^24; of workgroups a launch has fewer than 2^24: that is
+ *               (tokens_q heads / kv_heads / 32 + batch + 2) kv_heads, rounded up, and in the
+ *               backward also (tokens_k / 128 + batch + 2) heads and tokens_k / 4 + batch + 2
+ *               (QLORA_ERR_SHAPE).
  * Backward, from dO, O, lse (as the forward wrote them):
  *     dV = sum P dO, dS = P (dO V - sum dO O), dQ = scale dS K, dK = scale sum dS Q,
  * dK and dV summed over the heads that share them (sum dO O as sum P (dO V) for a

@@ -91,6 +91,31 @@ def test_attention_refuses_sizes(L, change, want):
     assert L.qlora_attention_plan(ctypes.byref(c), 256, (ctypes.c_int64 * 2)()) == want
 
 
+@pytest.mark.parametrize("most,over", [
+    (dict(tokens_q=32 * ((1 << 21) - 67), tokens_k=1, batch=64, heads=8, kv_heads=8), dict(tokens_q=32 * ((1 << 21) - 67) + 1)),
+    (dict(tokens_q=1, tokens_k=(1 << 30) - 1, batch=16, heads=128, kv_heads=8), dict(tokens_k=1 << 30)),
+    (dict(tokens_q=1 << 24, tokens_k=(1 << 30) - 1, batch=1 << 20, heads=8, kv_heads=8), dict(batch=3 << 19))])
+def test_attention_forward_limits(L, most, over):
+    """Either side of each; keys have no part in the forward's launches."""
+    out = (ctypes.c_int64 * 2)()
+    assert L.qlora_attention_plan(ctypes.byref(describe(**most)), 256, out) == 0
+    c = describe(**{**most, **over})
+    assert L.qlora_attention_plan(ctypes.byref(c), 256, out) == SHAPE and fwd(L, c) == bwd(L, c) == SHAPE
+
+
+@pytest.mark.parametrize("most,over", [
+    (dict(tokens_q=1, tokens_k=128 * ((1 << 17) - 67), batch=64, heads=128, kv_heads=8), dict(tokens_k=128 * ((1 << 17) - 67) + 1)),
+    (dict(tokens_q=1, tokens_k=4 * ((1 << 24) - 2 - 64) - 1, batch=64, heads=8, kv_heads=8), dict(tokens_k=4 * ((1 << 24) - 2 - 64))),
+    (dict(tokens_q=1, tokens_k=1, batch=(1 << 21) - 4, heads=8, kv_heads=1), dict(batch=(1 << 21) - 3))])
+def test_attention_backward_limits(L, most, over):
+    """The forward takes both sides of each."""
+    out, need = (ctypes.c_int64 * 2)(), lambda c: L.qlora_attention_workspace_bytes(BWD, ctypes.byref(c))
+    c = describe(**{**most, **over})
+    assert need(c) == 0 and bwd(L, c) == SHAPE and b"backward" in L.qlora_last_error()
+    assert L.qlora_attention_plan(ctypes.byref(c), 256, out) == 0
+    assert need(describe(**most)) > 0
+
+
 @pytest.mark.parametrize("name", ["q", "k", "v", "o"])
 def test_attention_refuses_tensors(L, name):
     call = lambda **t: (fwd(L, describe(), **t), bwd(L, describe(), **t))

@@ -453,6 +453,23 @@ def test_offsets_past_32_bits():
         assert torch.equal(dv, want[4]) and torch.equal(dk, want[3])
 
 
+def test_a_cache_of_many_rows():
+    """More rows of a cache, times heads, than a backward takes: the forward does."""
+    need_gpu()
+    h, hk, d, room, lk = 128, 1, 8, 1 << 26, [700, 30]
+    q, k, v, _ = _inputs([1, 1], lk, h, hk, d, BF16)
+    wide = [torch.empty(2 * room, hk, d, dtype=BF16, device="cuda") for _ in range(2)]
+    for x, y in zip((k, v), wide):
+        y[:lk[0]], y[room:room + lk[1]] = x[:lk[0]], x[lk[0]:]
+    ends = torch.arange(3, dtype=torch.int32, device="cuda")
+    o, lse = attention.attention_fwd(q, *wide, ends, ends * room, lengths_k=torch.tensor(lk, dtype=torch.int32, device="cuda"))
+    want = attention_reference(q, k, v, [1, 1], lk, True)
+    close(o, want["o"], "o")
+    close(lse, want["lse"], "lse")
+    with pytest.raises(RuntimeError, match="backward"):
+        attention.attention_bwd(q, q, *wide, o, lse, ends, ends * room)
+
+
 def test_no_sequences():
     need_gpu()
     q, k, v, do = _inputs([5], [5], 2, 2, 64, BF16)
