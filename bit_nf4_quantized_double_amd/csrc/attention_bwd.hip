@@ -613,19 +613,24 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_kv(AttnArgs a) {
     const uint32_t lds0 = lds_offset(lds) + wave * 1024, rows0 = lds_offset(wave == 0 ? &s_lse[0][0] : &s_delta[0][0]);
     auto direct = [&](int32_t rt, int buf) {
       const int32_t tok0 = rt * BQ / group, left = rt < r1 ? nq - tok0 : 0;  // whole tokens: group divides BQ
-      const LdsSource rq = lds_source(a.q.p + (left > 0 ? q_at + tok0 * a.q.token : 0), 0x7fffffff);
-      const LdsSource ro = lds_source(a.dout.p + (left > 0 ? d_at + tok0 * a.dout.token : 0), 0x7fffffff);
+      // (descriptors of the tile's size would check every offset, but cost fp16, whose
+      // registers are all taken, 4 %: the bounds-checked build does)
+      const int64_t q_tile = left > 0 ? q_at + tok0 * a.q.token : 0, d_tile = left > 0 ? d_at + tok0 * a.dout.token : 0;
+      const LdsSource rq = lds_source(a.q.p + q_tile, 0x7fffffff), ro = lds_source(a.dout.p + d_tile, 0x7fffffff);
 #pragma unroll
       for (int u = 0; u < PER; ++u) {
         const int32_t on = u * (256 / CH) / group;
         const bool ok = mytok + on < left && ch8 < (uint32_t)a.d;
-        load_to_lds16(rq, ok ? q_off + on * 2 * (uint32_t)a.q.token : kOOB, lds0 + buf * 2 * BYTES + u * 4096);
-        load_to_lds16(ro, ok ? d_off + on * 2 * (uint32_t)a.dout.token : kOOB, lds0 + buf * 2 * BYTES + BYTES + u * 4096);
+        const uint32_t qo = q_off + on * 2 * (uint32_t)a.q.token, go = d_off + on * 2 * (uint32_t)a.dout.token;
+        load_to_lds16(rq, ok && in_bounds(q_tile + qo / 2, 8, a.q.n) ? qo : kOOB, lds0 + buf * 2 * BYTES + u * 4096);
+        load_to_lds16(ro, ok && in_bounds(d_tile + go / 2, 8, a.dout.n) ? go : kOOB, lds0 + buf * 2 * BYTES + BYTES + u * 4096);
       }
       // rows past the last: zeros, and so P dO and dS Q are zero whatever P is
       if (wave < 2) {
-        const LdsSource rl = lds_source((wave == 0 ? a.lse2 : a.delta) + (left > 0 ? (q0 + tok0) * a.heads + head0 : 0), 0x7fffffff);
-        load_to_lds4(rl, lane < BQ && ltok < left ? l_off : kOOB, rows0 + buf * 256);
+        const int64_t l_tile = left > 0 ? (q0 + tok0) * a.heads + head0 : 0;
+        const LdsSource rl = lds_source((wave == 0 ? a.lse2 : a.delta) + l_tile, 0x7fffffff);
+        const bool ok = lane < BQ && ltok < left && in_bounds(l_tile + l_off / 4, 1, a.tq * a.heads);
+        load_to_lds4(rl, ok ? l_off : kOOB, rows0 + buf * 256);
       }
     };
     direct(rd, 0);

@@ -57,6 +57,23 @@ def test_attention(lq, lk, h, hk, d, causal, dtype):
     both(run)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("h,hk,d", [(8, 1, 128), (4, 2, 72), (16, 1, 64), (3, 3, 128)])
+def test_attention_heads_first(h, hk, d, dtype):
+    """[heads, tokens, d] tensors, the last head at the end of its buffer: whole tiles of
+    dK and dV read rows of heads that are far apart."""
+    need_gpu()
+    t = 517
+    q, do = (rand((h, t, d), i, dtype).transpose(0, 1) for i in (1, 2))
+    k, v = (rand((hk, t, d), i, dtype).transpose(0, 1) for i in (3, 4))
+
+    def run():
+        o, lse = attention.attention_fwd(q, k, v, cu([t]))
+        return (o, lse, *attention.attention_bwd(do, q, k, v, o, lse, cu([t])))
+
+    both(run)
+
+
 @pytest.mark.parametrize("ends", [[0, 500], [-7, 40, 30, 90], [90, 10, 2 ** 31 - 1], [-(2 ** 31), 5, 5]])
 def test_ends_outside_the_tensors(ends):
     """cu that does not ascend or lies outside, and lengths that do: whatever comes
