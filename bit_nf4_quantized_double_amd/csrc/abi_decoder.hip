@@ -221,6 +221,9 @@ int qlora_rope(const qlora_heads* Q, int64_t heads, const qlora_heads* K, int64_
     };
     if (!in_place(Q, Qo, heads) || !in_place(K, Ko, kv_heads))
       return fail(QLORA_ERR_INVALID_ARG, "in place, strides must be the same");
+    // heads of one are written while the other's are read
+    if (heads > 0 && kv_heads > 0 && (Qo->p == Ko->p || Qo->p == K->p || Ko->p == Q->p))
+      return fail(QLORA_ERR_INVALID_ARG, "Qo and Ko must be apart from each other and from the other's input");
     if (rot > 0) {
       if (!positions || !turns) return fail(QLORA_ERR_INVALID_ARG, "positions or turns is NULL");
       if (reinterpret_cast<uintptr_t>(positions) % (positions64 ? 8 : 4) || reinterpret_cast<uintptr_t>(turns) % 8)

@@ -159,7 +159,7 @@ def _turn(Q, K, positions, freqs: Frequencies, interleaved: bool, inverse: bool,
 def rotate(Q: torch.Tensor, K: torch.Tensor | None, positions: torch.Tensor, freqs: Frequencies, *,
            interleaved: bool = False, Q_out: torch.Tensor | None = None, K_out: torch.Tensor | None = None):
     """Returns (Q, K) turned to their positions.  ``Q_out`` and ``K_out`` may be Q
-    and K (in place).  K may be None."""
+    and K (in place), not each other or K and Q.  K may be None."""
     return _turn(Q, K, positions, freqs, bool(interleaved), False, Q_out, K_out)
 
 

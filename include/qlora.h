@@ -562,7 +562,9 @@ typedef struct {
  * backward.  The sines are made in fp32 from the angle modulo a turn, which is
  * exact for every position (turns wraps), and a result is rounded once.
  *   Q, K        in; K->p may be NULL with kv_heads 0
- *   Qo, Ko      out; may be Q and K themselves (same pointer and strides)
+ *   Qo, Ko      out; may be Q and K themselves (same pointer and strides), and are
+ *               otherwise apart from both and from each other (the same pointer:
+ *               QLORA_ERR_INVALID_ARG)
  *   positions   int32 [tokens], or int64 where `positions64`; negative ones too
  *   turns       device uint64 [rot / 2], 8-byte aligned
  * Any sizes, strides and 2-byte alignment; heads that can be read 16 bytes at a

@@ -49,6 +49,13 @@ def test_rope_refuses_other_strides_in_place(L):
     assert rope(L, k=heads(), hk=4, ko=heads(head=72, token=288)) == INVALID and b"strides" in L.qlora_last_error()
 
 
+def test_rope_refuses_outputs_that_are_the_other_input(L):
+    at = [heads(P + 0x10000 * i) for i in range(4)]
+    for q, k, qo, ko in ((0, 1, 2, 2), (0, 1, 1, 2), (0, 1, 2, 0), (0, 1, 1, 0), (0, 0, 0, 0), (0, 0, 0, 1)):
+        assert rope(L, q=at[q], k=at[k], hk=4, qo=at[qo], ko=at[ko]) == INVALID
+        assert b"apart" in L.qlora_last_error()
+
+
 def test_rope_has_nothing_to_do(L):
     assert rope(L, t=0, q=heads(0), qo=heads(0), pos=None, turns=None) == 0
     assert rope(L, h=0, q=heads(0), qo=heads(0)) == 0
