@@ -451,11 +451,11 @@ __global__ __launch_bounds__(16 * kStatParts) void k_ce_stats(CeArgs a, CeRound 
   const float lse = __builtin_fmaf(ref, 0.693359375f, __builtin_fmaf(ref, -2.12194440e-4f, logf(total)));
   if (in_bounds(m, 1, r.m)) {
     a.lse[m] = lse;
-    a.loss[m] = ignored ? 0.f : bad ? NAN : rest < mine ? log1pf(rest / mine) : lse - z;
+    a.loss[m] = ignored ? 0.f : bad ? NAN : rest < mine && z < INFINITY ? log1pf(rest / mine) : lse - z;
   }
   if constexpr (GRAD) {
     r.c1[m] = scale / total * (Half<E>::f16 ? 1.f / 32768.f : 1.f);
-    r.c2[m] = rest / total;
+    r.c2[m] = z == INFINITY ? NAN : rest / total;  // (an infinity less an infinity, as in the loss)
   }
 }
 

@@ -167,6 +167,24 @@ def test_ignored_and_invalid_targets():
     assert bool((a[0] == 0).all()) and bool((a[2] == 0).all())
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("v", [1, 50, 300])
+def test_a_target_whose_logit_is_infinite(v, dtype):
+    """It alone, every other one -inf: the loss is inf - inf, no zero, and the gradient
+    no number either; other tokens do not notice."""
+    need_gpu()
+    x, w, y = _inputs(20, 64, v, dtype)
+    w[:, 4] = -1
+    w[y[7], 4] = 1
+    clean = cross_entropy.linear_cross_entropy_grad(x, w, y)
+    x[7, 4] = float("inf")
+    loss, lse, dx = cross_entropy.linear_cross_entropy_grad(x, w, y)
+    alone, _ = cross_entropy.linear_cross_entropy_fwd(x, w, y)
+    assert bool(loss[7].isnan()) and bool(alone[7].isnan()) and float(lse[7]) == float("inf") and bool(dx[7].isnan().all())
+    keep = [i for i in range(20) if i != 7]
+    assert torch.equal(loss[keep], clean[0][keep]) and torch.equal(dx[keep], clean[2][keep])
+
+
 def test_no_tokens():
     need_gpu()
     x, w, y = rand((0, 64), 1), rand((10, 64), 2), torch.empty(0, dtype=torch.int64, device="cuda")
