@@ -46,9 +46,10 @@ struct Running {
 constexpr int kLeastKeys = 512;
 
 // KW = 1: 128 rows a workgroup, 32 a wave; tiles of 64 keys, double buffered,
-// shared by the waves.  Bound by the matrix cores, 56 % busy near 1.8 GHz, and the
-// waits between their products (8192 causal tokens, 32 heads of 128 on 8: 530 to 580
-// us, 0.95 to 1.04 PFLOP/s).  Each operand read from LDS serves one product; 64 rows a
+// shared by the waves.  Bound by the matrix cores, 57 % busy near 1.8 GHz, and the
+// vector instructions between their products, issued in 60 % of the cycles, the
+// products' own issue among them (8192 causal tokens, 32 heads of 128 on 8: 515 to 580
+// us, 0.95 to 1.07 PFLOP/s).  Each operand read from LDS serves one product; 64 rows a
 // wave would halve the reads (28 % of the cycles), but with 512 registers a lane the half
 // that only the matrix instructions can use costs 5 moves a product (440 -> 585 us for
 // four turns of a prompt, 64 heads on 8).

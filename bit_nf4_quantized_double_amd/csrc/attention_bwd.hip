@@ -18,7 +18,8 @@
 // infinities and NaNs of the second products' other operand are kept out of tiles
 // that are seen only in part.  dO's are added to dV at the end where they are
 // seen; Q's show in dK (and dV) through their rows' lse, which is a NaN; a K that
-// is not finite makes the dQ of the rows that see it NaN.
+// is not finite makes the dQ of the rows that see it NaN (and its own dK and dV,
+// through rows past the last, also where all scores are -inf).
 #include <algorithm>
 #include <climits>
 #include <type_traits>
@@ -192,9 +193,10 @@ __device__ __forceinline__ float to_range(float bound) {
 }
 
 // dQ: 128 rows a workgroup, 32 a wave, tiles of 64 keys.  Q, dO and dQ stay in
-// registers.  Bound by the matrix cores, 66 % busy near 1.8 GHz (8192 causal tokens, 32
+// registers.  Bound by the matrix cores, 67 % busy near 1.8 GHz (8192 causal tokens, 32
 // heads of 128 on 8: 690 to 770 us, 1.07 to 1.19 PFLOP/s); they wait for operands from
-// LDS, one read a product, and for the exponentials.
+// LDS, one read a product, and share the issue with vector instructions (50 % of the
+// cycles).
 template <typename E, int DB>
 __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
   constexpr int BN = 64, BM = 128;
@@ -385,7 +387,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_q(AttnArgs a) {
 // keys a wave with 512 registers a lane).  Operands come from LDS through a ring of
 // four, ahead of their products (six and eight were slower); exponentials are made
 // beside dO V^T and dS beside dV.  Bound by waits for operands, one or two of which
-// each product reads from LDS (36 % busy): matrix cores 48 % busy (8192 causal tokens,
+// each product reads from LDS (36 to 40 % busy): matrix cores 48 to 52 % busy (8192 causal tokens,
 // 32 heads of 128 on 8: 1.1 to 1.3 ms, 0.85 to 1.0 PFLOP/s), and 14 % of the time the last
 // workgroups leave places empty.  Waves that skip row tiles none of whose rows see
 // their keys: no faster.
@@ -625,7 +627,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_bwd_kv(AttnArgs a) {
         load_to_lds16(rq, ok && in_bounds(q_tile + qo / 2, 8, a.q.n) ? qo : kOOB, lds0 + buf * 2 * BYTES + u * 4096);
         load_to_lds16(ro, ok && in_bounds(d_tile + go / 2, 8, a.dout.n) ? go : kOOB, lds0 + buf * 2 * BYTES + BYTES + u * 4096);
       }
-      // rows past the last: zeros, and so P dO and dS Q are zero whatever P is
+      // rows past the last: zeros, and so P dO and dS Q are zero whatever P is (of a finite K)
       if (wave < 2) {
         const int64_t l_tile = left > 0 ? (q0 + tok0) * a.heads + head0 : 0;
         const LdsSource rl = lds_source((wave == 0 ? a.lse2 : a.delta) + l_tile, 0x7fffffff);

@@ -607,7 +607,8 @@ int qlora_rope(const qlora_heads *Q, int64_t heads, const qlora_heads *K, int64_
  *     dV = sum P dO, dS = P (dO V - sum dO O), dQ = scale dS K, dK = scale sum dS Q,
  * dK and dV summed over the heads that share them (sum dO O as sum P (dO V) for a
  * query that sees up to 32 keys: O is rounded).  P and dS are rounded to 16 bits for
- * the products.  A K that is not finite makes dQ of the queries that see it NaN.
+ * the products.  A K that is not finite makes dQ of the queries that see it NaN,
+ * and its own dK and dV may be NaN where the formula has a zero (every score -inf).
  * Same inputs, same bits: no atomics.  fp16: dS is kept in range by a power of two
  * from the largest finite |dO| and |V|, of the row for dQ and of the whole batch
  * for dK; what is 2^-30 below these bounds is lost.
